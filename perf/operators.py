@@ -331,7 +331,7 @@ def _run_own(s):
     if c["kind"] == "cells":
         handle = ep.LowLatencyHandle(s["src"], s["slot"], c["S"], c["E"], c["H"])
         return buf.low_latency_expert_ffn(s["packed"], s["count"], handle, s["w13"], s["w2"], out=s["out"])
-    rows = buf.expert_rows(s["ids"], s["prefix"])
+    rows = buf.expert_rows(s["ids"], s["prefix"], num_tokens=c["T"])
     y, saved = buf.expert_ffn(s["x"], rows, s["weights"], s["w13"], s["w2"], save=c["step"])
     if not c["step"]:
         return y
