@@ -6,6 +6,8 @@ Importing it requires the built library -- there is no CPU fallback.
 """
 
 from . import abi  # noqa: F401  (raises ImportError when libep.so is missing)
-from .buffer import Buffer, Handle, Layout, LowLatencyHandle  # noqa: F401
+from .buffer import (Buffer, ExpertRows, Handle, Layout, LowLatencyHandle,  # noqa: F401
+                     fp8_product, rms_norm, rms_norm_backward)
 
-__all__ = ["Buffer", "Handle", "Layout", "LowLatencyHandle", "abi"]
+__all__ = ["Buffer", "ExpertRows", "Handle", "Layout", "LowLatencyHandle", "abi", "fp8_product",
+           "rms_norm", "rms_norm_backward"]

@@ -30,7 +30,9 @@ EXPORTS = (
     "ep_handle_dims", "ep_handle_nbytes", "ep_handle_free", "ep_pool_trim", "ep_status_str",
     "ep_last_hip_error", "ep_version", "ep_set_tuning", "ep_tuning_list", "ep_ll_dispatch_fp8",
     "ep_ll_combine_fp8", "ep_mask_update", "ep_mask_clean", "ep_mask_query", "ep_lb_prefetch_weights",
-    "ep_lb_reduce_grads", "ep_pool_stats", "ep_get_dispatch_layout_noalloc",
+    "ep_lb_reduce_grads", "ep_pool_stats", "ep_get_dispatch_layout_noalloc", "ep_rms_norm",
+    "ep_rms_norm_backward_workspace", "ep_rms_norm_backward", "ep_fp8_product", "ep_ll_expert_ffn",
+    "ep_ll_expert_ffn_fp8", "ep_expert_rows", "ep_expert_ffn", "ep_expert_ffn_backward",
 )
 
 
@@ -50,6 +52,12 @@ class LayoutOut(ctypes.Structure):
                 ("send_head", ctypes.c_void_p),
                 ("recv_src_idx", ctypes.c_void_p),
                 ("recv_src_cap", ctypes.c_int64)]
+
+
+class ExpertGroups(ctypes.Structure):
+    _fields_ = [("num_rows", ctypes.c_int64), ("pair_cap", ctypes.c_int64),
+                ("expert_offsets", ctypes.c_void_p), ("pair_row", ctypes.c_void_p),
+                ("pair_slot", ctypes.c_void_p), ("row_pair", ctypes.c_void_p)]
 
 
 class EpError(RuntimeError):
@@ -72,6 +80,7 @@ def _load():
     import torch  # noqa: F401
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+    f32, sz, pgroups = ctypes.c_float, ctypes.c_size_t, ctypes.POINTER(ExpertGroups)
     pdims, pout = ctypes.POINTER(Dims), ctypes.POINTER(LayoutOut)
     sig = {
         "ep_max_recv_rows": (i64, [pdims]),
@@ -89,6 +98,15 @@ def _load():
         "ep_mask_query": (ctypes.c_int, [vp, i32, vp, vp]),
         "ep_lb_prefetch_weights": (ctypes.c_int, [vp, vp, vp, i32, i32, i64, vp]),
         "ep_lb_reduce_grads": (ctypes.c_int, [vp, vp, vp, i32, i32, i64, vp]),
+        "ep_rms_norm": (ctypes.c_int, [i32, i32, f32] + [vp] * 9),
+        "ep_rms_norm_backward_workspace": (sz, [i32, i32]),
+        "ep_rms_norm_backward": (ctypes.c_int, [i32, i32] + [vp] * 8 + [sz, vp]),
+        "ep_fp8_product": (ctypes.c_int, [i32, i32, i32] + [vp] * 6),
+        "ep_ll_expert_ffn": (ctypes.c_int, [pdims, i32, i32] + [vp] * 7),
+        "ep_ll_expert_ffn_fp8": (ctypes.c_int, [pdims, i32, i32] + [vp] * 11),
+        "ep_expert_rows": (ctypes.c_int, [pdims, vp, vp, i64, i64] + [vp] * 6),
+        "ep_expert_ffn": (ctypes.c_int, [pdims, i32, pgroups] + [vp] * 9),
+        "ep_expert_ffn_backward": (ctypes.c_int, [pdims, i32, pgroups] + [vp] * 15),
         "ep_handle_copy_layout": (ctypes.c_int, [vp, pout, vp]),
         "ep_handle_num_recv": (ctypes.c_int, [vp, ctypes.POINTER(i64)]),
         "ep_handle_dims": (ctypes.c_int, [vp, pdims]),

@@ -49,6 +49,114 @@ def _same_device(*ts):
         raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
 
 
+def _here(*ts):
+    """One device, the current one: kernels go to its current stream."""
+    _same_device(*ts)
+    t = next(t for t in ts if t is not None)
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _fp8_pair(pair, name: str, ndim: int, row_blocks: bool):
+    """Checks (codes, scales): codes float8_e4m3fn or uint8 with a last dimension
+    of whole 128-element blocks, and one fp32 scale per block of a row (or, with
+    row_blocks, per 128 x 128 block of a weight).  Returns both, codes as bytes."""
+    if not isinstance(pair, (tuple, list)) or len(pair) != 2:
+        raise TypeError(f"{name} must be a pair (codes, scales)")
+    q, sc = pair
+    if q.dtype == torch.float8_e4m3fn:
+        q = q.view(torch.uint8)
+    _need(q, torch.uint8, f"{name} codes", ndim)
+    _need(sc, torch.float32, f"{name} scales", ndim)
+    if q.shape[-1] % 128:
+        raise ValueError(f"{name}: rows must be whole 128-element blocks")
+    shape = list(q.shape)
+    shape[-1] //= 128
+    if row_blocks:
+        shape[-2] = -(-shape[-2] // 128)
+    _shape(sc, shape, f"{name} scales")
+    return q, sc
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+             residual: Optional[torch.Tensor] = None, use_fp8: bool = False, bf16_out: bool = True):
+    """Root-mean-square norm of bf16 rows x [T, H], with residual [T, H] added
+    first.  Returns (out, fp8, residual_out, rstd): out [T, H] bf16 (None without
+    bf16_out), with use_fp8 the pair (codes [T, H] float8_e4m3fn, scales [T, H/128])
+    in the format of low_latency_dispatch(use_fp8=True), the bf16 sum x + residual
+    (None without residual) and rstd [T] fp32, which the backward pass takes."""
+    _need(x, torch.bfloat16, "x", 2)
+    _need(weight, torch.bfloat16, "weight", 1)
+    T, H = x.shape
+    _shape(weight, (H,), "weight")
+    if residual is not None:
+        _need(residual, torch.bfloat16, "residual", 2)
+        _shape(residual, (T, H), "residual")
+    if not (use_fp8 or bf16_out):
+        raise ValueError("nothing to return: neither bf16_out nor use_fp8")
+    _here(x, weight, residual)
+    dev = x.device
+    out = torch.empty_like(x) if bf16_out else None
+    q = torch.empty((T, H), dtype=torch.uint8, device=dev) if use_fp8 else None
+    sc = torch.empty((T, H // 128), dtype=torch.float32, device=dev) if use_fp8 else None
+    res = torch.empty_like(x) if residual is not None else None
+    rstd = torch.empty(T, dtype=torch.float32, device=dev)
+    if use_fp8 and H % 128:
+        raise ValueError("use_fp8 needs rows of whole 128-element blocks")
+    if T > 0:
+        abi.check(abi.lib().ep_rms_norm(T, H, float(eps), abi.ptr(x), abi.ptr(residual),
+                                        abi.ptr(weight), abi.ptr(res), abi.ptr(out), abi.ptr(q),
+                                        abi.ptr(sc), abi.ptr(rstd), abi.current_stream()),
+                  "ep_rms_norm")
+    return out, (q.view(torch.float8_e4m3fn), sc) if use_fp8 else None, res, rstd
+
+
+def rms_norm_backward(dout: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                      dresidual: Optional[torch.Tensor] = None):
+    """Gradients of rms_norm: h is its residual_out (x without a residual), dresidual
+    the gradient that arrived at residual_out.  Returns (dx [T, H] bf16, the gradient
+    of x and of residual alike, and dweight [H] fp32)."""
+    _need(dout, torch.bfloat16, "dout", 2)
+    _need(h, torch.bfloat16, "h", 2)
+    _need(weight, torch.bfloat16, "weight", 1)
+    _need(rstd, torch.float32, "rstd", 1)
+    T, H = dout.shape
+    _shape(h, (T, H), "h")
+    _shape(weight, (H,), "weight")
+    _shape(rstd, (T,), "rstd")
+    if dresidual is not None:
+        _need(dresidual, torch.bfloat16, "dresidual", 2)
+        _shape(dresidual, (T, H), "dresidual")
+    _here(dout, h, weight, rstd, dresidual)
+    dx = torch.empty_like(dout)
+    dweight = torch.empty(H, dtype=torch.float32, device=dout.device)
+    size = int(abi.lib().ep_rms_norm_backward_workspace(T, H))
+    work = torch.empty(size, dtype=torch.uint8, device=dout.device)
+    abi.check(abi.lib().ep_rms_norm_backward(T, H, abi.ptr(dout), abi.ptr(h), abi.ptr(weight),
+                                             abi.ptr(rstd), abi.ptr(dresidual), abi.ptr(dx),
+                                             abi.ptr(dweight), abi.ptr(work), size,
+                                             abi.current_stream()), "ep_rms_norm_backward")
+    return dx, dweight
+
+
+def fp8_product(a, w) -> torch.Tensor:
+    """a (codes [M, K], scales [M, K/128]) times the transpose of w (codes [N, K],
+    scales [ceil(N/128), K/128]), both float8_e4m3fn with fp32 scales: bf16 [M, N],
+    summed in fp32."""
+    aq, asc = _fp8_pair(a, "a", 2, False)
+    wq, wsc = _fp8_pair(w, "w", 2, True)
+    (M, K), N = aq.shape, wq.shape[0]
+    _shape(wq, (N, K), "w codes")
+    _here(aq, asc, wq, wsc)
+    out = torch.empty((M, N), dtype=torch.bfloat16, device=aq.device)
+    if M > 0:
+        abi.check(abi.lib().ep_fp8_product(M, N, K, abi.ptr(aq), abi.ptr(asc), abi.ptr(wq),
+                                           abi.ptr(wsc), abi.ptr(out), abi.current_stream()),
+                  "ep_fp8_product")
+    return out
+
+
 @dataclass
 class Layout:
     """Device copies of a dispatch layout ("What the Handle Contains")."""
@@ -130,6 +238,22 @@ class LowLatencyHandle:
     num_slots: int
     num_experts: int
     hidden: int
+
+
+@dataclass
+class ExpertRows:
+    """Dispatched rows grouped by expert (expert_rows): pairs (row, slot) sorted by
+    (expert, row, slot).  The pair tensors have room for every slot of the batch."""
+
+    expert_offsets: torch.Tensor  # int32 [E + 1]
+    pair_row: torch.Tensor  # int32 [pairs], sign bit: the only pair of its row
+    pair_slot: torch.Tensor  # int32 [pairs], row * K + slot
+    row_pair: torch.Tensor  # int32 [rows, K], -1 for a slot without a pair
+
+    def _raw(self) -> abi.ExpertGroups:
+        return abi.ExpertGroups(self.row_pair.shape[0], self.pair_row.shape[0],
+                                self.expert_offsets.data_ptr(), self.pair_row.data_ptr(),
+                                self.pair_slot.data_ptr(), self.row_pair.data_ptr())
 
 
 class Buffer:
@@ -394,6 +518,167 @@ class Buffer:
                                           abi.ptr(out), abi.current_stream()),
                   "ep_ll_combine")
         return out, None, None
+
+    # ------------------------------------------------------------- experts
+    def _expert_weights(self, w13: torch.Tensor, w2: torch.Tensor, H: int) -> int:
+        """Checks bf16 expert weights w13 [E, 2 I, H], w2 [E, H, I]; returns I."""
+        _need(w13, torch.bfloat16, "w13", 3)
+        _need(w2, torch.bfloat16, "w2", 3)
+        inter = w2.shape[2]
+        _shape(w13, (self.num_experts, 2 * inter, H), "w13")
+        _shape(w2, (self.num_experts, H, inter), "w2")
+        return inter
+
+    def low_latency_expert_ffn(self, x, packed_count: torch.Tensor, handle: LowLatencyHandle, w13, w2,
+                               out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """The experts' gated feed-forward on the cells of low_latency_dispatch:
+        act = silu(x Wg^T) * (x Wu^T), out = act W2^T for every used cell, in
+        packed_x's layout [E/R, R, slots, H] bf16, which low_latency_combine takes.
+        x is packed_x (bf16; w13 [E, 2 I, H] with the gate's rows first, w2 [E, H, I],
+        bf16) or the FP8 pair of low_latency_dispatch(use_fp8=True) (w13 and w2 pairs
+        of codes and scales [E, 2 I/128, H/128], [E, H/128, I/128]; the activation is
+        quantised the same way between the products).  Unused cells of out are left
+        as they were.  packed_count must be that of the handle's dispatch."""
+        _need(packed_count, torch.int32, "packed_count", 2)
+        epr, R, S, H = self.num_local_experts, self.num_ranks, handle.num_slots, handle.hidden
+        _shape(packed_count, (epr, R), "packed_count")
+        if handle.num_experts != self.num_experts:
+            raise ValueError("handle was made for another number of experts")
+        T, K = handle.topk_slot.shape
+        d = self._dims(T, H, K)
+        cells = (epr, R, S)
+        fp8 = isinstance(x, (tuple, list))
+        if fp8:
+            q, sc = _fp8_pair(x, "x", 4, False)
+            _shape(q, cells + (H,), "x codes")
+            (q13, s13), (q2, s2) = _fp8_pair(w13, "w13", 3, True), _fp8_pair(w2, "w2", 3, True)
+            inter = q2.shape[2]
+            _shape(q13, (self.num_experts, 2 * inter, H), "w13 codes")
+            _shape(q2, (self.num_experts, H, inter), "w2 codes")
+            _here(q, sc, packed_count, q13, s13, q2, s2, handle.topk_slot, out)
+        else:
+            _need(x, torch.bfloat16, "x", 4)
+            _shape(x, cells + (H,), "x")
+            q = x
+            inter = self._expert_weights(w13, w2, H)
+            _here(x, packed_count, w13, w2, handle.topk_slot, out)
+        if out is None:
+            out = torch.empty(cells + (H,), dtype=torch.bfloat16, device=q.device)
+        else:
+            _need(out, torch.bfloat16, "out", 4)
+            _shape(out, cells + (H,), "out")
+        if T == 0:
+            return out
+        s = abi.current_stream()
+        if fp8:
+            aq = torch.empty(cells + (inter,), dtype=torch.uint8, device=q.device)
+            asc = torch.empty(cells + (inter // 128,), dtype=torch.float32, device=q.device)
+            abi.check(abi.lib().ep_ll_expert_ffn_fp8(
+                ctypes.byref(d), S, inter, abi.ptr(q), abi.ptr(sc), abi.ptr(packed_count), abi.ptr(q13),
+                abi.ptr(s13), abi.ptr(q2), abi.ptr(s2), abi.ptr(aq), abi.ptr(asc), abi.ptr(out), s),
+                "ep_ll_expert_ffn_fp8")
+        else:
+            act = torch.empty(cells + (inter,), dtype=torch.bfloat16, device=q.device)
+            abi.check(abi.lib().ep_ll_expert_ffn(
+                ctypes.byref(d), S, inter, abi.ptr(x), abi.ptr(packed_count), abi.ptr(w13), abi.ptr(w2),
+                abi.ptr(act), abi.ptr(out), s), "ep_ll_expert_ffn")
+        return out
+
+    def expert_rows(self, recv_topk_idx: torch.Tensor, layout,
+                    num_tokens: Optional[int] = None) -> ExpertRows:
+        """Groups dispatched rows by expert.  recv_topk_idx [rows, K] is dispatch's;
+        layout is its handle, or the rank_prefix_matrix (int32 [R]) together with
+        num_tokens, the tokens of the batch (without it there is room for every slot
+        of every row).  Rows at or past rank_prefix_matrix[-1] hold no pairs, so
+        worst-case buffers can be given whole."""
+        _need(recv_topk_idx, torch.int64, "recv_topk_idx", 2)
+        N, K = recv_topk_idx.shape
+        dev = recv_topk_idx.device
+        if isinstance(layout, Handle):
+            if layout.device != dev:
+                raise ValueError("handle was made on another device")
+            if layout.dims.num_experts != self.num_experts or layout.dims.num_ranks != self.num_ranks:
+                raise ValueError("handle was made for other experts or ranks")
+            num_tokens = layout.dims.num_tokens
+            prefix = torch.empty(self.num_ranks, dtype=torch.int32, device=dev)
+        else:
+            prefix = layout
+            _need(prefix, torch.int32, "rank_prefix_matrix", 1)
+            _shape(prefix, (self.num_ranks,), "rank_prefix_matrix")
+            num_tokens = N if num_tokens is None else int(num_tokens)
+        _here(recv_topk_idx, prefix)
+        if isinstance(layout, Handle):
+            out = abi.LayoutOut(None, None, None, prefix.data_ptr(), None, None, None, None, 0)
+            abi.check(abi.lib().ep_handle_copy_layout(layout.raw, ctypes.byref(out),
+                                                      abi.current_stream()), "ep_handle_copy_layout")
+        cap = min(num_tokens, N) * K
+        i32 = dict(dtype=torch.int32, device=dev)
+        rows = ExpertRows(torch.empty(self.num_experts + 1, **i32), torch.empty(cap, **i32),
+                          torch.empty(cap, **i32), torch.empty((N, K), **i32))
+        counts = torch.empty(self.num_experts, **i32)
+        abi.check(abi.lib().ep_expert_rows(
+            ctypes.byref(self._dims(num_tokens, 8, K)), abi.ptr(prefix), abi.ptr(recv_topk_idx), N, cap,
+            abi.ptr(counts), abi.ptr(rows.expert_offsets), abi.ptr(rows.pair_row),
+            abi.ptr(rows.pair_slot), abi.ptr(rows.row_pair), abi.current_stream()), "ep_expert_rows")
+        return rows
+
+    def _expert_args(self, x, rows: ExpertRows, topk_weights, w13, w2):
+        _need(x, torch.bfloat16, "x", 2)
+        N, H = x.shape
+        K = rows.row_pair.shape[1]
+        _shape(rows.row_pair, (N, K), "the rows' row_pair")
+        _shape(rows.expert_offsets, (self.num_experts + 1,), "the rows' expert_offsets")
+        _need(topk_weights, torch.float32, "topk_weights", 2)
+        _shape(topk_weights, (N, K), "topk_weights")
+        return N, H, K, self._expert_weights(w13, w2, H)
+
+    def expert_ffn(self, x: torch.Tensor, rows: ExpertRows, topk_weights: torch.Tensor,
+                   w13: torch.Tensor, w2: torch.Tensor, save: bool = False):
+        """The experts between dispatch and combine: for every row of x [rows, H]
+        (bf16) y = sum over its slots of topk_weights * (silu(x Wg^T) * (x Wu^T)) W2^T,
+        zero for a row without a slot.  w13 [E, 2 I, H] (the gate's rows first) and
+        w2 [E, H, I] are bf16.  Returns (y [rows, H] bf16, saved): saved is what
+        expert_ffn_backward takes, the fp32 g and u of every pair, None without save."""
+        N, H, K, inter = self._expert_args(x, rows, topk_weights, w13, w2)
+        _here(x, rows.row_pair, topk_weights, w13, w2)
+        dev, cap = x.device, rows.pair_row.shape[0]
+        y = torch.empty_like(x)
+        act = torch.empty((cap, inter), dtype=torch.bfloat16, device=dev)
+        terms = torch.empty((cap, H), dtype=torch.float32, device=dev)
+        saved = torch.empty((cap, 2 * inter), dtype=torch.float32, device=dev) if save else None
+        raw = rows._raw()
+        abi.check(abi.lib().ep_expert_ffn(
+            ctypes.byref(self._dims(0, H, K)), inter, ctypes.byref(raw), abi.ptr(x),
+            abi.ptr(topk_weights), abi.ptr(w13), abi.ptr(w2), abi.ptr(act), abi.ptr(saved),
+            abi.ptr(terms), abi.ptr(y), abi.current_stream()), "ep_expert_ffn")
+        return y, saved
+
+    def expert_ffn_backward(self, dy: torch.Tensor, x: torch.Tensor, rows: ExpertRows,
+                            topk_weights: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor,
+                            saved: torch.Tensor):
+        """Gradients of expert_ffn given dy [rows, H] bf16.  Returns (dx [rows, H] bf16,
+        dtopk_weights [rows, K] fp32, dw13, dw2 bf16): dispatch's cached handle makes dy
+        from the combined rows' gradient, combine sums dx and dtopk_weights back."""
+        N, H, K, inter = self._expert_args(x, rows, topk_weights, w13, w2)
+        _need(dy, torch.bfloat16, "dy", 2)
+        _shape(dy, (N, H), "dy")
+        cap, dev = rows.pair_row.shape[0], x.device
+        _need(saved, torch.float32, "saved", 2)
+        _shape(saved, (cap, 2 * inter), "saved")
+        _here(dy, x, rows.row_pair, topk_weights, w13, w2, saved)
+        bf = dict(dtype=torch.bfloat16, device=dev)
+        f32 = dict(dtype=torch.float32, device=dev)
+        dgu, act = torch.empty((cap, 2 * inter), **bf), torch.empty((cap, inter), **bf)
+        terms, parts = torch.empty((cap, H), **f32), torch.empty((cap, -(-inter // 256)), **f32)
+        dx, dweights = torch.empty_like(x), torch.empty((N, K), **f32)
+        dw13, dw2 = torch.empty_like(w13), torch.empty_like(w2)
+        raw = rows._raw()
+        abi.check(abi.lib().ep_expert_ffn_backward(
+            ctypes.byref(self._dims(0, H, K)), inter, ctypes.byref(raw), abi.ptr(dy), abi.ptr(x),
+            abi.ptr(topk_weights), abi.ptr(w13), abi.ptr(w2), abi.ptr(saved), abi.ptr(dgu),
+            abi.ptr(act), abi.ptr(terms), abi.ptr(parts), abi.ptr(dx), abi.ptr(dweights),
+            abi.ptr(dw13), abi.ptr(dw2), abi.current_stream()), "ep_expert_ffn_backward")
+        return dx, dweights, dw13, dw2
 
     # ------------------------------------------------------ load balancing
     @staticmethod

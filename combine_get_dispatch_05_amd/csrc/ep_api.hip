@@ -102,6 +102,28 @@ int hip_fail(hipError_t e)
     return EP_ERR_HIP;
 }
 
+}  // namespace
+
+namespace ep {
+
+int api_hip_error(hipError_t e) { return hip_fail(e); }
+
+void api_trace_push(const char *name)
+{
+    if (roctx().push != nullptr)
+        roctx().push(name);
+}
+
+void api_trace_pop()
+{
+    if (roctx().push != nullptr)
+        roctx().pop();
+}
+
+}  // namespace ep
+
+namespace {
+
 // ------------------------------------------------------------------ pool
 //
 // A freed arena remembers the stream it was freed on and is handed out again

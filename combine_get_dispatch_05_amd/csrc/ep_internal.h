@@ -122,6 +122,84 @@ hipError_t launch_lb_prefetch_weights(const void *expert_weights, void *redundan
                                       const int64_t *mapping, int num_replicas, int num_experts,
                                       int64_t elems, hipStream_t stream);
 
+// ---------------------------------------------------------------- experts
+
+// Rows grouped by expert (ep_expert_rows): pairs sorted by (expert, row, slot).
+// pair_row's sign bit marks the only pair of its row.
+struct ExpertFfn {
+    int experts, hidden, inter, topk;
+    int64_t rows;   // token rows
+    int64_t pairs;  // capacity of the pair arrays
+    const int32_t *offsets, *pair_row, *pair_slot, *row_pair;
+    const float *weights;  // [rows][topk]
+};
+
+hipError_t launch_expert_rows(int E, int epr, int K, int64_t rows, const int32_t *prefix,
+                              const int64_t *ids, int64_t cap, int32_t *counts, int32_t *offsets,
+                              int32_t *pair_row, int32_t *pair_slot, int32_t *row_pair,
+                              hipStream_t stream);
+
+// Column tiles of the routing weight's partial gradients.
+int expert_ffn_tiles(int inter);
+
+hipError_t launch_expert_ffn(const ExpertFfn &f, const void *x, const void *w13, const void *w2,
+                             void *act, float *gate_up, float *terms, void *y, hipStream_t stream);
+
+hipError_t launch_expert_ffn_backward(const ExpertFfn &f, const void *dy, const void *x, const void *w13,
+                                      const void *w2, const float *gate_up, void *dgu, void *wact,
+                                      float *parts, float *terms, void *dx, float *dweight, void *dw13,
+                                      void *dw2, hipStream_t stream);
+
+hipError_t launch_ll_expert_ffn(int E, int R, int slots, int H, int I, int64_t max_pairs,
+                                const int32_t *counts, const void *packed, const void *w13,
+                                const void *w2, void *act, void *out, hipStream_t stream);
+
+// FP8 operands: e4m3 codes, and fp32 scales [row][K/128] of the token rows and
+// [ceil(N/128)][K/128] of a weight.
+hipError_t launch_fp8_product(int64_t M, int N, int K, const void *a_q, const float *a_scale,
+                              const void *w_q, const float *w_scale, void *out, hipStream_t stream);
+
+hipError_t launch_ll_expert_ffn_fp8(int E, int R, int slots, int H, int I, int64_t max_pairs,
+                                    const int32_t *counts, const void *packed_q,
+                                    const float *packed_scale, const void *w13_q,
+                                    const float *w13_scale, const void *w2_q, const float *w2_scale,
+                                    void *act_q, float *act_scale, void *out, hipStream_t stream);
+
+hipError_t launch_rms_norm(int64_t T, int H, float eps, const void *x, const void *residual,
+                           const void *weight, void *residual_out, void *out, void *out_q,
+                           float *out_scale, float *rstd, hipStream_t stream);
+
+// Rows of fp32 partial sums of dweight that the backward pass writes.
+int rms_norm_parts(int64_t T, int H);
+
+hipError_t launch_rms_norm_backward(int64_t T, int H, const void *dout, const void *h,
+                                    const void *weight, const float *rstd, const void *dresidual,
+                                    void *dx, float *dweight, float *parts, hipStream_t stream);
+
+// A block for each row.  A dimension of a launch holds fewer than 2^32 threads,
+// so rows past 2^20 go into y; the kernel drops the excess.
+constexpr int64_t kRowGrid = int64_t(1) << 20;
+inline dim3 row_grid(int64_t rows)
+{
+    return rows <= kRowGrid ? dim3(unsigned(rows))
+                            : dim3(unsigned(kRowGrid), unsigned((rows + kRowGrid - 1) / kRowGrid));
+}
+// Blocks of one launch of a 512-thread kernel (the same limit).
+constexpr int64_t kMaxTileBlocks = int64_t(1) << 22;
+
+// Row tile height: the largest whose last tile is not mostly padding at the
+// average number of rows a group can have.
+inline int tile_rows(int64_t rows, int64_t groups)
+{
+    const int64_t avg = rows / (groups > 0 ? groups : 1);
+    return avg > 160 ? 256 : avg > 64 ? 128 : 64;
+}
+
+// Shared with the entry points outside ep_api.hip.
+int api_hip_error(hipError_t e);
+void api_trace_push(const char *name);
+void api_trace_pop();
+
 // Launch-shape overrides (never change results).  (-1, ...) restores the
 // default choice.  Return false for a shape that is not compiled in.
 bool set_dispatch_tuning(int g, int vpt, int code);

@@ -1,0 +1,679 @@
+// experts.hip -- the experts between a dispatch and its combine, in bf16:
+// rows grouped by expert, the gated feed-forward over them, and its gradients.
+//
+// For pair p = (row, slot) of expert e, with x the row and w its routing weight,
+//   g = x Wg^T, u = x Wu^T, a = g sigmoid(g) u, z = a W2^T, y_row += w z
+// and, given dy,
+//   d = dy W2, dw = a . d, da = w d, du = da silu(g), dg = da u s (1 + g (1 - s)), s = sigmoid(g)
+//   dx_row += [dg du] W13, dW13 = sum_p [dg du]^T x, dW2 = sum_p dy^T (w a).
+#include "few_rows.h"
+
+namespace ep {
+
+namespace {
+
+// ------------------------------------------------------------- grouping
+
+constexpr int kGroupBlock = 1024;
+
+// Rows of expert e's rank, clamped to the rows that exist.
+__device__ __forceinline__ void rank_rows(const int32_t *prefix, int r, int64_t n, int64_t &a,
+                                          int64_t &b)
+{
+    a = r > 0 ? prefix[r - 1] : 0;
+    b = prefix[r];
+    a = a < 0 ? 0 : (a < n ? a : n);
+    b = b < a ? a : (b < n ? b : n);
+}
+
+// One block for each expert counts its pairs; together they also mark every
+// (row, slot) as having no pair.
+__global__ __launch_bounds__(kGroupBlock) void count_pairs_kernel(
+    const int64_t *__restrict__ ids, const int32_t *__restrict__ prefix, int64_t n, int K, int epr,
+    int32_t *__restrict__ counts, int32_t *__restrict__ row_pair)
+{
+    const int e = blockIdx.x, r = e / epr, le = e % epr;
+    for (int64_t i = int64_t(e) * kGroupBlock + threadIdx.x; i < n * K;
+         i += int64_t(gridDim.x) * kGroupBlock)
+        row_pair[i] = -1;
+    int64_t a, b;
+    rank_rows(prefix, r, n, a, b);
+    int c = 0;
+    for (int64_t i = a * K + threadIdx.x; i < b * K; i += kGroupBlock)
+        c += ids[i] == le;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1)
+        c += __shfl_xor(c, d);
+    __shared__ int s[kGroupBlock / kWave];
+    if ((threadIdx.x & 63) == 0)
+        s[threadIdx.x >> 6] = c;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int t = 0;
+        for (int w = 0; w < kGroupBlock / kWave; ++w)
+            t += s[w];
+        counts[e] = t;
+    }
+}
+
+// One block for each expert: its pairs' places, in (row, slot) order behind the
+// pairs of the experts before it.
+__global__ __launch_bounds__(kGroupBlock) void place_pairs_kernel(
+    const int64_t *__restrict__ ids, const int32_t *__restrict__ prefix, int64_t n, int K, int E,
+    int epr, const int32_t *__restrict__ counts, int64_t cap, int32_t *__restrict__ offsets,
+    int32_t *__restrict__ pair_row, int32_t *__restrict__ pair_slot, int32_t *__restrict__ row_pair)
+{
+    const int e = blockIdx.x, r = e / epr, le = e % epr;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __shared__ int s[kGroupBlock / kWave];
+    int c = 0;
+    for (int i = threadIdx.x; i < e; i += kGroupBlock)
+        c += counts[i];
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1)
+        c += __shfl_xor(c, d);
+    if (lane == 0)
+        s[wave] = c;
+    __syncthreads();
+    int base = 0;
+    for (int w = 0; w < kGroupBlock / kWave; ++w)
+        base += s[w];
+    // a count past the capacity (ids that no dispatch wrote) leaves the tail out
+    const int icap = int(cap);
+    if (threadIdx.x == 0) {
+        offsets[e] = base < icap ? base : icap;
+        if (e == E - 1) {
+            const int end = base + counts[e];
+            offsets[E] = end < icap ? end : icap;
+        }
+    }
+    int64_t a, b;
+    rank_rows(prefix, r, n, a, b);
+    for (int64_t i0 = a * K; i0 < b * K; i0 += kGroupBlock) {
+        const int64_t i = i0 + threadIdx.x;
+        const bool hit = i < b * K && ids[i] == le;
+        const uint64_t m = wave_ballot(hit);
+        __syncthreads();
+        if (lane == 0)
+            s[wave] = __popcll(m);
+        __syncthreads();
+        int before = 0, total = 0;
+        for (int w = 0; w < kGroupBlock / kWave; ++w) {
+            before += w < wave ? s[w] : 0;
+            total += s[w];
+        }
+        if (hit) {
+            const int pos = base + before + __popcll(m & lanemask_lt());
+            if (pos < icap) {
+                const int64_t row = i / K;
+                int live = 0;
+                for (int k = 0; k < K; ++k) {
+                    const int64_t v = ids[row * K + k];
+                    live += v >= 0 && v < epr;
+                }
+                pair_row[pos] = int32_t(row) | (live == 1 ? int32_t(0x80000000u) : 0);
+                pair_slot[pos] = int32_t(i);
+                row_pair[i] = pos;
+            }
+        }
+        base += total;
+    }
+}
+
+// --------------------------------------------------------- tile epilogues
+//
+// Each is called by every thread with its accumulators acc[mt][nt] (row
+// m0 + mt * 16 + lane % 16, columns n0 + nt * 16 + 4 (lane / 16) .. + 3).
+
+// Rows of a pair's product: the only pair of its row goes straight to the
+// row's bf16 output (rounded once), a row of several keeps fp32 terms for the
+// sum that follows.  weight: routing weights by pair slot (nullable).
+struct PairOut {
+    static constexpr bool kBlockWide = false;
+    const int32_t *pair_row, *pair_slot;
+    const float *weight;
+    uint16_t *out;  // [rows][N]
+    float *terms;   // [pairs][N]
+    template <int MT, int NW>
+    __device__ __forceinline__ void store(const Tile &t, int64_t start, int m0, int n0, int N,
+                                          const f32x4 (&acc)[MT][NW], int lane) const
+    {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int m = m0 + mt * 16 + (lane & 15);
+            if (m >= t.rows)
+                continue;
+            const int64_t p = start + m;
+            const int32_t r = pair_row[p];
+            const float w = weight != nullptr ? weight[pair_slot[p]] : 1.0f;
+#pragma unroll
+            for (int nt = 0; nt < NW; ++nt) {
+                const int n = n0 + nt * 16 + (lane >> 4) * 4;
+                if (n >= N)
+                    continue;
+                const f32x4 v = acc[mt][nt] * w;
+                if (r < 0)
+                    *reinterpret_cast<uint2 *>(out + int64_t(r & kRowMask) * N + n) = pack4(v);
+                else
+                    *reinterpret_cast<f32x4 *>(terms + p * N + n) = v;
+            }
+        }
+    }
+};
+
+// Gate and up columns in one tile: act = silu(g) u in bf16 (what the second
+// product's matrix instructions take) and, for a backward pass, g and u in
+// fp32: the routing weights' gradient is an fp32 result that bf16 copies would
+// hold to three digits.
+struct GatedOut {
+    static constexpr bool kBlockWide = false;
+    uint16_t *act;  // [.][I]
+    float *gu;      // [.][2 I], nullable
+    template <int MT, int NW>
+    __device__ __forceinline__ void store(const Tile &t, int64_t start, int m0, int n0, int I,
+                                          const f32x4 (&acc)[MT][NW], int lane) const
+    {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int m = m0 + mt * 16 + (lane & 15);
+            if (m >= t.rows)
+                continue;
+            const int64_t p = start + m;
+#pragma unroll
+            for (int nt = 0; nt < NW / 2; ++nt) {
+                const int n = n0 + nt * 16 + (lane >> 4) * 4;
+                if (n >= I)
+                    continue;
+                const f32x4 g = acc[mt][nt], u = acc[mt][nt + NW / 2];
+                f32x4 a;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    a[i] = g[i] * sigmoidf(g[i]) * u[i];
+                *reinterpret_cast<uint2 *>(act + p * I + n) = pack4(a);
+                if (gu != nullptr) {
+                    *reinterpret_cast<f32x4 *>(gu + p * 2 * I + n) = g;
+                    *reinterpret_cast<f32x4 *>(gu + p * 2 * I + I + n) = u;
+                }
+            }
+        }
+    }
+};
+
+// d = dy W2 in the accumulators: the gate's backward, the weighted activation
+// for dW2, and the tile's share of the routing weight's gradient, summed in a
+// fixed order over lanes, then waves, then (in rows_kernel) tiles.
+struct GatedBack {
+    const int32_t *pair_slot;
+    const float *weight;
+    const float *gu;      // [pairs][2 I]
+    uint16_t *dgu;        // [pairs][2 I]
+    uint16_t *wact;       // [pairs][I]
+    float *dweight_part;  // [pairs][tiles]
+    int tiles;
+};
+
+// ------------------------------------------------------------ tile kernels
+
+// BM rows of one group by BN columns.  Two LDS stages: while the waves work on
+// one, the other fills; one barrier a K step both publishes the filled stage
+// and retires the one that was read.
+template <int BM, bool PCOL, Form F, class Epi>
+__global__ __launch_bounds__(NT) void tile_kernel(TileArgs a, Groups G, Epi epi)
+{
+    constexpr int MT = BM / 32;  // 16-row tiles of a wave
+    using QS = RowStage<BM, NT>;
+    using PR = RowStage<BN, NT>;
+    using PC = ColStage<BN, NT>;
+    constexpr int kP = PR::kBytes, kQ = QS::kBytes;
+    __shared__ __attribute__((aligned(128))) char smem[2 * (kP + kQ)];
+    __shared__ int scan[NT / kWave];
+    unsigned tm, tn;
+    tile_of_block(blockIdx.x, a.mt, a.nt, tm, tn);
+    const Tile t = find_tile<BM, NT>(G, int(tm), scan);
+    if (t.group < 0)
+        return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int wm = wave >> 2, wn = wave & 3;
+    const int64_t start = group_start(G, t.group);
+    const char *pw = a.p + int64_t(group_expert(G, t.group)) * a.p_expert;
+    lds_char *lds = (lds_char *)smem;
+    const int n0 = int(tn) * (F == Form::kGated ? BN / 2 : BN);
+
+    QS qs;
+    qs.init(tid, [&](int r) {
+        int m = t.m0 + r;
+        m = m < t.rows ? m : t.rows - 1;
+        const int64_t row = a.q_rows != nullptr ? int64_t(a.q_rows[start + m] & kRowMask) : start + m;
+        return a.q + row * a.ldq;
+    });
+    PR pr;
+    PC pc;
+    if constexpr (PCOL) {
+        pc.init(tid, n0, a.N);
+    } else {
+        pr.init(tid, [&](int r) {
+            int n;
+            if constexpr (F == Form::kGated) {  // each wave: 32 gate columns, then their up columns
+                n = n0 + (r >> 6) * 32 + (r & 31);
+                n = n < a.N ? n : a.N - 1;
+                n += (r & 32) ? a.N : 0;
+            } else {
+                n = n0 + r;
+                n = n < a.N ? n : a.N - 1;
+            }
+            return pw + int64_t(n) * a.ldp;
+        });
+    }
+    const int steps = (a.K + 63) / 64;
+    const int64_t kbytes = int64_t(a.K) * 2;
+    auto issue = [&](int s, int buf) {
+        lds_char *b = lds + buf * (kP + kQ);
+        if constexpr (PCOL)
+            pc.issue(b, wave, s * 64, a.K, [&](int, int k) { return pw + int64_t(k) * a.ldp; });
+        else
+            pr.issue(b, wave, int64_t(s) * kStepBytes, kbytes);
+        qs.issue(b + kP, wave, int64_t(s) * kStepBytes, kbytes);
+    };
+
+    f32x4 acc[MT][4] = {};
+    issue(0, 0);
+    for (int s = 0; s < steps; ++s) {
+        landed<0>();
+        __syncthreads();  // stage s is in LDS, stage s - 1 is read
+        if (s + 1 < steps)
+            issue(s + 1, (s + 1) & 1);
+        const lds_char *pb = lds + (s & 1) * (kP + kQ), *qb = pb + kP;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            bf16x8 pf[4], qf[MT];
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt) {
+                if constexpr (PCOL)
+                    pf[nt] = PC::frag(pb, wn * 64 + nt * 16, ks, lane);
+                else
+                    pf[nt] = *(const __attribute__((address_space(3))) bf16x8 *)PR::at(
+                        pb, wn * 64 + nt * 16 + (lane & 15), ks * 4 + (lane >> 4));
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                qf[mt] = *(const __attribute__((address_space(3))) bf16x8 *)QS::at(
+                    qb, wm * (BM / 2) + mt * 16 + (lane & 15), ks * 4 + (lane >> 4));
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt)
+                    acc[mt][nt] = mfma_bf16(pf[nt], qf[mt], acc[mt][nt]);
+        }
+    }
+
+    const int mw = t.m0 + wm * (BM / 2);
+    if constexpr (F == Form::kBack) {
+        const int I = a.N, nw = n0 + wn * 64;
+        float *part = reinterpret_cast<float *>(smem);  // [4][BM]
+        __syncthreads();
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int m = mw + mt * 16 + (lane & 15);
+            const int64_t p = start + m;
+            float dw = 0.0f;
+            if (m < t.rows) {
+                const float w = epi.weight[epi.pair_slot[p]];
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt) {
+                    const int n = nw + nt * 16 + (lane >> 4) * 4;
+                    if (n >= I)
+                        continue;
+                    const f32x4 g = *reinterpret_cast<const f32x4 *>(epi.gu + p * 2 * I + n);
+                    const f32x4 u = *reinterpret_cast<const f32x4 *>(epi.gu + p * 2 * I + I + n);
+                    f32x4 dg, du, wa;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float sg = sigmoidf(g[i]), d = acc[mt][nt][i], si = g[i] * sg;
+                        dw += si * u[i] * d;
+                        wa[i] = w * si * u[i];
+                        du[i] = w * d * si;
+                        dg[i] = w * d * u[i] * sg * (1.0f + g[i] * (1.0f - sg));
+                    }
+                    *reinterpret_cast<uint2 *>(epi.dgu + p * 2 * I + n) = pack4(dg);
+                    *reinterpret_cast<uint2 *>(epi.dgu + p * 2 * I + I + n) = pack4(du);
+                    *reinterpret_cast<uint2 *>(epi.wact + p * I + n) = pack4(wa);
+                }
+            }
+            dw += __shfl_xor(dw, 16);
+            dw += __shfl_xor(dw, 32);
+            if (lane < 16)
+                part[wn * BM + wm * (BM / 2) + mt * 16 + lane] = dw;
+        }
+        __syncthreads();
+        if (tid < BM && t.m0 + tid < t.rows)
+            epi.dweight_part[(start + t.m0 + tid) * epi.tiles + tn] =
+                (part[tid] + part[BM + tid]) + (part[2 * BM + tid] + part[3 * BM + tid]);
+    } else {
+        const int nw = n0 + wn * (F == Form::kGated ? 32 : 64);
+        epi.store(t, start, mw, nw, a.N, acc, lane);
+    }
+}
+
+// out[e][m][n] = sum over the group's rows k of Q[k][m] P[k][n], 256 x 256 a
+// block; QG / PG: the operand's rows are picked by pair_row.  A group without
+// rows writes zeros.
+template <bool QG, bool PG>
+__global__ __launch_bounds__(NT) void weight_grad_kernel(const char *q, int64_t ldq, const char *p,
+                                                         int64_t ldp, const int32_t *pair_row,
+                                                         const int32_t *offsets, int M, int N,
+                                                         unsigned mt, unsigned nt, uint16_t *out)
+{
+    constexpr int B = 256;
+    using CS = ColStage<B, NT>;
+    __shared__ __attribute__((aligned(128))) char smem[4 * CS::kBytes];
+    lds_char *lds = (lds_char *)smem;
+    const int e = blockIdx.x / (mt * nt);
+    unsigned tm, tn;
+    tile_of_block(blockIdx.x % (mt * nt), mt, nt, tm, tn);
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int wm = wave >> 2, wn = wave & 3;
+    const int start = offsets[e], rows = offsets[e + 1] - start;
+    const int steps = (rows + 63) / 64;
+    CS qs, ps;
+    qs.init(tid, int(tm) * B, M);
+    ps.init(tid, int(tn) * B, N);
+    // both operands' chunks of a thread lie in the same k rows
+    int idx[CS::J], nxt[CS::J] = {};
+    auto fetch = [&](int s) {
+#pragma unroll
+        for (int j = 0; j < CS::J; ++j) {
+            const int k = s * 64 + qs.k[j];
+            if (k < rows)
+                nxt[j] = pair_row[start + k] & kRowMask;
+        }
+    };
+    auto issue = [&](int s, int buf) {
+#pragma unroll
+        for (int j = 0; j < CS::J; ++j)
+            idx[j] = nxt[j];
+        lds_char *b = lds + buf * 2 * CS::kBytes;
+        ps.issue(b, wave, s * 64, rows, [&](int j, int k) {
+            return p + (PG ? int64_t(idx[j]) : int64_t(start) + k) * ldp;
+        });
+        qs.issue(b + CS::kBytes, wave, s * 64, rows, [&](int j, int k) {
+            return q + (QG ? int64_t(idx[j]) : int64_t(start) + k) * ldq;
+        });
+    };
+    f32x4 acc[8][4] = {};
+    if (steps > 0) {
+        fetch(0);
+        issue(0, 0);
+        if (steps > 1)
+            fetch(1);
+    }
+    for (int s = 0; s < steps; ++s) {
+        landed<0>();
+        __syncthreads();
+        if (s + 1 < steps) {
+            issue(s + 1, (s + 1) & 1);
+            if (s + 2 < steps)
+                fetch(s + 2);
+        }
+        const lds_char *pb = lds + (s & 1) * 2 * CS::kBytes, *qb = pb + CS::kBytes;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            bf16x8 pf[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                pf[i] = CS::frag(pb, wn * 64 + i * 16, ks, lane);
+#pragma unroll
+            for (int m = 0; m < 8; ++m) {
+                const bf16x8 qf = CS::frag(qb, wm * 128 + m * 16, ks, lane);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[m][i] = mfma_bf16(pf[i], qf, acc[m][i]);
+            }
+        }
+    }
+    uint16_t *o = out + int64_t(e) * M * N;
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+        const int mm = int(tm) * B + wm * 128 + m * 16 + (lane & 15);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = int(tn) * B + wn * 64 + i * 16 + (lane >> 4) * 4;
+            if (mm < M && n < N)
+                *reinterpret_cast<uint2 *>(o + int64_t(mm) * N + n) = pack4(acc[m][i]);
+        }
+    }
+}
+
+// ------------------------------------------------------------ row sums
+
+// Rows with no pair (zero) or several (their fp32 terms in slot order); rows of
+// one pair are already written.  With parts: also every slot's routing-weight
+// gradient, the sum of its pair's column tiles in order.
+__global__ __launch_bounds__(256) void rows_kernel(const int32_t *__restrict__ row_pair, int64_t rows, int K, int N,
+                                                   const int32_t *__restrict__ pair_row,
+                                                   const float *__restrict__ terms,
+                                                   uint16_t *__restrict__ out,
+                                                   const float *__restrict__ parts, int tiles,
+                                                   float *__restrict__ dweight)
+{
+    const int64_t row = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
+    if (row >= rows)
+        return;
+    __shared__ int pairs[kMaxTopk];
+    __shared__ int live;
+    const int tid = threadIdx.x;
+    if (tid < kWave) {
+        const int p = tid < K ? row_pair[row * K + tid] : -1;
+        const uint64_t m = wave_ballot(p >= 0);
+        if (p >= 0)
+            pairs[__popcll(m & lanemask_lt())] = p;
+        if (tid == 0)
+            live = __popcll(m);
+        if (dweight != nullptr && tid < K) {
+            float d = 0.0f;
+            if (p >= 0)
+                for (int t = 0; t < tiles; ++t)
+                    d += parts[int64_t(p) * tiles + t];
+            dweight[row * K + tid] = d;
+        }
+    }
+    __syncthreads();
+    const int n = live;
+    if (n == 1 && pair_row[pairs[0]] < 0)
+        return;
+    for (int c = tid * 4; c < N; c += 1024) {
+        f32x4 v = {};
+        for (int k = 0; k < n; ++k)
+            v += *reinterpret_cast<const f32x4 *>(terms + int64_t(pairs[k]) * N + c);
+        *reinterpret_cast<uint2 *>(out + row * N + c) = pack4(v);
+    }
+}
+
+// --------------------------------------------------------------- launches
+
+template <bool PCOL, Form F, class Epi>
+hipError_t launch_tiles(TileArgs a, const Groups &G, int64_t max_tiles_rows, const Epi &epi,
+                        const char *what, hipStream_t stream)
+{
+    const int bm = tile_rows(max_tiles_rows, G.num);
+    // every group can end in one part tile, and no more tiles than rows exist
+    int64_t mt = max_tiles_rows / bm + (G.num < max_tiles_rows ? G.num : max_tiles_rows);
+    const int cols = F == Form::kGated ? BN / 2 : BN;
+    a.nt = unsigned((a.N + cols - 1) / cols);
+    if (mt * a.nt > kMaxTileBlocks)
+        return hipErrorInvalidValue;
+    a.mt = unsigned(mt);
+    if (mt == 0)
+        return hipSuccess;
+    if (log_enabled())
+        log_launch("%s: rows<=%lld groups=%d N=%d K=%d tile=%dx%d blocks=%lld", what,
+                   (long long)max_tiles_rows, G.num, a.N, a.K, bm, BN, (long long)mt * a.nt);
+    const dim3 grid(unsigned(mt * a.nt));
+    if (bm == 256)
+        hipLaunchKernelGGL((tile_kernel<256, PCOL, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
+    else if (bm == 128)
+        hipLaunchKernelGGL((tile_kernel<128, PCOL, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
+    else
+        hipLaunchKernelGGL((tile_kernel<64, PCOL, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
+    return hipGetLastError();
+}
+
+Groups contiguous(const int32_t *offsets, int num)
+{
+    return Groups{offsets, nullptr, 0, num, 1, num, 1, kNoLimit};
+}
+
+hipError_t launch_rows(const ExpertFfn &f, const float *terms, void *out, const float *parts, int tiles,
+                       float *dweight, hipStream_t stream)
+{
+    if (f.rows == 0)
+        return hipSuccess;
+    if (log_enabled())
+        log_launch("expert rows sum: rows=%lld H=%d K=%d", (long long)f.rows, f.hidden, f.topk);
+    hipLaunchKernelGGL(rows_kernel, row_grid(f.rows), dim3(256), 0, stream, f.row_pair, f.rows, f.topk,
+                       f.hidden, f.pair_row, terms, static_cast<uint16_t *>(out), parts, tiles, dweight);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int expert_ffn_tiles(int inter) { return (inter + BN - 1) / BN; }
+
+hipError_t launch_expert_rows(int E, int epr, int K, int64_t rows, const int32_t *prefix,
+                              const int64_t *ids, int64_t cap, int32_t *counts, int32_t *offsets,
+                              int32_t *pair_row, int32_t *pair_slot, int32_t *row_pair,
+                              hipStream_t stream)
+{
+    if (log_enabled())
+        log_launch("expert_rows: rows=%lld K=%d E=%d blocks=%d x 2", (long long)rows, K, E, E);
+    hipLaunchKernelGGL(count_pairs_kernel, dim3(E), dim3(kGroupBlock), 0, stream, ids, prefix, rows, K,
+                       epr, counts, row_pair);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL(place_pairs_kernel, dim3(E), dim3(kGroupBlock), 0, stream, ids, prefix, rows, K,
+                       E, epr, counts, cap, offsets, pair_row, pair_slot, row_pair);
+    return hipGetLastError();
+}
+
+hipError_t launch_expert_ffn(const ExpertFfn &f, const void *x, const void *w13, const void *w2,
+                             void *act, float *gate_up, float *terms, void *y, hipStream_t stream)
+{
+    const int H = f.hidden, I = f.inter;
+    const Groups G = contiguous(f.offsets, f.experts);
+    TileArgs a{};
+    a.q = static_cast<const char *>(x);
+    a.q_rows = f.pair_row;
+    a.ldq = int64_t(H) * 2;
+    a.p = static_cast<const char *>(w13);
+    a.p_expert = int64_t(2) * I * H * 2;
+    a.ldp = int64_t(H) * 2;
+    a.N = I;
+    a.K = H;
+    hipError_t e = launch_tiles<false, Form::kGated>(
+        a, G, f.pairs, GatedOut{static_cast<uint16_t *>(act), gate_up}, "expert_ffn gated", stream);
+    if (e != hipSuccess)
+        return e;
+    a.q = static_cast<const char *>(act);
+    a.q_rows = nullptr;
+    a.ldq = int64_t(I) * 2;
+    a.p = static_cast<const char *>(w2);
+    a.p_expert = int64_t(I) * H * 2;
+    a.ldp = int64_t(I) * 2;
+    a.N = H;
+    a.K = I;
+    e = launch_tiles<false, Form::kPlain>(
+        a, G, f.pairs,
+        PairOut{f.pair_row, f.pair_slot, f.weights, static_cast<uint16_t *>(y), terms},
+        "expert_ffn down", stream);
+    if (e != hipSuccess)
+        return e;
+    return launch_rows(f, terms, y, nullptr, 0, nullptr, stream);
+}
+
+hipError_t launch_expert_ffn_backward(const ExpertFfn &f, const void *dy, const void *x, const void *w13,
+                                      const void *w2, const float *gate_up, void *dgu, void *wact,
+                                      float *parts, float *terms, void *dx, float *dweight, void *dw13,
+                                      void *dw2, hipStream_t stream)
+{
+    const int H = f.hidden, I = f.inter, tiles = expert_ffn_tiles(I);
+    const Groups G = contiguous(f.offsets, f.experts);
+    TileArgs a{};
+    a.q = static_cast<const char *>(dy);
+    a.q_rows = f.pair_row;
+    a.ldq = int64_t(H) * 2;
+    a.p = static_cast<const char *>(w2);
+    a.p_expert = int64_t(I) * H * 2;
+    a.ldp = int64_t(I) * 2;
+    a.N = I;
+    a.K = H;
+    hipError_t e = launch_tiles<true, Form::kBack>(
+        a, G, f.pairs,
+        GatedBack{f.pair_slot, f.weights, gate_up, static_cast<uint16_t *>(dgu),
+                  static_cast<uint16_t *>(wact), parts, tiles},
+        "expert_ffn gate backward", stream);
+    if (e != hipSuccess)
+        return e;
+    a.q = static_cast<const char *>(dgu);
+    a.q_rows = nullptr;
+    a.ldq = int64_t(2) * I * 2;
+    a.p = static_cast<const char *>(w13);
+    a.p_expert = int64_t(2) * I * H * 2;
+    a.ldp = int64_t(H) * 2;
+    a.N = H;
+    a.K = 2 * I;
+    e = launch_tiles<true, Form::kPlain>(
+        a, G, f.pairs, PairOut{f.pair_row, f.pair_slot, nullptr, static_cast<uint16_t *>(dx), terms},
+        "expert_ffn dx", stream);
+    if (e != hipSuccess)
+        return e;
+    e = launch_rows(f, terms, dx, parts, tiles, dweight, stream);
+    if (e != hipSuccess)
+        return e;
+    auto grid = [](int m, int n) { return unsigned((m + 255) / 256) * unsigned((n + 255) / 256); };
+    const unsigned hm = (H + 255) / 256, in = (I + 255) / 256, gm = (2 * I + 255) / 256;
+    if (log_enabled())
+        log_launch("expert_ffn dW: experts=%d blocks=%lld + %lld", f.experts,
+                   (long long)f.experts * grid(H, I), (long long)f.experts * grid(2 * I, H));
+    hipLaunchKernelGGL((weight_grad_kernel<true, false>), dim3(unsigned(f.experts) * hm * in), dim3(NT),
+                       0, stream, static_cast<const char *>(dy), int64_t(H) * 2,
+                       static_cast<const char *>(wact), int64_t(I) * 2, f.pair_row, f.offsets, H, I, hm,
+                       in, static_cast<uint16_t *>(dw2));
+    e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL((weight_grad_kernel<false, true>), dim3(unsigned(f.experts) * gm * hm), dim3(NT),
+                       0, stream, static_cast<const char *>(dgu), int64_t(2) * I * 2,
+                       static_cast<const char *>(x), int64_t(H) * 2, f.pair_row, f.offsets, 2 * I, H, gm,
+                       hm, static_cast<uint16_t *>(dw13));
+    return hipGetLastError();
+}
+
+hipError_t launch_ll_expert_ffn(int E, int R, int slots, int H, int I, int64_t max_pairs,
+                                const int32_t *counts, const void *packed, const void *w13,
+                                const void *w2, void *act, void *out, hipStream_t stream)
+{
+    const Groups G{nullptr, counts, slots, E, R, E / R, 1, kNoLimit};
+    TileArgs a{};
+    a.q = static_cast<const char *>(packed);
+    a.ldq = int64_t(H) * 2;
+    a.p = static_cast<const char *>(w13);
+    a.p_expert = int64_t(2) * I * H * 2;
+    a.ldp = int64_t(H) * 2;
+    a.N = I;
+    a.K = H;
+    hipError_t e = launch_tiles<false, Form::kGated>(
+        a, G, max_pairs, GatedOut{static_cast<uint16_t *>(act), nullptr}, "ll_expert_ffn gated", stream);
+    if (e != hipSuccess)
+        return e;
+    a.q = static_cast<const char *>(act);
+    a.ldq = int64_t(I) * 2;
+    a.p = static_cast<const char *>(w2);
+    a.p_expert = int64_t(I) * H * 2;
+    a.ldp = int64_t(I) * 2;
+    a.N = H;
+    a.K = I;
+    return launch_tiles<false, Form::kPlain>(a, G, max_pairs, RowOut{static_cast<uint16_t *>(out)},
+                                             "ll_expert_ffn down", stream);
+}
+
+}  // namespace ep

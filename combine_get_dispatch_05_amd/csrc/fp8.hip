@@ -1,0 +1,303 @@
+// fp8.hip -- products of FP8 (e4m3) operands with an fp32 scale for each block
+// of 128, and the experts' gated feed-forward on low-latency cells in FP8:
+//   D[m, n] = sum_b sq[m, b] sp[n / 128, b] sum_{k in block b} q[m, k] p[n, k].
+// One matrix instruction sums exactly one block of K (16 x 16 x 128), so the
+// scales are applied once a step to its fp32 result.
+#include "few_rows.h"
+
+namespace ep {
+
+namespace {
+
+// act = silu(g) u of one 128-column block per row, as codes and a scale: amax
+// over the block's WN waves through LDS, then code = e4m3(a * (448 / amax)),
+// scale = amax / 448, the format of the FP8 dispatch.
+struct GatedFp8Out {
+    static constexpr bool kBlockWide = true;
+    uint8_t *codes;  // [.][I]
+    float *scales;   // [.][I / 128]
+    // mbase: this wave's first row inside the tile; ROWS: rows of the tile
+    template <int MT, int NW, int WN, int ROWS>
+    __device__ __forceinline__ void store_block(const Tile &t, int64_t start, bool active, int wn,
+                                                int mbase, int n0, int I, f32x4 (&acc)[MT][NW],
+                                                int lane) const
+    {
+        __shared__ float amaxs[WN][ROWS];
+        if (active) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                float big = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NW / 2; ++i) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float g = acc[m][i][k];
+                        const float v = g * sigmoidf(g) * acc[m][i + NW / 2][k];
+                        acc[m][i][k] = v;
+                        big = fmaxf(big, fabsf(v));
+                    }
+                }
+                big = fmaxf(big, __shfl_xor(big, 16));
+                big = fmaxf(big, __shfl_xor(big, 32));
+                if (lane < 16)
+                    amaxs[wn][mbase + m * 16 + lane] = big;
+            }
+        }
+        __syncthreads();
+        if (!active)
+            return;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int r = mbase + m * 16 + (lane & 15);
+            if (t.m0 + r >= t.rows)
+                continue;
+            float amax = amaxs[0][r];
+#pragma unroll
+            for (int w = 1; w < WN; ++w)
+                amax = fmaxf(amax, amaxs[w][r]);
+            amax = amax < 1e-4f ? 1e-4f : amax;
+            const float inv = 448.0f / amax;
+            const int64_t row = start + t.m0 + r;
+            if (wn == 0 && lane < 16)
+                scales[row * (I >> 7) + (n0 >> 7)] = amax / 448.0f;
+#pragma unroll
+            for (int i = 0; i < NW / 2; ++i) {
+                const f32x4 v = acc[m][i] * inv;
+                int c = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+                c = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], c, true);
+                *reinterpret_cast<int *>(codes + row * I + n0 + i * 16 + (lane >> 4) * 4) = c;
+            }
+        }
+    }
+};
+
+// BM rows of one group by BN columns: the bf16 tile kernel's loop with K steps
+// of one scale block.  The step's token scales are staged beside the rows.
+template <int BM, Form F, class Epi>
+__global__ __launch_bounds__(NT) void fp8_tile_kernel(FewArgs a, unsigned gmt, Groups G, Epi epi)
+{
+    constexpr int MT = BM / 32;
+    using QS = RowStage<BM, NT>;
+    using PR = RowStage<BN, NT>;
+    constexpr int kP = PR::kBytes, kQ = QS::kBytes, kStage = kP + kQ + BM * 4;
+    __shared__ __attribute__((aligned(128))) char smem[2 * kStage];
+    __shared__ int scan[NT / kWave];
+    unsigned tm, tn;
+    tile_of_block(blockIdx.x, gmt, a.nt, tm, tn);
+    const Tile t = find_tile<BM, NT>(G, int(tm), scan);
+    if (t.group < 0)
+        return;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 2, wn = wave & 3;
+    const int64_t start = group_start(G, t.group);
+    const int e = group_expert(G, t.group);
+    const char *pw = a.p + int64_t(e) * a.p_expert;
+    lds_char *lds = (lds_char *)smem;
+    const int n0 = int(tn) * (F == Form::kGated ? BN / 2 : BN);
+    const int steps = a.kbytes >> 7;
+
+    QS qs;
+    qs.init(tid, [&](int r) {
+        const int m = t.m0 + r;
+        return a.q + (start + (m < t.rows ? m : t.rows - 1)) * a.ldq;
+    });
+    PR pr;
+    pr.init(tid, [&](int r) {
+        int n;
+        if constexpr (F == Form::kGated) {
+            n = n0 + (r >> 6) * 32 + (r & 31) + ((r & 32) ? a.N : 0);
+        } else {
+            n = n0 + r;
+            n = n < a.N ? n : a.N - 1;
+        }
+        return pw + int64_t(n) * a.ldp;
+    });
+    const int mclamp = t.m0 + tid < t.rows ? t.m0 + tid : t.rows - 1;
+    const char *sq = reinterpret_cast<const char *>(a.q_scale + (start + mclamp) * steps);
+    auto issue = [&](int s, int buf) {
+        lds_char *b = lds + buf * kStage;
+        pr.issue(b, wave, int64_t(s) * kStepBytes, a.kbytes);
+        qs.issue(b + kP, wave, int64_t(s) * kStepBytes, a.kbytes);
+        if (wave < BM / kWave)
+            load_lds4(sq + int64_t(s) * 4, b + kP + kQ + wave * kWave * 4);
+    };
+    // this wave's weight scales: one block of columns, or one of gate and one of up
+    const int nb = F == Form::kGated ? n0 : n0 + wn * 64;
+    const float *sp0 = a.p_scale + e * a.p_scales + int64_t((nb < a.N ? nb : a.N - 1) >> 7) * steps;
+    const float *sp1 = F == Form::kGated ? sp0 + int64_t(a.N >> 7) * steps : sp0;
+
+    f32x4 acc[MT][4] = {};
+    issue(0, 0);
+    float w0 = sp0[0], w1 = F == Form::kGated ? sp1[0] : 0.0f;
+    for (int s = 0; s < steps; ++s) {
+        landed<0>();
+        __syncthreads();
+        float c0 = w0, c1 = F == Form::kGated ? w1 : w0;
+        asm volatile("" : "+v"(c0), "+v"(c1));  // their wait belongs here, before the next stage's loads
+        if (s + 1 < steps) {
+            issue(s + 1, (s + 1) & 1);
+            w0 = sp0[s + 1];
+            if constexpr (F == Form::kGated)
+                w1 = sp1[s + 1];
+        }
+        const lds_char *pb = lds + (s & 1) * kStage, *qb = pb + kP;
+        const __attribute__((address_space(3))) float *sc =
+            (const __attribute__((address_space(3))) float *)(qb + kQ);
+        auto frag = [&](const lds_char *base, int r) {
+            Frag f;
+            f.lo = *(const __attribute__((address_space(3))) i32x4 *)QS::at(base, r, lane >> 4);
+            f.hi = *(const __attribute__((address_space(3))) i32x4 *)QS::at(base, r, 4 + (lane >> 4));
+            return f;
+        };
+        Frag pf[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            pf[i] = frag(pb, wn * 64 + i * 16 + (lane & 15));
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int r = wm * (BM / 2) + m * 16 + (lane & 15);
+            const Frag qf = frag(qb, r);
+            const float s0 = sc[r] * c0, s1 = F == Form::kGated ? sc[r] * c1 : s0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[m][i] += mfma_step_fp8(pf[i], qf) * (i < 2 ? s0 : s1);
+        }
+    }
+    const int nw = n0 + wn * (F == Form::kGated ? 32 : 64);
+    if constexpr (Epi::kBlockWide)
+        epi.template store_block<MT, 4, 4, BM>(t, start, true, wn, wm * (BM / 2), nw, a.N, acc, lane);
+    else
+        epi.store(t, start, t.m0 + wm * (BM / 2), nw, a.N, acc, lane);
+}
+
+template <Form F, class Epi>
+hipError_t launch_fp8_tiles(FewArgs a, const Groups &G, int64_t rows, int64_t max_tiles, const Epi &epi,
+                            const char *what, hipStream_t stream)
+{
+    const int bm = tile_rows(rows, G.num);
+    const int cols = F == Form::kGated ? BN / 2 : BN;
+    a.nt = unsigned((a.N + cols - 1) / cols);
+    const int64_t mt = rows / bm + (max_tiles < rows ? max_tiles : rows);
+    if (mt * a.nt > kMaxTileBlocks)
+        return hipErrorInvalidValue;
+    if (mt == 0)
+        return hipSuccess;
+    if (log_enabled())
+        log_launch("%s: rows<=%lld groups=%d N=%d K=%d tile=%dx%d blocks=%lld", what, (long long)rows,
+                   G.num, a.N, a.kbytes, bm, BN, (long long)mt * a.nt);
+    const dim3 grid(unsigned(mt * a.nt));
+    if (bm == 256)
+        hipLaunchKernelGGL((fp8_tile_kernel<256, F, Epi>), grid, dim3(NT), 0, stream, a, unsigned(mt), G, epi);
+    else if (bm == 128)
+        hipLaunchKernelGGL((fp8_tile_kernel<128, F, Epi>), grid, dim3(NT), 0, stream, a, unsigned(mt), G, epi);
+    else
+        hipLaunchKernelGGL((fp8_tile_kernel<64, F, Epi>), grid, dim3(NT), 0, stream, a, unsigned(mt), G, epi);
+    return hipGetLastError();
+}
+
+template <int WN, int WK, int NW, int MT, Form F, class Epi>
+hipError_t launch_fp8_few(FewArgs a, const Groups &G, const Epi &epi, const char *what,
+                          hipStream_t stream)
+{
+    constexpr int cols = WN * (F == Form::kGated ? NW / 2 : NW) * 16;
+    a.nt = unsigned((a.N + cols - 1) / cols);
+    const int64_t blocks = int64_t(a.nt) * G.num;
+    if (blocks > kMaxTileBlocks)
+        return hipErrorInvalidValue;
+    if (log_enabled())
+        log_launch("%s: groups=%d N=%d K=%d few rows %d cols=%d waves=%dx%d blocks=%lld", what, G.num,
+                   a.N, a.kbytes, MT * 16, cols, WN, WK, (long long)blocks);
+    hipLaunchKernelGGL((few_rows_kernel<true, WN, WK, NW, MT, F, Epi>), dim3(unsigned(blocks)),
+                       dim3(WN * WK * kWave), 0, stream, a, G, epi);
+    return hipGetLastError();
+}
+
+constexpr int kFewRows = 64;  // groups of at most this many rows take the few-rows kernel
+
+// Groups of few rows by one kernel, the others by the tile kernel: both walk
+// the groups on the device, which alone knows their rows.
+template <Form F, class Epi>
+hipError_t launch_fp8_groups(const FewArgs &a, Groups G, int64_t max_pairs, const Epi &epi,
+                             const char *what, hipStream_t stream)
+{
+    const int64_t avg = max_pairs / G.num;
+    const bool few = avg <= kFewRows / 2;
+    if (few) {
+        Groups F1 = G;
+        F1.max_rows = kFewRows;
+        hipError_t e = avg <= 8
+            ? launch_fp8_few<4, 2, 4, 1, F>(a, F1, epi, what, stream)
+            : launch_fp8_few<4, 2, 4, 2, F>(a, F1, epi, what, stream);
+        if (e != hipSuccess)
+            return e;
+        if (G.slots <= kFewRows || max_pairs <= kFewRows)
+            return hipSuccess;
+        G.min_rows = kFewRows + 1;
+    }
+    // the groups that the tile kernel is left with hold at least min_rows each
+    const int64_t groups = max_pairs / G.min_rows;
+    return launch_fp8_tiles<F>(a, G, max_pairs, groups < G.num ? groups : G.num, epi, what, stream);
+}
+
+}  // namespace
+
+hipError_t launch_fp8_product(int64_t M, int N, int K, const void *a_q, const float *a_scale,
+                              const void *w_q, const float *w_scale, void *out, hipStream_t stream)
+{
+    const Groups G{nullptr, nullptr, int32_t(M), 1, 1, 1, 1, kNoLimit};
+    FewArgs a{};
+    a.q = static_cast<const char *>(a_q);
+    a.q_scale = a_scale;
+    a.ldq = K;
+    a.p = static_cast<const char *>(w_q);
+    a.p_scale = w_scale;
+    a.ldp = K;
+    a.N = N;
+    a.kbytes = K;
+    const RowOut epi{static_cast<uint16_t *>(out)};
+    if (M <= 16)
+        return launch_fp8_few<1, 8, 1, 1, Form::kPlain>(a, G, epi, "fp8_product", stream);
+    if (M <= kFewRows)
+        return launch_fp8_few<1, 8, 1, 4, Form::kPlain>(a, G, epi, "fp8_product", stream);
+    return launch_fp8_tiles<Form::kPlain>(a, G, M, 1, epi, "fp8_product", stream);
+}
+
+hipError_t launch_ll_expert_ffn_fp8(int E, int R, int slots, int H, int I, int64_t max_pairs,
+                                    const int32_t *counts, const void *packed_q,
+                                    const float *packed_scale, const void *w13_q,
+                                    const float *w13_scale, const void *w2_q, const float *w2_scale,
+                                    void *act_q, float *act_scale, void *out, hipStream_t stream)
+{
+    const Groups G{nullptr, counts, slots, E, R, E / R, 1, kNoLimit};
+    FewArgs a{};
+    a.q = static_cast<const char *>(packed_q);
+    a.q_scale = packed_scale;
+    a.ldq = H;
+    a.p = static_cast<const char *>(w13_q);
+    a.p_scale = w13_scale;
+    a.p_expert = int64_t(2) * I * H;
+    a.p_scales = int64_t(2) * (I / 128) * (H / 128);
+    a.ldp = H;
+    a.N = I;
+    a.kbytes = H;
+    hipError_t e = launch_fp8_groups<Form::kGated>(
+        a, G, max_pairs, GatedFp8Out{static_cast<uint8_t *>(act_q), act_scale},
+        "ll_expert_ffn_fp8 gated", stream);
+    if (e != hipSuccess)
+        return e;
+    a.q = static_cast<const char *>(act_q);
+    a.q_scale = act_scale;
+    a.ldq = I;
+    a.p = static_cast<const char *>(w2_q);
+    a.p_scale = w2_scale;
+    a.p_expert = int64_t(I) * H;
+    a.p_scales = int64_t(I / 128) * (H / 128);
+    a.ldp = I;
+    a.N = H;
+    a.kbytes = I;
+    return launch_fp8_groups<Form::kPlain>(a, G, max_pairs, RowOut{static_cast<uint16_t *>(out)},
+                                           "ll_expert_ffn_fp8 down", stream);
+}
+
+}  // namespace ep

@@ -348,6 +348,145 @@ int ep_lb_reduce_grads(const void *redundant_grads, void *expert_grads, const in
                        int32_t num_replicas, int32_t num_experts, int64_t elems_per_expert,
                        ep_stream_t stream);
 
+/*
+ * Root-mean-square norm of token rows, in front of the routing:
+ *   s = fp32(x) + fp32(residual),  rstd = 1 / sqrt(mean(s^2) + eps),  y = s * rstd * weight
+ *   residual_out = bf16_rne(s),  out = bf16_rne(y)
+ *   out_q, out_scale: y in the FP8 format of ep_ll_dispatch_fp8 (e4m3 codes, one
+ *     fp32 scale per 128 elements), quantised from the fp32 y.
+ * x, residual, residual_out, out [num_tokens][hidden] bf16, weight [hidden] bf16,
+ * out_q [num_tokens][hidden] (8-byte aligned), out_scale [num_tokens][hidden/128],
+ * rstd [num_tokens] fp32.  residual, out, out_q and rstd are nullable (out or
+ * out_q is required); residual_out needs residual and may be the same memory as
+ * residual or x.  out_q needs hidden % 128 == 0 (EP_ERR_ALIGN) and out_scale.
+ * eps must be finite and not negative.  No host sync.
+ */
+int ep_rms_norm(int32_t num_tokens, int32_t hidden, float eps, const void *x,
+                const void *residual, const void *weight, void *residual_out, void *out,
+                void *out_q, float *out_scale, float *rstd, ep_stream_t stream);
+
+/*
+ * Gradients of ep_rms_norm at the normed rows h (its residual_out, or x
+ * without a residual) and the rstd it returned:
+ *   a = dout * weight,  xh = h * rstd
+ *   dx = bf16_rne(rstd * (a - xh * mean(a * xh)) + dresidual)
+ *   dweight = sum over tokens of dout * xh   (fp32, in a fixed order)
+ * dx is the gradient of x and of residual alike; dresidual (nullable) is the
+ * gradient that arrived at residual_out.  dweight [hidden] fp32 is overwritten
+ * (zeros without tokens).  workspace: ep_rms_norm_backward_workspace() bytes,
+ * 16-byte aligned, the caller's (EP_ERR_CAPACITY if workspace_bytes is less).
+ */
+size_t ep_rms_norm_backward_workspace(int32_t num_tokens, int32_t hidden);
+int ep_rms_norm_backward(int32_t num_tokens, int32_t hidden, const void *dout, const void *h,
+                         const void *weight, const float *rstd, const void *dresidual, void *dx,
+                         float *dweight, void *workspace, size_t workspace_bytes,
+                         ep_stream_t stream);
+
+/*
+ * Product of FP8 rows with an FP8 weight, one fp32 scale per 128 inner
+ * elements of a row and per 128 x 128 block of the weight:
+ *   out[m][n] = bf16_rne( sum_b a_scale[m][b] * w_scale[n / 128][b]
+ *                         * sum_{k in block b} a[m][k] * w[n][k] ),  fp32 sums.
+ * a_q [m][k] and w_q [n][k] e4m3 codes, 16-byte aligned; a_scale [m][k/128],
+ * w_scale [ceil(n/128)][k/128]; out [m][n] bf16.  k % 128 == 0 and n % 8 == 0
+ * (EP_ERR_ALIGN), k and n at most 2^20.  No host sync.
+ */
+int ep_fp8_product(int32_t m, int32_t n, int32_t k, const void *a_q, const float *a_scale,
+                   const void *w_q, const float *w_scale, void *out, ep_stream_t stream);
+
+/*
+ * The experts' gated feed-forward on low-latency cells (packed_x and
+ * packed_count as ep_ll_dispatch left them).  For a used cell with row x of
+ * expert e, and I = inter:
+ *   g = x Wg^T,  u = x Wu^T,  act = g * sigmoid(g) * u,  out = act W2^T
+ * w13 [E][2 I][H] bf16 holds expert e's Wg rows, then its Wu rows; w2 [E][H][I]
+ * bf16; E is indexed by the expert id (r * E/R + le for cell block [le][r]).
+ * act [E/R][R][num_slots][I] bf16 is workspace; the activation is rounded to
+ * bf16 between the products (fp32 sums in both).  out has packed_x's layout;
+ * unused cells are neither read nor written.  Counts above num_slots are taken
+ * as num_slots.  num_tokens and num_topk bound the used cells: the counts must
+ * add up to at most num_tokens * num_topk (experts past that are left out).
+ * inter % 8 == 0 (EP_ERR_ALIGN).  No host sync.
+ */
+int ep_ll_expert_ffn(const ep_dims *dims, int32_t num_slots, int32_t inter, const void *packed_x,
+                     const int32_t *packed_count, const void *w13, const void *w2, void *act,
+                     void *out, ep_stream_t stream);
+
+/*
+ * ep_ll_expert_ffn on the cells of ep_ll_dispatch_fp8 with FP8 weights (one
+ * scale per 128 x 128 block: w13_scale [E][2 I/128][H/128], w2_scale
+ * [E][H/128][I/128]).  Between the products the activation is quantised, from
+ * its fp32 value, in the same format: act_q [E/R][R][num_slots][I] codes and
+ * act_scale [..][I/128] are workspace.  out is bf16.  hidden % 128 == 0 and
+ * inter % 128 == 0 (EP_ERR_ALIGN).
+ */
+int ep_ll_expert_ffn_fp8(const ep_dims *dims, int32_t num_slots, int32_t inter,
+                         const void *packed_q, const float *packed_scale,
+                         const int32_t *packed_count, const void *w13_q, const float *w13_scale,
+                         const void *w2_q, const float *w2_scale, void *act_q, float *act_scale,
+                         void *out, ep_stream_t stream);
+
+/*
+ * Dispatched rows grouped by expert.  A pair is a valid slot of a row:
+ * recv_topk_idx[row][k] in [0, E/R), row in segment r as rank_prefix (the
+ * layout's rank_prefix_matrix) has it; its expert is r * E/R + the id.  Rows at
+ * or past rank_prefix[R-1] hold no pairs, whatever their ids.  Pairs are sorted
+ * by (expert, row, slot).
+ *   recv_topk_idx  int64 [num_rows][K]
+ *   expert_offsets int32 [E + 1]   expert e's pairs are [e], ..., [e + 1] - 1
+ *   pair_row       int32 [pair_cap] row of the pair; the sign bit is set when it
+ *                                   is the only pair of its row
+ *   pair_slot      int32 [pair_cap] row * K + slot
+ *   row_pair       int32 [num_rows][K] the slot's pair, -1 if none
+ *   counts         int32 [E] workspace (the pairs of each expert)
+ * pair_cap must be at least min(num_tokens, num_rows) * K (EP_ERR_CAPACITY): a
+ * dispatch gives each of its num_tokens * K slots to one row.  Pairs past it
+ * are left out.  num_rows * K and pair_cap at most 2^31 - 1.  No host sync.
+ */
+int ep_expert_rows(const ep_dims *dims, const int32_t *rank_prefix, const int64_t *recv_topk_idx,
+                   int64_t num_rows, int64_t pair_cap, int32_t *counts, int32_t *expert_offsets,
+                   int32_t *pair_row, int32_t *pair_slot, int32_t *row_pair, ep_stream_t stream);
+
+/* What ep_expert_rows wrote, for the calls below. */
+typedef struct ep_expert_groups {
+    int64_t num_rows;
+    int64_t pair_cap;
+    const int32_t *expert_offsets;
+    const int32_t *pair_row;
+    const int32_t *pair_slot;
+    const int32_t *row_pair;
+} ep_expert_groups;
+
+/*
+ * The experts between ep_dispatch and ep_combine: for every row of x
+ * [num_rows][hidden] (bf16, packed rows)
+ *   y[row] = bf16_rne( sum over its pairs, slot ascending, of
+ *                      topk_weights[row][slot] * (act W2^T) ),  act as above,
+ * a row without pairs giving +0.  topk_weights fp32 [num_rows][K], w13 and w2
+ * as for ep_ll_expert_ffn.  Workspaces: act [pair_cap][inter] bf16, terms
+ * [pair_cap][hidden] fp32 (16-byte aligned).  gate_up [pair_cap][2 inter] fp32
+ * (nullable) receives g and u, which the backward pass needs.  Of dims, the
+ * tokens and channels are not used.  inter % 8 == 0 (EP_ERR_ALIGN).
+ */
+int ep_expert_ffn(const ep_dims *dims, int32_t inter, const ep_expert_groups *groups,
+                  const void *x, const float *topk_weights, const void *w13, const void *w2,
+                  void *act, float *gate_up, float *terms, void *y, ep_stream_t stream);
+
+/*
+ * Gradients of ep_expert_ffn given dy [num_rows][hidden] bf16:
+ *   dx [num_rows][hidden] bf16 (+0 for rows without pairs), dtopk_weights
+ *   [num_rows][K] fp32 (0 for slots without a pair), dw13 [E][2 inter][hidden]
+ *   and dw2 [E][hidden][inter] bf16 (zeros for experts without pairs), each
+ *   overwritten.  All sums are fp32 in a fixed order.
+ * Workspaces: dgate_up [pair_cap][2 inter] bf16, act [pair_cap][inter] bf16,
+ * terms [pair_cap][hidden] fp32, parts [pair_cap][ceil(inter / 256)] fp32.
+ */
+int ep_expert_ffn_backward(const ep_dims *dims, int32_t inter, const ep_expert_groups *groups,
+                           const void *dy, const void *x, const float *topk_weights,
+                           const void *w13, const void *w2, const float *gate_up, void *dgate_up,
+                           void *act, float *terms, float *parts, void *dx, float *dtopk_weights,
+                           void *dw13, void *dw2, ep_stream_t stream);
+
 /* Copy the handle's layout into caller buffers (fields may be NULL); same
  * shapes and capacity rule as ep_get_dispatch_layout. */
 int ep_handle_copy_layout(ep_handle *handle, ep_layout_out *out, ep_stream_t stream);
@@ -425,7 +564,8 @@ const char *ep_last_hip_error(void);
  * ep_get_dispatch_layout, ep_dispatch and ep_combine; 2.1: ep_ll_combine_fp8;
  * 2.2: ep_pool_stats and the capped pool; 2.3: ep_get_dispatch_layout_noalloc
  * and EP_ERR_TOO_LARGE; 2.4: the destination-major dispatch and gather-form
- * combine tuning shapes (code X*10000). */
+ * combine tuning shapes (code X*10000).  The expert operations (ep_rms_norm to
+ * ep_expert_ffn_backward) were added without a new number: look the symbol up. */
 int ep_version(void);
 
 #ifdef __cplusplus
