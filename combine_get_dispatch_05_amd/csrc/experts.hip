@@ -214,9 +214,7 @@ struct GatedBack {
 
 // ------------------------------------------------------------ tile kernels
 
-// BM rows of one group by BN columns.  Two LDS stages: while the waves work on
-// one, the other fills; one barrier a K step both publishes the filled stage
-// and retires the one that was read.
+// BM rows of one group by BN columns, with as many LDS stages as fit.
 template <int BM, bool PCOL, Form F, class Epi>
 __global__ __launch_bounds__(NT) void tile_kernel(TileArgs a, Groups G, Epi epi)
 {
@@ -224,20 +222,18 @@ __global__ __launch_bounds__(NT) void tile_kernel(TileArgs a, Groups G, Epi epi)
     using QS = RowStage<BM, NT>;
     using PR = RowStage<BN, NT>;
     using PC = ColStage<BN, NT>;
-    constexpr int kP = PR::kBytes, kQ = QS::kBytes;
-    __shared__ __attribute__((aligned(128))) char smem[2 * (kP + kQ)];
-    __shared__ int scan[NT / kWave];
-    unsigned tm, tn;
-    tile_of_block(blockIdx.x, a.mt, a.nt, tm, tn);
-    const Tile t = find_tile<BM, NT>(G, int(tm), scan);
+    constexpr int kP = PR::kBytes, kStage = kP + QS::kBytes, ST = BM == 256 ? 2 : 3;
+    __shared__ __attribute__((aligned(128))) char smem[ST * kStage];
+    const Tile t = find_tile<BM, NT>(G, blockIdx.x, a.nt);
     if (t.group < 0)
         return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
     const int64_t start = group_start(G, t.group);
     const char *pw = a.p + int64_t(group_expert(G, t.group)) * a.p_expert;
     lds_char *lds = (lds_char *)smem;
-    const int n0 = int(tn) * (F == Form::kGated ? BN / 2 : BN);
+    const int n0 = t.n * (F == Form::kGated ? BN / 2 : BN);
 
     QS qs;
     qs.init(tid, [&](int r) {
@@ -266,45 +262,29 @@ __global__ __launch_bounds__(NT) void tile_kernel(TileArgs a, Groups G, Epi epi)
     }
     const int steps = (a.K + 63) / 64;
     const int64_t kbytes = int64_t(a.K) * 2;
-    auto issue = [&](int s, int buf) {
-        lds_char *b = lds + buf * (kP + kQ);
-        if constexpr (PCOL)
-            pc.issue(b, wave, s * 64, a.K, [&](int, int k) { return pw + int64_t(k) * a.ldp; });
+    auto stage = [&](int s) -> lds_char * { return lds + (ST == 2 ? s & 1 : s % ST) * kStage; };
+    auto issue = [&](int s, int part) {
+        if (part == 1)
+            qs.template issue<true>(stage(s) + kP, wave, int64_t(s) * kStepBytes, kbytes);
+        else if constexpr (PCOL)
+            pc.issue(stage(s), wave, s * 64, a.K, [&](int, int k) { return pw + int64_t(k) * a.ldp; });
         else
-            pr.issue(b, wave, int64_t(s) * kStepBytes, kbytes);
-        qs.issue(b + kP, wave, int64_t(s) * kStepBytes, kbytes);
+            pr.template issue<true>(stage(s), wave, int64_t(s) * kStepBytes, kbytes);
     };
-
+    auto frag_p = [&](int s, int i, int ks) {
+        const int c = wn * 64 + i * 16;
+        if constexpr (PCOL)
+            return PC::frag(stage(s), c, ks, lane);
+        else
+            return PR::frag(stage(s), c, ks, lane);
+    };
+    auto frag_q = [&](int s, int m, int ks) {
+        return QS::frag(stage(s) + kP, wm * (BM / 2) + m * 16, ks, lane);
+    };
     f32x4 acc[MT][4] = {};
-    issue(0, 0);
-    for (int s = 0; s < steps; ++s) {
-        landed<0>();
-        __syncthreads();  // stage s is in LDS, stage s - 1 is read
-        if (s + 1 < steps)
-            issue(s + 1, (s + 1) & 1);
-        const lds_char *pb = lds + (s & 1) * (kP + kQ), *qb = pb + kP;
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            bf16x8 pf[4], qf[MT];
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                if constexpr (PCOL)
-                    pf[nt] = PC::frag(pb, wn * 64 + nt * 16, ks, lane);
-                else
-                    pf[nt] = *(const __attribute__((address_space(3))) bf16x8 *)PR::at(
-                        pb, wn * 64 + nt * 16 + (lane & 15), ks * 4 + (lane >> 4));
-            }
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-                qf[mt] = *(const __attribute__((address_space(3))) bf16x8 *)QS::at(
-                    qb, wm * (BM / 2) + mt * 16 + (lane & 15), ks * 4 + (lane >> 4));
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
-                    acc[mt][nt] = mfma_bf16(pf[nt], qf[mt], acc[mt][nt]);
-        }
-    }
+    Bf16Phases<MT, decltype(frag_p), decltype(frag_q)> ph{acc, frag_p, frag_q};
+    take_turns<decltype(ph)::kPhases, ST, PR::J + QS::J>(
+        steps, wm, issue, [&](int s, int i) { ph.read(s, i); }, [&](int, int i) { ph.compute(i); });
 
     const int mw = t.m0 + wm * (BM / 2);
     if constexpr (F == Form::kBack) {
@@ -346,7 +326,7 @@ __global__ __launch_bounds__(NT) void tile_kernel(TileArgs a, Groups G, Epi epi)
         }
         __syncthreads();
         if (tid < BM && t.m0 + tid < t.rows)
-            epi.dweight_part[(start + t.m0 + tid) * epi.tiles + tn] =
+            epi.dweight_part[(start + t.m0 + tid) * epi.tiles + t.n] =
                 (part[tid] + part[BM + tid]) + (part[2 * BM + tid] + part[3 * BM + tid]);
     } else {
         const int nw = n0 + wn * (F == Form::kGated ? 32 : 64);
@@ -370,7 +350,8 @@ __global__ __launch_bounds__(NT) void weight_grad_kernel(const char *q, int64_t 
     const int e = blockIdx.x / (mt * nt);
     unsigned tm, tn;
     tile_of_block(blockIdx.x % (mt * nt), mt, nt, tm, tn);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
     const int start = offsets[e], rows = offsets[e + 1] - start;
     const int steps = (rows + 63) / 64;
@@ -387,48 +368,33 @@ __global__ __launch_bounds__(NT) void weight_grad_kernel(const char *q, int64_t 
                 nxt[j] = pair_row[start + k] & kRowMask;
         }
     };
-    auto issue = [&](int s, int buf) {
+    auto stage = [&](int s) -> lds_char * { return lds + (s & 1) * 2 * CS::kBytes; };
+    auto issue = [&](int s, int part) {
+        if (part == 0) {
 #pragma unroll
-        for (int j = 0; j < CS::J; ++j)
-            idx[j] = nxt[j];
-        lds_char *b = lds + buf * 2 * CS::kBytes;
-        ps.issue(b, wave, s * 64, rows, [&](int j, int k) {
-            return p + (PG ? int64_t(idx[j]) : int64_t(start) + k) * ldp;
-        });
-        qs.issue(b + CS::kBytes, wave, s * 64, rows, [&](int j, int k) {
-            return q + (QG ? int64_t(idx[j]) : int64_t(start) + k) * ldq;
-        });
+            for (int j = 0; j < CS::J; ++j)
+                idx[j] = nxt[j];
+            ps.issue(stage(s), wave, s * 64, rows, [&](int j, int k) {
+                return p + (PG ? int64_t(idx[j]) : int64_t(start) + k) * ldp;
+            });
+        } else {
+            qs.issue(stage(s) + CS::kBytes, wave, s * 64, rows, [&](int j, int k) {
+                return q + (QG ? int64_t(idx[j]) : int64_t(start) + k) * ldq;
+            });
+            if (s + 1 < steps)
+                fetch(s + 1);
+        }
+    };
+    auto frag_p = [&](int s, int i, int ks) { return CS::frag(stage(s), wn * 64 + i * 16, ks, lane); };
+    auto frag_q = [&](int s, int m, int ks) {
+        return CS::frag(stage(s) + CS::kBytes, wm * 128 + m * 16, ks, lane);
     };
     f32x4 acc[8][4] = {};
     if (steps > 0) {
         fetch(0);
-        issue(0, 0);
-        if (steps > 1)
-            fetch(1);
-    }
-    for (int s = 0; s < steps; ++s) {
-        landed<0>();
-        __syncthreads();
-        if (s + 1 < steps) {
-            issue(s + 1, (s + 1) & 1);
-            if (s + 2 < steps)
-                fetch(s + 2);
-        }
-        const lds_char *pb = lds + (s & 1) * 2 * CS::kBytes, *qb = pb + CS::kBytes;
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            bf16x8 pf[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                pf[i] = CS::frag(pb, wn * 64 + i * 16, ks, lane);
-#pragma unroll
-            for (int m = 0; m < 8; ++m) {
-                const bf16x8 qf = CS::frag(qb, wm * 128 + m * 16, ks, lane);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[m][i] = mfma_bf16(pf[i], qf, acc[m][i]);
-            }
-        }
+        Bf16Phases<8, decltype(frag_p), decltype(frag_q)> ph{acc, frag_p, frag_q};
+        take_turns<4, 2, 2 * CS::J>(
+            steps, wm, issue, [&](int s, int i) { ph.read(s, i); }, [&](int, int i) { ph.compute(i); });
     }
     uint16_t *o = out + int64_t(e) * M * N;
 #pragma unroll
@@ -501,7 +467,6 @@ hipError_t launch_tiles(TileArgs a, const Groups &G, int64_t max_tiles_rows, con
     a.nt = unsigned((a.N + cols - 1) / cols);
     if (mt * a.nt > kMaxTileBlocks)
         return hipErrorInvalidValue;
-    a.mt = unsigned(mt);
     if (mt == 0)
         return hipSuccess;
     if (log_enabled())

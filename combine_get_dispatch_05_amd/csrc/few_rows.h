@@ -60,7 +60,7 @@ __global__ __launch_bounds__(WN *WK *kWave) void few_rows_kernel(FewArgs a, Grou
     constexpr int kCols = WN * (F == Form::kGated ? NW / 2 : NW) * 16;  // of a block
     constexpr int kWaveCols = kCols / WN;
     __shared__ f32x4 sums[WK > 1 ? (WK - 1) * WN * MT * NW * kWave : 1];
-    const int g = blockIdx.x / a.nt, tn = blockIdx.x % a.nt;
+    const int g = blockIdx.x / a.nt, tn = int(blockIdx.x % a.nt);
     const int rows = group_rows(G, g);
     if (rows == 0)
         return;
@@ -174,7 +174,7 @@ __global__ __launch_bounds__(WN *WK *kWave) void few_rows_kernel(FewArgs a, Grou
                             acc[m][i] += sums[(((w * WN + wn) * MT + m) * NW + i) * kWave + lane];
             }
         }
-        const Tile t{g, m0, rows};
+        const Tile t{g, m0, rows, tn};
         if constexpr (Epi::kBlockWide)
             epi.template store_block<MT, NW, WN, 16 * MT>(t, start, wk == 0, wn, 0, n0, a.N, acc, lane);
         else if (wk == 0)

@@ -74,17 +74,14 @@ struct GatedFp8Out {
 // BM rows of one group by BN columns: the bf16 tile kernel's loop with K steps
 // of one scale block.  The step's token scales are staged beside the rows.
 template <int BM, Form F, class Epi>
-__global__ __launch_bounds__(NT) void fp8_tile_kernel(FewArgs a, unsigned gmt, Groups G, Epi epi)
+__global__ __launch_bounds__(NT) void fp8_tile_kernel(FewArgs a, Groups G, Epi epi)
 {
     constexpr int MT = BM / 32;
     using QS = RowStage<BM, NT>;
     using PR = RowStage<BN, NT>;
-    constexpr int kP = PR::kBytes, kQ = QS::kBytes, kStage = kP + kQ + BM * 4;
-    __shared__ __attribute__((aligned(128))) char smem[2 * kStage];
-    __shared__ int scan[NT / kWave];
-    unsigned tm, tn;
-    tile_of_block(blockIdx.x, gmt, a.nt, tm, tn);
-    const Tile t = find_tile<BM, NT>(G, int(tm), scan);
+    constexpr int kP = PR::kBytes, kQ = QS::kBytes, kStage = kP + kQ + (BM + kWave) * 4, ST = BM == 256 ? 2 : 3;
+    __shared__ __attribute__((aligned(128))) char smem[ST * kStage];
+    const Tile t = find_tile<BM, NT>(G, blockIdx.x, a.nt);
     if (t.group < 0)
         return;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -94,7 +91,7 @@ __global__ __launch_bounds__(NT) void fp8_tile_kernel(FewArgs a, unsigned gmt, G
     const int e = group_expert(G, t.group);
     const char *pw = a.p + int64_t(e) * a.p_expert;
     lds_char *lds = (lds_char *)smem;
-    const int n0 = int(tn) * (F == Form::kGated ? BN / 2 : BN);
+    const int n0 = t.n * (F == Form::kGated ? BN / 2 : BN);
     const int steps = a.kbytes >> 7;
 
     QS qs;
@@ -113,57 +110,81 @@ __global__ __launch_bounds__(NT) void fp8_tile_kernel(FewArgs a, unsigned gmt, G
         }
         return pw + int64_t(n) * a.ldp;
     });
-    const int mclamp = t.m0 + tid < t.rows ? t.m0 + tid : t.rows - 1;
-    const char *sq = reinterpret_cast<const char *>(a.q_scale + (start + mclamp) * steps);
-    auto issue = [&](int s, int buf) {
-        lds_char *b = lds + buf * kStage;
-        pr.issue(b, wave, int64_t(s) * kStepBytes, a.kbytes);
-        qs.issue(b + kP, wave, int64_t(s) * kStepBytes, a.kbytes);
-        if (wave < BM / kWave)
-            load_lds4(sq + int64_t(s) * 4, b + kP + kQ + wave * kWave * 4);
-    };
-    // this wave's weight scales: one block of columns, or one of gate and one of up
-    const int nb = F == Form::kGated ? n0 : n0 + wn * 64;
-    const float *sp0 = a.p_scale + e * a.p_scales + int64_t((nb < a.N ? nb : a.N - 1) >> 7) * steps;
-    const float *sp1 = F == Form::kGated ? sp0 + int64_t(a.N >> 7) * steps : sp0;
-
-    f32x4 acc[MT][4] = {};
-    issue(0, 0);
-    float w0 = sp0[0], w1 = F == Form::kGated ? sp1[0] : 0.0f;
-    for (int s = 0; s < steps; ++s) {
-        landed<0>();
-        __syncthreads();
-        float c0 = w0, c1 = F == Form::kGated ? w1 : w0;
-        asm volatile("" : "+v"(c0), "+v"(c1));  // their wait belongs here, before the next stage's loads
-        if (s + 1 < steps) {
-            issue(s + 1, (s + 1) & 1);
-            w0 = sp0[s + 1];
-            if constexpr (F == Form::kGated)
-                w1 = sp1[s + 1];
-        }
-        const lds_char *pb = lds + (s & 1) * kStage, *qb = pb + kP;
-        const __attribute__((address_space(3))) float *sc =
-            (const __attribute__((address_space(3))) float *)(qb + kQ);
-        auto frag = [&](const lds_char *base, int r) {
-            Frag f;
-            f.lo = *(const __attribute__((address_space(3))) i32x4 *)QS::at(base, r, lane >> 4);
-            f.hi = *(const __attribute__((address_space(3))) i32x4 *)QS::at(base, r, 4 + (lane >> 4));
-            return f;
-        };
-        Frag pf[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            pf[i] = frag(pb, wn * 64 + i * 16 + (lane & 15));
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int r = wm * (BM / 2) + m * 16 + (lane & 15);
-            const Frag qf = frag(qb, r);
-            const float s0 = sc[r] * c0, s1 = F == Form::kGated ? sc[r] * c1 : s0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                acc[m][i] += mfma_step_fp8(pf[i], qf) * (i < 2 ? s0 : s1);
-        }
+    // Scales are staged behind the rows, one load a wave, so that every wave counts
+    // the same loads: waves 0 to 3 the BM token scales (some twice where BM is
+    // less than 256), the others the two weight scales of the tile: its column
+    // blocks, or its gate block and its up block.
+    const char *sq;
+    if (wave < 4) {
+        const int m = t.m0 + tid % BM;
+        sq = reinterpret_cast<const char *>(a.q_scale + (start + (m < t.rows ? m : t.rows - 1)) * steps);
+    } else {
+        int nb = n0 + (F == Form::kGated ? 0 : (lane & 1) * 128);
+        nb = (nb < a.N ? nb : a.N - 1) >> 7;
+        if (F == Form::kGated)
+            nb += (lane & 1) * (a.N >> 7);
+        sq = reinterpret_cast<const char *>(a.p_scale + e * a.p_scales + int64_t(nb) * steps);
     }
+    const int sdst = kP + kQ + (wave < 4 ? wave % (BM / kWave) : BM / kWave) * kWave * 4;
+    auto stage = [&](int s) -> lds_char * { return lds + (ST == 2 ? s & 1 : s % ST) * kStage; };
+    auto issue = [&](int s, int part) {
+        lds_char *b = stage(s);
+        if (part == 0) {
+            pr.template issue<false>(b, wave, int64_t(s) * kStepBytes, a.kbytes);
+        } else {
+            qs.template issue<false>(b + kP, wave, int64_t(s) * kStepBytes, a.kbytes);
+            load_lds4(sq + int64_t(s) * 4, b + sdst);
+        }
+    };
+    auto frag = [&](const lds_char *base, int r) {
+        Frag f;
+        f.lo = *(const __attribute__((address_space(3))) i32x4 *)QS::at(base, r, lane >> 4);
+        f.hi = *(const __attribute__((address_space(3))) i32x4 *)QS::at(base, r, 4 + (lane >> 4));
+        return f;
+    };
+    constexpr int PH = MT >= 4 ? MT / 2 : 1, MQ = MT / PH;  // two row tiles a phase
+    f32x4 acc[MT][4] = {};
+    Frag pf[4], qf[MQ];
+    float sc[MQ], c0 = 0.0f, c1 = 0.0f;
+    take_turns<PH, ST, PR::J + QS::J + 1>(
+        steps, wm, issue,
+        [&](int s, int ph) {
+            const lds_char *pb = stage(s), *qb = pb + kP;
+            if (ph == 0) {
+                const __attribute__((address_space(3))) float *w =
+                    (const __attribute__((address_space(3))) float *)(qb + kQ + BM * 4);
+                c0 = w[F == Form::kGated ? 0 : wn >> 1];
+                c1 = F == Form::kGated ? w[1] : c0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    pf[i] = frag(pb, wn * 64 + i * 16 + (lane & 15));
+            }
+#pragma unroll
+            for (int m = 0; m < MQ; ++m) {
+                const int r = wm * (BM / 2) + (ph * MQ + m) * 16 + (lane & 15);
+                qf[m] = frag(qb, r);
+                sc[m] = *(const __attribute__((address_space(3))) float *)(qb + kQ + r * 4);
+            }
+        },
+        [&](int, int ph) {
+#pragma unroll
+            for (int m = 0; m < MQ; ++m) {
+                hold(qf[m].lo);
+                hold(qf[m].hi);
+            }
+#pragma unroll
+            for (int m = 0; m < MQ; ++m) {
+                const float s0 = sc[m] * c0, s1 = F == Form::kGated ? sc[m] * c1 : s0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[ph * MQ + m][i] += mfma_step_fp8(pf[i], qf[m]) * (i < 2 ? s0 : s1);
+            }
+#pragma unroll
+            for (int m = 0; m < MQ; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    hold(acc[ph * MQ + m][i]);
+        });
     const int nw = n0 + wn * (F == Form::kGated ? 32 : 64);
     if constexpr (Epi::kBlockWide)
         epi.template store_block<MT, 4, 4, BM>(t, start, true, wn, wm * (BM / 2), nw, a.N, acc, lane);
@@ -188,11 +209,11 @@ hipError_t launch_fp8_tiles(FewArgs a, const Groups &G, int64_t rows, int64_t ma
                    G.num, a.N, a.kbytes, bm, BN, (long long)mt * a.nt);
     const dim3 grid(unsigned(mt * a.nt));
     if (bm == 256)
-        hipLaunchKernelGGL((fp8_tile_kernel<256, F, Epi>), grid, dim3(NT), 0, stream, a, unsigned(mt), G, epi);
+        hipLaunchKernelGGL((fp8_tile_kernel<256, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
     else if (bm == 128)
-        hipLaunchKernelGGL((fp8_tile_kernel<128, F, Epi>), grid, dim3(NT), 0, stream, a, unsigned(mt), G, epi);
+        hipLaunchKernelGGL((fp8_tile_kernel<128, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
     else
-        hipLaunchKernelGGL((fp8_tile_kernel<64, F, Epi>), grid, dim3(NT), 0, stream, a, unsigned(mt), G, epi);
+        hipLaunchKernelGGL((fp8_tile_kernel<64, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
     return hipGetLastError();
 }
 

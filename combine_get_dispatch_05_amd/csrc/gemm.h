@@ -17,6 +17,10 @@
 // Both are staged by the loads that write LDS directly, 16 bytes a lane, in
 // K steps of 128 bytes (64 bf16 or 128 FP8 values).  LDS is written in lane
 // order, so the bank swizzle is applied to the global address instead.
+//
+// The eight waves of a block are two groups of four, one wave of each on every
+// SIMD, and take turns (take_turns): while one group's wave keeps the matrix
+// core busy, the other reads its next fragments from LDS and sends off loads.
 #pragma once
 
 #include "ep_internal.h"
@@ -93,10 +97,12 @@ struct RowStage {
             ptr[j] = row_ptr(r) + cb[j];
         }
     }
-    // Stage K bytes [kb, kb + 128); kbytes: all K bytes of the operand.
+    // Stage K bytes [kb, kb + 128); kbytes: all K bytes of the operand (a whole
+    // number of steps where TAIL is false).
+    template <bool TAIL>
     __device__ __forceinline__ void issue(lds_char *base, int wave, int64_t kb, int64_t kbytes)
     {
-        const bool whole = kb + kStepBytes <= kbytes;
+        const bool whole = !TAIL || kb + kStepBytes <= kbytes;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             const char *p = ptr[j] + kb;
@@ -109,6 +115,13 @@ struct RowStage {
     static __device__ __forceinline__ const lds_char *at(const lds_char *base, int r, int ch)
     {
         return base + r * kStepBytes + ((ch ^ ((r >> 1) & 7)) << 4);
+    }
+    // bf16 fragment of 16 rows from r0 and the 32 k values of half ks: lane l
+    // gets row r0 + l % 16, k = ks * 32 + (l / 16) * 8 .. + 7.
+    static __device__ __forceinline__ bf16x8 frag(const lds_char *base, int r0, int ks, int lane)
+    {
+        return *(const __attribute__((address_space(3))) bf16x8 *)at(base, r0 + (lane & 15),
+                                                                     ks * 4 + (lane >> 4));
     }
 };
 
@@ -180,7 +193,21 @@ constexpr int32_t kRowMask = 0x7fffffff;  // pair_row without its "only pair of 
 // each; kBack: the gate's backward.
 enum class Form { kPlain, kGated, kBack };
 
-__device__ __forceinline__ float sigmoidf(float v) { return 1.0f / (1.0f + expf(-v)); }
+// 1 / (1 + e^-v), good to a few units in the last place.  e^-v = 2^t (1 + r ln 2)
+// with t = -v / ln 2 rounded and r what the rounding lost; one Newton step on the
+// hardware reciprocal.  Below -87 the result would no longer be a normal number.
+// (The library's exponential and division took 13 us of a 254 us tile.)
+__device__ __forceinline__ float sigmoidf(float v)
+{
+    constexpr float kLog2e = 1.44269504f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.69314718f;
+    v = v < -87.0f ? -87.0f : v;
+    const float t = -v * kLog2e;
+    const float r = fmaf(-v, kLog2e, -t) - v * kLog2eLow;
+    const float e = __builtin_amdgcn_exp2f(t);
+    const float d = 1.0f + fmaf(e, r * kLn2, e);
+    const float q = __builtin_amdgcn_rcpf(d);
+    return fmaf(q, fmaf(-d, q, 1.0f), q);
+}
 
 __device__ __forceinline__ uint2 pack4(f32x4 v)
 {
@@ -195,7 +222,7 @@ struct TileArgs {
     int64_t p_expert;         // bytes of an expert's weight
     int64_t ldp;              // bytes of a weight row
     int N, K;                 // columns (I for the gated form) and inner length
-    unsigned mt, nt;          // grid of row and column tiles
+    unsigned nt;              // column tiles
 };
 
 // ------------------------------------------------------------------ tiles
@@ -237,53 +264,8 @@ struct Tile {
     int group;
     int m0;    // first row of the tile inside its group
     int rows;  // rows of the group
+    int n;     // column tile
 };
-
-// The tile-th row tile over all groups (each cut into ceil(rows / BM)), or
-// group = -1 past the last.  Every thread of the block takes part; s: NT/64 + 1
-// ints of LDS.
-template <int BM, int NT>
-__device__ __forceinline__ Tile find_tile(const Groups &G, int tile, int *s)
-{
-    constexpr int W = NT / kWave;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    __shared__ int found[3];
-    if (threadIdx.x == 0)
-        found[0] = -1;
-    int base = 0;
-    for (int g0 = 0; g0 < G.num; g0 += NT) {
-        const int g = g0 + threadIdx.x;
-        const int rows = g < G.num ? group_rows(G, g) : 0;
-        const int t = (rows + BM - 1) / BM;
-        int pre = t;
-#pragma unroll
-        for (int d = 1; d < kWave; d <<= 1) {
-            const int o = __shfl_up(pre, d);
-            pre += lane >= d ? o : 0;
-        }
-        if (lane == 63)
-            s[wave] = pre;
-        __syncthreads();
-        int before = base, total = base;
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            const int v = s[w];
-            before += w < wave ? v : 0;
-            total += v;
-        }
-        const int first = before + pre - t;
-        if (tile >= first && tile < first + t) {
-            found[0] = g;
-            found[1] = (tile - first) * BM;
-            found[2] = rows;
-        }
-        __syncthreads();
-        base = total;
-        if (tile < base)
-            break;
-    }
-    return Tile{found[0], found[1], found[2]};
-}
 
 // Block id -> (row tile, column tile).  Consecutive blocks go round the eight
 // XCDs, so each XCD is given a contiguous run of the tile order; in it, bands
@@ -305,10 +287,209 @@ __device__ __forceinline__ void tile_of_block(unsigned b, unsigned mt, unsigned 
     m = band * kBand + r % h;
 }
 
+// The tile of block b, over all groups (each cut into ceil(rows / BM) row
+// tiles) and nt column tiles; group = -1 for a block past the last.  The order
+// is laid over the tiles that there are, not over the grid, which is as large
+// as the rows could make it: otherwise the empty end would fall to one XCD.
+// Every thread takes part.
+template <int BM, int NT>
+__device__ __forceinline__ Tile find_tile(const Groups &G, unsigned b, unsigned nt)
+{
+    constexpr int W = NT / kWave;
+    __shared__ int s[W], found[4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    auto tiles_of = [&](int g, int &rows) {
+        rows = g < G.num ? group_rows(G, g) : 0;
+        return (rows + BM - 1) / BM;
+    };
+    auto scan = [&](int t, int &total) {  // exclusive sum of t over the block
+        int pre = t;
+#pragma unroll
+        for (int d = 1; d < kWave; d <<= 1) {
+            const int o = __shfl_up(pre, d);
+            pre += lane >= d ? o : 0;
+        }
+        __syncthreads();
+        if (lane == 63)
+            s[wave] = pre;
+        __syncthreads();
+        int before = 0;
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const int v = s[w];
+            before += w < wave ? v : 0;
+            total += v;
+        }
+        return before + pre - t;
+    };
+    if (threadIdx.x == 0)
+        found[0] = -1;
+    int rows = 0, total = 0;
+    int t = tiles_of(threadIdx.x, rows);
+    int first = scan(t, total);
+    int all = total;
+    for (int g0 = NT; g0 < G.num; g0 += NT) {  // more groups than threads: the sum first
+        int r, n;
+        scan(tiles_of(g0 + threadIdx.x, r), n);
+        all += n;
+    }
+    if (b >= unsigned(all) * nt)
+        return Tile{-1, 0, 0, 0};
+    unsigned tm, tn;
+    tile_of_block(b, unsigned(all), nt, tm, tn);
+    for (int g0 = 0, base = 0;;) {
+        if (int(tm) >= base + first && int(tm) < base + first + t) {
+            found[0] = g0 + threadIdx.x;
+            found[1] = (int(tm) - base - first) * BM;
+            found[2] = rows;
+        }
+        base += total;
+        g0 += NT;
+        if (int(tm) < base || g0 >= G.num)
+            break;
+        t = tiles_of(g0 + threadIdx.x, rows);
+        first = scan(t, total);
+    }
+    __syncthreads();
+    return Tile{found[0], found[1], found[2], int(tn)};
+}
+
 __device__ __forceinline__ f32x4 mfma_bf16(bf16x8 a, bf16x8 b, f32x4 c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
+
+// A barrier that is only that: no wait for loads in flight, and nothing the
+// compiler may move across.
+__device__ __forceinline__ void turn()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_barrier" : : : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Ties a value to its place among the barriers: matrix instructions touch no
+// memory, so only what they read keeps them from being moved across one.
+template <class T>
+__device__ __forceinline__ void hold(T &v)
+{
+    asm volatile("" : "+v"(v));
+}
+
+// The K loop.  A stage is worked off in PH phases, each of them a read half
+// (read(s, ph): LDS reads, and the loads of stage s + ST - 1) and a compute half
+// (compute(s, ph): matrix instructions only), with a barrier after each; the
+// second group runs one half behind the first, so one group reads while the
+// other computes.  One stage in turn (8192 x 4096 x 7168 bf16, 256 x 256 tiles):
+// 1454 TFLOP/s, against 1153 with both groups in step and one barrier a stage.
+//
+// Stage s + 1 is waited for (all but the loads of later stages, LOADS each) in
+// the read half of stage s's last phase; the barrier after it publishes it.
+// Stage s + ST - 1 goes where stage s - 1 was: the second group's last reads of
+// that one ended, with its wait, before the barrier that opens stage s.
+template <int PH, int ST, int LOADS, class Issue, class Read, class Compute>
+__device__ __forceinline__ void take_turns(int steps, int group, Issue issue, Read read, Compute compute)
+{
+    constexpr int kLater = ST > 2 ? LOADS * (ST - 2) : 0;
+#pragma unroll
+    for (int s = 0; s < ST - 1; ++s)
+        if (s < steps) {
+            issue(s, 0);
+            issue(s, 1);
+        }
+    if (steps >= ST - 1)
+        landed<kLater>();
+    else
+        landed<0>();
+    turn();
+    if (group == 1)
+        turn();
+    for (int s = 0; s < steps; ++s) {
+#pragma unroll
+        for (int ph = 0; ph < PH; ++ph) {
+            read(s, ph);
+            if (s + ST - 1 < steps) {
+                if (ph == 0)
+                    issue(s + ST - 1, 0);
+                if (ph == (PH > 1 ? 1 : 0))
+                    issue(s + ST - 1, 1);
+            }
+            if (ph == PH - 1) {
+                if (s + ST - 1 < steps)
+                    landed<kLater>();
+                else
+                    landed<0>();
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+            turn();
+            compute(s, ph);
+            turn();
+        }
+    }
+    if (group == 0)
+        turn();
+}
+
+// The phases of a bf16 stage for a wave of MT x 4 16 x 16 tiles: the half ks of
+// the stage's K and, where MT is 8, the half of the rows.  P's fragments of the
+// second half are read ahead in part, which evens out the reads of the phases.
+template <int MT, class FragP, class FragQ>
+struct Bf16Phases {
+    static constexpr int kPhases = MT == 8 ? 4 : MT == 4 ? 2 : 1;
+    static constexpr int MQ = MT == 8 ? 4 : MT;  // row tiles of a phase
+    f32x4 (&acc)[MT][4];
+    FragP frag_p;  // (stage, column tile, ks)
+    FragQ frag_q;  // (stage, row tile, ks)
+    bf16x8 p[2][4], q[kPhases == 1 ? 2 : 1][MQ];
+    __device__ __forceinline__ void read(int s, int ph)
+    {
+        if constexpr (kPhases == 1) {
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    p[ks][i] = frag_p(s, i, ks);
+#pragma unroll
+                for (int m = 0; m < MQ; ++m)
+                    q[ks][m] = frag_q(s, m, ks);
+            }
+        } else {
+            const int ks = kPhases == 4 ? ph >> 1 : ph;
+            const int mh = kPhases == 4 ? ph & 1 : 0;
+            if (ph == 0 || kPhases == 2) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    p[ks][i] = frag_p(s, i, ks);
+            }
+#pragma unroll
+            for (int m = 0; m < MQ; ++m)
+                q[0][m] = frag_q(s, mh * 4 + m, ks);
+            if (kPhases == 4 && (ph == 1 || ph == 2)) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    p[1][(ph - 1) * 2 + i] = frag_p(s, (ph - 1) * 2 + i, 1);
+            }
+        }
+    }
+    __device__ __forceinline__ void compute(int ph)
+    {
+#pragma unroll
+        for (int m = 0; m < MQ; ++m) {
+            hold(q[0][m]);
+            if constexpr (kPhases == 1)
+                hold(q[1][m]);
+        }
+        const int ks0 = kPhases == 4 ? ph >> 1 : ph, mh = kPhases == 4 ? ph & 1 : 0;
+#pragma unroll
+        for (int k = 0; k < (kPhases == 1 ? 2 : 1); ++k)
+#pragma unroll
+            for (int m = 0; m < MQ; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[mh * 4 + m][i] = mfma_bf16(p[kPhases == 1 ? k : ks0][i], q[k][m], acc[mh * 4 + m][i]);
+    }
+};
 
 // Rows in the order of the groups themselves (low-latency cells).
 struct RowOut {
