@@ -12,6 +12,11 @@ namespace ep {
 
 namespace {
 
+template <int N>
+struct Rows {
+    static constexpr int value = N;
+};
+
 // ------------------------------------------------------------- grouping
 
 constexpr int kGroupBlock = 1024;
@@ -141,22 +146,19 @@ struct PairOut {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const int m = m0 + mt * 16 + (lane & 15);
-            if (m >= t.rows)
-                continue;
+            const bool live = m < t.rows;
             const int64_t p = start + m;
-            const int32_t r = pair_row[p];
-            const float w = weight != nullptr ? weight[pair_slot[p]] : 1.0f;
+            const int32_t r = live ? pair_row[p] : 0;
+            const float w = live && weight != nullptr ? weight[pair_slot[p]] : 1.0f;
+            f32x4 v[NW];
 #pragma unroll
             for (int nt = 0; nt < NW; ++nt) {
+                v[nt] = acc[mt][nt] * w;
                 const int n = n0 + nt * 16 + (lane >> 4) * 4;
-                if (n >= N)
-                    continue;
-                const f32x4 v = acc[mt][nt] * w;
-                if (r < 0)
-                    *reinterpret_cast<uint2 *>(out + int64_t(r & kRowMask) * N + n) = pack4(v);
-                else
-                    *reinterpret_cast<f32x4 *>(terms + p * N + n) = v;
+                if (live && r >= 0 && n < N)
+                    *reinterpret_cast<f32x4 *>(terms + p * N + n) = v[nt];
             }
+            store_bf16_row<NW>(r < 0 ? out + int64_t(r & kRowMask) * N : nullptr, n0, N, v, lane);
         }
     }
 };
@@ -176,25 +178,22 @@ struct GatedOut {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const int m = m0 + mt * 16 + (lane & 15);
-            if (m >= t.rows)
-                continue;
+            const bool live = m < t.rows;
             const int64_t p = start + m;
+            f32x4 a[NW / 2];
 #pragma unroll
             for (int nt = 0; nt < NW / 2; ++nt) {
                 const int n = n0 + nt * 16 + (lane >> 4) * 4;
-                if (n >= I)
-                    continue;
                 const f32x4 g = acc[mt][nt], u = acc[mt][nt + NW / 2];
-                f32x4 a;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    a[i] = g[i] * sigmoidf(g[i]) * u[i];
-                *reinterpret_cast<uint2 *>(act + p * I + n) = pack4(a);
-                if (gu != nullptr) {
+                    a[nt][i] = g[i] * sigmoidf(g[i]) * u[i];
+                if (gu != nullptr && live && n < I) {
                     *reinterpret_cast<f32x4 *>(gu + p * 2 * I + n) = g;
                     *reinterpret_cast<f32x4 *>(gu + p * 2 * I + I + n) = u;
                 }
             }
+            store_bf16_row<NW / 2>(live ? act + p * I : nullptr, n0, I, a, lane);
         }
     }
 };
@@ -203,6 +202,7 @@ struct GatedOut {
 // for dW2, and the tile's share of the routing weight's gradient, summed in a
 // fixed order over lanes, then waves, then (in rows_kernel) tiles.
 struct GatedBack {
+    static constexpr bool kBlockWide = true;
     const int32_t *pair_slot;
     const float *weight;
     const float *gu;      // [pairs][2 I]
@@ -210,66 +210,120 @@ struct GatedBack {
     uint16_t *wact;       // [pairs][I]
     float *dweight_part;  // [pairs][tiles]
     int tiles;
+    // mbase: the wave's first row inside the tile of ROWS rows
+    template <int MT, int NW, int WN, int ROWS>
+    __device__ __forceinline__ void store_block(const Tile &t, int64_t start, bool, int wn, int mbase, int n0,
+                                                int I, f32x4 (&acc)[MT][NW], int lane) const
+    {
+        __shared__ float part[WN][ROWS];
+        const int tid = threadIdx.x;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int m = t.m0 + mbase + mt * 16 + (lane & 15);
+            const bool live = m < t.rows;
+            const int64_t p = start + m;
+            const float w = live ? weight[pair_slot[p]] : 0.0f;
+            float dw = 0.0f;
+#pragma unroll
+            for (int h = 0; h < NW; h += 2) {
+                f32x4 dg[2], du[2], wa[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int n = n0 + (h + k) * 16 + (lane >> 4) * 4;
+                    const bool in = live && n < I;
+                    f32x4 g = {}, u = {};
+                    if (in) {
+                        g = *reinterpret_cast<const f32x4 *>(gu + p * 2 * I + n);
+                        u = *reinterpret_cast<const f32x4 *>(gu + p * 2 * I + I + n);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float sg = sigmoidf(g[i]), d = acc[mt][h + k][i], si = g[i] * sg;
+                        dw += in ? si * u[i] * d : 0.0f;
+                        wa[k][i] = w * si * u[i];
+                        du[k][i] = w * d * si;
+                        dg[k][i] = w * d * u[i] * sg * (1.0f + g[i] * (1.0f - sg));
+                    }
+                }
+                store_bf16_row<2>(live ? dgu + p * 2 * I : nullptr, n0 + h * 16, I, dg, lane);
+                store_bf16_row<2>(live ? dgu + p * 2 * I + I : nullptr, n0 + h * 16, I, du, lane);
+                store_bf16_row<2>(live ? wact + p * I : nullptr, n0 + h * 16, I, wa, lane);
+                __builtin_amdgcn_sched_barrier(0);  // a pair at a time: more would not fit the registers
+            }
+            dw += __shfl_xor(dw, 16);
+            dw += __shfl_xor(dw, 32);
+            if (lane < 16)
+                part[wn][mbase + mt * 16 + lane] = dw;
+        }
+        __syncthreads();
+        if (tid < ROWS && t.m0 + tid < t.rows)
+            dweight_part[(start + t.m0 + tid) * tiles + t.n] =
+                (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+    }
 };
 
 // ------------------------------------------------------------ tile kernels
 
-// BM rows of one group by BN columns, with as many LDS stages as fit.
+// Tiles of BM rows of one group by BN columns, with as many LDS stages as fit.
+// A block works through every gridDim.x-th tile: it looks up the next one while
+// the first stage of this one arrives, and sends off the next one's first stage
+// before it stores this one.  A group's last tile of at most BM / 2 rows is
+// computed at half the height.
 template <int BM, bool PCOL, Form F, class Epi>
 __global__ __launch_bounds__(NT) void tile_kernel(TileArgs a, Groups G, Epi epi)
 {
-    constexpr int MT = BM / 32;  // 16-row tiles of a wave
     using QS = RowStage<BM, NT>;
-    using PR = RowStage<BN, NT>;
+    using PR = NearRowStage<BN, NT>;
     using PC = ColStage<BN, NT>;
     constexpr int kP = PR::kBytes, kStage = kP + QS::kBytes, ST = BM == 256 ? 2 : 3;
     __shared__ __attribute__((aligned(128))) char smem[ST * kStage];
-    const Tile t = find_tile<BM, NT>(G, blockIdx.x, a.nt);
-    if (t.group < 0)
-        return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
-    const int64_t start = group_start(G, t.group);
-    const char *pw = a.p + int64_t(group_expert(G, t.group)) * a.p_expert;
     lds_char *lds = (lds_char *)smem;
-    const int n0 = t.n * (F == Form::kGated ? BN / 2 : BN);
-
-    QS qs;
-    qs.init(tid, [&](int r) {
-        int m = t.m0 + r;
-        m = m < t.rows ? m : t.rows - 1;
-        const int64_t row = a.q_rows != nullptr ? int64_t(a.q_rows[start + m] & kRowMask) : start + m;
-        return a.q + row * a.ldq;
-    });
-    PR pr;
-    PC pc;
-    if constexpr (PCOL) {
-        pc.init(tid, n0, a.N);
-    } else {
-        pr.init(tid, [&](int r) {
-            int n;
-            if constexpr (F == Form::kGated) {  // each wave: 32 gate columns, then their up columns
-                n = n0 + (r >> 6) * 32 + (r & 31);
-                n = n < a.N ? n : a.N - 1;
-                n += (r & 32) ? a.N : 0;
-            } else {
-                n = n0 + r;
-                n = n < a.N ? n : a.N - 1;
-            }
-            return pw + int64_t(n) * a.ldp;
-        });
-    }
     const int steps = (a.K + 63) / 64;
     const int64_t kbytes = int64_t(a.K) * 2;
     auto stage = [&](int s) -> lds_char * { return lds + (ST == 2 ? s & 1 : s % ST) * kStage; };
+
+    QS qs;
+    PR pr;
+    PC pc;
+    const char *pw = nullptr;
+    int row_at[QS::J];  // places of this thread's rows
+    auto find_rows = [&](const Tile &t) {
+        const int64_t start = group_start(G, t.group);
+#pragma unroll
+        for (int j = 0; j < QS::J; ++j) {
+            int m = t.m0 + ((j * NT + tid) >> 3);
+            m = m < t.rows ? m : t.rows - 1;
+            row_at[j] = a.q_rows != nullptr ? a.q_rows[start + m] & kRowMask : m;
+        }
+    };
+    auto set_up = [&](const Tile &t) {
+        const int n0 = t.n * (F == Form::kGated ? BN / 2 : BN);
+        pw = a.p + int64_t(group_expert(G, t.group)) * a.p_expert;
+        const char *q = a.q_rows != nullptr ? a.q : a.q + group_start(G, t.group) * a.ldq;
+        qs.init(tid, [&](int j, int) { return q + int64_t(row_at[j]) * a.ldq; });
+        if constexpr (PCOL) {
+            pc.init(tid, n0, a.N);
+        } else {
+            // gated: of each wave's 64 LDS rows 32 are gate columns, 32 their up columns;
+            // waves 4 to 7 stage the latter
+            const bool up = F == Form::kGated && wave >= 4;
+            pr.init(tid, pw + (int64_t(n0) + (up ? a.N : 0)) * a.ldp, [&](int, int r) {
+                int n = F == Form::kGated ? (r >> 6) * 32 + (r & 31) : r;
+                n = n0 + n < a.N ? n : a.N - 1 - n0;
+                return uint32_t(n) * uint32_t(a.ldp);
+            });
+        }
+    };
     auto issue = [&](int s, int part) {
         if (part == 1)
             qs.template issue<true>(stage(s) + kP, wave, int64_t(s) * kStepBytes, kbytes);
         else if constexpr (PCOL)
-            pc.issue(stage(s), wave, s * 64, a.K, [&](int, int k) { return pw + int64_t(k) * a.ldp; });
+            pc.issue(stage(s), tid, wave, pw, a.ldp, s * 64, a.K);
         else
-            pr.template issue<true>(stage(s), wave, int64_t(s) * kStepBytes, kbytes);
+            pr.template issue<true>(stage(s), tid, wave, int64_t(s) * kStepBytes, kbytes);
     };
     auto frag_p = [&](int s, int i, int ks) {
         const int c = wn * 64 + i * 16;
@@ -278,94 +332,87 @@ __global__ __launch_bounds__(NT) void tile_kernel(TileArgs a, Groups G, Epi epi)
         else
             return PR::frag(stage(s), c, ks, lane);
     };
-    auto frag_q = [&](int s, int m, int ks) {
-        return QS::frag(stage(s) + kP, wm * (BM / 2) + m * 16, ks, lane);
-    };
-    f32x4 acc[MT][4] = {};
-    Bf16Phases<MT, decltype(frag_p), decltype(frag_q)> ph{acc, frag_p, frag_q};
-    take_turns<decltype(ph)::kPhases, ST, PR::J + QS::J>(
-        steps, wm, issue, [&](int s, int i) { ph.read(s, i); }, [&](int, int i) { ph.compute(i); });
 
-    const int mw = t.m0 + wm * (BM / 2);
-    if constexpr (F == Form::kBack) {
-        const int I = a.N, nw = n0 + wn * 64;
-        float *part = reinterpret_cast<float *>(smem);  // [4][BM]
-        __syncthreads();
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const int m = mw + mt * 16 + (lane & 15);
-            const int64_t p = start + m;
-            float dw = 0.0f;
-            if (m < t.rows) {
-                const float w = epi.weight[epi.pair_slot[p]];
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    const int n = nw + nt * 16 + (lane >> 4) * 4;
-                    if (n >= I)
-                        continue;
-                    const f32x4 g = *reinterpret_cast<const f32x4 *>(epi.gu + p * 2 * I + n);
-                    const f32x4 u = *reinterpret_cast<const f32x4 *>(epi.gu + p * 2 * I + I + n);
-                    f32x4 dg, du, wa;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float sg = sigmoidf(g[i]), d = acc[mt][nt][i], si = g[i] * sg;
-                        dw += si * u[i] * d;
-                        wa[i] = w * si * u[i];
-                        du[i] = w * d * si;
-                        dg[i] = w * d * u[i] * sg * (1.0f + g[i] * (1.0f - sg));
-                    }
-                    *reinterpret_cast<uint2 *>(epi.dgu + p * 2 * I + n) = pack4(dg);
-                    *reinterpret_cast<uint2 *>(epi.dgu + p * 2 * I + I + n) = pack4(du);
-                    *reinterpret_cast<uint2 *>(epi.wact + p * I + n) = pack4(wa);
-                }
+    unsigned block = blockIdx.x;
+    Tile t = find_tile<BM, NT>(G, block, a.nt);
+    if (t.group < 0)
+        return;
+    find_rows(t);
+    set_up(t);
+    open_stages<ST>(steps, issue);
+    auto work = [&](auto rows_tag) {
+        constexpr int R = decltype(rows_tag)::value, MT = R / 32;  // rows computed, row tiles of a wave
+        auto frag_q = [&](int s, int m, int ks) {
+            return QS::frag(stage(s) + kP, wm * (R / 2) + m * 16, ks, lane);
+        };
+        f32x4 acc[MT][4] = {};
+        Bf16Phases<MT, decltype(frag_p), decltype(frag_q)> ph{acc, frag_p, frag_q};
+        take_turns<decltype(ph)::kPhases, ST, PR::J + QS::J>(
+            steps, wm, issue, [&](int s, int i) { ph.read(s, i); }, [&](int, int i) { ph.compute(i); });
+        return [&, acc](const Tile &c) mutable {
+            const int64_t start = group_start(G, c.group);
+            const int n0 = c.n * (F == Form::kGated ? BN / 2 : BN) + wn * (F == Form::kGated ? 32 : 64);
+            if constexpr (Epi::kBlockWide)
+                epi.template store_block<MT, 4, 4, R>(c, start, true, wn, wm * (R / 2), n0, a.N, acc, lane);
+            else
+                epi.store(c, start, c.m0 + wm * (R / 2), n0, a.N, acc, lane);
+        };
+    };
+    for (;;) {
+        block += gridDim.x;
+        const Tile next = find_tile<BM, NT>(G, block, a.nt);
+        if (next.group >= 0)
+            find_rows(next);
+        const Tile cur = t;
+        auto finish = [&](auto store) {
+            if (next.group >= 0) {
+                set_up(next);
+                open_stages<ST>(steps, issue);
             }
-            dw += __shfl_xor(dw, 16);
-            dw += __shfl_xor(dw, 32);
-            if (lane < 16)
-                part[wn * BM + wm * (BM / 2) + mt * 16 + lane] = dw;
-        }
-        __syncthreads();
-        if (tid < BM && t.m0 + tid < t.rows)
-            epi.dweight_part[(start + t.m0 + tid) * epi.tiles + t.n] =
-                (part[tid] + part[BM + tid]) + (part[2 * BM + tid] + part[3 * BM + tid]);
-    } else {
-        const int nw = n0 + wn * (F == Form::kGated ? 32 : 64);
-        epi.store(t, start, mw, nw, a.N, acc, lane);
+            store(cur);
+        };
+        if (BM > 64 && cur.rows - cur.m0 <= BM / 2)
+            finish(work(Rows<(BM > 64 ? BM / 2 : BM)>{}));
+        else
+            finish(work(Rows<BM>{}));
+        if (next.group < 0)
+            break;
+        t = next;
     }
 }
 
 // out[e][m][n] = sum over the group's rows k of Q[k][m] P[k][n], 256 x 256 a
-// block; QG / PG: the operand's rows are picked by pair_row.  A group without
-// rows writes zeros.
+// tile; QG / PG: the operand's rows are picked by pair_row.  A group without
+// rows writes zeros.  Blocks work through the tiles as in tile_kernel.
+struct GradArgs {
+    const char *q, *p;
+    int64_t ldq, ldp;  // bytes of a row
+    const int32_t *pair_row, *offsets;
+    int experts, M, N;
+    unsigned mt, nt;
+    uint16_t *out;
+};
+
 template <bool QG, bool PG>
-__global__ __launch_bounds__(NT) void weight_grad_kernel(const char *q, int64_t ldq, const char *p,
-                                                         int64_t ldp, const int32_t *pair_row,
-                                                         const int32_t *offsets, int M, int N,
-                                                         unsigned mt, unsigned nt, uint16_t *out)
+__global__ __launch_bounds__(NT) void weight_grad_kernel(GradArgs a)
 {
     constexpr int B = 256;
     using CS = ColStage<B, NT>;
     __shared__ __attribute__((aligned(128))) char smem[4 * CS::kBytes];
     lds_char *lds = (lds_char *)smem;
-    const int e = blockIdx.x / (mt * nt);
-    unsigned tm, tn;
-    tile_of_block(blockIdx.x % (mt * nt), mt, nt, tm, tn);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
-    const int start = offsets[e], rows = offsets[e + 1] - start;
-    const int steps = (rows + 63) / 64;
     CS qs, ps;
-    qs.init(tid, int(tm) * B, M);
-    ps.init(tid, int(tn) * B, N);
+    int start = 0, rows = 0, steps = 0;
     // both operands' chunks of a thread lie in the same k rows
     int idx[CS::J], nxt[CS::J] = {};
     auto fetch = [&](int s) {
 #pragma unroll
         for (int j = 0; j < CS::J; ++j) {
-            const int k = s * 64 + qs.k[j];
+            const int k = s * 64 + CS::k_of(tid, j);
             if (k < rows)
-                nxt[j] = pair_row[start + k] & kRowMask;
+                nxt[j] = a.pair_row[start + k] & kRowMask;
         }
     };
     auto stage = [&](int s) -> lds_char * { return lds + (s & 1) * 2 * CS::kBytes; };
@@ -374,38 +421,64 @@ __global__ __launch_bounds__(NT) void weight_grad_kernel(const char *q, int64_t 
 #pragma unroll
             for (int j = 0; j < CS::J; ++j)
                 idx[j] = nxt[j];
-            ps.issue(stage(s), wave, s * 64, rows, [&](int j, int k) {
-                return p + (PG ? int64_t(idx[j]) : int64_t(start) + k) * ldp;
-            });
+            if constexpr (PG)
+                ps.issue(stage(s), tid, wave, a.p, a.ldp, s * 64, rows, idx);
+            else
+                ps.issue(stage(s), tid, wave, a.p + start * a.ldp, a.ldp, s * 64, rows);
         } else {
-            qs.issue(stage(s) + CS::kBytes, wave, s * 64, rows, [&](int j, int k) {
-                return q + (QG ? int64_t(idx[j]) : int64_t(start) + k) * ldq;
-            });
+            if constexpr (QG)
+                qs.issue(stage(s) + CS::kBytes, tid, wave, a.q, a.ldq, s * 64, rows, idx);
+            else
+                qs.issue(stage(s) + CS::kBytes, tid, wave, a.q + start * a.ldq, a.ldq, s * 64, rows);
             if (s + 1 < steps)
                 fetch(s + 1);
         }
     };
-    auto frag_p = [&](int s, int i, int ks) { return CS::frag(stage(s), wn * 64 + i * 16, ks, lane); };
-    auto frag_q = [&](int s, int m, int ks) {
-        return CS::frag(stage(s) + CS::kBytes, wm * 128 + m * 16, ks, lane);
+    const unsigned per = a.mt * a.nt, total = per * unsigned(a.experts);
+    unsigned tm = 0, tn = 0, e = 0;
+    auto set_up = [&](unsigned block) {
+        // a contiguous run of the tiles for each XCD, as tile_of_block has it
+        const unsigned x = block % kXcds, i = block / kXcds, share = total / kXcds, extra = total % kXcds;
+        const unsigned id = x * share + (x < extra ? x : extra) + i;
+        e = id / per;
+        const unsigned r = id % per, band = r / (kBand * a.nt), c = r % (kBand * a.nt);
+        const unsigned left = a.mt - band * kBand, h = left < kBand ? left : kBand;
+        tm = band * kBand + c % h;
+        tn = c / h;
+        start = uniform(a.offsets[e]);
+        rows = uniform(a.offsets[e + 1]) - start;
+        steps = (rows + 63) / 64;
+        qs.init(tid, int(tm) * B, a.M);
+        ps.init(tid, int(tn) * B, a.N);
+        if (steps > 0)
+            fetch(0);
+        open_stages<2>(steps, issue);
     };
-    f32x4 acc[8][4] = {};
-    if (steps > 0) {
-        fetch(0);
+    unsigned block = blockIdx.x;
+    if (block >= total)
+        return;
+    set_up(block);
+    for (;;) {
+        auto frag_p = [&](int s, int i, int ks) { return CS::frag(stage(s), wn * 64 + i * 16, ks, lane); };
+        auto frag_q = [&](int s, int m, int ks) {
+            return CS::frag(stage(s) + CS::kBytes, wm * 128 + m * 16, ks, lane);
+        };
+        f32x4 acc[8][4] = {};
         Bf16Phases<8, decltype(frag_p), decltype(frag_q)> ph{acc, frag_p, frag_q};
         take_turns<4, 2, 2 * CS::J>(
             steps, wm, issue, [&](int s, int i) { ph.read(s, i); }, [&](int, int i) { ph.compute(i); });
-    }
-    uint16_t *o = out + int64_t(e) * M * N;
+        uint16_t *o = a.out + int64_t(e) * a.M * a.N;
+        const int m0 = int(tm) * B + wm * 128, n0 = int(tn) * B + wn * 64;
+        block += gridDim.x;
+        if (block < total)
+            set_up(block);
 #pragma unroll
-    for (int m = 0; m < 8; ++m) {
-        const int mm = int(tm) * B + wm * 128 + m * 16 + (lane & 15);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int n = int(tn) * B + wn * 64 + i * 16 + (lane >> 4) * 4;
-            if (mm < M && n < N)
-                *reinterpret_cast<uint2 *>(o + int64_t(mm) * N + n) = pack4(acc[m][i]);
+        for (int m = 0; m < 8; ++m) {
+            const int mm = m0 + m * 16 + (lane & 15);
+            store_bf16_row<4>(mm < a.M ? o + int64_t(mm) * a.N : nullptr, n0, a.N, acc[m], lane);
         }
+        if (block >= total)
+            break;
     }
 }
 
@@ -472,7 +545,8 @@ hipError_t launch_tiles(TileArgs a, const Groups &G, int64_t max_tiles_rows, con
     if (log_enabled())
         log_launch("%s: rows<=%lld groups=%d N=%d K=%d tile=%dx%d blocks=%lld", what,
                    (long long)max_tiles_rows, G.num, a.N, a.K, bm, BN, (long long)mt * a.nt);
-    const dim3 grid(unsigned(mt * a.nt));
+    const int64_t cus = compute_units();
+    const dim3 grid(unsigned(mt * a.nt < cus ? mt * a.nt : cus));
     if (bm == 256)
         hipLaunchKernelGGL((tile_kernel<256, PCOL, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
     else if (bm == 128)
@@ -500,6 +574,15 @@ hipError_t launch_rows(const ExpertFfn &f, const float *terms, void *out, const 
 }
 
 }  // namespace
+
+int compute_units()
+{
+    int dev = 0, n = 0;
+    if (hipGetDevice(&dev) != hipSuccess ||
+        hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < kXcds)
+        return 256;
+    return n / kXcds * kXcds;  // whole rounds of the XCDs: a block stays with one run of tiles
+}
 
 int expert_ffn_tiles(int inter) { return (inter + BN - 1) / BN; }
 
@@ -599,17 +682,37 @@ hipError_t launch_expert_ffn_backward(const ExpertFfn &f, const void *dy, const 
     if (log_enabled())
         log_launch("expert_ffn dW: experts=%d blocks=%lld + %lld", f.experts,
                    (long long)f.experts * grid(H, I), (long long)f.experts * grid(2 * I, H));
-    hipLaunchKernelGGL((weight_grad_kernel<true, false>), dim3(unsigned(f.experts) * hm * in), dim3(NT),
-                       0, stream, static_cast<const char *>(dy), int64_t(H) * 2,
-                       static_cast<const char *>(wact), int64_t(I) * 2, f.pair_row, f.offsets, H, I, hm,
-                       in, static_cast<uint16_t *>(dw2));
+    GradArgs w{};
+    w.pair_row = f.pair_row;
+    w.offsets = f.offsets;
+    w.experts = f.experts;
+    auto blocks = [&] {
+        const int64_t n = int64_t(f.experts) * w.mt * w.nt, cus = compute_units();
+        return dim3(unsigned(n < cus ? n : cus));
+    };
+    w.q = static_cast<const char *>(dy);
+    w.ldq = int64_t(H) * 2;
+    w.p = static_cast<const char *>(wact);
+    w.ldp = int64_t(I) * 2;
+    w.M = H;
+    w.N = I;
+    w.mt = hm;
+    w.nt = in;
+    w.out = static_cast<uint16_t *>(dw2);
+    hipLaunchKernelGGL((weight_grad_kernel<true, false>), blocks(), dim3(NT), 0, stream, w);
     e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL((weight_grad_kernel<false, true>), dim3(unsigned(f.experts) * gm * hm), dim3(NT),
-                       0, stream, static_cast<const char *>(dgu), int64_t(2) * I * 2,
-                       static_cast<const char *>(x), int64_t(H) * 2, f.pair_row, f.offsets, 2 * I, H, gm,
-                       hm, static_cast<uint16_t *>(dw13));
+    w.q = static_cast<const char *>(dgu);
+    w.ldq = int64_t(2) * I * 2;
+    w.p = static_cast<const char *>(x);
+    w.ldp = int64_t(H) * 2;
+    w.M = 2 * I;
+    w.N = H;
+    w.mt = gm;
+    w.nt = hm;
+    w.out = static_cast<uint16_t *>(dw13);
+    hipLaunchKernelGGL((weight_grad_kernel<false, true>), blocks(), dim3(NT), 0, stream, w);
     return hipGetLastError();
 }
 

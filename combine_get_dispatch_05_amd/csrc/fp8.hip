@@ -78,7 +78,7 @@ __global__ __launch_bounds__(NT) void fp8_tile_kernel(FewArgs a, Groups G, Epi e
 {
     constexpr int MT = BM / 32;
     using QS = RowStage<BM, NT>;
-    using PR = RowStage<BN, NT>;
+    using PR = NearRowStage<BN, NT>;
     constexpr int kP = PR::kBytes, kQ = QS::kBytes, kStage = kP + kQ + (BM + kWave) * 4, ST = BM == 256 ? 2 : 3;
     __shared__ __attribute__((aligned(128))) char smem[ST * kStage];
     const Tile t = find_tile<BM, NT>(G, blockIdx.x, a.nt);
@@ -95,20 +95,16 @@ __global__ __launch_bounds__(NT) void fp8_tile_kernel(FewArgs a, Groups G, Epi e
     const int steps = a.kbytes >> 7;
 
     QS qs;
-    qs.init(tid, [&](int r) {
+    qs.init(tid, [&](int, int r) {
         const int m = t.m0 + r;
         return a.q + (start + (m < t.rows ? m : t.rows - 1)) * a.ldq;
     });
     PR pr;
-    pr.init(tid, [&](int r) {
-        int n;
-        if constexpr (F == Form::kGated) {
-            n = n0 + (r >> 6) * 32 + (r & 31) + ((r & 32) ? a.N : 0);
-        } else {
-            n = n0 + r;
-            n = n < a.N ? n : a.N - 1;
-        }
-        return pw + int64_t(n) * a.ldp;
+    const bool up = F == Form::kGated && wave >= 4;  // as in the bf16 tile
+    pr.init(tid, pw + (int64_t(n0) + (up ? a.N : 0)) * a.ldp, [&](int, int r) {
+        int n = F == Form::kGated ? (r >> 6) * 32 + (r & 31) : r;
+        n = n0 + n < a.N ? n : a.N - 1 - n0;
+        return uint32_t(n) * uint32_t(a.ldp);
     });
     // Scales are staged behind the rows, one load a wave, so that every wave counts
     // the same loads: waves 0 to 3 the BM token scales (some twice where BM is
@@ -130,7 +126,7 @@ __global__ __launch_bounds__(NT) void fp8_tile_kernel(FewArgs a, Groups G, Epi e
     auto issue = [&](int s, int part) {
         lds_char *b = stage(s);
         if (part == 0) {
-            pr.template issue<false>(b, wave, int64_t(s) * kStepBytes, a.kbytes);
+            pr.template issue<false>(b, tid, wave, int64_t(s) * kStepBytes, a.kbytes);
         } else {
             qs.template issue<false>(b + kP, wave, int64_t(s) * kStepBytes, a.kbytes);
             load_lds4(sq + int64_t(s) * 4, b + sdst);
@@ -146,6 +142,7 @@ __global__ __launch_bounds__(NT) void fp8_tile_kernel(FewArgs a, Groups G, Epi e
     f32x4 acc[MT][4] = {};
     Frag pf[4], qf[MQ];
     float sc[MQ], c0 = 0.0f, c1 = 0.0f;
+    open_stages<ST>(steps, issue);
     take_turns<PH, ST, PR::J + QS::J + 1>(
         steps, wm, issue,
         [&](int s, int ph) {

@@ -57,6 +57,14 @@ __device__ __forceinline__ void load_lds16(const char *src, lds_char *dst)
                  : "v"(src), "s"(lds_at(dst))
                  : "memory");
 }
+// The same from base + off, base the same for the whole wave.
+__device__ __forceinline__ void load_lds16(const char *base, uint32_t off, lds_char *dst)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :
+                 : "v"(off), "s"(base), "s"(lds_at(dst))
+                 : "memory");
+}
 __device__ __forceinline__ void load_lds4(const char *src, lds_char *dst)
 {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
@@ -64,6 +72,15 @@ __device__ __forceinline__ void load_lds4(const char *src, lds_char *dst)
                  : "v"(src), "s"(lds_at(dst))
                  : "memory");
 }
+// A value that is the same in every lane, told to the compiler.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ const char *uniform(const char *p)
+{
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = uint32_t(uniform(int(uint32_t(v)))), hi = uint32_t(uniform(int(uint32_t(v >> 32))));
+    return reinterpret_cast<const char *>(uint64_t(lo) | uint64_t(hi) << 32);
+}
+
 // Every load of this wave but the last N has landed.
 template <int N>
 __device__ __forceinline__ void landed()
@@ -84,7 +101,7 @@ struct RowStage {
     const char *ptr[J];
     int cb[J];  // byte of the chunk inside the K step
 
-    // row_ptr(r): the address of LDS row r at k = 0 (any valid row for rows
+    // row_ptr(j, r): the address of LDS row r (this thread's j-th) at k = 0 (any valid row for rows
     // past the end: their results are never stored).
     template <class F>
     __device__ __forceinline__ void init(int tid, F row_ptr)
@@ -94,7 +111,7 @@ struct RowStage {
             const int q = j * NT + tid;
             const int r = q >> 3;
             cb[j] = ((q & 7) ^ ((r >> 1) & 7)) * 16;
-            ptr[j] = row_ptr(r) + cb[j];
+            ptr[j] = row_ptr(j, r) + cb[j];
         }
     }
     // Stage K bytes [kb, kb + 128); kbytes: all K bytes of the operand (a whole
@@ -125,6 +142,49 @@ struct RowStage {
     }
 };
 
+// The same for rows that lie within 4 GB of one address: 32-bit offsets, half the
+// registers, and no address arithmetic in the loop.
+template <int ROWS, int NT>
+struct NearRowStage {
+    static constexpr int J = ROWS * 8 / NT;
+    static constexpr int kBytes = ROWS * kStepBytes;
+    const char *base;  // uniform
+    uint32_t off[J];
+    // row_off(j, r): offset of LDS row r from base_
+    template <class F>
+    __device__ __forceinline__ void init(int tid, const char *base_, F row_off)
+    {
+        base = uniform(base_);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int q = j * NT + tid;
+            const int r = q >> 3;
+            off[j] = row_off(j, r) + ((q & 7) ^ ((r >> 1) & 7)) * 16;
+        }
+    }
+    template <bool TAIL>
+    __device__ __forceinline__ void issue(lds_char *lds, int tid, int wave, int64_t kb, int64_t kbytes)
+    {
+        if (!TAIL || kb + kStepBytes <= kbytes) {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                load_lds16(base + kb, off[j], lds + (j * NT + wave * kWave) * 16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int q = j * NT + tid;
+                const int cb = ((q & 7) ^ ((q >> 4) & 7)) * 16;
+                load_lds16(kb + cb >= kbytes ? reinterpret_cast<const char *>(kZero16) : base + kb + off[j],
+                           lds + (j * NT + wave * kWave) * 16);
+            }
+        }
+    }
+    static __device__ __forceinline__ bf16x8 frag(const lds_char *lds, int r0, int ks, int lane)
+    {
+        return RowStage<ROWS, NT>::frag(lds, r0, ks, lane);
+    }
+};
+
 // Operand with its own index contiguous: 64 k rows of COLS bf16.  Chunk c of
 // k row r lies at c ^ 2 g(r), g(r) = (r & 3) | ((r >> 3) & 1) << 2: the
 // sixteen 32-byte runs that one transposing read touches then spread over
@@ -134,36 +194,54 @@ struct ColStage {
     static constexpr int CH = COLS / 8;  // 16-byte chunks of a k row
     static constexpr int J = 64 * CH / NT;
     static constexpr int kBytes = 64 * COLS * 2;
-    int k[J];   // k row inside the step
-    int cb[J];  // byte of the (clamped) column inside a row of memory
+    int cb[J];  // byte of this thread's (clamped) column inside a row of memory
 
     static __device__ __forceinline__ int g2(int r) { return ((r & 3) | (((r >> 3) & 1) << 2)) << 1; }
+    static __device__ __forceinline__ int k_of(int tid, int j) { return (j * NT + tid) / CH; }
 
     // n0: first column of the tile, n: columns of the operand (a multiple of 8)
     __device__ __forceinline__ void init(int tid, int n0, int n)
     {
+        static_assert(CH >= 16, "the swizzle reaches over sixteen chunks");
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             const int q = j * NT + tid;
-            k[j] = q / CH;
-            int c = n0 + ((q % CH) ^ g2(k[j])) * 8;
+            int c = n0 + ((q % CH) ^ g2(q / CH)) * 8;
             c = c < n ? c : n - 8;
             cb[j] = c * 2;
         }
     }
-    // row_ptr(j, k): address of memory row k (k < kn), for this thread's j-th chunk
-    template <class F>
-    __device__ __forceinline__ void issue(lds_char *base, int wave, int k0, int kn, F row_ptr)
+    // Rows k0 .. k0 + 63 of memory, those past kn as zeros; row 0 at base, ld
+    // bytes apart.
+    __device__ __forceinline__ void issue(lds_char *lds, int tid, int wave, const char *base, int64_t ld,
+                                          int k0, int kn)
+    {
+        const char *first = uniform(base + k0 * ld);
+        if (k0 + 64 <= kn) {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                load_lds16(first, uint32_t(k_of(tid, j)) * uint32_t(ld) + cb[j],
+                           lds + (j * NT + wave * kWave) * 16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int k = k_of(tid, j);
+                load_lds16(k0 + k < kn ? first + k * ld + cb[j] : reinterpret_cast<const char *>(kZero16),
+                           lds + (j * NT + wave * kWave) * 16);
+            }
+        }
+    }
+    // The same with row[j] the memory row of this thread's j-th chunk.
+    __device__ __forceinline__ void issue(lds_char *lds, int tid, int wave, const char *base, int64_t ld,
+                                          int k0, int kn, const int (&row)[J])
     {
         const bool whole = k0 + 64 <= kn;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const char *p;
-            if (whole || k0 + k[j] < kn)
-                p = row_ptr(j, k0 + k[j]) + cb[j];
-            else
+            const char *p = base + row[j] * ld + cb[j];
+            if (!whole && k0 + k_of(tid, j) >= kn)
                 p = reinterpret_cast<const char *>(kZero16);
-            load_lds16(p, base + (j * NT + wave * kWave) * 16);
+            load_lds16(p, lds + (j * NT + wave * kWave) * 16);
         }
     }
     // Fragment of 16 columns from c0 and the 32 k values of half ks: lane l
@@ -214,6 +292,34 @@ __device__ __forceinline__ uint2 pack4(f32x4 v)
     return make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
+// The bf16 stores of a wave's NW 16 x 16 tiles of one row tile: a lane holds four
+// columns of each tile, 8 bytes; swapping with the neighbouring 16 lanes gives
+// it eight of one tile, so that four lanes write 64 bytes of a row together.
+// row: this lane's row of the output (its column 0); n0: the first column.
+template <int NW>
+__device__ __forceinline__ void store_bf16_row(uint16_t *row, int n0, int N, const f32x4 (&v)[NW], int lane)
+{
+    const int g = lane >> 4;
+    if constexpr (NW % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < NW; i += 2) {
+            const uint2 a = pack4(v[i]), b = pack4(v[i + 1]);
+            const auto x = __builtin_amdgcn_permlane16_swap(a.x, b.x, false, false);
+            const auto y = __builtin_amdgcn_permlane16_swap(a.y, b.y, false, false);
+            const int n = n0 + (i + (g & 1)) * 16 + (g >> 1) * 8;
+            if (row != nullptr && n < N)
+                *reinterpret_cast<u32x4 *>(row + n) = u32x4{x[0], y[0], x[1], y[1]};
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+            const int n = n0 + i * 16 + g * 4;
+            if (row != nullptr && n < N)
+                *reinterpret_cast<uint2 *>(row + n) = pack4(v[i]);
+        }
+    }
+}
+
 struct TileArgs {
     const char *q;            // rows of tokens
     const int32_t *q_rows;    // their places (nullable: in group order)
@@ -253,7 +359,7 @@ __device__ __forceinline__ int group_rows(const Groups &G, int g)
 }
 __device__ __forceinline__ int64_t group_start(const Groups &G, int g)
 {
-    return G.offsets != nullptr ? int64_t(G.offsets[g]) : int64_t(g) * G.slots;
+    return G.offsets != nullptr ? int64_t(uniform(G.offsets[g])) : int64_t(g) * G.slots;
 }
 __device__ __forceinline__ int group_expert(const Groups &G, int g)
 {
@@ -334,6 +440,7 @@ __device__ __forceinline__ Tile find_tile(const Groups &G, unsigned b, unsigned 
         scan(tiles_of(g0 + threadIdx.x, r), n);
         all += n;
     }
+    all = uniform(all);
     if (b >= unsigned(all) * nt)
         return Tile{-1, 0, 0, 0};
     unsigned tm, tn;
@@ -352,7 +459,7 @@ __device__ __forceinline__ Tile find_tile(const Groups &G, unsigned b, unsigned 
         first = scan(t, total);
     }
     __syncthreads();
-    return Tile{found[0], found[1], found[2], int(tn)};
+    return Tile{uniform(found[0]), uniform(found[1]), uniform(found[2]), int(tn)};
 }
 
 __device__ __forceinline__ f32x4 mfma_bf16(bf16x8 a, bf16x8 b, f32x4 c)
@@ -388,16 +495,23 @@ __device__ __forceinline__ void hold(T &v)
 // the read half of stage s's last phase; the barrier after it publishes it.
 // Stage s + ST - 1 goes where stage s - 1 was: the second group's last reads of
 // that one ended, with its wait, before the barrier that opens stage s.
-template <int PH, int ST, int LOADS, class Issue, class Read, class Compute>
-__device__ __forceinline__ void take_turns(int steps, int group, Issue issue, Read read, Compute compute)
+//
+// The first ST - 1 stages are sent off by open_stages, which a block working
+// through several tiles calls for the next tile before it stores this one.
+template <int ST, class Issue>
+__device__ __forceinline__ void open_stages(int steps, Issue issue)
 {
-    constexpr int kLater = ST > 2 ? LOADS * (ST - 2) : 0;
 #pragma unroll
     for (int s = 0; s < ST - 1; ++s)
         if (s < steps) {
             issue(s, 0);
             issue(s, 1);
         }
+}
+template <int PH, int ST, int LOADS, class Issue, class Read, class Compute>
+__device__ __forceinline__ void take_turns(int steps, int group, Issue issue, Read read, Compute compute)
+{
+    constexpr int kLater = ST > 2 ? LOADS * (ST - 2) : 0;
     if (steps >= ST - 1)
         landed<kLater>();
     else
@@ -502,16 +616,13 @@ struct RowOut {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const int m = m0 + mt * 16 + (lane & 15);
-            if (m >= t.rows)
-                continue;
-#pragma unroll
-            for (int nt = 0; nt < NW; ++nt) {
-                const int n = n0 + nt * 16 + (lane >> 4) * 4;
-                if (n < N)
-                    *reinterpret_cast<uint2 *>(out + (start + m) * N + n) = pack4(acc[mt][nt]);
-            }
+            store_bf16_row<NW>(m < t.rows ? out + (start + m) * N : nullptr, n0, N, acc[mt], lane);
         }
     }
 };
+
+// Compute units of the current device: the blocks of a launch whose blocks
+// each fill one and work through tiles.
+int compute_units();
 
 }  // namespace ep
