@@ -204,7 +204,7 @@ hipError_t launch_fp8_tiles(FewArgs a, const Groups &G, int64_t rows, int64_t ma
     if (log_enabled())
         log_launch("%s: rows<=%lld groups=%d N=%d K=%d tile=%dx%d blocks=%lld", what, (long long)rows,
                    G.num, a.N, a.kbytes, bm, BN, (long long)mt * a.nt);
-    const dim3 grid(unsigned(mt * a.nt));
+    const dim3 grid(unsigned(blocks_for_tiles(mt * a.nt)));
     if (bm == 256)
         hipLaunchKernelGGL((fp8_tile_kernel<256, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
     else if (bm == 128)

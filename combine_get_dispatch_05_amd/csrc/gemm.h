@@ -373,19 +373,13 @@ struct Tile {
     int n;     // column tile
 };
 
-// Block id -> (row tile, column tile).  Consecutive blocks go round the eight
-// XCDs, so each XCD is given a contiguous run of the tile order; in it, bands
-// of kBand row tiles are crossed column by column, which keeps both operands
-// of the blocks that run together in the XCD's own L2.
+// The order of mt x nt tiles: bands of kBand row tiles, crossed column by column,
+// which keeps both operands of the blocks that run together in an L2.
 constexpr int kXcds = 8;
 constexpr int kBand = 4;
-__device__ __forceinline__ void tile_of_block(unsigned b, unsigned mt, unsigned nt, unsigned &m,
+__device__ __forceinline__ void tile_in_bands(unsigned id, unsigned mt, unsigned nt, unsigned &m,
                                               unsigned &n)
 {
-    const unsigned total = mt * nt;
-    const unsigned per = total / kXcds, extra = total % kXcds;
-    const unsigned x = b % kXcds, i = b / kXcds;
-    const unsigned id = x * per + (x < extra ? x : extra) + i;
     const unsigned band = id / (kBand * nt), r = id % (kBand * nt);
     const unsigned left = mt - band * kBand;
     const unsigned h = left < kBand ? left : kBand;
@@ -393,37 +387,52 @@ __device__ __forceinline__ void tile_of_block(unsigned b, unsigned mt, unsigned 
     m = band * kBand + r % h;
 }
 
-// The tile of block b, over all groups (each cut into ceil(rows / BM) row
-// tiles) and nt column tiles; group = -1 for a block past the last.  The order
-// is laid over the tiles that there are, not over the grid, which is as large
-// as the rows could make it: otherwise the empty end would fall to one XCD.
-// Every thread takes part.
+// The i-th of XCD x's contiguous share of n items, or -1 past its last.
+__device__ __forceinline__ int64_t share_of_xcd(unsigned n, unsigned x, unsigned i)
+{
+    const unsigned per = n / kXcds, extra = n % kXcds;
+    if (i >= per + (x < extra))
+        return -1;
+    return int64_t(x) * per + (x < extra ? x : extra) + i;
+}
+
+// The tile of block b, over all groups (each cut into row tiles of BM) and nt
+// column tiles; group = -1 past the last.  Consecutive blocks go round the
+// eight XCDs, so each XCD has a contiguous run of the order.  First come the
+// tiles of more than BM / 2 rows, in bands, then the groups' shorter last tiles,
+// which cost half: in the order of the groups they would leave some blocks
+// with a round more of whole tiles than others (experts of about 1024 rows: 9
+// rounds of blocks for 8.5 rounds of work).  The order is laid over the tiles
+// that there are, not over the grid.  Every thread of the block takes part.
 template <int BM, int NT>
 __device__ __forceinline__ Tile find_tile(const Groups &G, unsigned b, unsigned nt)
 {
     constexpr int W = NT / kWave;
-    __shared__ int s[W], found[4];
+    __shared__ uint64_t s[W];
+    __shared__ int found[3];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    auto tiles_of = [&](int g, int &rows) {
+    // low half: whole tiles, high half: the part tile
+    auto tiles_of = [&](int g, int &rows) -> uint64_t {
         rows = g < G.num ? group_rows(G, g) : 0;
-        return (rows + BM - 1) / BM;
+        const unsigned rest = unsigned(rows) % BM;
+        return uint64_t(unsigned(rows) / BM + (rest > BM / 2)) | uint64_t(rest > 0 && rest <= BM / 2) << 32;
     };
-    auto scan = [&](int t, int &total) {  // exclusive sum of t over the block
-        int pre = t;
+    auto scan = [&](uint64_t t, uint64_t &total) {  // exclusive sum of t over the block
+        uint64_t pre = t;
 #pragma unroll
         for (int d = 1; d < kWave; d <<= 1) {
-            const int o = __shfl_up(pre, d);
+            const uint64_t o = __shfl_up(pre, d);
             pre += lane >= d ? o : 0;
         }
         __syncthreads();
         if (lane == 63)
             s[wave] = pre;
         __syncthreads();
-        int before = 0;
+        uint64_t before = 0;
         total = 0;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            const int v = s[w];
+            const uint64_t v = s[w];
             before += w < wave ? v : 0;
             total += v;
         }
@@ -431,29 +440,44 @@ __device__ __forceinline__ Tile find_tile(const Groups &G, unsigned b, unsigned 
     };
     if (threadIdx.x == 0)
         found[0] = -1;
-    int rows = 0, total = 0;
-    int t = tiles_of(threadIdx.x, rows);
-    int first = scan(t, total);
-    int all = total;
+    int rows = 0;
+    uint64_t total = 0;
+    uint64_t t = tiles_of(threadIdx.x, rows);
+    uint64_t first = scan(t, total);
+    uint64_t all = total;
     for (int g0 = NT; g0 < G.num; g0 += NT) {  // more groups than threads: the sum first
-        int r, n;
+        int r;
+        uint64_t n;
         scan(tiles_of(g0 + threadIdx.x, r), n);
         all += n;
     }
-    all = uniform(all);
-    if (b >= unsigned(all) * nt)
-        return Tile{-1, 0, 0, 0};
-    unsigned tm, tn;
-    tile_of_block(b, unsigned(all), nt, tm, tn);
-    for (int g0 = 0, base = 0;;) {
-        if (int(tm) >= base + first && int(tm) < base + first + t) {
+    const unsigned whole = uniform(int(uint32_t(all))), part = uniform(int(uint32_t(all >> 32)));
+    unsigned tm = 0, tn = 0;
+    const unsigned x = b % kXcds, i = b / kXcds;
+    int64_t id = share_of_xcd(whole * nt, x, i);
+    const bool is_whole = id >= 0;
+    if (is_whole) {
+        tile_in_bands(unsigned(id), whole, nt, tm, tn);
+    } else {
+        // this XCD's whole tiles are i's first ones
+        const unsigned mine = whole * nt / kXcds + (x < whole * nt % kXcds);
+        id = share_of_xcd(part * nt, x, i - mine);
+        if (id < 0)
+            return Tile{-1, 0, 0, 0};
+        tile_in_bands(unsigned(id), part, nt, tm, tn);
+    }
+    uint64_t base = 0;
+    for (int g0 = 0;;) {
+        const unsigned at = is_whole ? uint32_t(base + first) : uint32_t((base + first) >> 32);
+        const unsigned n = is_whole ? uint32_t(t) : uint32_t(t >> 32);
+        if (tm >= at && tm < at + n) {
             found[0] = g0 + threadIdx.x;
-            found[1] = (int(tm) - base - first) * BM;
+            found[1] = is_whole ? int(tm - at) * BM : rows / BM * BM;
             found[2] = rows;
         }
         base += total;
         g0 += NT;
-        if (int(tm) < base || g0 >= G.num)
+        if (tm < (is_whole ? uint32_t(base) : uint32_t(base >> 32)) || g0 >= G.num)
             break;
         t = tiles_of(g0 + threadIdx.x, rows);
         first = scan(t, total);
@@ -620,6 +644,10 @@ struct RowOut {
         }
     }
 };
+
+// Blocks that reach every tile: an XCD's run of whole tiles and its run of part
+// tiles can each be one longer than an eighth.
+inline int64_t blocks_for_tiles(int64_t tiles) { return (tiles / kXcds + 2) * kXcds; }
 
 // Compute units of the current device: the blocks of a launch whose blocks
 // each fill one and work through tiles.
