@@ -187,12 +187,13 @@ inline dim3 row_grid(int64_t rows)
 // Blocks of one launch of a 512-thread kernel (the same limit).
 constexpr int64_t kMaxTileBlocks = int64_t(1) << 22;
 
-// Row tile height: the largest whose last tile is not mostly padding at the
-// average number of rows a group can have.
+// Row tile of the tile kernels.  A 256-row tile reads a group's weight once for
+// up to 256 rows and shortens its last tile to what is there; below 64 rows a
+// group on average its rows are few enough for 64-row tiles, whose third LDS
+// stage hides more of the weight's latency.
 inline int tile_rows(int64_t rows, int64_t groups)
 {
-    const int64_t avg = rows / (groups > 0 ? groups : 1);
-    return avg > 160 ? 256 : avg > 64 ? 128 : 64;
+    return rows / (groups > 0 ? groups : 1) > 64 ? 256 : 64;
 }
 
 // Shared with the entry points outside ep_api.hip.

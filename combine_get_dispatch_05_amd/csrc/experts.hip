@@ -12,11 +12,6 @@ namespace ep {
 
 namespace {
 
-template <int N>
-struct Rows {
-    static constexpr int value = N;
-};
-
 // ------------------------------------------------------------- grouping
 
 constexpr int kGroupBlock = 1024;
@@ -29,6 +24,23 @@ __device__ __forceinline__ void rank_rows(const int32_t *prefix, int r, int64_t 
     b = prefix[r];
     a = a < 0 ? 0 : (a < n ? a : n);
     b = b < a ? a : (b < n ? b : n);
+}
+
+// A thread takes kIds slots in a row, so that a block of 1024 goes through 8192
+// slots between two barriers (one slot a thread took 57 us for 32 experts whose
+// ranks hold 32768 slots each).
+constexpr int kIds = 8;
+
+// Bit j: slot i + j (before end) names local expert le.
+__device__ __forceinline__ unsigned slots_of(const int64_t *ids, int64_t i, int64_t end, int le)
+{
+    unsigned m = 0;
+#pragma unroll
+    for (int j = 0; j < kIds; ++j) {
+        const int64_t v = i + j < end ? ids[i + j] : -1;
+        m |= unsigned(v == le) << j;
+    }
+    return m;
 }
 
 // One block for each expert counts its pairs; together they also mark every
@@ -44,8 +56,8 @@ __global__ __launch_bounds__(kGroupBlock) void count_pairs_kernel(
     int64_t a, b;
     rank_rows(prefix, r, n, a, b);
     int c = 0;
-    for (int64_t i = a * K + threadIdx.x; i < b * K; i += kGroupBlock)
-        c += ids[i] == le;
+    for (int64_t i = a * K + threadIdx.x * kIds; i < b * K; i += kGroupBlock * kIds)
+        c += __popc(slots_of(ids, i, b * K, le));
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1)
         c += __shfl_xor(c, d);
@@ -68,9 +80,10 @@ __global__ __launch_bounds__(kGroupBlock) void place_pairs_kernel(
     int epr, const int32_t *__restrict__ counts, int64_t cap, int32_t *__restrict__ offsets,
     int32_t *__restrict__ pair_row, int32_t *__restrict__ pair_slot, int32_t *__restrict__ row_pair)
 {
+    constexpr int W = kGroupBlock / kWave;
     const int e = blockIdx.x, r = e / epr, le = e % epr;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    __shared__ int s[kGroupBlock / kWave];
+    __shared__ int s[2][W];
     int c = 0;
     for (int i = threadIdx.x; i < e; i += kGroupBlock)
         c += counts[i];
@@ -78,11 +91,11 @@ __global__ __launch_bounds__(kGroupBlock) void place_pairs_kernel(
     for (int d = 32; d > 0; d >>= 1)
         c += __shfl_xor(c, d);
     if (lane == 0)
-        s[wave] = c;
+        s[1][wave] = c;
     __syncthreads();
     int base = 0;
-    for (int w = 0; w < kGroupBlock / kWave; ++w)
-        base += s[w];
+    for (int w = 0; w < W; ++w)
+        base += s[1][w];
     // a count past the capacity (ids that no dispatch wrote) leaves the tail out
     const int icap = int(cap);
     if (threadIdx.x == 0) {
@@ -94,32 +107,39 @@ __global__ __launch_bounds__(kGroupBlock) void place_pairs_kernel(
     }
     int64_t a, b;
     rank_rows(prefix, r, n, a, b);
-    for (int64_t i0 = a * K; i0 < b * K; i0 += kGroupBlock) {
-        const int64_t i = i0 + threadIdx.x;
-        const bool hit = i < b * K && ids[i] == le;
-        const uint64_t m = wave_ballot(hit);
-        __syncthreads();
-        if (lane == 0)
-            s[wave] = __popcll(m);
-        __syncthreads();
-        int before = 0, total = 0;
-        for (int w = 0; w < kGroupBlock / kWave; ++w) {
-            before += w < wave ? s[w] : 0;
-            total += s[w];
+    int flip = 0;
+    for (int64_t i0 = a * K; i0 < b * K; i0 += kGroupBlock * kIds, flip ^= 1) {
+        const int64_t i = i0 + threadIdx.x * kIds;
+        unsigned hits = slots_of(ids, i, b * K, le);
+        const int mine = __popc(hits);
+        int pre = mine;
+#pragma unroll
+        for (int d = 1; d < kWave; d <<= 1) {
+            const int o = __shfl_up(pre, d);
+            pre += lane >= d ? o : 0;
         }
-        if (hit) {
-            const int pos = base + before + __popcll(m & lanemask_lt());
-            if (pos < icap) {
-                const int64_t row = i / K;
-                int live = 0;
-                for (int k = 0; k < K; ++k) {
-                    const int64_t v = ids[row * K + k];
-                    live += v >= 0 && v < epr;
-                }
-                pair_row[pos] = int32_t(row) | (live == 1 ? int32_t(0x80000000u) : 0);
-                pair_slot[pos] = int32_t(i);
-                row_pair[i] = pos;
+        if (lane == 63)
+            s[flip][wave] = pre;
+        __syncthreads();  // two rows of s in turn: the next round but one writes this one again
+        int before = 0, total = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const int v = s[flip][w];
+            before += w < wave ? v : 0;
+            total += v;
+        }
+        for (int pos = base + before + pre - mine; hits != 0 && pos < icap; ++pos) {
+            const int64_t at = i + __ffs(hits) - 1;
+            hits &= hits - 1;
+            const int64_t row = at / K;
+            int live = 0;
+            for (int k = 0; k < K; ++k) {
+                const int64_t v = ids[row * K + k];
+                live += v >= 0 && v < epr;
             }
+            pair_row[pos] = int32_t(row) | (live == 1 ? int32_t(0x80000000u) : 0);
+            pair_slot[pos] = int32_t(at);
+            row_pair[at] = pos;
         }
         base += total;
     }
@@ -267,8 +287,7 @@ struct GatedBack {
 // Tiles of BM rows of one group by BN columns, with as many LDS stages as fit.
 // A block works through every gridDim.x-th tile: it looks up the next one while
 // the first stage of this one arrives, and sends off the next one's first stage
-// before it stores this one.  A group's last tile of at most BM / 2 rows is
-// computed at half the height.
+// before it stores this one.
 template <int BM, bool PCOL, Form F, class Epi>
 __global__ __launch_bounds__(NT) void tile_kernel(TileArgs a, Groups G, Epi epi)
 {
@@ -371,10 +390,7 @@ __global__ __launch_bounds__(NT) void tile_kernel(TileArgs a, Groups G, Epi epi)
             }
             store(cur);
         };
-        if (BM > 64 && cur.rows - cur.m0 <= BM / 2)
-            finish(work(Rows<(BM > 64 ? BM / 2 : BM)>{}));
-        else
-            finish(work(Rows<BM>{}));
+        at_height<BM>(cur.rows - cur.m0, [&](auto rows) { finish(work(rows)); });
         if (next.group < 0)
             break;
         t = next;
@@ -566,8 +582,6 @@ hipError_t launch_tiles(TileArgs a, const Groups &G, int64_t max_tiles_rows, con
     const dim3 grid(unsigned(all < cus ? all : cus));
     if (bm == 256)
         hipLaunchKernelGGL((tile_kernel<256, PCOL, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
-    else if (bm == 128)
-        hipLaunchKernelGGL((tile_kernel<128, PCOL, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
     else
         hipLaunchKernelGGL((tile_kernel<64, PCOL, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
     return hipGetLastError();

@@ -71,122 +71,138 @@ struct GatedFp8Out {
     }
 };
 
-// BM rows of one group by BN columns: the bf16 tile kernel's loop with K steps
-// of one scale block.  The step's token scales are staged beside the rows.
+// Tiles of BM rows of one group by BN columns: the bf16 tile kernel's loop over
+// tiles, with K steps of one scale block.  The step's scales are staged behind
+// the rows, one load a wave, so that every wave counts the same loads: waves 0
+// to 3 the BM token scales (some twice where BM is 64), the others the two
+// weight scales of the tile: its column blocks, or its gate and its up block.
 template <int BM, Form F, class Epi>
 __global__ __launch_bounds__(NT) void fp8_tile_kernel(FewArgs a, Groups G, Epi epi)
 {
-    constexpr int MT = BM / 32;
-    using QS = RowStage<BM, NT>;
+    using QS = NearRowStage<BM, NT>;
     using PR = NearRowStage<BN, NT>;
     constexpr int kP = PR::kBytes, kQ = QS::kBytes, kStage = kP + kQ + (BM + kWave) * 4, ST = BM == 256 ? 2 : 3;
+    typedef const __attribute__((address_space(3))) float lds_float;
     __shared__ __attribute__((aligned(128))) char smem[ST * kStage];
-    const Tile t = find_tile<BM, NT>(G, blockIdx.x, a.nt);
-    if (t.group < 0)
-        return;
     const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = uniform(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
-    const int64_t start = group_start(G, t.group);
-    const int e = group_expert(G, t.group);
-    const char *pw = a.p + int64_t(e) * a.p_expert;
     lds_char *lds = (lds_char *)smem;
-    const int n0 = t.n * (F == Form::kGated ? BN / 2 : BN);
     const int steps = a.kbytes >> 7;
-
-    QS qs;
-    qs.init(tid, [&](int, int r) {
-        const int m = t.m0 + r;
-        return a.q + (start + (m < t.rows ? m : t.rows - 1)) * a.ldq;
-    });
-    PR pr;
-    const bool up = F == Form::kGated && wave >= 4;  // as in the bf16 tile
-    pr.init(tid, pw + (int64_t(n0) + (up ? a.N : 0)) * a.ldp, [&](int, int r) {
-        int n = F == Form::kGated ? (r >> 6) * 32 + (r & 31) : r;
-        n = n0 + n < a.N ? n : a.N - 1 - n0;
-        return uint32_t(n) * uint32_t(a.ldp);
-    });
-    // Scales are staged behind the rows, one load a wave, so that every wave counts
-    // the same loads: waves 0 to 3 the BM token scales (some twice where BM is
-    // less than 256), the others the two weight scales of the tile: its column
-    // blocks, or its gate block and its up block.
-    const char *sq;
-    if (wave < 4) {
-        const int m = t.m0 + tid % BM;
-        sq = reinterpret_cast<const char *>(a.q_scale + (start + (m < t.rows ? m : t.rows - 1)) * steps);
-    } else {
-        int nb = n0 + (F == Form::kGated ? 0 : (lane & 1) * 128);
-        nb = (nb < a.N ? nb : a.N - 1) >> 7;
-        if (F == Form::kGated)
-            nb += (lane & 1) * (a.N >> 7);
-        sq = reinterpret_cast<const char *>(a.p_scale + e * a.p_scales + int64_t(nb) * steps);
-    }
     const int sdst = kP + kQ + (wave < 4 ? wave % (BM / kWave) : BM / kWave) * kWave * 4;
     auto stage = [&](int s) -> lds_char * { return lds + (ST == 2 ? s & 1 : s % ST) * kStage; };
+
+    QS qs;
+    PR pr;
+    const char *sq = nullptr;  // this lane's scale
+    auto set_up = [&](const Tile &t) {
+        const int64_t start = group_start(G, t.group);
+        const int e = group_expert(G, t.group);
+        const int n0 = t.n * (F == Form::kGated ? BN / 2 : BN);
+        qs.init(tid, a.q + (start + t.m0) * a.ldq, [&](int, int r) {
+            const int last = t.rows - 1 - t.m0;
+            return uint32_t(r < last ? r : last) * uint32_t(a.ldq);
+        });
+        const bool up = F == Form::kGated && wave >= 4;  // as in the bf16 tile
+        pr.init(tid, a.p + int64_t(e) * a.p_expert + (int64_t(n0) + (up ? a.N : 0)) * a.ldp, [&](int, int r) {
+            int n = F == Form::kGated ? (r >> 6) * 32 + (r & 31) : r;
+            n = n0 + n < a.N ? n : a.N - 1 - n0;
+            return uint32_t(n) * uint32_t(a.ldp);
+        });
+        if (wave < 4) {
+            const int m = t.m0 + tid % BM;
+            sq = reinterpret_cast<const char *>(a.q_scale + (start + (m < t.rows ? m : t.rows - 1)) * steps);
+        } else {
+            int nb = n0 + (F == Form::kGated ? 0 : (lane & 1) * 128);
+            nb = (nb < a.N ? nb : a.N - 1) >> 7;
+            if (F == Form::kGated)
+                nb += (lane & 1) * (a.N >> 7);
+            sq = reinterpret_cast<const char *>(a.p_scale + e * a.p_scales + int64_t(nb) * steps);
+        }
+    };
     auto issue = [&](int s, int part) {
         lds_char *b = stage(s);
         if (part == 0) {
             pr.template issue<false>(b, tid, wave, int64_t(s) * kStepBytes, a.kbytes);
         } else {
-            qs.template issue<false>(b + kP, wave, int64_t(s) * kStepBytes, a.kbytes);
+            qs.template issue<false>(b + kP, tid, wave, int64_t(s) * kStepBytes, a.kbytes);
             load_lds4(sq + int64_t(s) * 4, b + sdst);
         }
     };
     auto frag = [&](const lds_char *base, int r) {
         Frag f;
-        f.lo = *(const __attribute__((address_space(3))) i32x4 *)QS::at(base, r, lane >> 4);
-        f.hi = *(const __attribute__((address_space(3))) i32x4 *)QS::at(base, r, 4 + (lane >> 4));
+        f.lo = *(const __attribute__((address_space(3))) i32x4 *)RowStage<BM, NT>::at(base, r, lane >> 4);
+        f.hi = *(const __attribute__((address_space(3))) i32x4 *)RowStage<BM, NT>::at(base, r, 4 + (lane >> 4));
         return f;
     };
-    constexpr int PH = MT >= 4 ? MT / 2 : 1, MQ = MT / PH;  // two row tiles a phase
-    f32x4 acc[MT][4] = {};
-    Frag pf[4], qf[MQ];
-    float sc[MQ], c0 = 0.0f, c1 = 0.0f;
+
+    unsigned block = blockIdx.x;
+    Tile t = find_tile<BM, NT>(G, block, a.nt);
+    if (t.group < 0)
+        return;
+    set_up(t);
     open_stages<ST>(steps, issue);
-    take_turns<PH, ST, PR::J + QS::J + 1>(
-        steps, wm, issue,
-        [&](int s, int ph) {
-            const lds_char *pb = stage(s), *qb = pb + kP;
-            if (ph == 0) {
-                const __attribute__((address_space(3))) float *w =
-                    (const __attribute__((address_space(3))) float *)(qb + kQ + BM * 4);
-                c0 = w[F == Form::kGated ? 0 : wn >> 1];
-                c1 = F == Form::kGated ? w[1] : c0;
+    for (;;) {
+        block += gridDim.x;
+        const Tile next = find_tile<BM, NT>(G, block, a.nt);
+        const Tile cur = t;
+        at_height<BM>(cur.rows - cur.m0, [&](auto rows_tag) {
+            constexpr int R = decltype(rows_tag)::value, MT = R / 32;
+            constexpr int MQ = 2, PH = MT / MQ;  // two row tiles a phase
+            f32x4 acc[MT][4] = {};
+            Frag pf[4], qf[MQ];
+            float sc[MQ], c0 = 0.0f, c1 = 0.0f;
+            take_turns<PH, ST, PR::J + QS::J + 1>(
+                steps, wm, issue,
+                [&](int s, int ph) {
+                    const lds_char *pb = stage(s), *qb = pb + kP;
+                    if (ph == 0) {
+                        lds_float *w = (lds_float *)(qb + kQ + BM * 4);
+                        c0 = w[F == Form::kGated ? 0 : wn >> 1];
+                        c1 = F == Form::kGated ? w[1] : c0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    pf[i] = frag(pb, wn * 64 + i * 16 + (lane & 15));
-            }
+                        for (int i = 0; i < 4; ++i)
+                            pf[i] = frag(pb, wn * 64 + i * 16 + (lane & 15));
+                    }
 #pragma unroll
-            for (int m = 0; m < MQ; ++m) {
-                const int r = wm * (BM / 2) + (ph * MQ + m) * 16 + (lane & 15);
-                qf[m] = frag(qb, r);
-                sc[m] = *(const __attribute__((address_space(3))) float *)(qb + kQ + r * 4);
-            }
-        },
-        [&](int, int ph) {
+                    for (int m = 0; m < MQ; ++m) {
+                        const int r = wm * (R / 2) + (ph * MQ + m) * 16 + (lane & 15);
+                        qf[m] = frag(qb, r);
+                        sc[m] = *(lds_float *)(qb + kQ + r * 4);
+                    }
+                },
+                [&](int, int ph) {
 #pragma unroll
-            for (int m = 0; m < MQ; ++m) {
-                hold(qf[m].lo);
-                hold(qf[m].hi);
-            }
+                    for (int m = 0; m < MQ; ++m) {
+                        hold(qf[m].lo);
+                        hold(qf[m].hi);
+                    }
 #pragma unroll
-            for (int m = 0; m < MQ; ++m) {
-                const float s0 = sc[m] * c0, s1 = F == Form::kGated ? sc[m] * c1 : s0;
+                    for (int m = 0; m < MQ; ++m) {
+                        const float s0 = sc[m] * c0, s1 = F == Form::kGated ? sc[m] * c1 : s0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[ph * MQ + m][i] += mfma_step_fp8(pf[i], qf[m]) * (i < 2 ? s0 : s1);
-            }
+                        for (int i = 0; i < 4; ++i)
+                            acc[ph * MQ + m][i] += mfma_step_fp8(pf[i], qf[m]) * (i < 2 ? s0 : s1);
+                    }
 #pragma unroll
-            for (int m = 0; m < MQ; ++m)
+                    for (int m = 0; m < MQ; ++m)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    hold(acc[ph * MQ + m][i]);
+                        for (int i = 0; i < 4; ++i)
+                            hold(acc[ph * MQ + m][i]);
+                });
+            const int64_t start = group_start(G, cur.group);
+            const int n0 = cur.n * (F == Form::kGated ? BN / 2 : BN) + wn * (F == Form::kGated ? 32 : 64);
+            if constexpr (Epi::kBlockWide)
+                epi.template store_block<MT, 4, 4, R>(cur, start, true, wn, wm * (R / 2), n0, a.N, acc, lane);
+            else
+                epi.store(cur, start, cur.m0 + wm * (R / 2), n0, a.N, acc, lane);
         });
-    const int nw = n0 + wn * (F == Form::kGated ? 32 : 64);
-    if constexpr (Epi::kBlockWide)
-        epi.template store_block<MT, 4, 4, BM>(t, start, true, wn, wm * (BM / 2), nw, a.N, acc, lane);
-    else
-        epi.store(t, start, t.m0 + wm * (BM / 2), nw, a.N, acc, lane);
+        if (next.group < 0)
+            break;
+        set_up(next);
+        open_stages<ST>(steps, issue);
+        t = next;
+    }
 }
 
 template <Form F, class Epi>
@@ -204,11 +220,10 @@ hipError_t launch_fp8_tiles(FewArgs a, const Groups &G, int64_t rows, int64_t ma
     if (log_enabled())
         log_launch("%s: rows<=%lld groups=%d N=%d K=%d tile=%dx%d blocks=%lld", what, (long long)rows,
                    G.num, a.N, a.kbytes, bm, BN, (long long)mt * a.nt);
-    const dim3 grid(unsigned(blocks_for_tiles(mt * a.nt)));
+    const int64_t cus = compute_units(), all = blocks_for_tiles(mt * a.nt);
+    const dim3 grid(unsigned(all < cus ? all : cus));
     if (bm == 256)
         hipLaunchKernelGGL((fp8_tile_kernel<256, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
-    else if (bm == 128)
-        hipLaunchKernelGGL((fp8_tile_kernel<128, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
     else
         hipLaunchKernelGGL((fp8_tile_kernel<64, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
     return hipGetLastError();

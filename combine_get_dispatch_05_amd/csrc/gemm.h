@@ -40,6 +40,15 @@ typedef __attribute__((address_space(3))) char lds_char;
 // that a tail adds exact zeros whatever lies behind a row (a NaN included).
 static __device__ __attribute__((aligned(16))) const unsigned int kZero16[4] = {0, 0, 0, 0};
 
+// A value that is the same in every lane, told to the compiler.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ const char *uniform(const char *p)
+{
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = uint32_t(uniform(int(uint32_t(v)))), hi = uint32_t(uniform(int(uint32_t(v >> 32))));
+    return reinterpret_cast<const char *>(uint64_t(lo) | uint64_t(hi) << 32);
+}
+
 // 16 (or 4) bytes a lane from src to dst + 16 (4) * lane, dst the same for the
 // whole wave.  In assembly because the compiler, which cannot tell the LDS
 // stages apart, makes every later LDS read wait for the loads in flight: that
@@ -62,7 +71,7 @@ __device__ __forceinline__ void load_lds16(const char *base, uint32_t off, lds_c
 {
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                  :
-                 : "v"(off), "s"(base), "s"(lds_at(dst))
+                 : "v"(off), "s"(uniform(base)), "s"(lds_at(dst))
                  : "memory");
 }
 __device__ __forceinline__ void load_lds4(const char *src, lds_char *dst)
@@ -72,15 +81,6 @@ __device__ __forceinline__ void load_lds4(const char *src, lds_char *dst)
                  : "v"(src), "s"(lds_at(dst))
                  : "memory");
 }
-// A value that is the same in every lane, told to the compiler.
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ const char *uniform(const char *p)
-{
-    const uint64_t v = reinterpret_cast<uint64_t>(p);
-    const uint32_t lo = uint32_t(uniform(int(uint32_t(v)))), hi = uint32_t(uniform(int(uint32_t(v >> 32))));
-    return reinterpret_cast<const char *>(uint64_t(lo) | uint64_t(hi) << 32);
-}
-
 // Every load of this wave but the last N has landed.
 template <int N>
 __device__ __forceinline__ void landed()
@@ -400,7 +400,7 @@ __device__ __forceinline__ int64_t share_of_xcd(unsigned n, unsigned x, unsigned
 // column tiles; group = -1 past the last.  Consecutive blocks go round the
 // eight XCDs, so each XCD has a contiguous run of the order.  First come the
 // tiles of more than BM / 2 rows, in bands, then the groups' shorter last tiles,
-// which cost half: in the order of the groups they would leave some blocks
+// which cost at most half: in the order of the groups they would leave some blocks
 // with a round more of whole tiles than others (experts of about 1024 rows: 9
 // rounds of blocks for 8.5 rounds of work).  The order is laid over the tiles
 // that there are, not over the grid.  Every thread of the block takes part.
@@ -569,12 +569,29 @@ __device__ __forceinline__ void take_turns(int steps, int group, Issue issue, Re
         turn();
 }
 
+// A tile's rows are computed at the least of these heights that holds them.
+template <int N>
+struct Rows {
+    static constexpr int value = N;
+};
+template <int BM, class F>
+__device__ __forceinline__ void at_height(int rows, F f)
+{
+    if (BM == 64 || rows <= 64)
+        return f(Rows<64>{});
+    if (rows <= 128)
+        return f(Rows<(BM > 64 ? 128 : 64)>{});
+    if (rows <= 192)
+        return f(Rows<(BM > 64 ? 192 : 64)>{});
+    f(Rows<BM>{});
+}
+
 // The phases of a bf16 stage for a wave of MT x 4 16 x 16 tiles: the half ks of
 // the stage's K and, where MT is 8, the half of the rows.  P's fragments of the
 // second half are read ahead in part, which evens out the reads of the phases.
 template <int MT, class FragP, class FragQ>
 struct Bf16Phases {
-    static constexpr int kPhases = MT == 8 ? 4 : MT == 4 ? 2 : 1;
+    static constexpr int kPhases = MT == 8 ? 4 : MT > 2 ? 2 : 1;
     static constexpr int MQ = MT == 8 ? 4 : MT;  // row tiles of a phase
     f32x4 (&acc)[MT][4];
     FragP frag_p;  // (stage, column tile, ks)
