@@ -160,6 +160,19 @@ def current_stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+def address(t):
+    """Raw device address of a tensor as an int (None -> None): what a void pointer
+    argument takes without an object made for it, for calls whose host time counts."""
+    return None if t is None else t.data_ptr()
+
+
+def raw_stream(device_index: int) -> int:
+    """The raw hipStream_t of torch's current stream on that device."""
+    import torch
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(device_index) if get else torch.cuda.current_stream(device_index).cuda_stream
+
+
 def tunings(op: str) -> list:
     """All compiled-in launch shapes of ``op`` ("dispatch" or "combine")."""
     a, b, c = ctypes.c_int(), ctypes.c_int(), ctypes.c_int()

@@ -49,33 +49,39 @@ def _same_device(*ts):
         raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
 
 
-def _here(*ts):
-    """One device, the current one: kernels go to its current stream."""
-    _same_device(*ts)
-    t = next(t for t in ts if t is not None)
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {t.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+def _row(t: torch.Tensor, dtype, shape, name: str):
+    """_need and _shape in one look where all is well: the small calls' host time counts."""
+    if not (t.dtype == dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
+        _need(t, dtype, name, len(shape))
+        _shape(t, shape, name)
+
+
+def _here(*ts) -> int:
+    """The index of the tensors' one device, which has to be the current one: kernels go
+    to its current stream."""
+    dev = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            _same_device(*ts)
+            raise ValueError(f"tensors are on {t.device}, the current device is cuda:{dev}")
+    return dev
 
 
 def _fp8_pair(pair, name: str, ndim: int, row_blocks: bool):
     """Checks (codes, scales): codes float8_e4m3fn or uint8 with a last dimension
     of whole 128-element blocks, and one fp32 scale per block of a row (or, with
-    row_blocks, per 128 x 128 block of a weight).  Returns both, codes as bytes."""
+    row_blocks, per 128 x 128 block of a weight).  Returns both."""
     if not isinstance(pair, (tuple, list)) or len(pair) != 2:
         raise TypeError(f"{name} must be a pair (codes, scales)")
     q, sc = pair
-    if q.dtype == torch.float8_e4m3fn:
-        q = q.view(torch.uint8)
-    _need(q, torch.uint8, f"{name} codes", ndim)
-    _need(sc, torch.float32, f"{name} scales", ndim)
-    if q.shape[-1] % 128:
+    if q.dtype != torch.float8_e4m3fn:
+        _need(q, torch.uint8, f"{name} codes", ndim)
+    elif not (q.dim() == ndim and q.is_cuda and q.is_contiguous()):
+        _need(q, torch.float8_e4m3fn, f"{name} codes", ndim)
+    *lead, rows, width = q.shape
+    if width % 128:
         raise ValueError(f"{name}: rows must be whole 128-element blocks")
-    shape = list(q.shape)
-    shape[-1] //= 128
-    if row_blocks:
-        shape[-2] = -(-shape[-2] // 128)
-    _shape(sc, shape, f"{name} scales")
+    _row(sc, torch.float32, (*lead, -(-rows // 128) if row_blocks else rows, width // 128), f"{name} scales")
     return q, sc
 
 
@@ -87,29 +93,26 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     in the format of low_latency_dispatch(use_fp8=True), the bf16 sum x + residual
     (None without residual) and rstd [T] fp32, which the backward pass takes."""
     _need(x, torch.bfloat16, "x", 2)
-    _need(weight, torch.bfloat16, "weight", 1)
     T, H = x.shape
-    _shape(weight, (H,), "weight")
+    _row(weight, torch.bfloat16, (H,), "weight")
     if residual is not None:
-        _need(residual, torch.bfloat16, "residual", 2)
-        _shape(residual, (T, H), "residual")
+        _row(residual, torch.bfloat16, (T, H), "residual")
     if not (use_fp8 or bf16_out):
         raise ValueError("nothing to return: neither bf16_out nor use_fp8")
-    _here(x, weight, residual)
-    dev = x.device
-    out = torch.empty_like(x) if bf16_out else None
-    q = torch.empty((T, H), dtype=torch.uint8, device=dev) if use_fp8 else None
-    sc = torch.empty((T, H // 128), dtype=torch.float32, device=dev) if use_fp8 else None
-    res = torch.empty_like(x) if residual is not None else None
-    rstd = torch.empty(T, dtype=torch.float32, device=dev)
     if use_fp8 and H % 128:
         raise ValueError("use_fp8 needs rows of whole 128-element blocks")
+    dev = _here(x, weight, residual)
+    out = torch.empty_like(x) if bf16_out else None
+    fp8 = (torch.empty_like(x, dtype=torch.float8_e4m3fn),
+           torch.empty((T, H // 128), dtype=torch.float32, device=x.device)) if use_fp8 else (None, None)
+    res = torch.empty_like(x) if residual is not None else None
+    rstd = torch.empty(T, dtype=torch.float32, device=x.device)
     if T > 0:
-        abi.check(abi.lib().ep_rms_norm(T, H, float(eps), abi.ptr(x), abi.ptr(residual),
-                                        abi.ptr(weight), abi.ptr(res), abi.ptr(out), abi.ptr(q),
-                                        abi.ptr(sc), abi.ptr(rstd), abi.current_stream()),
-                  "ep_rms_norm")
-    return out, (q.view(torch.float8_e4m3fn), sc) if use_fp8 else None, res, rstd
+        at = abi.address
+        abi.check(abi.lib().ep_rms_norm(T, H, eps, x.data_ptr(), at(residual), weight.data_ptr(), at(res),
+                                        at(out), at(fp8[0]), at(fp8[1]), rstd.data_ptr(),
+                                        abi.raw_stream(dev)), "ep_rms_norm")
+    return out, fp8 if use_fp8 else None, res, rstd
 
 
 def rms_norm_backward(dout: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
@@ -118,25 +121,21 @@ def rms_norm_backward(dout: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
     the gradient that arrived at residual_out.  Returns (dx [T, H] bf16, the gradient
     of x and of residual alike, and dweight [H] fp32)."""
     _need(dout, torch.bfloat16, "dout", 2)
-    _need(h, torch.bfloat16, "h", 2)
-    _need(weight, torch.bfloat16, "weight", 1)
-    _need(rstd, torch.float32, "rstd", 1)
     T, H = dout.shape
-    _shape(h, (T, H), "h")
-    _shape(weight, (H,), "weight")
-    _shape(rstd, (T,), "rstd")
+    _row(h, torch.bfloat16, (T, H), "h")
+    _row(weight, torch.bfloat16, (H,), "weight")
+    _row(rstd, torch.float32, (T,), "rstd")
     if dresidual is not None:
-        _need(dresidual, torch.bfloat16, "dresidual", 2)
-        _shape(dresidual, (T, H), "dresidual")
-    _here(dout, h, weight, rstd, dresidual)
+        _row(dresidual, torch.bfloat16, (T, H), "dresidual")
+    dev = _here(dout, h, weight, rstd, dresidual)
     dx = torch.empty_like(dout)
     dweight = torch.empty(H, dtype=torch.float32, device=dout.device)
-    size = int(abi.lib().ep_rms_norm_backward_workspace(T, H))
+    size = abi.lib().ep_rms_norm_backward_workspace(T, H)
     work = torch.empty(size, dtype=torch.uint8, device=dout.device)
-    abi.check(abi.lib().ep_rms_norm_backward(T, H, abi.ptr(dout), abi.ptr(h), abi.ptr(weight),
-                                             abi.ptr(rstd), abi.ptr(dresidual), abi.ptr(dx),
-                                             abi.ptr(dweight), abi.ptr(work), size,
-                                             abi.current_stream()), "ep_rms_norm_backward")
+    abi.check(abi.lib().ep_rms_norm_backward(T, H, dout.data_ptr(), h.data_ptr(), weight.data_ptr(),
+                                             rstd.data_ptr(), abi.address(dresidual), dx.data_ptr(),
+                                             dweight.data_ptr(), work.data_ptr(), size,
+                                             abi.raw_stream(dev)), "ep_rms_norm_backward")
     return dx, dweight
 
 
@@ -148,11 +147,11 @@ def fp8_product(a, w) -> torch.Tensor:
     wq, wsc = _fp8_pair(w, "w", 2, True)
     (M, K), N = aq.shape, wq.shape[0]
     _shape(wq, (N, K), "w codes")
-    _here(aq, asc, wq, wsc)
+    dev = _here(aq, asc, wq, wsc)
     out = torch.empty((M, N), dtype=torch.bfloat16, device=aq.device)
     if M > 0:
-        abi.check(abi.lib().ep_fp8_product(M, N, K, abi.ptr(aq), abi.ptr(asc), abi.ptr(wq),
-                                           abi.ptr(wsc), abi.ptr(out), abi.current_stream()),
+        abi.check(abi.lib().ep_fp8_product(M, N, K, aq.data_ptr(), asc.data_ptr(), wq.data_ptr(),
+                                           wsc.data_ptr(), out.data_ptr(), abi.raw_stream(dev)),
                   "ep_fp8_product")
     return out
 
@@ -555,13 +554,13 @@ class Buffer:
             inter = q2.shape[2]
             _shape(q13, (self.num_experts, 2 * inter, H), "w13 codes")
             _shape(q2, (self.num_experts, H, inter), "w2 codes")
-            _here(q, sc, packed_count, q13, s13, q2, s2, handle.topk_slot, out)
+            dev = _here(q, sc, packed_count, q13, s13, q2, s2, handle.topk_slot, out)
         else:
             _need(x, torch.bfloat16, "x", 4)
             _shape(x, cells + (H,), "x")
             q = x
             inter = self._expert_weights(w13, w2, H)
-            _here(x, packed_count, w13, w2, handle.topk_slot, out)
+            dev = _here(x, packed_count, w13, w2, handle.topk_slot, out)
         if out is None:
             out = torch.empty(cells + (H,), dtype=torch.bfloat16, device=q.device)
         else:
@@ -569,19 +568,19 @@ class Buffer:
             _shape(out, cells + (H,), "out")
         if T == 0:
             return out
-        s = abi.current_stream()
+        s = abi.raw_stream(dev)
         if fp8:
             aq = torch.empty(cells + (inter,), dtype=torch.uint8, device=q.device)
             asc = torch.empty(cells + (inter // 128,), dtype=torch.float32, device=q.device)
             abi.check(abi.lib().ep_ll_expert_ffn_fp8(
-                ctypes.byref(d), S, inter, abi.ptr(q), abi.ptr(sc), abi.ptr(packed_count), abi.ptr(q13),
-                abi.ptr(s13), abi.ptr(q2), abi.ptr(s2), abi.ptr(aq), abi.ptr(asc), abi.ptr(out), s),
+                ctypes.byref(d), S, inter, abi.address(q), abi.address(sc), abi.address(packed_count), abi.address(q13),
+                abi.address(s13), abi.address(q2), abi.address(s2), abi.address(aq), abi.address(asc), abi.address(out), s),
                 "ep_ll_expert_ffn_fp8")
         else:
             act = torch.empty(cells + (inter,), dtype=torch.bfloat16, device=q.device)
             abi.check(abi.lib().ep_ll_expert_ffn(
-                ctypes.byref(d), S, inter, abi.ptr(x), abi.ptr(packed_count), abi.ptr(w13), abi.ptr(w2),
-                abi.ptr(act), abi.ptr(out), s), "ep_ll_expert_ffn")
+                ctypes.byref(d), S, inter, abi.address(x), abi.address(packed_count), abi.address(w13), abi.address(w2),
+                abi.address(act), abi.address(out), s), "ep_ll_expert_ffn")
         return out
 
     def expert_rows(self, recv_topk_idx: torch.Tensor, layout,
@@ -606,20 +605,20 @@ class Buffer:
             _need(prefix, torch.int32, "rank_prefix_matrix", 1)
             _shape(prefix, (self.num_ranks,), "rank_prefix_matrix")
             num_tokens = N if num_tokens is None else int(num_tokens)
-        _here(recv_topk_idx, prefix)
+        index = _here(recv_topk_idx, prefix)
         if isinstance(layout, Handle):
             out = abi.LayoutOut(None, None, None, prefix.data_ptr(), None, None, None, None, 0)
             abi.check(abi.lib().ep_handle_copy_layout(layout.raw, ctypes.byref(out),
-                                                      abi.current_stream()), "ep_handle_copy_layout")
+                                                      abi.raw_stream(index)), "ep_handle_copy_layout")
         cap = min(num_tokens, N) * K
         i32 = dict(dtype=torch.int32, device=dev)
         rows = ExpertRows(torch.empty(self.num_experts + 1, **i32), torch.empty(cap, **i32),
                           torch.empty(cap, **i32), torch.empty((N, K), **i32))
         counts = torch.empty(self.num_experts, **i32)
         abi.check(abi.lib().ep_expert_rows(
-            ctypes.byref(self._dims(num_tokens, 8, K)), abi.ptr(prefix), abi.ptr(recv_topk_idx), N, cap,
-            abi.ptr(counts), abi.ptr(rows.expert_offsets), abi.ptr(rows.pair_row),
-            abi.ptr(rows.pair_slot), abi.ptr(rows.row_pair), abi.current_stream()), "ep_expert_rows")
+            ctypes.byref(self._dims(num_tokens, 8, K)), abi.address(prefix), abi.address(recv_topk_idx), N, cap,
+            abi.address(counts), abi.address(rows.expert_offsets), abi.address(rows.pair_row),
+            abi.address(rows.pair_slot), abi.address(rows.row_pair), abi.raw_stream(index)), "ep_expert_rows")
         return rows
 
     def _expert_args(self, x, rows: ExpertRows, topk_weights, w13, w2):
@@ -640,7 +639,7 @@ class Buffer:
         w2 [E, H, I] are bf16.  Returns (y [rows, H] bf16, saved): saved is what
         expert_ffn_backward takes, the fp32 g and u of every pair, None without save."""
         N, H, K, inter = self._expert_args(x, rows, topk_weights, w13, w2)
-        _here(x, rows.row_pair, topk_weights, w13, w2)
+        index = _here(x, rows.row_pair, topk_weights, w13, w2)
         dev, cap = x.device, rows.pair_row.shape[0]
         y = torch.empty_like(x)
         act = torch.empty((cap, inter), dtype=torch.bfloat16, device=dev)
@@ -648,9 +647,9 @@ class Buffer:
         saved = torch.empty((cap, 2 * inter), dtype=torch.float32, device=dev) if save else None
         raw = rows._raw()
         abi.check(abi.lib().ep_expert_ffn(
-            ctypes.byref(self._dims(0, H, K)), inter, ctypes.byref(raw), abi.ptr(x),
-            abi.ptr(topk_weights), abi.ptr(w13), abi.ptr(w2), abi.ptr(act), abi.ptr(saved),
-            abi.ptr(terms), abi.ptr(y), abi.current_stream()), "ep_expert_ffn")
+            ctypes.byref(self._dims(0, H, K)), inter, ctypes.byref(raw), abi.address(x),
+            abi.address(topk_weights), abi.address(w13), abi.address(w2), abi.address(act), abi.address(saved),
+            abi.address(terms), abi.address(y), abi.raw_stream(index)), "ep_expert_ffn")
         return y, saved
 
     def expert_ffn_backward(self, dy: torch.Tensor, x: torch.Tensor, rows: ExpertRows,
@@ -665,7 +664,7 @@ class Buffer:
         cap, dev = rows.pair_row.shape[0], x.device
         _need(saved, torch.float32, "saved", 2)
         _shape(saved, (cap, 2 * inter), "saved")
-        _here(dy, x, rows.row_pair, topk_weights, w13, w2, saved)
+        index = _here(dy, x, rows.row_pair, topk_weights, w13, w2, saved)
         bf = dict(dtype=torch.bfloat16, device=dev)
         f32 = dict(dtype=torch.float32, device=dev)
         dgu, act = torch.empty((cap, 2 * inter), **bf), torch.empty((cap, inter), **bf)
@@ -674,10 +673,10 @@ class Buffer:
         dw13, dw2 = torch.empty_like(w13), torch.empty_like(w2)
         raw = rows._raw()
         abi.check(abi.lib().ep_expert_ffn_backward(
-            ctypes.byref(self._dims(0, H, K)), inter, ctypes.byref(raw), abi.ptr(dy), abi.ptr(x),
-            abi.ptr(topk_weights), abi.ptr(w13), abi.ptr(w2), abi.ptr(saved), abi.ptr(dgu),
-            abi.ptr(act), abi.ptr(terms), abi.ptr(parts), abi.ptr(dx), abi.ptr(dweights),
-            abi.ptr(dw13), abi.ptr(dw2), abi.current_stream()), "ep_expert_ffn_backward")
+            ctypes.byref(self._dims(0, H, K)), inter, ctypes.byref(raw), abi.address(dy), abi.address(x),
+            abi.address(topk_weights), abi.address(w13), abi.address(w2), abi.address(saved), abi.address(dgu),
+            abi.address(act), abi.address(terms), abi.address(parts), abi.address(dx), abi.address(dweights),
+            abi.address(dw13), abi.address(dw2), abi.raw_stream(index)), "ep_expert_ffn_backward")
         return dx, dweights, dw13, dw2
 
     # ------------------------------------------------------ load balancing

@@ -187,13 +187,18 @@ inline dim3 row_grid(int64_t rows)
 // Blocks of one launch of a 512-thread kernel (the same limit).
 constexpr int64_t kMaxTileBlocks = int64_t(1) << 22;
 
+// Compute units of the current device, in whole rounds of its XCDs: the blocks of
+// a launch whose blocks each fill one and work through tiles.
+int compute_units();
+
 // Row tile of the tile kernels.  A 256-row tile reads a group's weight once for
-// up to 256 rows and shortens its last tile to what is there; below 64 rows a
-// group on average its rows are few enough for 64-row tiles, whose third LDS
-// stage hides more of the weight's latency.
-inline int tile_rows(int64_t rows, int64_t groups)
+// up to 256 rows and shortens its last tile to what is there.  64-row tiles
+// where a group has no more rows on average (their third LDS stage hides more
+// of the weight's latency), or where the larger ones would not fill the card.
+inline int tile_rows(int64_t rows, int64_t groups, int64_t column_tiles)
 {
-    return rows / (groups > 0 ? groups : 1) > 64 ? 256 : 64;
+    groups = groups > 0 ? groups : 1;
+    return rows / groups > 64 && (rows / 256 + groups) * column_tiles >= compute_units() ? 256 : 64;
 }
 
 // Shared with the entry points outside ep_api.hip.

@@ -379,7 +379,7 @@ __global__ __launch_bounds__(NT) void tile_kernel(TileArgs a, Groups G, Epi epi)
     };
     for (;;) {
         block += gridDim.x;
-        const Tile next = find_tile<BM, NT>(G, block, a.nt);
+        const Tile next = block < a.blocks ? find_tile<BM, NT>(G, block, a.nt) : Tile{-1, 0, 0, 0};
         if (next.group >= 0)
             find_rows(next);
         const Tile cur = t;
@@ -563,23 +563,24 @@ __global__ __launch_bounds__(256) void rows_kernel(const int32_t *__restrict__ r
 // --------------------------------------------------------------- launches
 
 template <bool PCOL, Form F, class Epi>
-hipError_t launch_tiles(TileArgs a, const Groups &G, int64_t max_tiles_rows, const Epi &epi,
+hipError_t launch_tiles(TileArgs a, const Groups &G, int64_t rows, int64_t groups, const Epi &epi,
                         const char *what, hipStream_t stream)
 {
-    const int bm = tile_rows(max_tiles_rows, G.num);
-    // every group can end in one part tile, and no more tiles than rows exist
-    int64_t mt = max_tiles_rows / bm + (G.num < max_tiles_rows ? G.num : max_tiles_rows);
     const int cols = F == Form::kGated ? BN / 2 : BN;
     a.nt = unsigned((a.N + cols - 1) / cols);
+    const int bm = tile_rows(rows, groups, a.nt);
+    // every group can end in one part tile, and no more tiles than rows exist
+    const int64_t mt = rows / bm + (groups < rows ? groups : rows);
     if (mt * a.nt > kMaxTileBlocks)
         return hipErrorInvalidValue;
     if (mt == 0)
         return hipSuccess;
     if (log_enabled())
         log_launch("%s: rows<=%lld groups=%d N=%d K=%d tile=%dx%d blocks=%lld", what,
-                   (long long)max_tiles_rows, G.num, a.N, a.K, bm, BN, (long long)mt * a.nt);
+                   (long long)rows, G.num, a.N, a.K, bm, BN, (long long)mt * a.nt);
     const int64_t cus = compute_units(), all = blocks_for_tiles(mt * a.nt);
     const dim3 grid(unsigned(all < cus ? all : cus));
+    a.blocks = unsigned(all);
     if (bm == 256)
         hipLaunchKernelGGL((tile_kernel<256, PCOL, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
     else
@@ -649,7 +650,7 @@ hipError_t launch_expert_ffn(const ExpertFfn &f, const void *x, const void *w13,
     a.N = I;
     a.K = H;
     hipError_t e = launch_tiles<false, Form::kGated>(
-        a, G, f.pairs, GatedOut{static_cast<uint16_t *>(act), gate_up}, "expert_ffn gated", stream);
+        a, G, f.pairs, f.experts, GatedOut{static_cast<uint16_t *>(act), gate_up}, "expert_ffn gated", stream);
     if (e != hipSuccess)
         return e;
     a.q = static_cast<const char *>(act);
@@ -661,7 +662,7 @@ hipError_t launch_expert_ffn(const ExpertFfn &f, const void *x, const void *w13,
     a.N = H;
     a.K = I;
     e = launch_tiles<false, Form::kPlain>(
-        a, G, f.pairs,
+        a, G, f.pairs, f.experts,
         PairOut{f.pair_row, f.pair_slot, f.weights, static_cast<uint16_t *>(y), terms},
         "expert_ffn down", stream);
     if (e != hipSuccess)
@@ -686,7 +687,7 @@ hipError_t launch_expert_ffn_backward(const ExpertFfn &f, const void *dy, const 
     a.N = I;
     a.K = H;
     hipError_t e = launch_tiles<true, Form::kBack>(
-        a, G, f.pairs,
+        a, G, f.pairs, f.experts,
         GatedBack{f.pair_slot, f.weights, gate_up, static_cast<uint16_t *>(dgu),
                   static_cast<uint16_t *>(wact), parts, tiles},
         "expert_ffn gate backward", stream);
@@ -701,7 +702,7 @@ hipError_t launch_expert_ffn_backward(const ExpertFfn &f, const void *dy, const 
     a.N = H;
     a.K = 2 * I;
     e = launch_tiles<true, Form::kPlain>(
-        a, G, f.pairs, PairOut{f.pair_row, f.pair_slot, nullptr, static_cast<uint16_t *>(dx), terms},
+        a, G, f.pairs, f.experts, PairOut{f.pair_row, f.pair_slot, nullptr, static_cast<uint16_t *>(dx), terms},
         "expert_ffn dx", stream);
     if (e != hipSuccess)
         return e;
@@ -752,16 +753,31 @@ hipError_t launch_ll_expert_ffn(int E, int R, int slots, int H, int I, int64_t m
                                 const void *w2, void *act, void *out, hipStream_t stream)
 {
     const Groups G{nullptr, counts, slots, E, R, E / R, 1, kNoLimit};
-    TileArgs a{};
+    FewArgs a{};
     a.q = static_cast<const char *>(packed);
     a.ldq = int64_t(H) * 2;
     a.p = static_cast<const char *>(w13);
     a.p_expert = int64_t(2) * I * H * 2;
     a.ldp = int64_t(H) * 2;
     a.N = I;
-    a.K = H;
-    hipError_t e = launch_tiles<false, Form::kGated>(
-        a, G, max_pairs, GatedOut{static_cast<uint16_t *>(act), nullptr}, "ll_expert_ffn gated", stream);
+    a.kbytes = H * 2;
+    auto tile_args = [&] {
+        TileArgs t{};
+        t.q = a.q;
+        t.ldq = a.ldq;
+        t.p = a.p;
+        t.p_expert = a.p_expert;
+        t.ldp = a.ldp;
+        t.N = a.N;
+        t.K = a.kbytes / 2;
+        return t;
+    };
+    const GatedOut gated{static_cast<uint16_t *>(act), nullptr};
+    hipError_t e = launch_cells<false, Form::kGated>(
+        a, G, max_pairs, gated, "ll_expert_ffn gated", stream, [&](const Groups &T, int64_t most) {
+            return launch_tiles<false, Form::kGated>(tile_args(), T, max_pairs, most, gated,
+                                                     "ll_expert_ffn gated tiles", stream);
+        });
     if (e != hipSuccess)
         return e;
     a.q = static_cast<const char *>(act);
@@ -770,9 +786,13 @@ hipError_t launch_ll_expert_ffn(int E, int R, int slots, int H, int I, int64_t m
     a.p_expert = int64_t(I) * H * 2;
     a.ldp = int64_t(I) * 2;
     a.N = H;
-    a.K = I;
-    return launch_tiles<false, Form::kPlain>(a, G, max_pairs, RowOut{static_cast<uint16_t *>(out)},
-                                             "ll_expert_ffn down", stream);
+    a.kbytes = I * 2;
+    const RowOut rows{static_cast<uint16_t *>(out)};
+    return launch_cells<false, Form::kPlain>(
+        a, G, max_pairs, rows, "ll_expert_ffn down", stream, [&](const Groups &T, int64_t most) {
+            return launch_tiles<false, Form::kPlain>(tile_args(), T, max_pairs, most, rows,
+                                                     "ll_expert_ffn down tiles", stream);
+        });
 }
 
 }  // namespace ep

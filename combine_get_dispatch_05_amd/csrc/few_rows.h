@@ -21,7 +21,40 @@ struct FewArgs {
     int N;                 // columns (I for the gated form)
     int kbytes;            // bytes of the inner dimension
     unsigned nt;           // column tiles
+    unsigned blocks;       // tile kernel: no tile from this block on
+    int active;            // groups that can hold rows, where fewer than all
 };
+
+// The j-th group that holds rows, or -1.  Every thread of the block takes part.
+template <int NTH>
+__device__ __forceinline__ int find_group(const Groups &G, int j)
+{
+    constexpr int W = NTH / kWave;
+    __shared__ int s[W], found;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (threadIdx.x == 0)
+        found = -1;
+    for (int g0 = 0, base = 0; g0 < G.num && j >= base; g0 += NTH) {
+        const int g = g0 + threadIdx.x;
+        const bool alive = g < G.num && group_rows(G, g) > 0;
+        const uint64_t m = wave_ballot(alive);
+        __syncthreads();
+        if (lane == 0)
+            s[wave] = __popcll(m);
+        __syncthreads();
+        int before = base;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const int v = s[w];
+            before += w < wave ? v : 0;
+            base += v;
+        }
+        if (alive && before + __popcll(m & lanemask_lt()) == j)
+            found = g;
+    }
+    __syncthreads();
+    return uniform(found);
+}
 
 // 32 bytes of a row for one K step: bytes [16 g, 16 g + 16) and 64 further on,
 // g = lane / 16.  Both operands use the same places, so their order inside the
@@ -52,7 +85,8 @@ __device__ __forceinline__ f32x4 mfma_step_bf16(const Frag &a, const Frag &b, f3
     return mfma_bf16(__builtin_bit_cast(bf16x8, a.hi), __builtin_bit_cast(bf16x8, b.hi), c);
 }
 
-// WN x WK waves: WN share out the columns, WK the K steps.  A wave holds NW
+// One block: kCols columns of one group, and of its rows every gridDim.y-th run of
+// 16 MT.  WN x WK waves: WN share out the columns, WK the K steps.  A wave holds NW
 // 16-column tiles (half gate, half up in the gated form) and MT 16-row tiles.
 template <bool FP8, int WN, int WK, int NW, int MT, Form F, class Epi>
 __global__ __launch_bounds__(WN *WK *kWave) void few_rows_kernel(FewArgs a, Groups G, Epi epi)
@@ -60,12 +94,19 @@ __global__ __launch_bounds__(WN *WK *kWave) void few_rows_kernel(FewArgs a, Grou
     constexpr int kCols = WN * (F == Form::kGated ? NW / 2 : NW) * 16;  // of a block
     constexpr int kWaveCols = kCols / WN;
     __shared__ f32x4 sums[WK > 1 ? (WK - 1) * WN * MT * NW * kWave : 1];
-    const int g = blockIdx.x / a.nt, tn = int(blockIdx.x % a.nt);
-    const int rows = group_rows(G, g);
-    if (rows == 0)
+    int g = blockIdx.x / a.nt;
+    const int tn = int(blockIdx.x % a.nt);
+    if (a.active < G.num) {
+        g = find_group<WN * WK * kWave>(G, g);
+        if (g < 0)
+            return;
+    }
+    const int rows = uniform(group_rows(G, g));
+    const int first = int(blockIdx.y) * 16 * MT, stride = int(gridDim.y) * 16 * MT;
+    if (first >= rows)
         return;
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = uniform(threadIdx.x >> 6);
     const int wn = wave % WN, wk = wave / WN;
     const int64_t start = group_start(G, g);
     const int e = group_expert(G, g);
@@ -89,7 +130,7 @@ __global__ __launch_bounds__(WN *WK *kWave) void few_rows_kernel(FewArgs a, Grou
     }
     const int steps = (a.kbytes + kStepBytes - 1) / kStepBytes;
     const int s0 = steps * wk / WK, s1 = steps * (wk + 1) / WK;
-    for (int m0 = 0; m0 < rows; m0 += 16 * MT) {
+    for (int m0 = first; m0 < rows; m0 += stride) {
         const char *qp[MT];
         const float *qs[MT];
 #pragma unroll
@@ -135,8 +176,8 @@ __global__ __launch_bounds__(WN *WK *kWave) void few_rows_kernel(FewArgs a, Grou
                 }
             }
         };
-        // two steps are in flight while two are used
-        constexpr int U = 2;
+        // U steps are in flight while U are used: as many as the registers hold
+        constexpr int U = NW + MT <= 3 ? 4 : NW + MT <= 5 && MT < 4 ? 2 : 1;
         Step cur[U], nxt[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -165,7 +206,7 @@ __global__ __launch_bounds__(WN *WK *kWave) void few_rows_kernel(FewArgs a, Grou
             }
             __syncthreads();
             if (wk == 0) {
-#pragma unroll
+#pragma unroll 1
                 for (int w = 0; w < WK - 1; ++w)
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
@@ -179,9 +220,73 @@ __global__ __launch_bounds__(WN *WK *kWave) void few_rows_kernel(FewArgs a, Grou
             epi.template store_block<MT, NW, WN, 16 * MT>(t, start, wk == 0, wn, 0, n0, a.N, acc, lane);
         else if (wk == 0)
             epi.store(t, start, m0, n0, a.N, acc, lane);
-        if (m0 + 16 * MT < rows)
+        if (m0 + stride < rows)
             __syncthreads();  // the sums are read before the next rows' are written
     }
+}
+
+// --------------------------------------------------------------- launches
+
+// Rows up to which a group takes this kernel: it reads the weight again (from L2)
+// for every 16 MT rows.
+constexpr int kFewRows = 64;
+
+template <bool FP8, int WN, int WK, int NW, int MT, Form F, class Epi>
+hipError_t launch_few_shape(FewArgs a, const Groups &G, int row_blocks, const Epi &epi, const char *what,
+                            hipStream_t stream)
+{
+    constexpr int cols = WN * (F == Form::kGated ? NW / 2 : NW) * 16;
+    a.nt = unsigned((a.N + cols - 1) / cols);
+    const int64_t blocks = int64_t(a.nt) * a.active;
+    if (blocks > kMaxTileBlocks || row_blocks > 65535)
+        return hipErrorInvalidValue;
+    if (log_enabled())
+        log_launch("%s: groups<=%d of %d N=%d K bytes=%d few rows %d cols=%d waves=%dx%d blocks=%lld x %d", what,
+                   a.active, G.num, a.N, a.kbytes, MT * 16, cols, WN, WK, (long long)blocks, row_blocks);
+    hipLaunchKernelGGL((few_rows_kernel<FP8, WN, WK, NW, MT, F, Epi>), dim3(unsigned(blocks), row_blocks),
+                       dim3(WN * WK * kWave), 0, stream, a, G, epi);
+    return hipGetLastError();
+}
+
+// avg: rows of an active group on average.  Blocks of 256 columns (128 gated)
+// where that makes one for every compute unit, else of 16, all eight waves
+// sharing out K: one token's eight experts of 768 x 2048 in 48 blocks took
+// %WIDE% us, in 384 %NARROW%.
+template <bool FP8, Form F, class Epi>
+hipError_t launch_few(FewArgs a, const Groups &G, int64_t avg, int row_blocks, const Epi &epi, const char *what,
+                      hipStream_t stream)
+{
+    if constexpr (!Epi::kBlockWide) {
+        const int wide = F == Form::kGated ? 128 : 256;
+        if (int64_t((a.N + wide - 1) / wide) * a.active * row_blocks < compute_units()) {
+            constexpr int NW = F == Form::kGated ? 2 : 1;
+            return avg <= 16 ? launch_few_shape<FP8, 1, 8, NW, 1, F>(a, G, row_blocks, epi, what, stream)
+                             : launch_few_shape<FP8, 1, 8, NW, 4, F>(a, G, row_blocks, epi, what, stream);
+        }
+    }
+    return avg <= 8 ? launch_few_shape<FP8, 4, 2, 4, 1, F>(a, G, row_blocks, epi, what, stream)
+                    : launch_few_shape<FP8, 4, 2, 4, 2, F>(a, G, row_blocks, epi, what, stream);
+}
+
+// The low-latency cells: groups of few rows by launch_few, the others by
+// tiles(G, most): both walk the groups on the device, which alone knows their
+// rows; most bounds the groups left for the tiles.
+template <bool FP8, Form F, class Epi, class Tiles>
+hipError_t launch_cells(FewArgs a, Groups G, int64_t max_pairs, const Epi &epi, const char *what,
+                        hipStream_t stream, Tiles tiles)
+{
+    a.active = int(max_pairs < G.num ? max_pairs : G.num);
+    const int64_t avg = max_pairs / a.active;
+    if (avg <= kFewRows / 2) {
+        Groups few = G;
+        few.max_rows = kFewRows;
+        hipError_t e = launch_few<FP8, F>(a, few, avg, 1, epi, what, stream);
+        if (e != hipSuccess || G.slots <= kFewRows || max_pairs <= kFewRows)
+            return e;
+        G.min_rows = kFewRows + 1;
+    }
+    const int64_t most = max_pairs / G.min_rows;
+    return tiles(G, most < G.num ? most : G.num);
 }
 
 }  // namespace ep

@@ -144,7 +144,7 @@ __global__ __launch_bounds__(NT) void fp8_tile_kernel(FewArgs a, Groups G, Epi e
     open_stages<ST>(steps, issue);
     for (;;) {
         block += gridDim.x;
-        const Tile next = find_tile<BM, NT>(G, block, a.nt);
+        const Tile next = block < a.blocks ? find_tile<BM, NT>(G, block, a.nt) : Tile{-1, 0, 0, 0};
         const Tile cur = t;
         at_height<BM>(cur.rows - cur.m0, [&](auto rows_tag) {
             constexpr int R = decltype(rows_tag)::value, MT = R / 32;
@@ -209,9 +209,9 @@ template <Form F, class Epi>
 hipError_t launch_fp8_tiles(FewArgs a, const Groups &G, int64_t rows, int64_t max_tiles, const Epi &epi,
                             const char *what, hipStream_t stream)
 {
-    const int bm = tile_rows(rows, G.num);
     const int cols = F == Form::kGated ? BN / 2 : BN;
     a.nt = unsigned((a.N + cols - 1) / cols);
+    const int bm = tile_rows(rows, max_tiles, a.nt);
     const int64_t mt = rows / bm + (max_tiles < rows ? max_tiles : rows);
     if (mt * a.nt > kMaxTileBlocks)
         return hipErrorInvalidValue;
@@ -222,55 +222,12 @@ hipError_t launch_fp8_tiles(FewArgs a, const Groups &G, int64_t rows, int64_t ma
                    G.num, a.N, a.kbytes, bm, BN, (long long)mt * a.nt);
     const int64_t cus = compute_units(), all = blocks_for_tiles(mt * a.nt);
     const dim3 grid(unsigned(all < cus ? all : cus));
+    a.blocks = unsigned(all);
     if (bm == 256)
         hipLaunchKernelGGL((fp8_tile_kernel<256, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
     else
         hipLaunchKernelGGL((fp8_tile_kernel<64, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
     return hipGetLastError();
-}
-
-template <int WN, int WK, int NW, int MT, Form F, class Epi>
-hipError_t launch_fp8_few(FewArgs a, const Groups &G, const Epi &epi, const char *what,
-                          hipStream_t stream)
-{
-    constexpr int cols = WN * (F == Form::kGated ? NW / 2 : NW) * 16;
-    a.nt = unsigned((a.N + cols - 1) / cols);
-    const int64_t blocks = int64_t(a.nt) * G.num;
-    if (blocks > kMaxTileBlocks)
-        return hipErrorInvalidValue;
-    if (log_enabled())
-        log_launch("%s: groups=%d N=%d K=%d few rows %d cols=%d waves=%dx%d blocks=%lld", what, G.num,
-                   a.N, a.kbytes, MT * 16, cols, WN, WK, (long long)blocks);
-    hipLaunchKernelGGL((few_rows_kernel<true, WN, WK, NW, MT, F, Epi>), dim3(unsigned(blocks)),
-                       dim3(WN * WK * kWave), 0, stream, a, G, epi);
-    return hipGetLastError();
-}
-
-constexpr int kFewRows = 64;  // groups of at most this many rows take the few-rows kernel
-
-// Groups of few rows by one kernel, the others by the tile kernel: both walk
-// the groups on the device, which alone knows their rows.
-template <Form F, class Epi>
-hipError_t launch_fp8_groups(const FewArgs &a, Groups G, int64_t max_pairs, const Epi &epi,
-                             const char *what, hipStream_t stream)
-{
-    const int64_t avg = max_pairs / G.num;
-    const bool few = avg <= kFewRows / 2;
-    if (few) {
-        Groups F1 = G;
-        F1.max_rows = kFewRows;
-        hipError_t e = avg <= 8
-            ? launch_fp8_few<4, 2, 4, 1, F>(a, F1, epi, what, stream)
-            : launch_fp8_few<4, 2, 4, 2, F>(a, F1, epi, what, stream);
-        if (e != hipSuccess)
-            return e;
-        if (G.slots <= kFewRows || max_pairs <= kFewRows)
-            return hipSuccess;
-        G.min_rows = kFewRows + 1;
-    }
-    // the groups that the tile kernel is left with hold at least min_rows each
-    const int64_t groups = max_pairs / G.min_rows;
-    return launch_fp8_tiles<F>(a, G, max_pairs, groups < G.num ? groups : G.num, epi, what, stream);
 }
 
 }  // namespace
@@ -289,10 +246,13 @@ hipError_t launch_fp8_product(int64_t M, int N, int K, const void *a_q, const fl
     a.N = N;
     a.kbytes = K;
     const RowOut epi{static_cast<uint16_t *>(out)};
-    if (M <= 16)
-        return launch_fp8_few<1, 8, 1, 1, Form::kPlain>(a, G, epi, "fp8_product", stream);
-    if (M <= kFewRows)
-        return launch_fp8_few<1, 8, 1, 4, Form::kPlain>(a, G, epi, "fp8_product", stream);
+    a.active = 1;
+    // up to 64 rows the weight's bytes are the cost; past that the few-rows kernel,
+    // with a block for each 64 rows, still wins where tiles would leave most
+    // compute units idle (333 x 1000 x 1152: %FEW% us, in 24 tiles %TILES%)
+    const int64_t chunks = (M + kFewRows - 1) / kFewRows;
+    if (M <= kFewRows || chunks * ((N + BN - 1) / BN) < compute_units() / 2)
+        return launch_few<true, Form::kPlain>(a, G, M, int(M <= 16 ? 1 : chunks), epi, "fp8_product", stream);
     return launch_fp8_tiles<Form::kPlain>(a, G, M, 1, epi, "fp8_product", stream);
 }
 
@@ -314,9 +274,12 @@ hipError_t launch_ll_expert_ffn_fp8(int E, int R, int slots, int H, int I, int64
     a.ldp = H;
     a.N = I;
     a.kbytes = H;
-    hipError_t e = launch_fp8_groups<Form::kGated>(
-        a, G, max_pairs, GatedFp8Out{static_cast<uint8_t *>(act_q), act_scale},
-        "ll_expert_ffn_fp8 gated", stream);
+    const GatedFp8Out gated{static_cast<uint8_t *>(act_q), act_scale};
+    hipError_t e = launch_cells<true, Form::kGated>(
+        a, G, max_pairs, gated, "ll_expert_ffn_fp8 gated", stream, [&](const Groups &T, int64_t most) {
+            return launch_fp8_tiles<Form::kGated>(a, T, max_pairs, most, gated, "ll_expert_ffn_fp8 gated tiles",
+                                                  stream);
+        });
     if (e != hipSuccess)
         return e;
     a.q = static_cast<const char *>(act_q);
@@ -329,8 +292,12 @@ hipError_t launch_ll_expert_ffn_fp8(int E, int R, int slots, int H, int I, int64
     a.ldp = I;
     a.N = H;
     a.kbytes = I;
-    return launch_fp8_groups<Form::kPlain>(a, G, max_pairs, RowOut{static_cast<uint16_t *>(out)},
-                                           "ll_expert_ffn_fp8 down", stream);
+    const RowOut rows{static_cast<uint16_t *>(out)};
+    return launch_cells<true, Form::kPlain>(
+        a, G, max_pairs, rows, "ll_expert_ffn_fp8 down", stream, [&](const Groups &T, int64_t most) {
+            return launch_fp8_tiles<Form::kPlain>(a, T, max_pairs, most, rows, "ll_expert_ffn_fp8 down tiles",
+                                                  stream);
+        });
 }
 
 }  // namespace ep

@@ -329,6 +329,7 @@ struct TileArgs {
     int64_t ldp;              // bytes of a weight row
     int N, K;                 // columns (I for the gated form) and inner length
     unsigned nt;              // column tiles
+    unsigned blocks;          // no tile from this block on
 };
 
 // ------------------------------------------------------------------ tiles
@@ -666,8 +667,5 @@ struct RowOut {
 // tiles can each be one longer than an eighth.
 inline int64_t blocks_for_tiles(int64_t tiles) { return (tiles / kXcds + 2) * kXcds; }
 
-// Compute units of the current device: the blocks of a launch whose blocks
-// each fill one and work through tiles.
-int compute_units();
 
 }  // namespace ep

@@ -287,9 +287,20 @@ __global__ __launch_bounds__(1024) void sum_parts_kernel(const float *__restrict
     __shared__ float s[16][64];
     const int col = blockIdx.x * 64 + (threadIdx.x & 63), g = threadIdx.x >> 6;
     float v = 0.0f;
-    if (col < H)
-        for (int p = g; p < n; p += 16)
+    if (col < H) {
+        int p = g;
+        for (; p + 112 < n; p += 128) {  // eight loads in flight
+            float l[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                l[i] = parts[int64_t(p + 16 * i) * H + col];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v += l[i];
+        }
+        for (; p < n; p += 16)
             v += parts[int64_t(p) * H + col];
+    }
     s[g][threadIdx.x & 63] = v;
     __syncthreads();
     if (g == 0 && col < H) {
