@@ -336,38 +336,61 @@ __global__ __launch_bounds__(NT) void tile_kernel(TileArgs a, Groups G, Epi epi)
             });
         }
     };
-    auto issue = [&](int s, int part) {
-        if (part == 1)
-            qs.template issue<true>(stage(s) + kP, wave, int64_t(s) * kStepBytes, kbytes);
-        else if constexpr (PCOL)
-            pc.issue(stage(s), tid, wave, pw, a.ldp, s * 64, a.K);
-        else
-            pr.template issue<true>(stage(s), tid, wave, int64_t(s) * kStepBytes, kbytes);
+    auto issue = [&](int part, int s) {
+        const int64_t kb = int64_t(s) * kStepBytes;
+        constexpr int JP = PR::J / 2, JQ = QS::J > 1 ? QS::J / 2 : 1;
+        if (part >= 2) {  // halves of the chunks, or all of them in the first
+            if (part == 2)
+                qs.template issue<true, 0, QS::J / JQ>(stage(s) + kP, tid, wave, kb, kbytes);
+            else if (QS::J > 1)
+                qs.template issue<true, 1, QS::J / JQ>(stage(s) + kP, tid, wave, kb, kbytes);
+        } else if constexpr (PCOL) {
+            if (part == 0)
+                pc.template issue<0, JP>(stage(s), tid, wave, pw, a.ldp, s * 64, a.K);
+            else
+                pc.template issue<JP, JP>(stage(s), tid, wave, pw, a.ldp, s * 64, a.K);
+        } else {
+            if (part == 0)
+                pr.template issue<true, 0, 2>(stage(s), tid, wave, kb, kbytes);
+            else
+                pr.template issue<true, 1, 2>(stage(s), tid, wave, kb, kbytes);
+        }
     };
-    auto frag_p = [&](int s, int i, int ks) {
-        const int c = wn * 64 + i * 16;
-        if constexpr (PCOL)
-            return PC::frag(stage(s), c, ks, lane);
+    auto open = [&] {
+        if constexpr (ST == 2)
+            open_pair(steps, issue);
         else
-            return PR::frag(stage(s), c, ks, lane);
+            open_ring<ST>(steps, issue);
     };
-
     unsigned block = blockIdx.x;
     Tile t = find_tile<BM, NT>(G, block, a.nt);
     if (t.group < 0)
         return;
     find_rows(t);
     set_up(t);
-    open_stages<ST>(steps, issue);
+    open();
     auto work = [&](auto rows_tag) {
         constexpr int R = decltype(rows_tag)::value, MT = R / 32;  // rows computed, row tiles of a wave
+        const int ln = here(lane);  // the LDS addresses of one height at a time
+        auto frag_p = [&](int s, int i, int ks) {
+            const int c = wn * 64 + i * 16;
+            if constexpr (PCOL)
+                return PC::frag(stage(s), c, ks, ln);
+            else
+                return PR::frag(stage(s), c, ks, ln);
+        };
         auto frag_q = [&](int s, int m, int ks) {
-            return QS::frag(stage(s) + kP, wm * (R / 2) + m * 16, ks, lane);
+            return QS::frag(stage(s) + kP, wm * (R / 2) + m * 16, ks, ln);
         };
         f32x4 acc[MT][4] = {};
-        Bf16Phases<MT, decltype(frag_p), decltype(frag_q)> ph{acc, frag_p, frag_q};
-        take_turns<decltype(ph)::kPhases, ST, PR::J + QS::J>(
-            steps, wm, issue, [&](int s, int i) { ph.read(s, i); }, [&](int, int i) { ph.compute(i); });
+        using Phases = Bf16Phases<MT, decltype(frag_p), decltype(frag_q)>;
+        Phases ph{acc, frag_p, frag_q};
+        auto read = [&](int s, int i) { ph.read(s, i); };
+        auto compute = [&](int, int i) { ph.compute(i); };
+        if constexpr (ST == 2)
+            turns_on_pair<Phases::kPhases, PR::J>(steps, wm, issue, read, compute);
+        else
+            turns_on_ring<Phases::kPhases, ST, PR::J + QS::J>(steps, wm, issue, read, compute);
         return [&, acc](const Tile &c) mutable {
             const int64_t start = group_start(G, c.group);
             const int n0 = c.n * (F == Form::kGated ? BN / 2 : BN) + wn * (F == Form::kGated ? 32 : 64);
@@ -386,7 +409,7 @@ __global__ __launch_bounds__(NT) void tile_kernel(TileArgs a, Groups G, Epi epi)
         auto finish = [&](auto store) {
             if (next.group >= 0) {
                 set_up(next);
-                open_stages<ST>(steps, issue);
+                open();
             }
             store(cur);
         };
@@ -414,17 +437,19 @@ __global__ __launch_bounds__(NT) void weight_grad_kernel(GradArgs a)
 {
     constexpr int B = 256;
     using CS = ColStage<B, NT>;
-    // Each wave keeps the stage's 64 picked rows to itself, a stage ahead, loaded
-    // straight into LDS like the stage: held in registers their copies from
-    // stage to stage waited for the loads (46 us a tile of 1024 rows, 29 without
-    // picking).  Slots 0 and 1 alternate, slot 2 is a tile's first stage.
-    constexpr int kSlot = kWave * 4;
-    __shared__ __attribute__((aligned(128))) char smem[4 * CS::kBytes + NT / kWave * 3 * kSlot];
+    // Each wave keeps the stages' 64 picked rows to itself, three stages ahead,
+    // loaded straight into LDS like the stages: held in registers their copies
+    // from stage to stage waited for the loads (46 us a tile of 1024 rows, 29
+    // without picking).  Slots 0 to 3 go round; a tile's first three stages have
+    // slots of their own, filled while the tile before is worked on, for which
+    // tiles take turns with two sets.
+    constexpr int kSlot = kWave * 4, kSlots = 10;
+    __shared__ __attribute__((aligned(128))) char smem[4 * CS::kBytes + NT / kWave * kSlots * kSlot];
     lds_char *lds = (lds_char *)smem;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = uniform(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
-    lds_char *picks = lds + 4 * CS::kBytes + wave * 3 * kSlot;
+    lds_char *picks = lds + 4 * CS::kBytes + wave * kSlots * kSlot;
     const unsigned per = a.mt * a.nt, total = per * unsigned(a.experts);
 
     struct Place {
@@ -448,40 +473,57 @@ __global__ __launch_bounds__(NT) void weight_grad_kernel(GradArgs a)
 
     CS qs, ps;
     Place t;
-    int steps = 0, idx[CS::J];
+    int steps = 0, set = 0;
+    auto slot = [&](int s) { return s < 3 ? 4 + set * 3 + s : s & 3; };
     auto stage = [&](int s) -> lds_char * { return lds + (s & 1) * 2 * CS::kBytes; };
-    auto issue = [&](int s, int part) {
-        if (part == 0) {
-            const lds_char *from = picks + (s == 0 ? 2 : s & 1) * kSlot;
+    auto issue = [&](int part, int s) {
+        constexpr int JH = CS::J / 2;
+        int idx[CS::J];
+        if (part < 2 ? PG : QG) {
+            const lds_char *from = picks + slot(s) * kSlot;
 #pragma unroll
-            for (int j = 0; j < CS::J; ++j)  // both operands' chunks of a thread lie in the same k rows
+            for (int j = 0; j < CS::J; ++j)
                 idx[j] = *(const __attribute__((address_space(3))) int *)(from + CS::k_of(tid, j) * 4) & kRowMask;
-            if (s + 1 < steps)
-                pick(t, s + 1, (s + 1) & 1);
-            if constexpr (PG)
-                ps.issue(stage(s), tid, wave, a.p, a.ldp, s * 64, t.rows, idx);
-            else
-                ps.issue(stage(s), tid, wave, a.p + t.start * a.ldp, a.ldp, s * 64, t.rows);
-        } else {
-            if constexpr (QG)
-                qs.issue(stage(s) + CS::kBytes, tid, wave, a.q, a.ldq, s * 64, t.rows, idx);
-            else
-                qs.issue(stage(s) + CS::kBytes, tid, wave, a.q + t.start * a.ldq, a.ldq, s * 64, t.rows);
         }
+        const char *p = a.p + (PG ? 0 : t.start * a.ldp), *q = a.q + (QG ? 0 : t.start * a.ldq);
+        lds_char *pb = stage(s), *qb = pb + CS::kBytes;
+        auto half = [&](CS &c, auto first, lds_char *to, const char *from, int64_t ld, auto gathered) {
+            constexpr int J0 = decltype(first)::value * JH;
+            if constexpr (decltype(gathered)::value != 0)
+                c.template issue<J0, JH>(to, tid, wave, from, ld, s * 64, t.rows, idx);
+            else
+                c.template issue<J0, JH>(to, tid, wave, from, ld, s * 64, t.rows);
+        };
+        if (part == 0 && s + 1 < steps && s >= 2)
+            pick(t, s + 1, slot(s + 1));  // used a stage from now: this is phase 2 of stage s - 2
+        if (part == 0)
+            half(ps, Rows<0>{}, pb, p, a.ldp, Rows<PG>{});
+        else if (part == 1)
+            half(ps, Rows<1>{}, pb, p, a.ldp, Rows<PG>{});
+        else if (part == 2)
+            half(qs, Rows<0>{}, qb, q, a.ldq, Rows<QG>{});
+        else
+            half(qs, Rows<1>{}, qb, q, a.ldq, Rows<QG>{});
+    };
+    auto pick_first = [&](const Place &next, int to) {
+#pragma unroll
+        for (int s = 0; s < 3; ++s)
+            if (s * 64 < next.rows)
+                pick(next, s, 4 + to * 3 + s);
     };
     auto set_up = [&](const Place &next) {  // its first rows have been picked and have landed
         t = next;
         steps = (t.rows + 63) / 64;
         qs.init(tid, int(t.tm) * B, a.M);
         ps.init(tid, int(t.tn) * B, a.N);
-        open_stages<2>(steps, issue);
+        if (steps > 0)
+            open_pair(steps, issue);
     };
     unsigned block = blockIdx.x;
     if (block >= total)
         return;
     const Place first = place(block);
-    if (first.rows > 0)
-        pick(first, 0, 2);
+    pick_first(first, 0);
     landed<0>();
     set_up(first);
     for (;;) {
@@ -490,8 +532,7 @@ __global__ __launch_bounds__(NT) void weight_grad_kernel(GradArgs a)
         Place next = cur;
         if (block < total) {
             next = place(block);
-            if (next.rows > 0)
-                pick(next, 0, 2);
+            pick_first(next, set ^ 1);
         }
         auto frag_p = [&](int s, int i, int ks) { return CS::frag(stage(s), wn * 64 + i * 16, ks, lane); };
         auto frag_q = [&](int s, int m, int ks) {
@@ -499,8 +540,11 @@ __global__ __launch_bounds__(NT) void weight_grad_kernel(GradArgs a)
         };
         f32x4 acc[8][4] = {};
         Bf16Phases<8, decltype(frag_p), decltype(frag_q)> ph{acc, frag_p, frag_q};
-        take_turns<4, 2, 0>(
+        // (the pick sent off with P makes one load more in flight than P's: the
+        // wait for all but P's reaches it too, which is in time)
+        turns_on_pair<4, CS::J>(
             steps, wm, issue, [&](int s, int i) { ph.read(s, i); }, [&](int, int i) { ph.compute(i); });
+        set ^= 1;
         if (block < total)
             set_up(next);
         uint16_t *o = a.out + int64_t(cur.e) * a.M * a.N;

@@ -21,7 +21,6 @@ struct FewArgs {
     int N;                 // columns (I for the gated form)
     int kbytes;            // bytes of the inner dimension
     unsigned nt;           // column tiles
-    unsigned blocks;       // tile kernel: no tile from this block on
     int active;            // groups that can hold rows, where fewer than all
 };
 

@@ -71,8 +71,9 @@ struct GatedFp8Out {
     }
 };
 
-// Tiles of BM rows of one group by BN columns: the bf16 tile kernel's loop over
-// tiles, with K steps of one scale block.  The step's scales are staged behind
+// BM rows of one group by BN columns: the bf16 tile kernel's loop with K steps of
+// one scale block, a tile a block (working through tiles takes registers that
+// the scaled sums need).  The step's scales are staged behind
 // the rows, one load a wave, so that every wave counts the same loads: waves 0
 // to 3 the BM token scales (some twice where BM is 64), the others the two
 // weight scales of the tile: its column blocks, or its gate and its up block.
@@ -120,14 +121,27 @@ __global__ __launch_bounds__(NT) void fp8_tile_kernel(FewArgs a, Groups G, Epi e
             sq = reinterpret_cast<const char *>(a.p_scale + e * a.p_scales + int64_t(nb) * steps);
         }
     };
-    auto issue = [&](int s, int part) {
+    auto issue = [&](int part, int s) {
+        const int64_t kb = int64_t(s) * kStepBytes;
+        constexpr int JQ = QS::J > 1 ? 2 : 1;
         lds_char *b = stage(s);
-        if (part == 0) {
-            pr.template issue<false>(b, tid, wave, int64_t(s) * kStepBytes, a.kbytes);
-        } else {
-            qs.template issue<false>(b + kP, tid, wave, int64_t(s) * kStepBytes, a.kbytes);
+        if (part == 0)
+            pr.template issue<false, 0, 2>(b, tid, wave, kb, a.kbytes);
+        else if (part == 1)
+            pr.template issue<false, 1, 2>(b, tid, wave, kb, a.kbytes);
+        else if (part == 2)
+            qs.template issue<false, 0, JQ>(b + kP, tid, wave, kb, a.kbytes);
+        else {
+            if (QS::J > 1)
+                qs.template issue<false, 1, JQ>(b + kP, tid, wave, kb, a.kbytes);
             load_lds4(sq + int64_t(s) * 4, b + sdst);
         }
+    };
+    auto open = [&] {
+        if constexpr (ST == 2)
+            open_pair(steps, issue);
+        else
+            open_ring<ST>(steps, issue);
     };
     auto frag = [&](const lds_char *base, int r) {
         Frag f;
@@ -136,73 +150,64 @@ __global__ __launch_bounds__(NT) void fp8_tile_kernel(FewArgs a, Groups G, Epi e
         return f;
     };
 
-    unsigned block = blockIdx.x;
-    Tile t = find_tile<BM, NT>(G, block, a.nt);
-    if (t.group < 0)
+    const Tile cur = find_tile<BM, NT>(G, blockIdx.x, a.nt);
+    if (cur.group < 0)
         return;
-    set_up(t);
-    open_stages<ST>(steps, issue);
-    for (;;) {
-        block += gridDim.x;
-        const Tile next = block < a.blocks ? find_tile<BM, NT>(G, block, a.nt) : Tile{-1, 0, 0, 0};
-        const Tile cur = t;
-        at_height<BM>(cur.rows - cur.m0, [&](auto rows_tag) {
-            constexpr int R = decltype(rows_tag)::value, MT = R / 32;
-            constexpr int MQ = 2, PH = MT / MQ;  // two row tiles a phase
-            f32x4 acc[MT][4] = {};
-            Frag pf[4], qf[MQ];
-            float sc[MQ], c0 = 0.0f, c1 = 0.0f;
-            take_turns<PH, ST, PR::J + QS::J + 1>(
-                steps, wm, issue,
-                [&](int s, int ph) {
-                    const lds_char *pb = stage(s), *qb = pb + kP;
-                    if (ph == 0) {
-                        lds_float *w = (lds_float *)(qb + kQ + BM * 4);
-                        c0 = w[F == Form::kGated ? 0 : wn >> 1];
-                        c1 = F == Form::kGated ? w[1] : c0;
+    set_up(cur);
+    open();
+    at_height<BM>(cur.rows - cur.m0, [&](auto rows_tag) {
+        constexpr int R = decltype(rows_tag)::value, MT = R / 32;
+        constexpr int MQ = 2, PH = MT / MQ;  // two row tiles a phase
+        f32x4 acc[MT][4] = {};
+        Frag pf[4], qf[MQ];
+        float sc[MQ], c0 = 0.0f, c1 = 0.0f;
+        auto read = [&](int s, int ph) {
+            const lds_char *pb = stage(s), *qb = pb + kP;
+            if (ph == 0) {
+                lds_float *w = (lds_float *)(qb + kQ + BM * 4);
+                c0 = w[F == Form::kGated ? 0 : wn >> 1];
+                c1 = F == Form::kGated ? w[1] : c0;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            pf[i] = frag(pb, wn * 64 + i * 16 + (lane & 15));
-                    }
+                for (int i = 0; i < 4; ++i)
+                    pf[i] = frag(pb, wn * 64 + i * 16 + (lane & 15));
+            }
 #pragma unroll
-                    for (int m = 0; m < MQ; ++m) {
-                        const int r = wm * (R / 2) + (ph * MQ + m) * 16 + (lane & 15);
-                        qf[m] = frag(qb, r);
-                        sc[m] = *(lds_float *)(qb + kQ + r * 4);
-                    }
-                },
-                [&](int, int ph) {
+            for (int m = 0; m < MQ; ++m) {
+                const int r = wm * (R / 2) + (ph * MQ + m) * 16 + (lane & 15);
+                qf[m] = frag(qb, r);
+                sc[m] = *(lds_float *)(qb + kQ + r * 4);
+            }
+        };
+        auto compute = [&](int, int ph) {
 #pragma unroll
-                    for (int m = 0; m < MQ; ++m) {
-                        hold(qf[m].lo);
-                        hold(qf[m].hi);
-                    }
+            for (int m = 0; m < MQ; ++m) {
+                hold(qf[m].lo);
+                hold(qf[m].hi);
+            }
 #pragma unroll
-                    for (int m = 0; m < MQ; ++m) {
-                        const float s0 = sc[m] * c0, s1 = F == Form::kGated ? sc[m] * c1 : s0;
+            for (int m = 0; m < MQ; ++m) {
+                const float s0 = sc[m] * c0, s1 = F == Form::kGated ? sc[m] * c1 : s0;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            acc[ph * MQ + m][i] += mfma_step_fp8(pf[i], qf[m]) * (i < 2 ? s0 : s1);
-                    }
+                for (int i = 0; i < 4; ++i)
+                    acc[ph * MQ + m][i] += mfma_step_fp8(pf[i], qf[m]) * (i < 2 ? s0 : s1);
+            }
 #pragma unroll
-                    for (int m = 0; m < MQ; ++m)
+            for (int m = 0; m < MQ; ++m)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            hold(acc[ph * MQ + m][i]);
-                });
-            const int64_t start = group_start(G, cur.group);
-            const int n0 = cur.n * (F == Form::kGated ? BN / 2 : BN) + wn * (F == Form::kGated ? 32 : 64);
-            if constexpr (Epi::kBlockWide)
-                epi.template store_block<MT, 4, 4, R>(cur, start, true, wn, wm * (R / 2), n0, a.N, acc, lane);
-            else
-                epi.store(cur, start, cur.m0 + wm * (R / 2), n0, a.N, acc, lane);
-        });
-        if (next.group < 0)
-            break;
-        set_up(next);
-        open_stages<ST>(steps, issue);
-        t = next;
-    }
+                for (int i = 0; i < 4; ++i)
+                    hold(acc[ph * MQ + m][i]);
+        };
+        if constexpr (ST == 2)
+            turns_on_pair<PH, PR::J>(steps, wm, issue, read, compute);
+        else
+            turns_on_ring<PH, ST, PR::J + QS::J + 1>(steps, wm, issue, read, compute);
+        const int64_t start = group_start(G, cur.group);
+        const int n0 = cur.n * (F == Form::kGated ? BN / 2 : BN) + wn * (F == Form::kGated ? 32 : 64);
+        if constexpr (Epi::kBlockWide)
+            epi.template store_block<MT, 4, 4, R>(cur, start, true, wn, wm * (R / 2), n0, a.N, acc, lane);
+        else
+            epi.store(cur, start, cur.m0 + wm * (R / 2), n0, a.N, acc, lane);
+    });
 }
 
 template <Form F, class Epi>
@@ -220,9 +225,7 @@ hipError_t launch_fp8_tiles(FewArgs a, const Groups &G, int64_t rows, int64_t ma
     if (log_enabled())
         log_launch("%s: rows<=%lld groups=%d N=%d K=%d tile=%dx%d blocks=%lld", what, (long long)rows,
                    G.num, a.N, a.kbytes, bm, BN, (long long)mt * a.nt);
-    const int64_t cus = compute_units(), all = blocks_for_tiles(mt * a.nt);
-    const dim3 grid(unsigned(all < cus ? all : cus));
-    a.blocks = unsigned(all);
+    const dim3 grid(unsigned(blocks_for_tiles(mt * a.nt)));
     if (bm == 256)
         hipLaunchKernelGGL((fp8_tile_kernel<256, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
     else

@@ -89,6 +89,22 @@ __device__ __forceinline__ void landed()
     asm volatile("s_waitcnt vmcnt(%0)" : : "i"(N) : "memory");
 }
 
+// Ties a value to its place among the barriers: matrix instructions touch no
+// memory, so only what they read keeps them from being moved across one.
+template <class T>
+__device__ __forceinline__ void hold(T &v)
+{
+    asm volatile("" : "+v"(v));
+}
+
+// A copy whose uses are computed where they stand: what only a last, partial stage
+// needs would otherwise be kept in registers through the whole loop.
+__device__ __forceinline__ int here(int v)
+{
+    hold(v);
+    return v;
+}
+
 constexpr int kStepBytes = 128;  // K bytes of one stage
 
 // Row-contiguous operand, ROWS rows staged by NT threads.  LDS row r holds its
@@ -99,7 +115,12 @@ struct RowStage {
     static constexpr int J = ROWS * 8 / NT;
     static constexpr int kBytes = ROWS * kStepBytes;
     const char *ptr[J];
-    int cb[J];  // byte of the chunk inside the K step
+    // byte of the thread's j-th chunk inside the K step
+    static __device__ __forceinline__ int byte_of(int tid, int j)
+    {
+        const int q = j * NT + tid;
+        return ((q & 7) ^ ((q >> 4) & 7)) * 16;
+    }
 
     // row_ptr(j, r): the address of LDS row r (this thread's j-th) at k = 0 (any valid row for rows
     // past the end: their results are never stored).
@@ -108,24 +129,25 @@ struct RowStage {
     {
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const int q = j * NT + tid;
-            const int r = q >> 3;
-            cb[j] = ((q & 7) ^ ((r >> 1) & 7)) * 16;
-            ptr[j] = row_ptr(j, r) + cb[j];
+            ptr[j] = row_ptr(j, (j * NT + tid) >> 3) + byte_of(tid, j);
         }
     }
     // Stage K bytes [kb, kb + 128); kbytes: all K bytes of the operand (a whole
     // number of steps where TAIL is false).
-    template <bool TAIL>
-    __device__ __forceinline__ void issue(lds_char *base, int wave, int64_t kb, int64_t kbytes)
+    // J0, JS: this thread's chunks J0, J0 + JS, ...
+    template <bool TAIL, int J0 = 0, int JS = 1>
+    __device__ __forceinline__ void issue(lds_char *base, int tid, int wave, int64_t kb, int64_t kbytes)
     {
-        const bool whole = !TAIL || kb + kStepBytes <= kbytes;
+        if (!TAIL || kb + kStepBytes <= kbytes) {
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const char *p = ptr[j] + kb;
-            if (!whole && kb + cb[j] >= kbytes)
-                p = reinterpret_cast<const char *>(kZero16);
-            load_lds16(p, base + (j * NT + wave * kWave) * 16);
+            for (int j = J0; j < J; j += JS)
+                load_lds16(ptr[j] + kb, base + (j * NT + wave * kWave) * 16);
+        } else {
+            tid = here(tid);
+#pragma unroll
+            for (int j = J0; j < J; j += JS)
+                load_lds16(kb + byte_of(tid, j) >= kbytes ? reinterpret_cast<const char *>(kZero16) : ptr[j] + kb,
+                           base + (j * NT + wave * kWave) * 16);
         }
     }
     // Chunk ch (0..7) of LDS row r.
@@ -159,22 +181,21 @@ struct NearRowStage {
         for (int j = 0; j < J; ++j) {
             const int q = j * NT + tid;
             const int r = q >> 3;
-            off[j] = row_off(j, r) + ((q & 7) ^ ((r >> 1) & 7)) * 16;
+            off[j] = row_off(j, r) + RowStage<ROWS, NT>::byte_of(tid, j);
         }
     }
-    template <bool TAIL>
+    template <bool TAIL, int J0 = 0, int JS = 1>
     __device__ __forceinline__ void issue(lds_char *lds, int tid, int wave, int64_t kb, int64_t kbytes)
     {
         if (!TAIL || kb + kStepBytes <= kbytes) {
 #pragma unroll
-            for (int j = 0; j < J; ++j)
+            for (int j = J0; j < J; j += JS)
                 load_lds16(base + kb, off[j], lds + (j * NT + wave * kWave) * 16);
         } else {
+            tid = here(tid);
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const int q = j * NT + tid;
-                const int cb = ((q & 7) ^ ((q >> 4) & 7)) * 16;
-                load_lds16(kb + cb >= kbytes ? reinterpret_cast<const char *>(kZero16) : base + kb + off[j],
+            for (int j = J0; j < J; j += JS) {
+                load_lds16(kb + RowStage<ROWS, NT>::byte_of(tid, j) >= kbytes ? reinterpret_cast<const char *>(kZero16) : base + kb + off[j],
                            lds + (j * NT + wave * kWave) * 16);
             }
         }
@@ -212,19 +233,22 @@ struct ColStage {
         }
     }
     // Rows k0 .. k0 + 63 of memory, those past kn as zeros; row 0 at base, ld
-    // bytes apart.
+    // bytes apart.  J0, JN: this thread's chunks J0 .. J0 + JN - 1 (the first half
+    // of them is the first half of the rows).
+    template <int J0 = 0, int JN = J>
     __device__ __forceinline__ void issue(lds_char *lds, int tid, int wave, const char *base, int64_t ld,
                                           int k0, int kn)
     {
         const char *first = uniform(base + k0 * ld);
         if (k0 + 64 <= kn) {
 #pragma unroll
-            for (int j = 0; j < J; ++j)
+            for (int j = J0; j < J0 + JN; ++j)
                 load_lds16(first, uint32_t(k_of(tid, j)) * uint32_t(ld) + cb[j],
                            lds + (j * NT + wave * kWave) * 16);
         } else {
+            tid = here(tid);
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
+            for (int j = J0; j < J0 + JN; ++j) {
                 const int k = k_of(tid, j);
                 load_lds16(k0 + k < kn ? first + k * ld + cb[j] : reinterpret_cast<const char *>(kZero16),
                            lds + (j * NT + wave * kWave) * 16);
@@ -232,16 +256,21 @@ struct ColStage {
         }
     }
     // The same with row[j] the memory row of this thread's j-th chunk.
+    template <int J0 = 0, int JN = J>
     __device__ __forceinline__ void issue(lds_char *lds, int tid, int wave, const char *base, int64_t ld,
                                           int k0, int kn, const int (&row)[J])
     {
-        const bool whole = k0 + 64 <= kn;
+        if (k0 + 64 <= kn) {
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const char *p = base + row[j] * ld + cb[j];
-            if (!whole && k0 + k_of(tid, j) >= kn)
-                p = reinterpret_cast<const char *>(kZero16);
-            load_lds16(p, lds + (j * NT + wave * kWave) * 16);
+            for (int j = J0; j < J0 + JN; ++j)
+                load_lds16(base + row[j] * ld + cb[j], lds + (j * NT + wave * kWave) * 16);
+        } else {
+            tid = here(tid);
+#pragma unroll
+            for (int j = J0; j < J0 + JN; ++j)
+                load_lds16(k0 + k_of(tid, j) < kn ? base + row[j] * ld + cb[j]
+                                                  : reinterpret_cast<const char *>(kZero16),
+                           lds + (j * NT + wave * kWave) * 16);
         }
     }
     // Fragment of 16 columns from c0 and the 32 k values of half ks: lane l
@@ -501,42 +530,41 @@ __device__ __forceinline__ void turn()
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// Ties a value to its place among the barriers: matrix instructions touch no
-// memory, so only what they read keeps them from being moved across one.
-template <class T>
-__device__ __forceinline__ void hold(T &v)
-{
-    asm volatile("" : "+v"(v));
-}
-
 // The K loop.  A stage is worked off in PH phases, each of them a read half
-// (read(s, ph): LDS reads, and the loads of stage s + ST - 1) and a compute half
+// (read(s, ph): LDS reads, and loads of later stages) and a compute half
 // (compute(s, ph): matrix instructions only), with a barrier after each; the
 // second group runs one half behind the first, so one group reads while the
-// other computes.  One stage in turn (8192 x 4096 x 7168 bf16, 256 x 256 tiles):
-// 1454 TFLOP/s, against 1153 with both groups in step and one barrier a stage.
+// other computes.  (8192 x 4096 x 7168 bf16, 256 x 256 tiles: 1454 TFLOP/s,
+// against 1153 with both groups in step and one barrier a stage.)
 //
-// Stage s + 1 is waited for (all but the loads of later stages, LOADS each) in
-// the read half of stage s's last phase; the barrier after it publishes it.
-// Stage s + ST - 1 goes where stage s - 1 was: the second group's last reads of
-// that one ended, with its wait, before the barrier that opens stage s.
-//
-// The first ST - 1 stages are sent off by open_stages, which a block working
-// through several tiles calls for the next tile before it stores this one.
+// Two rules hold everywhere.  A wait for a stage's loads stands in the read half
+// of the last phase before it, so the barrier after it publishes the stage to
+// both groups.  And LDS that a phase's reads were the last to use is loaded again
+// in the next phase's read half at the earliest: the second group's reads of the
+// phase before ended, with their wait, before the barrier that opens that half.
+__device__ __forceinline__ void end_of_reads()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+    turn();
+}
+
+// With ST >= 3 stages: stage s + ST - 1 goes where stage s - 1 was, from phase 0
+// on.  issue(part, s): parts 0 and 1 are P's halves, 2 and 3 Q's; LOADS a stage.
 template <int ST, class Issue>
-__device__ __forceinline__ void open_stages(int steps, Issue issue)
+__device__ __forceinline__ void open_ring(int steps, Issue issue)
 {
 #pragma unroll
     for (int s = 0; s < ST - 1; ++s)
         if (s < steps) {
-            issue(s, 0);
-            issue(s, 1);
+#pragma unroll
+            for (int part = 0; part < 4; ++part)
+                issue(part, s);
         }
 }
 template <int PH, int ST, int LOADS, class Issue, class Read, class Compute>
-__device__ __forceinline__ void take_turns(int steps, int group, Issue issue, Read read, Compute compute)
+__device__ __forceinline__ void turns_on_ring(int steps, int group, Issue issue, Read read, Compute compute)
 {
-    constexpr int kLater = ST > 2 ? LOADS * (ST - 2) : 0;
+    constexpr int kLater = LOADS * (ST - 2);
     if (steps >= ST - 1)
         landed<kLater>();
     else
@@ -548,11 +576,10 @@ __device__ __forceinline__ void take_turns(int steps, int group, Issue issue, Re
 #pragma unroll
         for (int ph = 0; ph < PH; ++ph) {
             read(s, ph);
-            if (s + ST - 1 < steps) {
-                if (ph == 0)
-                    issue(s + ST - 1, 0);
-                if (ph == (PH > 1 ? 1 : 0))
-                    issue(s + ST - 1, 1);
+            if (ph == 0 && s + ST - 1 < steps) {
+#pragma unroll
+                for (int part = 0; part < 4; ++part)
+                    issue(part, s + ST - 1);
             }
             if (ph == PH - 1) {
                 if (s + ST - 1 < steps)
@@ -560,8 +587,72 @@ __device__ __forceinline__ void take_turns(int steps, int group, Issue issue, Re
                 else
                     landed<0>();
             }
-            asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+            end_of_reads();
+            compute(s, ph);
             turn();
+        }
+    }
+    if (group == 0)
+        turn();
+}
+
+// With two stages, loaded a quarter a phase (a block's 64 KB take the L1 data
+// path half of a stage's time, so they are spread over all of it), each as its
+// last readers finish.  P's fragments are all read in the first half of the
+// phases and kept, so with four phases the halves of P of stage s + 2 are sent
+// off in phases 2 and 3 of stage s and the halves of Q of stage s + 1 in phases
+// 0 and 1 of stage s: P, the weight, which comes from memory, four and five
+// phases before its wait, Q three and two.
+// issue(part, s): parts 0 and 1 are P's halves, 2 and 3 Q's; LP: P's loads.
+template <class Issue>
+__device__ __forceinline__ void open_pair(int steps, Issue issue)
+{
+    issue(0, 0);
+    issue(1, 0);
+    issue(2, 0);
+    issue(3, 0);
+    if (steps > 1) {
+        issue(0, 1);
+        issue(1, 1);
+    }
+}
+template <int PH, int LP, class Issue, class Read, class Compute>
+__device__ __forceinline__ void turns_on_pair(int steps, int group, Issue issue, Read read, Compute compute)
+{
+    if (steps > 1)
+        landed<LP>();
+    else
+        landed<0>();
+    turn();
+    if (group == 1)
+        turn();
+    for (int s = 0; s < steps; ++s) {
+        const bool more = s + 2 < steps;
+#pragma unroll
+        for (int ph = 0; ph < PH; ++ph) {
+            read(s, ph);
+            if (ph == 0 && s + 1 < steps) {
+                if (PH == 1 && s > 0) {
+                    issue(0, s + 1);
+                    issue(1, s + 1);
+                }
+                issue(2, s + 1);
+            }
+            if (ph == (PH > 1) && s + 1 < steps)
+                issue(3, s + 1);
+            if (PH > 1 && more) {
+                if (ph == (PH == 4 ? 2 : PH - 1))
+                    issue(0, s + 2);
+                if (ph == PH - 1)
+                    issue(1, s + 2);
+            }
+            if (ph == PH - 1) {
+                if (PH > 1 && more)
+                    landed<LP>();
+                else
+                    landed<0>();
+            }
+            end_of_reads();
             compute(s, ph);
             turn();
         }
@@ -587,9 +678,9 @@ __device__ __forceinline__ void at_height(int rows, F f)
     f(Rows<BM>{});
 }
 
-// The phases of a bf16 stage for a wave of MT x 4 16 x 16 tiles: the half ks of
-// the stage's K and, where MT is 8, the half of the rows.  P's fragments of the
-// second half are read ahead in part, which evens out the reads of the phases.
+// The phases of a bf16 stage for a wave of MT x 4 16 x 16 tiles: with MT = 8 a
+// half of the rows and a half ks of the stage's K, with fewer a ks, with MT = 2
+// the whole stage.  P's fragments are all read in the first half of the phases.
 template <int MT, class FragP, class FragQ>
 struct Bf16Phases {
     static constexpr int kPhases = MT == 8 ? 4 : MT > 2 ? 2 : 1;
@@ -598,52 +689,39 @@ struct Bf16Phases {
     FragP frag_p;  // (stage, column tile, ks)
     FragQ frag_q;  // (stage, row tile, ks)
     bf16x8 p[2][4], q[kPhases == 1 ? 2 : 1][MQ];
+    static __device__ __forceinline__ int ks_of(int ph) { return kPhases == 4 ? ph & 1 : ph; }
+    static __device__ __forceinline__ int mh_of(int ph) { return kPhases == 4 ? ph >> 1 : 0; }
     __device__ __forceinline__ void read(int s, int ph)
     {
-        if constexpr (kPhases == 1) {
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    p[ks][i] = frag_p(s, i, ks);
-#pragma unroll
-                for (int m = 0; m < MQ; ++m)
-                    q[ks][m] = frag_q(s, m, ks);
-            }
-        } else {
-            const int ks = kPhases == 4 ? ph >> 1 : ph;
-            const int mh = kPhases == 4 ? ph & 1 : 0;
-            if (ph == 0 || kPhases == 2) {
+        for (int ks = 0; ks < 2; ++ks)
+            if (kPhases == 4 ? ph == ks : ph == 0) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     p[ks][i] = frag_p(s, i, ks);
             }
+#pragma unroll
+        for (int k = 0; k < (kPhases == 1 ? 2 : 1); ++k)
 #pragma unroll
             for (int m = 0; m < MQ; ++m)
-                q[0][m] = frag_q(s, mh * 4 + m, ks);
-            if (kPhases == 4 && (ph == 1 || ph == 2)) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    p[1][(ph - 1) * 2 + i] = frag_p(s, (ph - 1) * 2 + i, 1);
-            }
-        }
+                q[k][m] = frag_q(s, mh_of(ph) * 4 + m, kPhases == 1 ? k : ks_of(ph));
     }
     __device__ __forceinline__ void compute(int ph)
     {
 #pragma unroll
-        for (int m = 0; m < MQ; ++m) {
-            hold(q[0][m]);
-            if constexpr (kPhases == 1)
-                hold(q[1][m]);
-        }
-        const int ks0 = kPhases == 4 ? ph >> 1 : ph, mh = kPhases == 4 ? ph & 1 : 0;
+        for (int k = 0; k < (kPhases == 1 ? 2 : 1); ++k)
+#pragma unroll
+            for (int m = 0; m < MQ; ++m)
+                hold(q[k][m]);
 #pragma unroll
         for (int k = 0; k < (kPhases == 1 ? 2 : 1); ++k)
 #pragma unroll
             for (int m = 0; m < MQ; ++m)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[mh * 4 + m][i] = mfma_bf16(p[kPhases == 1 ? k : ks0][i], q[k][m], acc[mh * 4 + m][i]);
+                for (int i = 0; i < 4; ++i) {
+                    const int a = mh_of(ph) * 4 + m;
+                    acc[a][i] = mfma_bf16(p[kPhases == 1 ? k : ks_of(ph)][i], q[k][m], acc[a][i]);
+                }
     }
 };
 
