@@ -474,17 +474,19 @@ __global__ __launch_bounds__(NT) void weight_grad_kernel(GradArgs a)
     CS qs, ps;
     Place t;
     int steps = 0, set = 0;
+    int idx[CS::J];  // picked rows, read from LDS a phase before their first use
     auto slot = [&](int s) { return s < 3 ? 4 + set * 3 + s : s & 3; };
     auto stage = [&](int s) -> lds_char * { return lds + (s & 1) * 2 * CS::kBytes; };
     auto issue = [&](int part, int s) {
         constexpr int JH = CS::J / 2;
-        int idx[CS::J];
-        if (part < 2 ? PG : QG) {
-            const lds_char *from = picks + slot(s) * kSlot;
+        auto read_picks = [&](int of) {
+            const lds_char *from = picks + slot(of) * kSlot;
 #pragma unroll
             for (int j = 0; j < CS::J; ++j)
-                idx[j] = *(const __attribute__((address_space(3))) int *)(from + CS::k_of(tid, j) * 4) & kRowMask;
-        }
+                idx[j] = *(const __attribute__((address_space(3))) int *)(from + CS::k_of(tid, j) * 4);
+        };
+        if (PG && part == 0 && s < 2)
+            read_picks(s);
         const char *p = a.p + (PG ? 0 : t.start * a.ldp), *q = a.q + (QG ? 0 : t.start * a.ldq);
         lds_char *pb = stage(s), *qb = pb + CS::kBytes;
         auto half = [&](CS &c, auto first, lds_char *to, const char *from, int64_t ld, auto gathered) {
@@ -504,6 +506,10 @@ __global__ __launch_bounds__(NT) void weight_grad_kernel(GradArgs a)
             half(qs, Rows<0>{}, qb, q, a.ldq, Rows<QG>{});
         else
             half(qs, Rows<1>{}, qb, q, a.ldq, Rows<QG>{});
+        if (QG && part == 1)
+            read_picks(s);  // for Q of this stage, the next parts
+        if (PG && part == 3 && s > 0 && s + 1 < steps)
+            read_picks(s + 1);  // for P of the next one
     };
     auto pick_first = [&](const Place &next, int to) {
 #pragma unroll

@@ -105,6 +105,8 @@ __device__ __forceinline__ int here(int v)
     return v;
 }
 
+constexpr int32_t kRowMask = 0x7fffffff;  // pair_row without its "only pair of the row" bit
+
 constexpr int kStepBytes = 128;  // K bytes of one stage
 
 // Row-contiguous operand, ROWS rows staged by NT threads.  LDS row r holds its
@@ -255,7 +257,7 @@ struct ColStage {
             }
         }
     }
-    // The same with row[j] the memory row of this thread's j-th chunk.
+    // The same with row[j] the memory row of this thread's j-th chunk, as pair_row has it.
     template <int J0 = 0, int JN = J>
     __device__ __forceinline__ void issue(lds_char *lds, int tid, int wave, const char *base, int64_t ld,
                                           int k0, int kn, const int (&row)[J])
@@ -263,12 +265,12 @@ struct ColStage {
         if (k0 + 64 <= kn) {
 #pragma unroll
             for (int j = J0; j < J0 + JN; ++j)
-                load_lds16(base + row[j] * ld + cb[j], lds + (j * NT + wave * kWave) * 16);
+                load_lds16(base + (row[j] & kRowMask) * ld + cb[j], lds + (j * NT + wave * kWave) * 16);
         } else {
             tid = here(tid);
 #pragma unroll
             for (int j = J0; j < J0 + JN; ++j)
-                load_lds16(k0 + k_of(tid, j) < kn ? base + row[j] * ld + cb[j]
+                load_lds16(k0 + k_of(tid, j) < kn ? base + (row[j] & kRowMask) * ld + cb[j]
                                                   : reinterpret_cast<const char *>(kZero16),
                            lds + (j * NT + wave * kWave) * 16);
         }
@@ -294,7 +296,6 @@ struct ColStage {
 constexpr int NT = 512;  // threads of a tile block: 8 waves, 2 (tokens) x 4 (columns)
 constexpr int BN = 256;  // columns of a tile
 constexpr int kNoLimit = 0x7fffffff;
-constexpr int32_t kRowMask = 0x7fffffff;  // pair_row without its "only pair of the row" bit
 
 // kGated: the weight holds gate rows, then up rows, and a tile takes as many of
 // each; kBack: the gate's backward.
