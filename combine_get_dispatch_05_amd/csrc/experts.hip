@@ -606,7 +606,9 @@ __global__ __launch_bounds__(256) void rows_kernel(const int32_t *__restrict__ r
         f32x4 v = {};
         for (int k = 0; k < n; ++k)
             v += *reinterpret_cast<const f32x4 *>(terms + int64_t(pairs[k]) * N + c);
-        *reinterpret_cast<uint2 *>(out + row * N + c) = pack4(v);
+        typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+        const uint2 b = pack4(v);
+        __builtin_nontemporal_store(u32x2{b.x, b.y}, reinterpret_cast<u32x2 *>(out + row * N + c));
     }
 }
 

@@ -88,7 +88,7 @@ __device__ __forceinline__ f32x4 mfma_step_bf16(const Frag &a, const Frag &b, f3
 // 16 MT.  WN x WK waves: WN share out the columns, WK the K steps.  A wave holds NW
 // 16-column tiles (half gate, half up in the gated form) and MT 16-row tiles.
 template <bool FP8, int WN, int WK, int NW, int MT, Form F, class Epi>
-__global__ __launch_bounds__(WN *WK *kWave) void few_rows_kernel(FewArgs a, Groups G, Epi epi)
+__global__ __launch_bounds__(WN *WK *kWave, WN == 1 && MT == 1 ? 4 : 2) void few_rows_kernel(FewArgs a, Groups G, Epi epi)
 {
     constexpr int kCols = WN * (F == Form::kGated ? NW / 2 : NW) * 16;  // of a block
     constexpr int kWaveCols = kCols / WN;
@@ -176,7 +176,7 @@ __global__ __launch_bounds__(WN *WK *kWave) void few_rows_kernel(FewArgs a, Grou
             }
         };
         // U steps are in flight while U are used: as many as the registers hold
-        constexpr int U = NW + MT <= 3 ? 4 : NW + MT <= 5 && MT < 4 ? 2 : 1;
+        constexpr int U = NW + MT == 2 || (WN > 1 && MT == 1) ? 2 : 1;
         Step cur[U], nxt[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)

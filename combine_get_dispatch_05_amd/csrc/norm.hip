@@ -68,7 +68,7 @@ __device__ __forceinline__ void norm_store(const NormArgs &a, int64_t row, int v
         y[i] = s[i] * rstd * wf[i];
     const int64_t at = row * a.V + v;
     if (a.out != nullptr)
-        a.out[at] = pack8(y);
+        __builtin_nontemporal_store(pack8(y), &a.out[at]);
     if (a.out_q == nullptr)
         return;
     float amax = 0.0f;
@@ -85,7 +85,8 @@ __device__ __forceinline__ void norm_store(const NormArgs &a, int64_t row, int v
     q.x = __builtin_amdgcn_cvt_pk_fp8_f32(y[2] * inv, y[3] * inv, c, true);
     c = __builtin_amdgcn_cvt_pk_fp8_f32(y[4] * inv, y[5] * inv, 0, false);
     q.y = __builtin_amdgcn_cvt_pk_fp8_f32(y[6] * inv, y[7] * inv, c, true);
-    a.out_q[at] = q;
+    typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+    __builtin_nontemporal_store(u32x2{q.x, q.y}, reinterpret_cast<u32x2 *>(&a.out_q[at]));
     if ((v & 15) == 0)
         a.out_scale[at >> 4] = amax / 448.0f;
 }
@@ -129,7 +130,7 @@ __global__ __launch_bounds__(NTH) void rms_norm_kernel(NormArgs a)
                 for (int k = 0; k < 8; ++k)
                     sum += s[i][k] * s[i][k];
                 if (a.residual_out != nullptr)
-                    a.residual_out[base + v] = pack8(s[i]);
+                    __builtin_nontemporal_store(pack8(s[i]), &a.residual_out[base + v]);
             }
         }
     } else {
@@ -185,7 +186,7 @@ __device__ __forceinline__ void norm_back(const float (&d)[8], const float (&h)[
         const float g = rstd * (d[k] * w[k] - h[k] * rstd * c);
         r[k] = dres != nullptr ? g + r[k] : g;
     }
-    *dx = pack8(r);
+    __builtin_nontemporal_store(pack8(r), dx);
 }
 
 // Each block takes every gridDim.x-th row and sums its own part of dw: in
