@@ -163,22 +163,28 @@ struct PairOut {
     __device__ __forceinline__ void store(const Tile &t, int64_t start, int m0, int n0, int N,
                                           const f32x4 (&acc)[MT][NW], int lane) const
     {
+        // every row's place and weight before the first store: a load behind a store
+        // waits for it, and eight such waits a tile took longer than the stores
+        int32_t r[MT];
+        float w[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const int m = m0 + mt * 16 + (lane & 15);
-            const bool live = m < t.rows;
-            const int64_t p = start + m;
-            const int32_t r = live ? pair_row[p] : 0;
-            const float w = live && weight != nullptr ? weight[pair_slot[p]] : 1.0f;
+            r[mt] = m < t.rows ? pair_row[start + m] : 0;
+            w[mt] = m < t.rows && weight != nullptr ? weight[pair_slot[start + m]] : 1.0f;
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int m = m0 + mt * 16 + (lane & 15);
             f32x4 v[NW];
 #pragma unroll
             for (int nt = 0; nt < NW; ++nt) {
-                v[nt] = acc[mt][nt] * w;
+                v[nt] = acc[mt][nt] * w[mt];
                 const int n = n0 + nt * 16 + (lane >> 4) * 4;
-                if (live && r >= 0 && n < N)
-                    *reinterpret_cast<f32x4 *>(terms + p * N + n) = v[nt];
+                if (m < t.rows && r[mt] >= 0 && n < N)
+                    *reinterpret_cast<f32x4 *>(terms + (start + m) * N + n) = v[nt];
             }
-            store_bf16_row<NW>(r < 0 ? out + int64_t(r & kRowMask) * N : nullptr, n0, N, v, lane);
+            store_bf16_row<NW>(r[mt] < 0 ? out + int64_t(r[mt] & kRowMask) * N : nullptr, n0, N, v, lane);
         }
     }
 };
@@ -237,43 +243,61 @@ struct GatedBack {
     {
         __shared__ float part[WN][ROWS];
         const int tid = threadIdx.x;
+        float w[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const int m = t.m0 + mbase + mt * 16 + (lane & 15);
+            w[mt] = m < t.rows ? weight[pair_slot[start + m]] : 0.0f;
+        }
+        // g and u two column tiles at a time, the next two on their way before these
+        // are stored (a load behind a store waits for it)
+        f32x4 g[2][2], u[2][2];
+        auto load = [&](int i) {
+            const int m = t.m0 + mbase + (i >> 1) * 16 + (lane & 15);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int n = n0 + ((i & 1) * 2 + k) * 16 + (lane >> 4) * 4;
+                const bool in = m < t.rows && n < I;
+                const float *at = gu + (start + m) * 2 * I + n;
+                g[i & 1][k] = in ? *reinterpret_cast<const f32x4 *>(at) : f32x4{};
+                u[i & 1][k] = in ? *reinterpret_cast<const f32x4 *>(at + I) : f32x4{};
+            }
+        };
+        static_assert(NW == 4, "two pairs of column tiles");
+        load(0);
+        float dw = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) {
+            const int mt = i >> 1, h = (i & 1) * 2, m = t.m0 + mbase + mt * 16 + (lane & 15);
             const bool live = m < t.rows;
             const int64_t p = start + m;
-            const float w = live ? weight[pair_slot[p]] : 0.0f;
-            float dw = 0.0f;
+            if (i + 1 < 2 * MT)
+                load(i + 1);
+            f32x4 dg[2], du[2], wa[2];
 #pragma unroll
-            for (int h = 0; h < NW; h += 2) {
-                f32x4 dg[2], du[2], wa[2];
+            for (int k = 0; k < 2; ++k) {
+                const bool in = live && n0 + (h + k) * 16 + (lane >> 4) * 4 < I;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int n = n0 + (h + k) * 16 + (lane >> 4) * 4;
-                    const bool in = live && n < I;
-                    f32x4 g = {}, u = {};
-                    if (in) {
-                        g = *reinterpret_cast<const f32x4 *>(gu + p * 2 * I + n);
-                        u = *reinterpret_cast<const f32x4 *>(gu + p * 2 * I + I + n);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float sg = sigmoidf(g[i]), d = acc[mt][h + k][i], si = g[i] * sg;
-                        dw += in ? si * u[i] * d : 0.0f;
-                        wa[k][i] = w * si * u[i];
-                        du[k][i] = w * d * si;
-                        dg[k][i] = w * d * u[i] * sg * (1.0f + g[i] * (1.0f - sg));
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    const float gv = g[i & 1][k][j], uv = u[i & 1][k][j], d = acc[mt][h + k][j];
+                    const float sg = sigmoidf(gv), si = gv * sg;
+                    dw += in ? si * uv * d : 0.0f;
+                    wa[k][j] = w[mt] * si * uv;
+                    du[k][j] = w[mt] * d * si;
+                    dg[k][j] = w[mt] * d * uv * sg * (1.0f + gv * (1.0f - sg));
                 }
-                store_bf16_row<2>(live ? dgu + p * 2 * I : nullptr, n0 + h * 16, I, dg, lane);
-                store_bf16_row<2>(live ? dgu + p * 2 * I + I : nullptr, n0 + h * 16, I, du, lane);
-                store_bf16_row<2>(live ? wact + p * I : nullptr, n0 + h * 16, I, wa, lane);
-                __builtin_amdgcn_sched_barrier(0);  // a pair at a time: more would not fit the registers
             }
-            dw += __shfl_xor(dw, 16);
-            dw += __shfl_xor(dw, 32);
-            if (lane < 16)
-                part[wn][mbase + mt * 16 + lane] = dw;
+            store_bf16_row<2>(live ? dgu + p * 2 * I : nullptr, n0 + h * 16, I, dg, lane);
+            store_bf16_row<2>(live ? dgu + p * 2 * I + I : nullptr, n0 + h * 16, I, du, lane);
+            store_bf16_row<2>(live ? wact + p * I : nullptr, n0 + h * 16, I, wa, lane);
+            if (i & 1) {
+                dw += __shfl_xor(dw, 16);
+                dw += __shfl_xor(dw, 32);
+                if (lane < 16)
+                    part[wn][mbase + mt * 16 + lane] = dw;
+                dw = 0.0f;
+            }
+            __builtin_amdgcn_sched_barrier(0);  // one at a time: more would not fit the registers
         }
         __syncthreads();
         if (tid < ROWS && t.m0 + tid < t.rows)
