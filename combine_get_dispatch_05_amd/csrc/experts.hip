@@ -456,8 +456,12 @@ struct GradArgs {
     uint16_t *out;
 };
 
+constexpr int kPickSlots = 10;
+constexpr int kGradLds = 4 * ColStage<256, NT>::kBytes + NT / kWave * kPickSlots * kWave * 4;
+
+// Tiles block, block + gridDim.x, ... of one gradient.
 template <bool QG, bool PG>
-__global__ __launch_bounds__(NT) void weight_grad_kernel(GradArgs a)
+__device__ __forceinline__ void weight_grad(const GradArgs &a, lds_char *lds, unsigned block)
 {
     constexpr int B = 256;
     using CS = ColStage<B, NT>;
@@ -467,13 +471,11 @@ __global__ __launch_bounds__(NT) void weight_grad_kernel(GradArgs a)
     // without picking).  Slots 0 to 3 go round; a tile's first three stages have
     // slots of their own, filled while the tile before is worked on, for which
     // tiles take turns with two sets.
-    constexpr int kSlot = kWave * 4, kSlots = 10;
-    __shared__ __attribute__((aligned(128))) char smem[4 * CS::kBytes + NT / kWave * kSlots * kSlot];
-    lds_char *lds = (lds_char *)smem;
+    constexpr int kSlot = kWave * 4;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = uniform(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
-    lds_char *picks = lds + 4 * CS::kBytes + wave * kSlots * kSlot;
+    lds_char *picks = lds + 4 * CS::kBytes + wave * kPickSlots * kSlot;
     const unsigned per = a.mt * a.nt, total = per * unsigned(a.experts);
 
     struct Place {
@@ -549,7 +551,6 @@ __global__ __launch_bounds__(NT) void weight_grad_kernel(GradArgs a)
         if (steps > 0)
             open_pair(steps, issue);
     };
-    unsigned block = blockIdx.x;
     if (block >= total)
         return;
     const Place first = place(block);
@@ -587,6 +588,19 @@ __global__ __launch_bounds__(NT) void weight_grad_kernel(GradArgs a)
         if (block >= total)
             break;
     }
+}
+
+// Both weight gradients: dW2 (rows of dy picked), then dW13 (rows of x picked), so
+// that the second fills what the first leaves idle at its end.  Its tiles start
+// at the block after the first's last.
+__global__ __launch_bounds__(NT) void weight_grads_kernel(GradArgs dw2, GradArgs dw13)
+{
+    __shared__ __attribute__((aligned(128))) char smem[kGradLds];
+    lds_char *lds = (lds_char *)smem;
+    weight_grad<true, false>(dw2, lds, blockIdx.x);
+    __syncthreads();  // the first's last reads of its picks
+    const unsigned used = (dw2.mt * dw2.nt * unsigned(dw2.experts) + kXcds - 1) / kXcds * kXcds % gridDim.x;
+    weight_grad<false, true>(dw13, lds, (blockIdx.x + gridDim.x - used) % gridDim.x);
 }
 
 // ------------------------------------------------------------ row sums
@@ -794,10 +808,6 @@ hipError_t launch_expert_ffn_backward(const ExpertFfn &f, const void *dy, const 
     w.pair_row = f.pair_row;
     w.offsets = f.offsets;
     w.experts = f.experts;
-    auto blocks = [&] {
-        const int64_t n = int64_t(f.experts) * w.mt * w.nt, cus = compute_units();
-        return dim3(unsigned(n < cus ? n : cus));
-    };
     w.q = static_cast<const char *>(dy);
     w.ldq = int64_t(H) * 2;
     w.p = static_cast<const char *>(wact);
@@ -807,20 +817,20 @@ hipError_t launch_expert_ffn_backward(const ExpertFfn &f, const void *dy, const 
     w.mt = hm;
     w.nt = in;
     w.out = static_cast<uint16_t *>(dw2);
-    hipLaunchKernelGGL((weight_grad_kernel<true, false>), blocks(), dim3(NT), 0, stream, w);
-    e = hipGetLastError();
-    if (e != hipSuccess)
-        return e;
-    w.q = static_cast<const char *>(dgu);
-    w.ldq = int64_t(2) * I * 2;
-    w.p = static_cast<const char *>(x);
-    w.ldp = int64_t(H) * 2;
-    w.M = 2 * I;
-    w.N = H;
-    w.mt = gm;
-    w.nt = hm;
-    w.out = static_cast<uint16_t *>(dw13);
-    hipLaunchKernelGGL((weight_grad_kernel<false, true>), blocks(), dim3(NT), 0, stream, w);
+    GradArgs v = w;
+    v.q = static_cast<const char *>(dgu);
+    v.ldq = int64_t(2) * I * 2;
+    v.p = static_cast<const char *>(x);
+    v.ldp = int64_t(H) * 2;
+    v.M = 2 * I;
+    v.N = H;
+    v.mt = gm;
+    v.nt = hm;
+    v.out = static_cast<uint16_t *>(dw13);
+    // whole rounds of the XCDs, so that a block stays with one of them
+    const int64_t all = int64_t(f.experts) * (int64_t(hm) * in + int64_t(gm) * hm);
+    const int64_t cus = compute_units(), need = (all + 2 * kXcds - 1) / kXcds * kXcds;
+    hipLaunchKernelGGL(weight_grads_kernel, dim3(unsigned(need < cus ? need : cus)), dim3(NT), 0, stream, w, v);
     return hipGetLastError();
 }
 

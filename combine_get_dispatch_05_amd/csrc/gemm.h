@@ -397,6 +397,19 @@ __device__ __forceinline__ int group_expert(const Groups &G, int g)
     return G.offsets != nullptr ? g : (g % G.ranks) * G.epr + g / G.ranks;
 }
 
+// Inclusive sum over the wave, in the registers: inside each 16 lanes, then the
+// rows' last lanes passed on.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v)
+{
+    v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x111, 0xF, 0xF, true));
+    v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x112, 0xF, 0xF, true));
+    v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x114, 0xF, 0xF, true));
+    v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x118, 0xF, 0xF, true));
+    v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x142, 0xA, 0xF, false));
+    v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x143, 0xC, 0xF, false));
+    return v;
+}
+
 struct Tile {
     int group;
     int m0;    // first row of the tile inside its group
@@ -449,12 +462,7 @@ __device__ __forceinline__ Tile find_tile(const Groups &G, unsigned b, unsigned 
         return uint64_t(unsigned(rows) / BM + (rest > BM / 2)) | uint64_t(rest > 0 && rest <= BM / 2) << 32;
     };
     auto scan = [&](uint64_t t, uint64_t &total) {  // exclusive sum of t over the block
-        uint64_t pre = t;
-#pragma unroll
-        for (int d = 1; d < kWave; d <<= 1) {
-            const uint64_t o = __shfl_up(pre, d);
-            pre += lane >= d ? o : 0;
-        }
+        const uint64_t pre = uint64_t(wave_scan(uint32_t(t))) | uint64_t(wave_scan(uint32_t(t >> 32))) << 32;
         __syncthreads();
         if (lane == 63)
             s[wave] = pre;
