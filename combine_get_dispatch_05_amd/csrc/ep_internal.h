@@ -244,6 +244,15 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
     return bf16_rne(lo) | (bf16_rne(hi) << 16);
 }
 
+// The same rounding in one instruction (a NaN may come out with other payload
+// bits): for results of arithmetic, where the copies' bit rule does not apply.
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi)
+{
+    typedef float f32x2_t __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{lo, hi}, bf16x2_t));
+}
+
 __device__ __forceinline__ uint64_t wave_ballot(bool p) { return __ballot(p); }
 
 __device__ __forceinline__ uint64_t lanemask_lt()

@@ -319,7 +319,7 @@ __device__ __forceinline__ float sigmoidf(float v)
 
 __device__ __forceinline__ uint2 pack4(f32x4 v)
 {
-    return make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    return make_uint2(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]));
 }
 
 // The bf16 stores of a wave's NW 16 x 16 tiles of one row tile: a lane holds four

@@ -24,7 +24,7 @@ __device__ __forceinline__ u32x4 pack8(const float (&f)[8])
     u32x4 v;
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-        v[q] = pack_bf16x2(f[2 * q], f[2 * q + 1]);
+        v[q] = cvt_bf16x2(f[2 * q], f[2 * q + 1]);
     return v;
 }
 
