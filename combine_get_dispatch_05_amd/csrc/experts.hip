@@ -83,8 +83,8 @@ __global__ __launch_bounds__(kGroupBlock) void place_pairs_kernel(
     constexpr int W = kGroupBlock / kWave;
     const int e = blockIdx.x, r = e / epr, le = e % epr;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    __shared__ int s[2][W];
-    int c = 0;
+    __shared__ int64_t s[2][W];
+    int64_t c = 0;  // the counts of a prefix that is none can add up to more than 2^31
     for (int i = threadIdx.x; i < e; i += kGroupBlock)
         c += counts[i];
 #pragma unroll
@@ -93,16 +93,15 @@ __global__ __launch_bounds__(kGroupBlock) void place_pairs_kernel(
     if (lane == 0)
         s[1][wave] = c;
     __syncthreads();
-    int base = 0;
+    int64_t base = 0;
     for (int w = 0; w < W; ++w)
         base += s[1][w];
     // a count past the capacity (ids that no dispatch wrote) leaves the tail out
-    const int icap = int(cap);
     if (threadIdx.x == 0) {
-        offsets[e] = base < icap ? base : icap;
+        offsets[e] = int32_t(base < cap ? base : cap);
         if (e == E - 1) {
-            const int end = base + counts[e];
-            offsets[E] = end < icap ? end : icap;
+            const int64_t end = base + counts[e];
+            offsets[E] = int32_t(end < cap ? end : cap);
         }
     }
     int64_t a, b;
@@ -124,11 +123,11 @@ __global__ __launch_bounds__(kGroupBlock) void place_pairs_kernel(
         int before = 0, total = 0;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            const int v = s[flip][w];
+            const int v = int(s[flip][w]);
             before += w < wave ? v : 0;
             total += v;
         }
-        for (int pos = base + before + pre - mine; hits != 0 && pos < icap; ++pos) {
+        for (int64_t pos = base + before + pre - mine; hits != 0 && pos < cap; ++pos) {
             const int64_t at = i + __ffs(hits) - 1;
             hits &= hits - 1;
             const int64_t row = at / K;
@@ -139,7 +138,7 @@ __global__ __launch_bounds__(kGroupBlock) void place_pairs_kernel(
             }
             pair_row[pos] = int32_t(row) | (live == 1 ? int32_t(0x80000000u) : 0);
             pair_slot[pos] = int32_t(at);
-            row_pair[at] = pos;
+            row_pair[at] = int32_t(pos);
         }
         base += total;
     }
