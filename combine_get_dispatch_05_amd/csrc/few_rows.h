@@ -226,7 +226,7 @@ __global__ __launch_bounds__(WN *WK *kWave, WN == 1 && MT == 1 ? 4 : 2) void few
             }
         };
         // U steps are in flight while U are used: as many as the registers hold
-        constexpr int U = NW + MT == 2 || (WN > 1 && MT == 1 && !(FP8 && F == Form::kGated)) ? 2 : 1;
+        constexpr int U = NW + MT == 2 ? 2 : 1;
         Step cur[U], nxt[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
