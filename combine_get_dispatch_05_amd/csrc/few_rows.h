@@ -1,8 +1,9 @@
 // few_rows.h -- the products of groups that hold few rows (a decode batch, one
-// token): the weight is read once and its bytes are the whole cost, so it
-// goes from memory straight into the matrix instruction's registers, a wave
-// owning its own weight rows, and only the partial sums of waves that share an
-// output cross LDS.  bf16 or FP8 operands.
+// token): the weight is read once and its bytes are the whole cost.  Where there
+// are columns enough for every compute unit, it goes from memory straight into the
+// matrix instruction's registers, a wave owning its own weight rows
+// (few_rows_kernel); where there are not, the waves of a block share out K
+// (split_kernel).  bf16 or FP8 operands.
 #pragma once
 
 #include "gemm.h"
@@ -24,12 +25,13 @@ struct FewArgs {
     int active;            // groups that can hold rows, where fewer than all
 };
 
-// The j-th group that holds rows, or -1.  Every thread of the block takes part.
+// The j-th group that holds rows, or -1.  Every thread of the block takes part;
+// s: LDS of one int a wave and one more, free again afterwards.
 template <int NTH>
-__device__ __forceinline__ int find_group(const Groups &G, int j)
+__device__ __forceinline__ int find_group(const Groups &G, int j, int *s)
 {
     constexpr int W = NTH / kWave;
-    __shared__ int s[W], found;
+    int &found = s[W];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     if (threadIdx.x == 0)
         found = -1;
@@ -52,7 +54,9 @@ __device__ __forceinline__ int find_group(const Groups &G, int j)
             found = g;
     }
     __syncthreads();
-    return uniform(found);
+    const int g = found;
+    __syncthreads();
+    return uniform(g);
 }
 
 // 32 bytes of a row for one K step: bytes [16 g, 16 g + 16) and 64 further on,
@@ -119,7 +123,7 @@ __device__ __forceinline__ f32x4 mfma_step_bf16(const Frag &a, const Frag &b, f3
 // 16 MT.  WN x WK waves: WN share out the columns, WK the K steps.  A wave holds NW
 // 16-column tiles (half gate, half up in the gated form) and MT 16-row tiles.
 template <bool FP8, int WN, int WK, int NW, int MT, Form F, class Epi>
-__global__ __launch_bounds__(WN *WK *kWave, WN == 1 && MT == 1 ? 4 : 2) void few_rows_kernel(FewArgs a, Groups G, Epi epi)
+__global__ __launch_bounds__(WN *WK *kWave, 2) void few_rows_kernel(FewArgs a, Groups G, Epi epi)
 {
     constexpr int kCols = WN * (F == Form::kGated ? NW / 2 : NW) * 16;  // of a block
     constexpr int kWaveCols = kCols / WN;
@@ -127,7 +131,7 @@ __global__ __launch_bounds__(WN *WK *kWave, WN == 1 && MT == 1 ? 4 : 2) void few
     int g = blockIdx.x / a.nt;
     const int tn = int(blockIdx.x % a.nt);
     if (a.active < G.num) {
-        g = find_group<WN * WK * kWave>(G, g);
+        g = find_group<WN * WK * kWave>(G, g, reinterpret_cast<int *>(sums));
         if (g < 0)
             return;
     }
@@ -225,25 +229,14 @@ __global__ __launch_bounds__(WN *WK *kWave, WN == 1 && MT == 1 ? 4 : 2) void few
                         acc[m][i] = mfma_step_bf16(t.p[i], t.q[m], acc[m][i]);
             }
         };
-        // U steps are in flight while U are used: as many as the registers hold
-        constexpr int U = NW + MT == 2 ? 2 : 1;
-        Step cur[U], nxt[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (s0 + u < s1)
-                load(cur[u], s0 + u);
-        for (int s = s0; s < s1; s += U) {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (s + U + u < s1)
-                    load(nxt[u], s + U + u);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (s + u < s1)
-                    use(cur[u]);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                cur[u] = nxt[u];
+        Step cur, nxt;  // one step in flight while one is used
+        if (s0 < s1)
+            load(cur, s0);
+        for (int s = s0; s < s1; ++s) {
+            if (s + 1 < s1)
+                load(nxt, s + 1);
+            use(cur);
+            cur = nxt;
         }
         if constexpr (WK > 1) {
             if (wk > 0) {
@@ -274,47 +267,187 @@ __global__ __launch_bounds__(WN *WK *kWave, WN == 1 && MT == 1 ? 4 : 2) void few
     }
 }
 
+// Products whose blocks leave compute units idle: 16 MT rows by 64 columns (32
+// gate and their 32 up) a block, K shared out over the eight waves.  A wave stages
+// its own K steps in LDS of its own, whole 128-byte lines a row, and nobody else
+// reads them, so the loop has no barrier: as soon as a step is in registers the
+// next is sent off behind its matrix instructions.  The waves' sums meet at the end.
+constexpr int kSplitCols = 64;
+
+// 16 rows from r0 of a staged K step.
+__device__ __forceinline__ Frag staged_frag(const lds_char *base, int r0, int lane)
+{
+    using At = RowStage<16, kWave>;  // (where a chunk lies does not depend on the rows staged)
+    typedef const __attribute__((address_space(3))) i32x4 lds_i32x4;
+    Frag f;
+    f.lo = *(lds_i32x4 *)At::at(base, r0 + (lane & 15), lane >> 4);
+    f.hi = *(lds_i32x4 *)At::at(base, r0 + (lane & 15), 4 + (lane >> 4));
+    return f;
+}
+
+template <bool FP8, int MT, Form F, class Epi>
+__global__ __launch_bounds__(NT, MT == 1 ? 4 : 2) void split_kernel(FewArgs a, Groups G, Epi epi)
+{
+    static_assert(!FP8 || F == Form::kPlain, "a gated FP8 row needs a block of 128 columns");
+    constexpr int W = NT / kWave, NW = kSplitCols / 16;
+    constexpr int kCols = F == Form::kGated ? kSplitCols / 2 : kSplitCols;
+    using PR = NearRowStage<kSplitCols / 2, kWave>;
+    using QR = NearRowStage<16 * MT, kWave>;
+    constexpr int kQ = 2 * PR::kBytes, kOwn = kQ + QR::kBytes;
+    static_assert(kOwn >= MT * NW * kWave * 16, "a wave's sums take the place of its last step");
+    __shared__ __attribute__((aligned(128))) char smem[W * kOwn];
+    int g = blockIdx.x / a.nt;
+    const int n0 = int(blockIdx.x % a.nt) * kCols;
+    if (a.active < G.num) {
+        g = find_group<NT>(G, g, reinterpret_cast<int *>(smem));
+        if (g < 0)
+            return;
+    }
+    const int rows = uniform(group_rows(G, g));
+    const int lane = threadIdx.x & 63;
+    const int wave = uniform(threadIdx.x >> 6);
+    lds_char *own = (lds_char *)smem + wave * kOwn;
+    const int64_t start = group_start(G, g);
+    const int e = group_expert(G, g);
+    const int steps = (a.kbytes + kStepBytes - 1) / kStepBytes;
+    const int s0 = steps * wave / W, s1 = steps * (wave + 1) / W;
+    PR pr[2];  // gate and up columns, or the two halves
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int c0 = F == Form::kGated ? n0 : n0 + h * (kSplitCols / 2);
+        const int c = c0 < a.N ? c0 : a.N - 1;
+        const int64_t row = c + (F == Form::kGated ? h * int64_t(a.N) : 0);
+        pr[h].init(lane, a.p + int64_t(e) * a.p_expert + row * a.ldp, [&](int, int r) {
+            return uint32_t(c + r < a.N ? r : a.N - 1 - c) * uint32_t(a.ldp);
+        });
+    }
+    const float *ps = FP8 ? a.p_scale + e * a.p_scales + int64_t(n0 >> 7) * steps : nullptr;
+    for (int m0 = int(blockIdx.y) * 16 * MT; m0 < rows; m0 += int(gridDim.y) * 16 * MT) {
+        QR qr;
+        qr.init(lane, a.q + (start + m0) * a.ldq, [&](int, int r) {
+            return uint32_t(m0 + r < rows ? r : rows - 1 - m0) * uint32_t(a.ldq);
+        });
+        const float *qs[MT];
+        float next[MT], next_c = 0.0f;  // scales of the step on its way
+        if constexpr (FP8) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const int r = m0 + m * 16 + (lane & 15);
+                qs[m] = a.q_scale + (start + (r < rows ? r : rows - 1)) * steps;
+            }
+        }
+        auto send = [&](int s) {
+            const int64_t kb = int64_t(s) * kStepBytes;
+            if constexpr (FP8) {
+                next_c = ps[s];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    next[m] = qs[m][s];
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                pr[h].template issue<!FP8>(own + h * PR::kBytes, lane, 0, kb, a.kbytes);
+            qr.template issue<!FP8>(own + kQ, lane, 0, kb, a.kbytes);
+        };
+        f32x4 acc[MT][NW] = {};
+        if (s0 < s1)
+            send(s0);
+        for (int s = s0; s < s1; ++s) {
+            landed<0>();
+            Frag p[NW], q[MT];
+            float scale[MT];
+            if constexpr (FP8) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    scale[m] = next[m] * next_c;
+                    hold(scale[m]);  // here: behind send() it would wait for the next step's loads
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NW; ++i)
+                p[i] = staged_frag(own, i * 16, lane);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                q[m] = staged_frag(own + kQ, m * 16, lane);
+            // read before the same LDS is loaded again
+            asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+            if (s + 1 < s1)
+                send(s + 1);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < NW; ++i) {
+                    if constexpr (FP8)
+                        acc[m][i] += mfma_step_fp8(p[i], q[m]) * scale[m];
+                    else
+                        acc[m][i] = mfma_step_bf16(p[i], q[m], acc[m][i]);
+                }
+        }
+        f32x4 *sums = reinterpret_cast<f32x4 *>(smem);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < NW; ++i)
+                sums[wave * (kOwn / 16) + (m * NW + i) * kWave + lane] = acc[m][i];
+        __syncthreads();
+        if (wave < 2 * MT) {  // two column tiles each: neighbours, or a gate and its up tile
+            const int m = wave >> 1, h = wave & 1;
+            const int i0 = F == Form::kGated ? h : 2 * h, i1 = F == Form::kGated ? h + 2 : i0 + 1;
+            f32x4 sum[1][2] = {};
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                sum[0][0] += sums[w * (kOwn / 16) + (m * NW + i0) * kWave + lane];
+                sum[0][1] += sums[w * (kOwn / 16) + (m * NW + i1) * kWave + lane];
+            }
+            epi.store(Tile{g, m0, rows, int(blockIdx.x % a.nt)}, start, m0 + m * 16, n0 + h * (kCols / 2), a.N, sum,
+                      lane);
+        }
+        if (m0 + int(gridDim.y) * 16 * MT < rows)
+            __syncthreads();  // the sums are read before the next rows are staged
+    }
+}
+
 // --------------------------------------------------------------- launches
 
 // Rows up to which a group takes this kernel: it reads the weight again (from L2)
 // for every 16 MT rows.
 constexpr int kFewRows = 64;
 
-template <bool FP8, int WN, int WK, int NW, int MT, Form F, class Epi>
-hipError_t launch_few_shape(FewArgs a, const Groups &G, int row_blocks, const Epi &epi, const char *what,
-                            hipStream_t stream)
+template <class Kernel, class Epi>
+hipError_t launch_few_shape(Kernel kernel, FewArgs a, const Groups &G, int cols, int tile_rows, int row_blocks,
+                            const Epi &epi, const char *what, hipStream_t stream)
 {
-    constexpr int cols = WN * (F == Form::kGated ? NW / 2 : NW) * 16;
     a.nt = unsigned((a.N + cols - 1) / cols);
     const int64_t blocks = int64_t(a.nt) * a.active;
     if (blocks > kMaxTileBlocks || row_blocks > 65535)
         return hipErrorInvalidValue;
     if (log_enabled())
-        log_launch("%s: groups<=%d of %d N=%d K bytes=%d few rows %d cols=%d waves=%dx%d blocks=%lld x %d", what,
-                   a.active, G.num, a.N, a.kbytes, MT * 16, cols, WN, WK, (long long)blocks, row_blocks);
-    hipLaunchKernelGGL((few_rows_kernel<FP8, WN, WK, NW, MT, F, Epi>), dim3(unsigned(blocks), row_blocks),
-                       dim3(WN * WK * kWave), 0, stream, a, G, epi);
+        log_launch("%s: groups<=%d of %d N=%d K bytes=%d few rows %d cols=%d blocks=%lld x %d", what, a.active,
+                   G.num, a.N, a.kbytes, tile_rows, cols, (long long)blocks, row_blocks);
+    hipLaunchKernelGGL(kernel, dim3(unsigned(blocks), row_blocks), dim3(NT), 0, stream, a, G, epi);
     return hipGetLastError();
 }
 
 // avg: rows of an active group on average.  Blocks of 256 columns (128 gated)
-// where that makes one for every compute unit, else of 16, all eight waves
-// sharing out K: one token's eight experts of 768 x 2048 in 48 blocks took
-// %WIDE% us, in 384 %NARROW%.
+// where that makes one for every compute unit, else of 64 (32) with K split: one
+// token's eight bf16 experts of 768 x 2048, gated, took 34 us in 48 wide blocks.
 template <bool FP8, Form F, class Epi>
 hipError_t launch_few(FewArgs a, const Groups &G, int64_t avg, int row_blocks, const Epi &epi, const char *what,
                       hipStream_t stream)
 {
+    constexpr int wide = F == Form::kGated ? 128 : 256, split = wide / (256 / kSplitCols);
     if constexpr (!Epi::kBlockWide) {
-        const int wide = F == Form::kGated ? 128 : 256;
         if (int64_t((a.N + wide - 1) / wide) * a.active * row_blocks < compute_units()) {
-            constexpr int NW = F == Form::kGated ? 2 : 1;
-            return avg <= 16 ? launch_few_shape<FP8, 1, 8, NW, 1, F>(a, G, row_blocks, epi, what, stream)
-                             : launch_few_shape<FP8, 1, 8, NW, 4, F>(a, G, row_blocks, epi, what, stream);
+            if (avg <= 16)
+                return launch_few_shape(split_kernel<FP8, 1, F, Epi>, a, G, split, 16, row_blocks, epi, what, stream);
+            if (avg <= 32)
+                return launch_few_shape(split_kernel<FP8, 2, F, Epi>, a, G, split, 32, row_blocks, epi, what, stream);
+            return launch_few_shape(split_kernel<FP8, 4, F, Epi>, a, G, split, 64, row_blocks, epi, what, stream);
         }
     }
-    return avg <= 8 ? launch_few_shape<FP8, 4, 2, 4, 1, F>(a, G, row_blocks, epi, what, stream)
-                    : launch_few_shape<FP8, 4, 2, 4, 2, F>(a, G, row_blocks, epi, what, stream);
+    if (avg <= 8)
+        return launch_few_shape(few_rows_kernel<FP8, 4, 2, 4, 1, F, Epi>, a, G, wide, 16, row_blocks, epi, what, stream);
+    return launch_few_shape(few_rows_kernel<FP8, 4, 2, 4, 2, F, Epi>, a, G, wide, 32, row_blocks, epi, what, stream);
 }
 
 // The low-latency cells: groups of few rows by launch_few, the others by

@@ -143,12 +143,6 @@ __global__ __launch_bounds__(NT) void fp8_tile_kernel(FewArgs a, Groups G, Epi e
         else
             open_ring<ST>(steps, issue);
     };
-    auto frag = [&](const lds_char *base, int r) {
-        Frag f;
-        f.lo = *(const __attribute__((address_space(3))) i32x4 *)RowStage<BM, NT>::at(base, r, lane >> 4);
-        f.hi = *(const __attribute__((address_space(3))) i32x4 *)RowStage<BM, NT>::at(base, r, 4 + (lane >> 4));
-        return f;
-    };
 
     const Tile cur = find_tile<BM, NT>(G, blockIdx.x, a.nt);
     if (cur.group < 0)
@@ -169,12 +163,12 @@ __global__ __launch_bounds__(NT) void fp8_tile_kernel(FewArgs a, Groups G, Epi e
                 c1 = F == Form::kGated ? w[1] : c0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    pf[i] = frag(pb, wn * 64 + i * 16 + (lane & 15));
+                    pf[i] = staged_frag(pb, wn * 64 + i * 16, lane);
             }
 #pragma unroll
             for (int m = 0; m < MQ; ++m) {
                 const int r = wm * (R / 2) + (ph * MQ + m) * 16 + (lane & 15);
-                qf[m] = frag(qb, r);
+                qf[m] = staged_frag(qb, r - (lane & 15), lane);
                 sc[m] = *(lds_float *)(qb + kQ + r * 4);
             }
         };
@@ -250,12 +244,12 @@ hipError_t launch_fp8_product(int64_t M, int N, int K, const void *a_q, const fl
     a.kbytes = K;
     const RowOut epi{static_cast<uint16_t *>(out)};
     a.active = 1;
-    // up to 64 rows the weight's bytes are the cost; past that the few-rows kernel,
-    // with a block for each 64 rows, still wins where tiles would leave most
-    // compute units idle (333 x 1000 x 1152: %FEW% us, in 24 tiles %TILES%)
+    // past 64 rows a block of the few-rows kernels for each 64, as long as all of
+    // them run at once (512 x 2048 x 4096, 256 blocks: 12.7 us, in 64 x 256 tiles
+    // 23.9; 512 x 4096 x 4096, 512 blocks: 24.0 and 24.1)
     const int64_t chunks = (M + kFewRows - 1) / kFewRows;
-    if (M <= kFewRows || chunks * ((N + BN - 1) / BN) < compute_units() / 2)
-        return launch_few<true, Form::kPlain>(a, G, M, int(M <= 16 ? 1 : chunks), epi, "fp8_product", stream);
+    if (M <= kFewRows || chunks * ((N + kSplitCols - 1) / kSplitCols) <= compute_units())
+        return launch_few<true, Form::kPlain>(a, G, M, int(chunks), epi, "fp8_product", stream);
     return launch_fp8_tiles<Form::kPlain>(a, G, M, 1, epi, "fp8_product", stream);
 }
 
