@@ -113,6 +113,14 @@ __device__ __forceinline__ Wide widen(const Frag &f)
     }
     return w;
 }
+__device__ __forceinline__ f32x4 mfma_step_wide(const Wide &a, const Wide &b)
+{
+    f32x4 c = {};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        c = mfma_bf16(a.v[k], b.v[k], c);
+    return c;
+}
 __device__ __forceinline__ f32x4 mfma_step_bf16(const Frag &a, const Frag &b, f32x4 c)
 {
     c = mfma_bf16(__builtin_bit_cast(bf16x8, a.lo), __builtin_bit_cast(bf16x8, b.lo), c);
@@ -206,13 +214,8 @@ __global__ __launch_bounds__(WN *WK *kWave, 2) void few_rows_kernel(FewArgs a, G
                 for (int i = 0; i < NW; ++i) {
                     const Wide p = widen(t.p[i]);
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        f32x4 part = {};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            part = mfma_bf16(p.v[k], q[m].v[k], part);
-                        acc[m][i] += part * (t.sq[m] * t.sp[i >= NW / 2]);
-                    }
+                    for (int m = 0; m < MT; ++m)
+                        acc[m][i] += mfma_step_wide(p, q[m]) * (t.sq[m] * t.sp[i >= NW / 2]);
                     __builtin_amdgcn_sched_barrier(0);  // one tile at a time: more would not fit the registers
                 }
             } else if constexpr (FP8) {
@@ -272,7 +275,15 @@ __global__ __launch_bounds__(WN *WK *kWave, 2) void few_rows_kernel(FewArgs a, G
 // its own K steps in LDS of its own, whole 128-byte lines a row, and nobody else
 // reads them, so the loop has no barrier: as soon as a step is in registers the
 // next is sent off behind its matrix instructions.  The waves' sums meet at the end.
+// Gated FP8 rows, whose codes need the largest of 128 activations: 128 gate and
+// their 128 up columns a block, and four waves, which then fill the LDS.
 constexpr int kSplitCols = 64;
+template <bool BLOCK_WIDE>
+struct SplitShape {
+    static constexpr int kWaves = BLOCK_WIDE ? 4 : NT / kWave;
+    static constexpr int kCols = BLOCK_WIDE ? BN : kSplitCols;  // of the weight
+    static constexpr int kThreads = kWaves * kWave;
+};
 
 // 16 rows from r0 of a staged K step.
 __device__ __forceinline__ Frag staged_frag(const lds_char *base, int r0, int lane)
@@ -286,12 +297,14 @@ __device__ __forceinline__ Frag staged_frag(const lds_char *base, int r0, int la
 }
 
 template <bool FP8, int MT, Form F, class Epi>
-__global__ __launch_bounds__(NT, MT == 1 ? 4 : 2) void split_kernel(FewArgs a, Groups G, Epi epi)
+__global__ __launch_bounds__(SplitShape<Epi::kBlockWide>::kThreads, Epi::kBlockWide ? 1 : MT == 1 ? 4 : 2) void
+split_kernel(FewArgs a, Groups G, Epi epi)
 {
-    static_assert(!FP8 || F == Form::kPlain, "a gated FP8 row needs a block of 128 columns");
-    constexpr int W = NT / kWave, NW = kSplitCols / 16;
-    constexpr int kCols = F == Form::kGated ? kSplitCols / 2 : kSplitCols;
-    using PR = NearRowStage<kSplitCols / 2, kWave>;
+    using Shape = SplitShape<Epi::kBlockWide>;
+    constexpr int W = Shape::kWaves, NW = Shape::kCols / 16;
+    constexpr int kCols = F == Form::kGated ? Shape::kCols / 2 : Shape::kCols;
+    constexpr bool kWiden = FP8 && F == Form::kGated;
+    using PR = NearRowStage<Shape::kCols / 2, kWave>;
     using QR = NearRowStage<16 * MT, kWave>;
     constexpr int kQ = 2 * PR::kBytes, kOwn = kQ + QR::kBytes;
     static_assert(kOwn >= MT * NW * kWave * 16, "a wave's sums take the place of its last step");
@@ -299,7 +312,7 @@ __global__ __launch_bounds__(NT, MT == 1 ? 4 : 2) void split_kernel(FewArgs a, G
     int g = blockIdx.x / a.nt;
     const int n0 = int(blockIdx.x % a.nt) * kCols;
     if (a.active < G.num) {
-        g = find_group<NT>(G, g, reinterpret_cast<int *>(smem));
+        g = find_group<Shape::kThreads>(G, g, reinterpret_cast<int *>(smem));
         if (g < 0)
             return;
     }
@@ -314,7 +327,7 @@ __global__ __launch_bounds__(NT, MT == 1 ? 4 : 2) void split_kernel(FewArgs a, G
     PR pr[2];  // gate and up columns, or the two halves
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int c0 = F == Form::kGated ? n0 : n0 + h * (kSplitCols / 2);
+        const int c0 = F == Form::kGated ? n0 : n0 + h * (Shape::kCols / 2);
         const int c = c0 < a.N ? c0 : a.N - 1;
         const int64_t row = c + (F == Form::kGated ? h * int64_t(a.N) : 0);
         pr[h].init(lane, a.p + int64_t(e) * a.p_expert + row * a.ldp, [&](int, int r) {
@@ -322,13 +335,14 @@ __global__ __launch_bounds__(NT, MT == 1 ? 4 : 2) void split_kernel(FewArgs a, G
         });
     }
     const float *ps = FP8 ? a.p_scale + e * a.p_scales + int64_t(n0 >> 7) * steps : nullptr;
+    const float *ps_up = kWiden ? ps + int64_t(a.N >> 7) * steps : ps;
     for (int m0 = int(blockIdx.y) * 16 * MT; m0 < rows; m0 += int(gridDim.y) * 16 * MT) {
         QR qr;
         qr.init(lane, a.q + (start + m0) * a.ldq, [&](int, int r) {
             return uint32_t(m0 + r < rows ? r : rows - 1 - m0) * uint32_t(a.ldq);
         });
         const float *qs[MT];
-        float next[MT], next_c = 0.0f;  // scales of the step on its way
+        float next[MT], next_c = 0.0f, next_up = 0.0f;  // scales of the step on its way
         if constexpr (FP8) {
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
@@ -340,6 +354,7 @@ __global__ __launch_bounds__(NT, MT == 1 ? 4 : 2) void split_kernel(FewArgs a, G
             const int64_t kb = int64_t(s) * kStepBytes;
             if constexpr (FP8) {
                 next_c = ps[s];
+                next_up = kWiden ? ps_up[s] : 0.0f;
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
                     next[m] = qs[m][s];
@@ -355,12 +370,15 @@ __global__ __launch_bounds__(NT, MT == 1 ? 4 : 2) void split_kernel(FewArgs a, G
         for (int s = s0; s < s1; ++s) {
             landed<0>();
             Frag p[NW], q[MT];
-            float scale[MT];
+            float scale[2][MT];
             if constexpr (FP8) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
-                    scale[m] = next[m] * next_c;
-                    hold(scale[m]);  // here: behind send() it would wait for the next step's loads
+                    scale[0][m] = next[m] * next_c;
+                    scale[1][m] = next[m] * next_up;
+                    hold(scale[0][m]);  // here: behind send() it would wait for the next step's loads
+                    if (kWiden)
+                        hold(scale[1][m]);
                 }
             }
 #pragma unroll
@@ -373,15 +391,29 @@ __global__ __launch_bounds__(NT, MT == 1 ? 4 : 2) void split_kernel(FewArgs a, G
             asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
             if (s + 1 < s1)
                 send(s + 1);
+            if constexpr (kWiden) {
+                Wide qw[MT];
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+                for (int m = 0; m < MT; ++m)
+                    qw[m] = widen(q[m]);
 #pragma unroll
                 for (int i = 0; i < NW; ++i) {
-                    if constexpr (FP8)
-                        acc[m][i] += mfma_step_fp8(p[i], q[m]) * scale[m];
-                    else
-                        acc[m][i] = mfma_step_bf16(p[i], q[m], acc[m][i]);
+                    const Wide pw = widen(p[i]);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+                        acc[m][i] += mfma_step_wide(pw, qw[m]) * scale[i >= NW / 2][m];
                 }
+            } else {
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int i = 0; i < NW; ++i) {
+                        if constexpr (FP8)
+                            acc[m][i] += mfma_step_fp8(p[i], q[m]) * scale[0][m];
+                        else
+                            acc[m][i] = mfma_step_bf16(p[i], q[m], acc[m][i]);
+                    }
+            }
         }
         f32x4 *sums = reinterpret_cast<f32x4 *>(smem);
 #pragma unroll
@@ -390,7 +422,20 @@ __global__ __launch_bounds__(NT, MT == 1 ? 4 : 2) void split_kernel(FewArgs a, G
             for (int i = 0; i < NW; ++i)
                 sums[wave * (kOwn / 16) + (m * NW + i) * kWave + lane] = acc[m][i];
         __syncthreads();
-        if (wave < 2 * MT) {  // two column tiles each: neighbours, or a gate and its up tile
+        const Tile t{g, m0, rows, int(blockIdx.x % a.nt)};
+        if constexpr (Epi::kBlockWide) {  // wave w: 32 gate columns and their up columns
+            f32x4 sum[MT][4] = {};
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = 2 * wave + (i & 1) + (i >> 1) * (NW / 2);
+#pragma unroll
+                    for (int w = 0; w < W; ++w)
+                        sum[m][i] += sums[w * (kOwn / 16) + (m * NW + at) * kWave + lane];
+                }
+            epi.template store_block<MT, 4, W, 16 * MT>(t, start, true, wave, 0, n0 + wave * 32, a.N, sum, lane);
+        } else if (wave < 2 * MT) {  // two column tiles each: neighbours, or a gate and its up tile
             const int m = wave >> 1, h = wave & 1;
             const int i0 = F == Form::kGated ? h : 2 * h, i1 = F == Form::kGated ? h + 2 : i0 + 1;
             f32x4 sum[1][2] = {};
@@ -399,8 +444,7 @@ __global__ __launch_bounds__(NT, MT == 1 ? 4 : 2) void split_kernel(FewArgs a, G
                 sum[0][0] += sums[w * (kOwn / 16) + (m * NW + i0) * kWave + lane];
                 sum[0][1] += sums[w * (kOwn / 16) + (m * NW + i1) * kWave + lane];
             }
-            epi.store(Tile{g, m0, rows, int(blockIdx.x % a.nt)}, start, m0 + m * 16, n0 + h * (kCols / 2), a.N, sum,
-                      lane);
+            epi.store(t, start, m0 + m * 16, n0 + h * (kCols / 2), a.N, sum, lane);
         }
         if (m0 + int(gridDim.y) * 16 * MT < rows)
             __syncthreads();  // the sums are read before the next rows are staged
@@ -414,8 +458,8 @@ __global__ __launch_bounds__(NT, MT == 1 ? 4 : 2) void split_kernel(FewArgs a, G
 constexpr int kFewRows = 64;
 
 template <class Kernel, class Epi>
-hipError_t launch_few_shape(Kernel kernel, FewArgs a, const Groups &G, int cols, int tile_rows, int row_blocks,
-                            const Epi &epi, const char *what, hipStream_t stream)
+hipError_t launch_few_shape(Kernel kernel, int threads, FewArgs a, const Groups &G, int cols, int tile_rows,
+                            int row_blocks, const Epi &epi, const char *what, hipStream_t stream)
 {
     a.nt = unsigned((a.N + cols - 1) / cols);
     const int64_t blocks = int64_t(a.nt) * a.active;
@@ -424,7 +468,7 @@ hipError_t launch_few_shape(Kernel kernel, FewArgs a, const Groups &G, int cols,
     if (log_enabled())
         log_launch("%s: groups<=%d of %d N=%d K bytes=%d few rows %d cols=%d blocks=%lld x %d", what, a.active,
                    G.num, a.N, a.kbytes, tile_rows, cols, (long long)blocks, row_blocks);
-    hipLaunchKernelGGL(kernel, dim3(unsigned(blocks), row_blocks), dim3(NT), 0, stream, a, G, epi);
+    hipLaunchKernelGGL(kernel, dim3(unsigned(blocks), row_blocks), dim3(threads), 0, stream, a, G, epi);
     return hipGetLastError();
 }
 
@@ -435,19 +479,22 @@ template <bool FP8, Form F, class Epi>
 hipError_t launch_few(FewArgs a, const Groups &G, int64_t avg, int row_blocks, const Epi &epi, const char *what,
                       hipStream_t stream)
 {
-    constexpr int wide = F == Form::kGated ? 128 : 256, split = wide / (256 / kSplitCols);
-    if constexpr (!Epi::kBlockWide) {
-        if (int64_t((a.N + wide - 1) / wide) * a.active * row_blocks < compute_units()) {
-            if (avg <= 16)
-                return launch_few_shape(split_kernel<FP8, 1, F, Epi>, a, G, split, 16, row_blocks, epi, what, stream);
-            if (avg <= 32)
-                return launch_few_shape(split_kernel<FP8, 2, F, Epi>, a, G, split, 32, row_blocks, epi, what, stream);
-            return launch_few_shape(split_kernel<FP8, 4, F, Epi>, a, G, split, 64, row_blocks, epi, what, stream);
-        }
+    using Split = SplitShape<Epi::kBlockWide>;
+    constexpr int wide = F == Form::kGated ? BN / 2 : BN, split = wide / (BN / Split::kCols), threads = Split::kThreads;
+    auto launch = [&](auto kernel, int n, int cols, int tile_rows) {
+        return launch_few_shape(kernel, n, a, G, cols, tile_rows, row_blocks, epi, what, stream);
+    };
+    if (int64_t((a.N + wide - 1) / wide) * a.active * row_blocks < compute_units()) {
+        if (avg <= 16)
+            return launch(split_kernel<FP8, 1, F, Epi>, threads, split, 16);
+        if (avg <= 32 || Epi::kBlockWide)
+            return launch(split_kernel<FP8, 2, F, Epi>, threads, split, 32);
+        if constexpr (!Epi::kBlockWide)
+            return launch(split_kernel<FP8, 4, F, Epi>, threads, split, 64);
     }
     if (avg <= 8)
-        return launch_few_shape(few_rows_kernel<FP8, 4, 2, 4, 1, F, Epi>, a, G, wide, 16, row_blocks, epi, what, stream);
-    return launch_few_shape(few_rows_kernel<FP8, 4, 2, 4, 2, F, Epi>, a, G, wide, 32, row_blocks, epi, what, stream);
+        return launch(few_rows_kernel<FP8, 4, 2, 4, 1, F, Epi>, NT, wide, 16);
+    return launch(few_rows_kernel<FP8, 4, 2, 4, 2, F, Epi>, NT, wide, 32);
 }
 
 // The low-latency cells: groups of few rows by launch_few, the others by
