@@ -472,41 +472,59 @@ hipError_t launch_few_shape(Kernel kernel, int threads, FewArgs a, const Groups 
     return hipGetLastError();
 }
 
-// avg: rows of an active group on average.  Blocks of 256 columns (128 gated)
-// where that makes one for every compute unit, else of 64 (32) with K split: one
-// token's eight bf16 experts of 768 x 2048, gated, took 34 us in 48 wide blocks.
+// Rows of a group up to which wide blocks beat tiles (16 experts of 2048 x 7168:
+// bf16 of 4 rows 260 against 273 us, of 25 rows 457 against 280; FP8 64 experts of
+// 768 x 2048, 4 rows 72.0 against 75.6, 8 rows 76.5 against 68.8).
+template <bool FP8>
+constexpr int kWideRows = FP8 ? 4 : 8;
+
+// Whether blocks of 256 columns (128 gated) would leave compute units idle; then
+// they take 64 (32) columns and split K: one token's eight bf16 experts of
+// 768 x 2048, gated, 11.6 us in 192 blocks, 34 in 48 wide ones.
+template <Form F>
+bool splits_k(const FewArgs &a, int64_t row_blocks)
+{
+    constexpr int wide = F == Form::kGated ? BN / 2 : BN;
+    return int64_t((a.N + wide - 1) / wide) * a.active * row_blocks < compute_units();
+}
+
+// avg: rows of an active group on average.
 template <bool FP8, Form F, class Epi>
 hipError_t launch_few(FewArgs a, const Groups &G, int64_t avg, int row_blocks, const Epi &epi, const char *what,
                       hipStream_t stream)
 {
     using Split = SplitShape<Epi::kBlockWide>;
-    constexpr int wide = F == Form::kGated ? BN / 2 : BN, split = wide / (BN / Split::kCols), threads = Split::kThreads;
+    constexpr int wide = F == Form::kGated ? BN / 2 : BN, split = wide / (BN / Split::kCols);
+    constexpr int threads = Split::kThreads;
     auto launch = [&](auto kernel, int n, int cols, int tile_rows) {
         return launch_few_shape(kernel, n, a, G, cols, tile_rows, row_blocks, epi, what, stream);
     };
-    if (int64_t((a.N + wide - 1) / wide) * a.active * row_blocks < compute_units()) {
-        if (avg <= 16)
-            return launch(split_kernel<FP8, 1, F, Epi>, threads, split, 16);
-        if (avg <= 32 || Epi::kBlockWide)
-            return launch(split_kernel<FP8, 2, F, Epi>, threads, split, 32);
-        if constexpr (!Epi::kBlockWide)
-            return launch(split_kernel<FP8, 4, F, Epi>, threads, split, 64);
-    }
-    if (avg <= 8)
+    if (!splits_k<F>(a, row_blocks))
         return launch(few_rows_kernel<FP8, 4, 2, 4, 1, F, Epi>, NT, wide, 16);
-    return launch(few_rows_kernel<FP8, 4, 2, 4, 2, F, Epi>, NT, wide, 32);
+    if constexpr (!Epi::kBlockWide) {
+        if (avg > 32)
+            return launch(split_kernel<FP8, 4, F, Epi>, threads, split, 64);
+        if (avg > 16)
+            return launch(split_kernel<FP8, 2, F, Epi>, threads, split, 32);
+    }
+    return launch(split_kernel<FP8, 1, F, Epi>, threads, split, 16);
 }
 
 // The low-latency cells: groups of few rows by launch_few, the others by
 // tiles(G, most): both walk the groups on the device, which alone knows their
-// rows; most bounds the groups left for the tiles.
+// rows; most bounds the groups left for the tiles.  With K split the border is
+// where groups of more than 64 rows become common (eight bf16 experts of
+// 768 x 2048 with 40 rows each: 26.2 against 39.7 us, with 60: 57.5 against 40.4),
+// for gated FP8, whose blocks take 16 rows, lower (8 rows: 18.9 against 24.0 us, 12
+// rows: 27.9 against 24.0).
 template <bool FP8, Form F, class Epi, class Tiles>
 hipError_t launch_cells(FewArgs a, Groups G, int64_t max_pairs, const Epi &epi, const char *what,
                         hipStream_t stream, Tiles tiles)
 {
     a.active = int(max_pairs < G.num ? max_pairs : G.num);
     const int64_t avg = max_pairs / a.active;
-    if (avg <= kFewRows / 2) {
+    const int most_avg = splits_k<F>(a, 1) ? Epi::kBlockWide ? 8 : 48 : kWideRows<FP8>;
+    if (avg <= most_avg) {
         Groups few = G;
         few.max_rows = kFewRows;
         hipError_t e = launch_few<FP8, F>(a, few, avg, 1, epi, what, stream);

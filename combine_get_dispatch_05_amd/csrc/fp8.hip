@@ -77,7 +77,8 @@ struct GatedFp8Out {
 // the rows, one load a wave, so that every wave counts the same loads: waves 0
 // to 3 the BM token scales (some twice where BM is 64), the others the two
 // weight scales of the tile: its column blocks, or its gate and its up block.
-template <int BM, Form F, class Epi>
+// WIDEN: both operands to bf16 first, as in few_rows.h.
+template <int BM, bool WIDEN, Form F, class Epi>
 __global__ __launch_bounds__(NT) void fp8_tile_kernel(FewArgs a, Groups G, Epi epi)
 {
     using QS = NearRowStage<BM, NT>;
@@ -178,12 +179,30 @@ __global__ __launch_bounds__(NT) void fp8_tile_kernel(FewArgs a, Groups G, Epi e
                 hold(qf[m].lo);
                 hold(qf[m].hi);
             }
+            float s0[MQ], s1[MQ];
 #pragma unroll
             for (int m = 0; m < MQ; ++m) {
-                const float s0 = sc[m] * c0, s1 = F == Form::kGated ? sc[m] * c1 : s0;
+                s0[m] = sc[m] * c0;
+                s1[m] = F == Form::kGated ? sc[m] * c1 : s0[m];
+            }
+            if constexpr (WIDEN) {
+                Wide q[MQ];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[ph * MQ + m][i] += mfma_step_fp8(pf[i], qf[m]) * (i < 2 ? s0 : s1);
+                for (int m = 0; m < MQ; ++m)
+                    q[m] = widen(qf[m]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const Wide p = widen(pf[i]);
+#pragma unroll
+                    for (int m = 0; m < MQ; ++m)
+                        acc[ph * MQ + m][i] += mfma_step_wide(p, q[m]) * (i < 2 ? s0[m] : s1[m]);
+                }
+            } else {
+#pragma unroll
+                for (int m = 0; m < MQ; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[ph * MQ + m][i] += mfma_step_fp8(pf[i], qf[m]) * (i < 2 ? s0[m] : s1[m]);
             }
 #pragma unroll
             for (int m = 0; m < MQ; ++m)
@@ -204,6 +223,13 @@ __global__ __launch_bounds__(NT) void fp8_tile_kernel(FewArgs a, Groups G, Epi e
     });
 }
 
+// Activations of a batch below which one of them in a neighbouring 8-bit code
+// shows in the norm of the result: a large one, 10 times their mean square's root
+// and a sixteenth off, is 0.6 of that root, 1.7e-3 of the norm of 2^17 of them, as
+// much as the result's own rounding.  Those batches pay for widening (100 tokens on eight experts,
+// 2048 x 4096: 56 us instead of 42).
+constexpr int64_t kFewActivations = int64_t(1) << 17;
+
 template <Form F, class Epi>
 hipError_t launch_fp8_tiles(FewArgs a, const Groups &G, int64_t rows, int64_t max_tiles, const Epi &epi,
                             const char *what, hipStream_t stream)
@@ -220,10 +246,15 @@ hipError_t launch_fp8_tiles(FewArgs a, const Groups &G, int64_t rows, int64_t ma
         log_launch("%s: rows<=%lld groups=%d N=%d K=%d tile=%dx%d blocks=%lld", what, (long long)rows,
                    G.num, a.N, a.kbytes, bm, BN, (long long)mt * a.nt);
     const dim3 grid(unsigned(blocks_for_tiles(mt * a.nt)));
+    if constexpr (F == Form::kGated)
+        if (bm == 64 && rows * a.N < kFewActivations) {
+            hipLaunchKernelGGL((fp8_tile_kernel<64, true, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
+            return hipGetLastError();
+        }
     if (bm == 256)
-        hipLaunchKernelGGL((fp8_tile_kernel<256, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
+        hipLaunchKernelGGL((fp8_tile_kernel<256, false, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
     else
-        hipLaunchKernelGGL((fp8_tile_kernel<64, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
+        hipLaunchKernelGGL((fp8_tile_kernel<64, false, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
     return hipGetLastError();
 }
 
@@ -244,11 +275,13 @@ hipError_t launch_fp8_product(int64_t M, int N, int K, const void *a_q, const fl
     a.kbytes = K;
     const RowOut epi{static_cast<uint16_t *>(out)};
     a.active = 1;
-    // past 64 rows a block of the few-rows kernels for each 64, as long as all of
-    // them run at once (512 x 2048 x 4096, 256 blocks: 12.7 us, in 64 x 256 tiles
-    // 23.9; 512 x 4096 x 4096, 512 blocks: 24.0 and 24.1)
+    // K is split up to 64 rows where that fills idle compute units, past that in a
+    // block for each 64 as long as all of them run at once (512 x 2048 x 4096, 256
+    // blocks: 12.7 us, in 64 x 256 tiles 23.9; 512 x 4096 x 4096, 512 blocks: 24.0
+    // and 24.1).
     const int64_t chunks = (M + kFewRows - 1) / kFewRows;
-    if (M <= kFewRows || chunks * ((N + kSplitCols - 1) / kSplitCols) <= compute_units())
+    const bool once = chunks * ((N + kSplitCols - 1) / kSplitCols) <= compute_units();
+    if (splits_k<Form::kPlain>(a, chunks) ? M <= kFewRows || once : M <= kWideRows<true>)
         return launch_few<true, Form::kPlain>(a, G, M, int(chunks), epi, "fp8_product", stream);
     return launch_fp8_tiles<Form::kPlain>(a, G, M, 1, epi, "fp8_product", stream);
 }
