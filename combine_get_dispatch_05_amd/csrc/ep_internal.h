@@ -194,11 +194,14 @@ int compute_units();
 // Row tile of the tile kernels.  A 256-row tile reads a group's weight once for
 // up to 256 rows and shortens its last tile to what is there.  64-row tiles
 // where a group has no more rows on average (their third LDS stage hides more
-// of the weight's latency), or where the larger ones would not fill the card.
+// of the weight's latency; 64 experts of 51 rows, 352 x 256: 11.1 against 15.0 us),
+// or where the larger ones, which take 2.5 times as long, leave half of the card
+// idle (FP8, K = 2048: 1500 x 4096, 96 tiles, 30.7 against 35.0 us; 3000 x 4096, 208
+// tiles, 46.2 against 38.1).
 inline int tile_rows(int64_t rows, int64_t groups, int64_t column_tiles)
 {
     groups = groups > 0 ? groups : 1;
-    return rows / groups > 64 && (rows / 256 + groups) * column_tiles >= compute_units() ? 256 : 64;
+    return rows / groups > 64 && (rows / 256 + groups) * column_tiles * 2 > compute_units() ? 256 : 64;
 }
 
 // Shared with the entry points outside ep_api.hip.
