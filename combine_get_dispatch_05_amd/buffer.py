@@ -573,14 +573,14 @@ class Buffer:
             aq = torch.empty(cells + (inter,), dtype=torch.uint8, device=q.device)
             asc = torch.empty(cells + (inter // 128,), dtype=torch.float32, device=q.device)
             abi.check(abi.lib().ep_ll_expert_ffn_fp8(
-                ctypes.byref(d), S, inter, abi.address(q), abi.address(sc), abi.address(packed_count), abi.address(q13),
-                abi.address(s13), abi.address(q2), abi.address(s2), abi.address(aq), abi.address(asc), abi.address(out), s),
-                "ep_ll_expert_ffn_fp8")
+                ctypes.byref(d), S, inter, abi.address(q), abi.address(sc), abi.address(packed_count),
+                abi.address(q13), abi.address(s13), abi.address(q2), abi.address(s2), abi.address(aq),
+                abi.address(asc), abi.address(out), s), "ep_ll_expert_ffn_fp8")
         else:
             act = torch.empty(cells + (inter,), dtype=torch.bfloat16, device=q.device)
             abi.check(abi.lib().ep_ll_expert_ffn(
-                ctypes.byref(d), S, inter, abi.address(x), abi.address(packed_count), abi.address(w13), abi.address(w2),
-                abi.address(act), abi.address(out), s), "ep_ll_expert_ffn")
+                ctypes.byref(d), S, inter, abi.address(x), abi.address(packed_count), abi.address(w13),
+                abi.address(w2), abi.address(act), abi.address(out), s), "ep_ll_expert_ffn")
         return out
 
     def expert_rows(self, recv_topk_idx: torch.Tensor, layout,

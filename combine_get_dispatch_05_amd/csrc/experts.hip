@@ -44,7 +44,10 @@ __device__ __forceinline__ unsigned slots_of(const int64_t *ids, int64_t i, int6
 }
 
 // One block for each expert counts its pairs; together they also mark every
-// (row, slot) as having no pair.
+// (row, slot) as having no pair.  Each reads the whole id table (from L2), which
+// for the experts of one node is less than a sort would move: 11 us, and 15 for the
+// places, for 21 thousand rows of 8 slots and 32 experts; 3.8 and 6.0 for 3 thousand
+// of 6 and 64.
 __global__ __launch_bounds__(kGroupBlock) void count_pairs_kernel(
     const int64_t *__restrict__ ids, const int32_t *__restrict__ prefix, int64_t n, int K, int epr,
     int32_t *__restrict__ counts, int32_t *__restrict__ row_pair)
@@ -310,7 +313,11 @@ struct GatedBack {
 // Tiles of BM rows of one group by BN columns, with as many LDS stages as fit.
 // A block works through every gridDim.x-th tile: it looks up the next one while
 // the first stage of this one arrives, and sends off the next one's first stage
-// before it stores this one.
+// before it stores this one.  At 32 experts of 2048 x 7168 with about 1024 rows each
+// the gated product takes 1.79 ms (1077 TFLOP/s; the product of equal 8192 x 8192 x
+// 8192 matrices reaches 1620 on the same card), the down product 1.08, the gate's
+// backward 1.28, dx 1.89: the matrix cores' clock under load and the wait for a
+// stage's loads, which two stages of 64 KB do not hide, are what is left.
 template <int BM, bool PCOL, Form F, class Epi>
 __global__ __launch_bounds__(NT) void tile_kernel(TileArgs a, Groups G, Epi epi)
 {
@@ -591,7 +598,8 @@ __device__ __forceinline__ void weight_grad(const GradArgs &a, lds_char *lds, un
 
 // Both weight gradients: dW2 (rows of dy picked), then dW13 (rows of x picked), so
 // that the second fills what the first leaves idle at its end.  Its tiles start
-// at the block after the first's last.
+// at the block after the first's last.  (The 32 experts above: 3.3 ms, 874 TFLOP/s;
+// K is a group's rows, and both operands come through the transposing read.)
 __global__ __launch_bounds__(NT) void weight_grads_kernel(GradArgs dw2, GradArgs dw13)
 {
     __shared__ __attribute__((aligned(128))) char smem[kGradLds];
@@ -606,7 +614,8 @@ __global__ __launch_bounds__(NT) void weight_grads_kernel(GradArgs dw2, GradArgs
 
 // Rows with no pair (zero) or several (their fp32 terms in slot order); rows of
 // one pair are already written.  With parts: also every slot's routing-weight
-// gradient, the sum of its pair's column tiles in order.
+// gradient, the sum of its pair's column tiles in order.  Bound by HBM (21 thousand
+// rows of 7168: 155 us).
 __global__ __launch_bounds__(256) void rows_kernel(const int32_t *__restrict__ row_pair, int64_t rows, int K, int N,
                                                    const int32_t *__restrict__ pair_row,
                                                    const float *__restrict__ terms,

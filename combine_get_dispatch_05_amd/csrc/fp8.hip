@@ -77,6 +77,10 @@ struct GatedFp8Out {
 // the rows, one load a wave, so that every wave counts the same loads: waves 0
 // to 3 the BM token scales (some twice where BM is 64), the others the two
 // weight scales of the tile: its column blocks, or its gate and its up block.
+// 8192 x 4096 x 7168: 232 us, 2.07 PFLOP/s (the FP8 product of equal 8192 x 8192 x
+// 8192 matrices reaches 3.2 on the same card), bound by the scaled sums, which take
+// vector instructions that the matrix cores wait for.  64 experts of 2048 x 7168 with
+// 128 rows each: 0.52 and 0.30 ms, 3.0 GB at 3.6 TB/s.
 // WIDEN: both operands to bf16 first, as in few_rows.h.
 template <int BM, bool WIDEN, Form F, class Epi>
 __global__ __launch_bounds__(NT) void fp8_tile_kernel(FewArgs a, Groups G, Epi epi)

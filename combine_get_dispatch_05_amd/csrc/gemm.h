@@ -197,7 +197,8 @@ struct NearRowStage {
             tid = here(tid);
 #pragma unroll
             for (int j = J0; j < J; j += JS) {
-                load_lds16(kb + RowStage<ROWS, NT>::byte_of(tid, j) >= kbytes ? reinterpret_cast<const char *>(kZero16) : base + kb + off[j],
+                const bool past = kb + RowStage<ROWS, NT>::byte_of(tid, j) >= kbytes;
+                load_lds16(past ? reinterpret_cast<const char *>(kZero16) : base + kb + off[j],
                            lds + (j * NT + wave * kWave) * 16);
             }
         }
