@@ -85,3 +85,45 @@ def test_fp8_activations_of_small_batches_keep_their_codes(monkeypatch, T, H, I,
     plain = base.ffn_ref
     monkeypatch.setattr(base, "ffn_ref", lambda x, w13, w2, fp8=False: plain(x, w13, w2))
     base.test_low_latency_expert_ffn_fp8(T, H, I, E, R, K, 0.0)
+
+
+@pytest.mark.parametrize("M,N,K", [(12, 200, 384), (40, 200, 384), (300, 200, 384), (5000, 520, 256)])
+def test_not_finite_row_of_a_product_stays_alone(M, N, K):
+    g = base.gen(M)
+    (q, sc), w = base.fp8_rows(g, (M, K)), base.fp8_weight(g, (N, K))
+    want = base.epm.fp8_product((q, sc), w)
+    sc = sc.clone()
+    sc[M // 3] = float("nan")
+    sc[M - 1, 0] = float("inf")
+    got = base.epm.fp8_product((q, sc), w)
+    keep = torch.ones(M, dtype=torch.bool, device="cuda")
+    keep[M // 3] = keep[M - 1] = False
+    assert torch.equal(got[keep], want[keep])
+    assert got[M // 3].isnan().all() and not got[M - 1].isfinite().any()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("T,E,R,K", [(6, 8, 4, 2), (60, 4, 2, 2), (200, 3, 1, 2)])
+def test_unused_cells_and_experts_may_hold_anything(T, E, R, K, fp8):
+    g = base.gen(T)
+    H, I = 256, 128
+    topk, _ = base.routing(g, T, E, K, 0.1)
+    topk = torch.where(topk == 1, -1, topk)  # expert 1 has no row
+    buf = base.epm.Buffer(R, E)
+    packed, count, h, _, _ = buf.low_latency_dispatch(base.normal(g, (T, H)), topk, T + 2, use_fp8=fp8)
+    if fp8:
+        w13, w2 = base.fp8_weight(g, (E, 2 * I, H)), base.fp8_weight(g, (E, H, I))
+        cells, weights = packed[1], (w13[1], w2[1])
+    else:
+        w13, w2 = base.normal(g, (E, 2 * I, H), H ** -0.5), base.normal(g, (E, H, I), I ** -0.5)
+        cells, weights = packed, (w13, w2)
+    unused = torch.arange(T + 2, device="cuda") >= count[..., None]
+    outs = []
+    for fill in (0.0, float("nan")):
+        cells[unused] = fill
+        for w in weights:
+            w[1] = fill
+        out = torch.full((E // R, R, T + 2, H), 7.0, dtype=torch.bfloat16, device="cuda")
+        outs.append(buf.low_latency_expert_ffn(packed, count, h, w13, w2, out=out))
+    assert (outs[0][unused] == 7.0).all() and outs[0].isfinite().all()
+    assert torch.equal(outs[0], outs[1])
