@@ -686,6 +686,51 @@ hipError_t launch_tiles(TileArgs a, const Groups &G, int64_t rows, int64_t group
     return hipGetLastError();
 }
 
+// A forward product: K split or tiles.
+template <Form F, class Epi>
+hipError_t launch_bf16(const FewArgs &a, const Groups &G, int64_t pairs, int64_t most_rows, const Epi &epi,
+                       const char *what, hipStream_t stream)
+{
+    return launch_groups<false, F>(a, G, pairs, most_rows, epi, what, stream, [&](const Groups &T, int64_t most) {
+        TileArgs t{};
+        t.q = a.q;
+        t.q_rows = a.q_rows;
+        t.ldq = a.ldq;
+        t.p = a.p;
+        t.p_expert = a.p_expert;
+        t.ldp = a.ldp;
+        t.N = a.N;
+        t.K = a.kbytes / 2;
+        return launch_tiles<false, F>(t, T, pairs, most, epi, what, stream);
+    });
+}
+
+// The products with w13 and with w2.
+FewArgs gated_args(const void *x, const void *w13, int H, int I)
+{
+    FewArgs a{};
+    a.q = static_cast<const char *>(x);
+    a.ldq = int64_t(H) * 2;
+    a.p = static_cast<const char *>(w13);
+    a.p_expert = int64_t(2) * I * H * 2;
+    a.ldp = int64_t(H) * 2;
+    a.N = I;
+    a.kbytes = H * 2;
+    return a;
+}
+FewArgs down_args(const void *act, const void *w2, int H, int I)
+{
+    FewArgs a{};
+    a.q = static_cast<const char *>(act);
+    a.ldq = int64_t(I) * 2;
+    a.p = static_cast<const char *>(w2);
+    a.p_expert = int64_t(I) * H * 2;
+    a.ldp = int64_t(I) * 2;
+    a.N = H;
+    a.kbytes = I * 2;
+    return a;
+}
+
 Groups contiguous(const int32_t *offsets, int num)
 {
     return Groups{offsets, nullptr, 0, num, 1, num, 1, kNoLimit};
@@ -738,31 +783,16 @@ hipError_t launch_expert_ffn(const ExpertFfn &f, const void *x, const void *w13,
 {
     const int H = f.hidden, I = f.inter;
     const Groups G = contiguous(f.offsets, f.experts);
-    TileArgs a{};
-    a.q = static_cast<const char *>(x);
+    const int64_t most_rows = f.pairs / f.topk;  // the batch's tokens: each has one row with an expert
+    FewArgs a = gated_args(x, w13, H, I);
     a.q_rows = f.pair_row;
-    a.ldq = int64_t(H) * 2;
-    a.p = static_cast<const char *>(w13);
-    a.p_expert = int64_t(2) * I * H * 2;
-    a.ldp = int64_t(H) * 2;
-    a.N = I;
-    a.K = H;
-    hipError_t e = launch_tiles<false, Form::kGated>(
-        a, G, f.pairs, f.experts, GatedOut{static_cast<uint16_t *>(act), gate_up}, "expert_ffn gated", stream);
+    hipError_t e = launch_bf16<Form::kGated>(
+        a, G, f.pairs, most_rows, GatedOut{static_cast<uint16_t *>(act), gate_up}, "expert_ffn gated", stream);
     if (e != hipSuccess)
         return e;
-    a.q = static_cast<const char *>(act);
-    a.q_rows = nullptr;
-    a.ldq = int64_t(I) * 2;
-    a.p = static_cast<const char *>(w2);
-    a.p_expert = int64_t(I) * H * 2;
-    a.ldp = int64_t(I) * 2;
-    a.N = H;
-    a.K = I;
-    e = launch_tiles<false, Form::kPlain>(
-        a, G, f.pairs, f.experts,
-        PairOut{f.pair_row, f.pair_slot, f.weights, static_cast<uint16_t *>(y), terms},
-        "expert_ffn down", stream);
+    e = launch_bf16<Form::kPlain>(down_args(act, w2, H, I), G, f.pairs, most_rows,
+                                  PairOut{f.pair_row, f.pair_slot, f.weights, static_cast<uint16_t *>(y), terms},
+                                  "expert_ffn down", stream);
     if (e != hipSuccess)
         return e;
     return launch_rows(f, terms, y, nullptr, 0, nullptr, stream);
@@ -847,46 +877,13 @@ hipError_t launch_ll_expert_ffn(int E, int R, int slots, int H, int I, int64_t m
                                 const void *w2, void *act, void *out, hipStream_t stream)
 {
     const Groups G{nullptr, counts, slots, E, R, E / R, 1, kNoLimit};
-    FewArgs a{};
-    a.q = static_cast<const char *>(packed);
-    a.ldq = int64_t(H) * 2;
-    a.p = static_cast<const char *>(w13);
-    a.p_expert = int64_t(2) * I * H * 2;
-    a.ldp = int64_t(H) * 2;
-    a.N = I;
-    a.kbytes = H * 2;
-    auto tile_args = [&] {
-        TileArgs t{};
-        t.q = a.q;
-        t.ldq = a.ldq;
-        t.p = a.p;
-        t.p_expert = a.p_expert;
-        t.ldp = a.ldp;
-        t.N = a.N;
-        t.K = a.kbytes / 2;
-        return t;
-    };
-    const GatedOut gated{static_cast<uint16_t *>(act), nullptr};
-    hipError_t e = launch_cells<false, Form::kGated>(
-        a, G, max_pairs, gated, "ll_expert_ffn gated", stream, [&](const Groups &T, int64_t most) {
-            return launch_tiles<false, Form::kGated>(tile_args(), T, max_pairs, most, gated,
-                                                     "ll_expert_ffn gated tiles", stream);
-        });
+    hipError_t e = launch_bf16<Form::kGated>(gated_args(packed, w13, H, I), G, max_pairs, slots,
+                                             GatedOut{static_cast<uint16_t *>(act), nullptr},
+                                             "ll_expert_ffn gated", stream);
     if (e != hipSuccess)
         return e;
-    a.q = static_cast<const char *>(act);
-    a.ldq = int64_t(I) * 2;
-    a.p = static_cast<const char *>(w2);
-    a.p_expert = int64_t(I) * H * 2;
-    a.ldp = int64_t(I) * 2;
-    a.N = H;
-    a.kbytes = I * 2;
-    const RowOut rows{static_cast<uint16_t *>(out)};
-    return launch_cells<false, Form::kPlain>(
-        a, G, max_pairs, rows, "ll_expert_ffn down", stream, [&](const Groups &T, int64_t most) {
-            return launch_tiles<false, Form::kPlain>(tile_args(), T, max_pairs, most, rows,
-                                                     "ll_expert_ffn down tiles", stream);
-        });
+    return launch_bf16<Form::kPlain>(down_args(act, w2, H, I), G, max_pairs, slots,
+                                     RowOut{static_cast<uint16_t *>(out)}, "ll_expert_ffn down", stream);
 }
 
 }  // namespace ep

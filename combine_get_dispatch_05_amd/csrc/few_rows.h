@@ -1,9 +1,7 @@
 // few_rows.h -- the products of groups that hold few rows (a decode batch, one
-// token): the weight is read once and its bytes are the whole cost.  Where there
-// are columns enough for every compute unit, it goes from memory straight into the
-// matrix instruction's registers, a wave owning its own weight rows
-// (few_rows_kernel); where there are not, the waves of a block share out K
-// (split_kernel).  bf16 or FP8 operands.
+// token) or few tiles: the weight is read once and its bytes are the cost, and a
+// tile's wave groups, which take turns, would wait for each step of K.  bf16 or
+// FP8 operands.
 #pragma once
 
 #include "gemm.h"
@@ -12,6 +10,7 @@ namespace ep {
 
 struct FewArgs {
     const char *q;         // token rows, in group order
+    const int32_t *q_rows; // or, where given, picked by pair_row
     const float *q_scale;  // FP8: [row][K / 128]
     int64_t ldq;           // bytes of a token row
     const char *p;         // weights
@@ -24,6 +23,13 @@ struct FewArgs {
     unsigned nt;           // column tiles
     int active;            // groups that can hold rows, where fewer than all
 };
+
+// The token row of a group's m-th row (its last one past the end).
+__device__ __forceinline__ int64_t token_row(const FewArgs &a, int64_t start, int rows, int m)
+{
+    const int64_t at = start + (m < rows ? m : rows - 1);
+    return a.q_rows != nullptr ? a.q_rows[at] & kRowMask : at;
+}
 
 // The j-th group that holds rows, or -1.  Every thread of the block takes part;
 // s: LDS of one int a wave and one more, free again afterwards.
@@ -65,14 +71,6 @@ __device__ __forceinline__ int find_group(const Groups &G, int j, int *s)
 struct Frag {
     i32x4 lo, hi;
 };
-__device__ __forceinline__ Frag load_frag(const char *p, int kb, int kbytes)
-{
-    Frag f;
-    const i32x4 z = {};
-    f.lo = kb < kbytes ? *reinterpret_cast<const i32x4 *>(p) : z;
-    f.hi = kb + 64 < kbytes ? *reinterpret_cast<const i32x4 *>(p + 64) : z;
-    return f;
-}
 
 // One scale block of K.  The instruction adds the products of each eight
 // neighbouring k after aligning them to the largest, 2^E, and drops what lies
@@ -127,156 +125,14 @@ __device__ __forceinline__ f32x4 mfma_step_bf16(const Frag &a, const Frag &b, f3
     return mfma_bf16(__builtin_bit_cast(bf16x8, a.hi), __builtin_bit_cast(bf16x8, b.hi), c);
 }
 
-// HBM bounds it: 128 tokens on 256 FP8 experts of 2048 x 7168, 11.1 GB, take 1.27 ms
-// gated and 0.64 down, 5.8 TB/s (a copy, which also writes, reaches 5.4).
-// One block: kCols columns of one group, and of its rows every gridDim.y-th run of
-// 16 MT.  WN x WK waves: WN share out the columns, WK the K steps.  A wave holds NW
-// 16-column tiles (half gate, half up in the gated form) and MT 16-row tiles.
-template <bool FP8, int WN, int WK, int NW, int MT, Form F, class Epi>
-__global__ __launch_bounds__(WN *WK *kWave, 2) void few_rows_kernel(FewArgs a, Groups G, Epi epi)
-{
-    constexpr int kCols = WN * (F == Form::kGated ? NW / 2 : NW) * 16;  // of a block
-    constexpr int kWaveCols = kCols / WN;
-    __shared__ f32x4 sums[WK > 1 ? (WK - 1) * WN * MT * NW * kWave : 1];
-    int g = blockIdx.x / a.nt;
-    const int tn = int(blockIdx.x % a.nt);
-    if (a.active < G.num) {
-        g = find_group<WN * WK * kWave>(G, g, reinterpret_cast<int *>(sums));
-        if (g < 0)
-            return;
-    }
-    const int rows = uniform(group_rows(G, g));
-    const int first = int(blockIdx.y) * 16 * MT, stride = int(gridDim.y) * 16 * MT;
-    if (first >= rows)
-        return;
-    const int lane = threadIdx.x & 63;
-    const int wave = uniform(threadIdx.x >> 6);
-    const int wn = wave % WN, wk = wave / WN;
-    const int64_t start = group_start(G, g);
-    const int e = group_expert(G, g);
-    const char *pw = a.p + int64_t(e) * a.p_expert;
-    const int n0 = tn * kCols + wn * kWaveCols;
-    const int kl = (lane >> 4) * 16;
-    const char *pp[NW];
-    const float *ps[2] = {nullptr, nullptr};
-    const int kblocks = a.kbytes >> 7;
-#pragma unroll
-    for (int i = 0; i < NW; ++i) {
-        const bool up = F == Form::kGated && i >= NW / 2;
-        int n = n0 + (up ? i - NW / 2 : i) * 16 + (lane & 15);
-        n = (n < a.N ? n : a.N - 1) + (up ? a.N : 0);
-        pp[i] = pw + int64_t(n) * a.ldp + kl;
-    }
-    if constexpr (FP8) {
-        const int nb = n0 < a.N ? n0 : a.N - 1;
-        ps[0] = a.p_scale + e * a.p_scales + int64_t(nb >> 7) * kblocks;
-        ps[1] = F == Form::kGated ? ps[0] + int64_t(a.N >> 7) * kblocks : ps[0];
-    }
-    const int steps = (a.kbytes + kStepBytes - 1) / kStepBytes;
-    const int s0 = steps * wk / WK, s1 = steps * (wk + 1) / WK;
-    for (int m0 = first; m0 < rows; m0 += stride) {
-        const char *qp[MT];
-        const float *qs[MT];
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            int m = m0 + i * 16 + (lane & 15);
-            m = m < rows ? m : rows - 1;
-            qp[i] = a.q + (start + m) * a.ldq + kl;
-            qs[i] = FP8 ? a.q_scale + (start + m) * kblocks : nullptr;
-        }
-        f32x4 acc[MT][NW] = {};
-        struct Step {
-            Frag p[NW], q[MT];
-            float sp[2], sq[MT];
-        };
-        auto load = [&](Step &t, int s) {
-            const int64_t kb = int64_t(s) * kStepBytes;
-            const int left = a.kbytes - int(kb);
-#pragma unroll
-            for (int i = 0; i < NW; ++i)
-                t.p[i] = load_frag(pp[i] + kb, kl, left);
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-                t.q[i] = load_frag(qp[i] + kb, kl, left);
-            if constexpr (FP8) {
-                t.sp[0] = ps[0][s];
-                t.sp[1] = F == Form::kGated ? ps[1][s] : t.sp[0];
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-                    t.sq[i] = qs[i][s];
-            }
-        };
-        auto use = [&](const Step &t) {
-            if constexpr (FP8 && F == Form::kGated) {
-                Wide q[MT];
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    q[m] = widen(t.q[m]);
-#pragma unroll
-                for (int i = 0; i < NW; ++i) {
-                    const Wide p = widen(t.p[i]);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-                        acc[m][i] += mfma_step_wide(p, q[m]) * (t.sq[m] * t.sp[i >= NW / 2]);
-                    __builtin_amdgcn_sched_barrier(0);  // one tile at a time: more would not fit the registers
-                }
-            } else if constexpr (FP8) {
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int i = 0; i < NW; ++i)
-                        acc[m][i] += mfma_step_fp8(t.p[i], t.q[m]) * (t.sq[m] * t.sp[0]);
-            } else {
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int i = 0; i < NW; ++i)
-                        acc[m][i] = mfma_step_bf16(t.p[i], t.q[m], acc[m][i]);
-            }
-        };
-        Step cur, nxt;  // one step in flight while one is used
-        if (s0 < s1)
-            load(cur, s0);
-        for (int s = s0; s < s1; ++s) {
-            if (s + 1 < s1)
-                load(nxt, s + 1);
-            use(cur);
-            cur = nxt;
-        }
-        if constexpr (WK > 1) {
-            if (wk > 0) {
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int i = 0; i < NW; ++i)
-                        sums[((((wk - 1) * WN + wn) * MT + m) * NW + i) * kWave + lane] = acc[m][i];
-            }
-            __syncthreads();
-            if (wk == 0) {
-#pragma unroll 1
-                for (int w = 0; w < WK - 1; ++w)
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-#pragma unroll
-                        for (int i = 0; i < NW; ++i)
-                            acc[m][i] += sums[(((w * WN + wn) * MT + m) * NW + i) * kWave + lane];
-            }
-        }
-        const Tile t{g, m0, rows, tn};
-        if constexpr (Epi::kBlockWide)
-            epi.template store_block<MT, NW, WN, 16 * MT>(t, start, wk == 0, wn, 0, n0, a.N, acc, lane);
-        else if (wk == 0)
-            epi.store(t, start, m0, n0, a.N, acc, lane);
-        if (m0 + stride < rows)
-            __syncthreads();  // the sums are read before the next rows' are written
-    }
-}
-
-// Products whose blocks leave compute units idle: 16 MT rows by 64 columns (32
-// gate and their 32 up) a block, K shared out over the eight waves.  A wave stages
-// its own K steps in LDS of its own, whole 128-byte lines a row, and nobody else
-// reads them, so the loop has no barrier: as soon as a step is in registers the
-// next is sent off behind its matrix instructions.  The waves' sums meet at the end.
+// 16 MT rows by 64 columns (32 gate and their 32 up) a block, K shared out over the
+// eight waves.  A wave stages its own K steps in LDS of its own, whole 128-byte
+// lines a row, and nobody else reads them, so the loop has no barrier: as soon as
+// a step is in registers the next is sent off behind its matrix instructions.  The
+// waves' sums meet at the end.  HBM bounds it where experts are many (128 tokens
+// on 256 FP8 experts of 2048 x 7168, 11.1 GB: 1.86 ms, 6.0 TB/s; loading the weight
+// into registers, a wave its own 64 columns, 1.89), the latency of a launch and of
+// a wave's two to four steps where they are few (one row of 2048 by 7168: 5.0 us).
 // Gated FP8 rows, whose codes need the largest of 128 activations: 128 gate and
 // their 128 up columns a block, and four waves, which then fill the LDS.
 constexpr int kSplitCols = 64;
@@ -307,7 +163,7 @@ split_kernel(FewArgs a, Groups G, Epi epi)
     constexpr int kCols = F == Form::kGated ? Shape::kCols / 2 : Shape::kCols;
     constexpr bool kWiden = FP8 && F == Form::kGated;
     using PR = NearRowStage<Shape::kCols / 2, kWave>;
-    using QR = NearRowStage<16 * MT, kWave>;
+    using QR = RowStage<16 * MT, kWave>;
     constexpr int kQ = 2 * PR::kBytes, kOwn = kQ + QR::kBytes;
     static_assert(kOwn >= MT * NW * kWave * 16, "a wave's sums take the place of its last step");
     __shared__ __attribute__((aligned(128))) char smem[W * kOwn];
@@ -340,17 +196,13 @@ split_kernel(FewArgs a, Groups G, Epi epi)
     const float *ps_up = kWiden ? ps + int64_t(a.N >> 7) * steps : ps;
     for (int m0 = int(blockIdx.y) * 16 * MT; m0 < rows; m0 += int(gridDim.y) * 16 * MT) {
         QR qr;
-        qr.init(lane, a.q + (start + m0) * a.ldq, [&](int, int r) {
-            return uint32_t(m0 + r < rows ? r : rows - 1 - m0) * uint32_t(a.ldq);
-        });
+        qr.init(lane, [&](int, int r) { return a.q + token_row(a, start, rows, m0 + r) * a.ldq; });
         const float *qs[MT];
         float next[MT], next_c = 0.0f, next_up = 0.0f;  // scales of the step on its way
         if constexpr (FP8) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const int r = m0 + m * 16 + (lane & 15);
-                qs[m] = a.q_scale + (start + (r < rows ? r : rows - 1)) * steps;
-            }
+            for (int m = 0; m < MT; ++m)
+                qs[m] = a.q_scale + token_row(a, start, rows, m0 + m * 16 + (lane & 15)) * steps;
         }
         auto send = [&](int s) {
             const int64_t kb = int64_t(s) * kStepBytes;
@@ -455,10 +307,6 @@ split_kernel(FewArgs a, Groups G, Epi epi)
 
 // --------------------------------------------------------------- launches
 
-// Rows up to which a group takes this kernel: it reads the weight again (from L2)
-// for every 16 MT rows.
-constexpr int kFewRows = 64;
-
 template <class Kernel, class Epi>
 hipError_t launch_few_shape(Kernel kernel, int threads, FewArgs a, const Groups &G, int cols, int tile_rows,
                             int row_blocks, const Epi &epi, const char *what, hipStream_t stream)
@@ -474,64 +322,66 @@ hipError_t launch_few_shape(Kernel kernel, int threads, FewArgs a, const Groups 
     return hipGetLastError();
 }
 
-// Rows of a group up to which wide blocks beat tiles (16 experts of 2048 x 7168:
-// bf16 of 4 rows 260 against 273 us, of 25 rows 457 against 280; FP8 64 experts of
-// 768 x 2048, 4 rows 72.0 against 75.6, 8 rows 76.5 against 68.8).
-template <bool FP8>
-constexpr int kWideRows = FP8 ? 4 : 8;
-
-// Whether blocks of 256 columns (128 gated) would leave compute units idle; then
-// they take 64 (32) columns and split K: one token's eight bf16 experts of
-// 768 x 2048, gated, 11.6 us in 192 blocks, 34 in 48 wide ones.
-template <Form F>
-bool splits_k(const FewArgs &a, int64_t row_blocks)
+// Rows of a block, for groups of avg rows.
+template <class Epi>
+int split_rows(int64_t avg)
 {
-    constexpr int wide = F == Form::kGated ? BN / 2 : BN;
-    return int64_t((a.N + wide - 1) / wide) * a.active * row_blocks < compute_units();
+    return Epi::kBlockWide || avg <= 16 ? 16 : avg <= 32 ? 32 : 64;
 }
 
-// avg: rows of an active group on average.
+// row_blocks: blocks for a group's rows, which they share out.
 template <bool FP8, Form F, class Epi>
-hipError_t launch_few(FewArgs a, const Groups &G, int64_t avg, int row_blocks, const Epi &epi, const char *what,
-                      hipStream_t stream)
+hipError_t launch_split(FewArgs a, const Groups &G, int64_t avg, int row_blocks, const Epi &epi, const char *what,
+                        hipStream_t stream)
 {
     using Split = SplitShape<Epi::kBlockWide>;
-    constexpr int wide = F == Form::kGated ? BN / 2 : BN, split = wide / (BN / Split::kCols);
-    constexpr int threads = Split::kThreads;
-    auto launch = [&](auto kernel, int n, int cols, int tile_rows) {
-        return launch_few_shape(kernel, n, a, G, cols, tile_rows, row_blocks, epi, what, stream);
+    constexpr int cols = F == Form::kGated ? Split::kCols / 2 : Split::kCols;
+    const int rows = split_rows<Epi>(avg);
+    auto launch = [&](auto kernel) {
+        return launch_few_shape(kernel, Split::kThreads, a, G, cols, rows, row_blocks, epi, what, stream);
     };
-    if (!splits_k<F>(a, row_blocks))
-        return launch(few_rows_kernel<FP8, 4, 2, 4, 1, F, Epi>, NT, wide, 16);
     if constexpr (!Epi::kBlockWide) {
-        if (avg > 32)
-            return launch(split_kernel<FP8, 4, F, Epi>, threads, split, 64);
-        if (avg > 16)
-            return launch(split_kernel<FP8, 2, F, Epi>, threads, split, 32);
+        if (rows == 64)
+            return launch(split_kernel<FP8, 4, F, Epi>);
+        if (rows == 32)
+            return launch(split_kernel<FP8, 2, F, Epi>);
     }
-    return launch(split_kernel<FP8, 1, F, Epi>, threads, split, 16);
+    return launch(split_kernel<FP8, 1, F, Epi>);
 }
 
-// The low-latency cells: groups of few rows by launch_few, the others by
-// tiles(G, most): both walk the groups on the device, which alone knows their
-// rows; most bounds the groups left for the tiles.  With K split the border is
-// where groups of more than 64 rows become common (eight bf16 experts of
-// 768 x 2048 with 40 rows each: 26.2 against 39.7 us, with 60: 57.5 against 40.4),
-// for gated FP8, whose blocks take 16 rows, lower (8 rows: 18.9 against 24.0 us, 12
-// rows: 27.9 against 24.0).
+// Groups whose rows only the device knows: at most max_pairs in all, most_rows in
+// one of them (more are handled, but slowly).  K is split up to 8 rows a group on
+// average (16 bf16 experts of 2048 x 7168: 1 row 178 against 210 us in tiles, 8 rows
+// 254 against 267, 16 rows, where a second run reads the weight again, 335 against
+// 275), and up to 64 in at most two rounds of blocks, where the weight comes from
+// the cache the second time (eight of 768 x 2048, 50 rows: 23.8 against 39.7 us; 64 of
+// 352 x 256, 51 rows, three rounds: 17 against 13); not so for gated FP8, whose
+// blocks take 16 rows (eight of 768 x 2048, 8 rows: 18.9 against 24.0 us, 12 rows: 27.9
+// against 24.0).  Blocks walk a group's rows: where one group could take more than
+// 16 runs, those of over 64 rows are left to tiles(G, most).
 template <bool FP8, Form F, class Epi, class Tiles>
-hipError_t launch_cells(FewArgs a, Groups G, int64_t max_pairs, const Epi &epi, const char *what,
-                        hipStream_t stream, Tiles tiles)
+hipError_t launch_groups(FewArgs a, Groups G, int64_t max_pairs, int64_t most_rows, const Epi &epi,
+                         const char *what, hipStream_t stream, Tiles tiles)
 {
+    if (max_pairs == 0)
+        return hipSuccess;
+    constexpr int kFewRows = 64, kRuns = 16;
+    constexpr int cols = F == Form::kGated ? SplitShape<Epi::kBlockWide>::kCols / 2 : kSplitCols;
+    most_rows = most_rows < max_pairs ? most_rows : max_pairs;
     a.active = int(max_pairs < G.num ? max_pairs : G.num);
-    const int64_t avg = max_pairs / a.active;
-    const int most_avg = splits_k<F>(a, 1) ? Epi::kBlockWide ? 8 : 48 : kWideRows<FP8>;
-    if (avg <= most_avg) {
-        Groups few = G;
-        few.max_rows = kFewRows;
-        hipError_t e = launch_few<FP8, F>(a, few, avg, 1, epi, what, stream);
-        if (e != hipSuccess || G.slots <= kFewRows || max_pairs <= kFewRows)
+    const int64_t avg = max_pairs / a.active, blocks = int64_t((a.N + cols - 1) / cols) * a.active;
+    const bool few = avg <= 8 || (!Epi::kBlockWide && avg <= 64 && blocks <= 2 * compute_units());
+    if (few && blocks <= kMaxTileBlocks) {
+        const int64_t rows = split_rows<Epi>(avg);
+        const bool all = most_rows <= kRuns * rows;
+        if (!all)
+            G.max_rows = kFewRows;
+        const int64_t runs = ((all ? most_rows : kFewRows) + rows - 1) / rows, room = compute_units() / blocks;
+        const hipError_t e = launch_split<FP8, F>(a, G, avg, int(runs < room ? runs : room > 1 ? room : 1), epi, what,
+                                                  stream);
+        if (e != hipSuccess || all)
             return e;
+        G.max_rows = kNoLimit;
         G.min_rows = kFewRows + 1;
     }
     const int64_t most = max_pairs / G.min_rows;

@@ -279,14 +279,13 @@ hipError_t launch_fp8_product(int64_t M, int N, int K, const void *a_q, const fl
     a.kbytes = K;
     const RowOut epi{static_cast<uint16_t *>(out)};
     a.active = 1;
-    // K is split up to 64 rows where that fills idle compute units, past that in a
-    // block for each 64 as long as all of them run at once (512 x 2048 x 4096, 256
-    // blocks: 12.7 us, in 64 x 256 tiles 23.9; 512 x 4096 x 4096, 512 blocks: 24.0
-    // and 24.1).
-    const int64_t chunks = (M + kFewRows - 1) / kFewRows;
-    const bool once = chunks * ((N + kSplitCols - 1) / kSplitCols) <= compute_units();
-    if (splits_k<Form::kPlain>(a, chunks) ? M <= kFewRows || once : M <= kWideRows<true>)
-        return launch_few<true, Form::kPlain>(a, G, M, int(chunks), epi, "fp8_product", stream);
+    // K is split for up to 16 rows (16 x 16384 x 4096: 12.5 us, in 64-row tiles 23.6),
+    // past that in a block for each 64 as long as all of them run at once (512 x 2048
+    // x 4096, 256 blocks: 12.7 us, in tiles 23.9; 512 x 4096 x 4096, 512 blocks:
+    // 24.0 and 24.1).
+    const int64_t chunks = (M + 63) / 64;
+    if (M <= 16 || chunks * ((N + kSplitCols - 1) / kSplitCols) <= compute_units())
+        return launch_split<true, Form::kPlain>(a, G, M, int(chunks), epi, "fp8_product", stream);
     return launch_fp8_tiles<Form::kPlain>(a, G, M, 1, epi, "fp8_product", stream);
 }
 
@@ -309,8 +308,8 @@ hipError_t launch_ll_expert_ffn_fp8(int E, int R, int slots, int H, int I, int64
     a.N = I;
     a.kbytes = H;
     const GatedFp8Out gated{static_cast<uint8_t *>(act_q), act_scale};
-    hipError_t e = launch_cells<true, Form::kGated>(
-        a, G, max_pairs, gated, "ll_expert_ffn_fp8 gated", stream, [&](const Groups &T, int64_t most) {
+    hipError_t e = launch_groups<true, Form::kGated>(
+        a, G, max_pairs, slots, gated, "ll_expert_ffn_fp8 gated", stream, [&](const Groups &T, int64_t most) {
             return launch_fp8_tiles<Form::kGated>(a, T, max_pairs, most, gated, "ll_expert_ffn_fp8 gated tiles",
                                                   stream);
         });
@@ -327,8 +326,8 @@ hipError_t launch_ll_expert_ffn_fp8(int E, int R, int slots, int H, int I, int64
     a.N = H;
     a.kbytes = I;
     const RowOut rows{static_cast<uint16_t *>(out)};
-    return launch_cells<true, Form::kPlain>(
-        a, G, max_pairs, rows, "ll_expert_ffn_fp8 down", stream, [&](const Groups &T, int64_t most) {
+    return launch_groups<true, Form::kPlain>(
+        a, G, max_pairs, slots, rows, "ll_expert_ffn_fp8 down", stream, [&](const Groups &T, int64_t most) {
             return launch_fp8_tiles<Form::kPlain>(a, T, max_pairs, most, rows, "ll_expert_ffn_fp8 down tiles",
                                                   stream);
         });

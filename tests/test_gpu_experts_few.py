@@ -1,6 +1,6 @@
 """The products of few rows or few tiles at the borders between their kernels: K
-split over a block's waves, wide blocks, tiles of 64 rows, and batches whose groups
-take different ones.  References and bounds are those of test_gpu_experts.py."""
+split over a block's waves, tiles of 64 rows, and batches whose groups take
+different ones.  References and bounds are those of test_gpu_experts.py."""
 
 from __future__ import annotations
 
@@ -23,7 +23,7 @@ def _announce(request):
 
 
 # M: one, two and four row tiles, a block for each 64 rows, as many blocks as
-# compute units and one run more; N: inside one block, wide enough for wide blocks
+# compute units and one run more; N: inside one block, more blocks than compute units
 @pytest.mark.parametrize("M,N,K", [(2, 8, 128), (16, 72, 1408), (17, 1000, 256), (32, 64, 4096), (33, 72, 1152),
                                    (64, 7168, 128), (129, 40, 640), (700, 512, 384), (4090, 200, 256),
                                    (4100, 200, 256), (16384, 64, 128), (3, 66000, 128), (5, 66000, 128),
@@ -44,7 +44,7 @@ def skewed(monkeypatch):
     monkeypatch.setattr(base, "routing", routing)
 
 
-# rows of a group on average: 1, 2, 12, 24, 48; wide blocks (64 experts x 4); past 64 rows
+# rows of a group on average: 1, 2, 12, 24, 48, 4 of many, past 64
 CELLS = [(5, 264, 72, 16, 4, 4, 0.0), (16, 1024, 128, 64, 8, 8, 0.1), (12, 328, 200, 2, 1, 2, 0.0),
          (24, 72, 136, 2, 1, 2, 0.0), (48, 520, 64, 2, 2, 2, 0.0), (64, 1024, 512, 64, 4, 4, 0.0),
          (70, 264, 136, 3, 3, 2, 0.1)]
@@ -55,7 +55,9 @@ def test_low_latency_expert_ffn(T, H, I, E, R, K, mask):
     base.test_low_latency_expert_ffn(T, H, I, E, R, K, mask)
 
 
-@pytest.mark.parametrize("T,H,I,E,R,K", [(60, 200, 72, 64, 8, 2), (100, 136, 200, 64, 8, 2), (64, 1024, 512, 64, 4, 4)])
+# the crowded expert's rows in one block's runs, in several blocks, and in tiles (past 16 runs)
+@pytest.mark.parametrize("T,H,I,E,R,K", [(60, 200, 72, 64, 8, 2), (100, 136, 200, 64, 8, 2), (64, 1024, 512, 64, 4, 4),
+                                         (300, 72, 64, 128, 8, 2), (90, 64, 40, 8, 2, 2)])
 def test_low_latency_expert_ffn_skewed(monkeypatch, T, H, I, E, R, K):
     skewed(monkeypatch)
     base.test_low_latency_expert_ffn(T, H, I, E, R, K, 0.0)
@@ -71,7 +73,8 @@ def test_low_latency_expert_ffn_fp8(T, H, I, E, R, K, mask):
     base.test_low_latency_expert_ffn_fp8(T, H, I, E, R, K, mask)
 
 
-@pytest.mark.parametrize("T,H,I,E,R,K", [(60, 256, 128, 64, 8, 2), (100, 128, 256, 64, 8, 2), (64, 1024, 512, 64, 4, 4)])
+@pytest.mark.parametrize("T,H,I,E,R,K", [(60, 256, 128, 64, 8, 2), (100, 128, 256, 64, 8, 2), (64, 1024, 512, 64, 4, 4),
+                                         (300, 128, 128, 128, 8, 2), (20, 128, 128, 8, 2, 2)])
 def test_low_latency_expert_ffn_fp8_skewed(monkeypatch, T, H, I, E, R, K):
     skewed(monkeypatch)
     base.test_low_latency_expert_ffn_fp8(T, H, I, E, R, K, 0.0)
@@ -127,3 +130,18 @@ def test_unused_cells_and_experts_may_hold_anything(T, E, R, K, fp8):
         outs.append(buf.low_latency_expert_ffn(packed, count, h, w13, w2, out=out))
     assert (outs[0][unused] == 7.0).all() and outs[0].isfinite().all()
     assert torch.equal(outs[0], outs[1])
+
+
+# dispatched rows on the few-rows kernels: rows of an expert 1, 12, 24 and 40 on average,
+# many experts, one expert past 64 rows beside small ones, widths that end inside a K step
+DISPATCHED = [(3, 200, 72, 16, 4, 4, 0.0, False), (12, 328, 136, 2, 1, 2, 0.0, False),
+              (24, 72, 200, 2, 2, 2, 0.1, False), (40, 136, 64, 3, 3, 3, 0.0, False),
+              (64, 1024, 512, 64, 4, 4, 0.0, False), (100, 136, 200, 64, 8, 2, 0.0, True),
+              (300, 72, 64, 128, 8, 2, 0.0, True)]
+
+
+@pytest.mark.parametrize("T,H,I,E,R,K,mask,skew", DISPATCHED)
+def test_expert_ffn_and_gradients(monkeypatch, T, H, I, E, R, K, mask, skew):
+    if skew:
+        skewed(monkeypatch)
+    base.test_expert_ffn_and_gradients(T, H, I, E, R, K, mask, False)
