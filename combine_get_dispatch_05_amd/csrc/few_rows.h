@@ -322,21 +322,20 @@ hipError_t launch_few_shape(Kernel kernel, int threads, FewArgs a, const Groups 
     return hipGetLastError();
 }
 
-// Rows of a block, for groups of avg rows.
+// Rows of a block, for groups of that many rows.
 template <class Epi>
-int split_rows(int64_t avg)
+int split_rows(int64_t rows)
 {
-    return Epi::kBlockWide || avg <= 16 ? 16 : avg <= 32 ? 32 : 64;
+    return Epi::kBlockWide || rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
-// row_blocks: blocks for a group's rows, which they share out.
+// rows: of a block; row_blocks: blocks for a group's rows, which they share out.
 template <bool FP8, Form F, class Epi>
-hipError_t launch_split(FewArgs a, const Groups &G, int64_t avg, int row_blocks, const Epi &epi, const char *what,
+hipError_t launch_split(FewArgs a, const Groups &G, int rows, int row_blocks, const Epi &epi, const char *what,
                         hipStream_t stream)
 {
     using Split = SplitShape<Epi::kBlockWide>;
     constexpr int cols = F == Form::kGated ? Split::kCols / 2 : Split::kCols;
-    const int rows = split_rows<Epi>(avg);
     auto launch = [&](auto kernel) {
         return launch_few_shape(kernel, Split::kThreads, a, G, cols, rows, row_blocks, epi, what, stream);
     };
@@ -372,12 +371,14 @@ hipError_t launch_groups(FewArgs a, Groups G, int64_t max_pairs, int64_t most_ro
     const int64_t avg = max_pairs / a.active, blocks = int64_t((a.N + cols - 1) / cols) * a.active;
     const bool few = avg <= 8 || (!Epi::kBlockWide && avg <= 64 && blocks <= 2 * compute_units());
     if (few && blocks <= kMaxTileBlocks) {
-        const int64_t rows = split_rows<Epi>(avg);
+        // most groups in one run (eight bf16 experts of 768 x 2048, 12 rows: 19.4 us in
+        // blocks of 32, 25.1 in blocks of 16; 24 rows: 20.2 in blocks of 32, 22.1 of 64)
+        const int rows = split_rows<Epi>(avg + avg / 8 + 4);
         const bool all = most_rows <= kRuns * rows;
         if (!all)
             G.max_rows = kFewRows;
         const int64_t runs = ((all ? most_rows : kFewRows) + rows - 1) / rows, room = compute_units() / blocks;
-        const hipError_t e = launch_split<FP8, F>(a, G, avg, int(runs < room ? runs : room > 1 ? room : 1), epi, what,
+        const hipError_t e = launch_split<FP8, F>(a, G, rows, int(runs < room ? runs : room > 1 ? room : 1), epi, what,
                                                   stream);
         if (e != hipSuccess || all)
             return e;

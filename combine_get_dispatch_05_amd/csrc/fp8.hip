@@ -285,7 +285,7 @@ hipError_t launch_fp8_product(int64_t M, int N, int K, const void *a_q, const fl
     // 24.0 and 24.1).
     const int64_t chunks = (M + 63) / 64;
     if (M <= 16 || chunks * ((N + kSplitCols - 1) / kSplitCols) <= compute_units())
-        return launch_split<true, Form::kPlain>(a, G, M, int(chunks), epi, "fp8_product", stream);
+        return launch_split<true, Form::kPlain>(a, G, split_rows<RowOut>(M), int(chunks), epi, "fp8_product", stream);
     return launch_fp8_tiles<Form::kPlain>(a, G, M, 1, epi, "fp8_product", stream);
 }
 
