@@ -314,9 +314,9 @@ struct GatedBack {
 // A block works through every gridDim.x-th tile: it looks up the next one while
 // the first stage of this one arrives, and sends off the next one's first stage
 // before it stores this one.  At 32 experts of 2048 x 7168 with about 1024 rows each
-// the gated product takes 1.79 ms (1077 TFLOP/s; the product of equal 8192 x 8192 x
-// 8192 matrices reaches 1620 on the same card), the down product 1.08, the gate's
-// backward 1.28, dx 1.89: the matrix cores' clock under load and the wait for a
+// the gated product takes 1.75 ms (1100 TFLOP/s; the product of equal 8192 x 8192 x
+// 8192 matrices reaches 1620 on the same card), the down product 1.05, the gate's
+// backward 1.27, dx 1.89: the matrix cores' clock under load and the wait for a
 // stage's loads, which two stages of 64 KB do not hide, are what is left.
 template <int BM, bool PCOL, Form F, class Epi>
 __global__ __launch_bounds__(NT) void tile_kernel(TileArgs a, Groups G, Epi epi)

@@ -130,7 +130,7 @@ __device__ __forceinline__ f32x4 mfma_step_bf16(const Frag &a, const Frag &b, f3
 // lines a row, and nobody else reads them, so the loop has no barrier: as soon as
 // a step is in registers the next is sent off behind its matrix instructions.  The
 // waves' sums meet at the end.  HBM bounds it where experts are many (128 tokens
-// on 256 FP8 experts of 2048 x 7168, 11.1 GB: 1.86 ms, 6.0 TB/s; loading the weight
+// on 256 FP8 experts of 2048 x 7168, 11.1 GB: 1.79 ms, 6.2 TB/s; loading the weight
 // into registers, a wave its own 64 columns, 1.89), the latency of a launch and of
 // a wave's two to four steps where they are few (one row of 2048 by 7168: 5.0 us).
 // Gated FP8 rows, whose codes need the largest of 128 activations: 128 gate and
