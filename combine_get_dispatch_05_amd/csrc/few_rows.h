@@ -85,6 +85,13 @@ __device__ __forceinline__ f32x4 mfma_step_fp8(const Frag &a, const Frag &b)
                                                             0x7f7f7f7f);
 }
 
+// Activations of a batch below which one of them in a neighbouring 8-bit code
+// shows in the norm of the result: a large one, 10 times their mean square's root
+// and a sixteenth off, is 0.6 of that root, 1.7e-3 of the norm of 2^17 of them, as
+// much as the result's own rounding.  Those batches pay for widening (eight experts
+// of 768 x 2048, 16 rows each: 30 us instead of 24).
+constexpr int64_t kFewActivations = int64_t(1) << 17;
+
 // The gated form's FP8 fragments are widened to bf16, exactly, and multiplied in
 // full fp32 sums: there the alignment would show, on a few rows, where it moves
 // an activation across a rounding border of its own 8-bit code, and the memory,
@@ -326,7 +333,7 @@ hipError_t launch_few_shape(Kernel kernel, int threads, FewArgs a, const Groups 
 template <class Epi>
 int split_rows(int64_t rows)
 {
-    return Epi::kBlockWide || rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    return rows <= 16 ? 16 : Epi::kBlockWide || rows <= 32 ? 32 : 64;
 }
 
 // rows: of a block; row_blocks: blocks for a group's rows, which they share out.
@@ -339,12 +346,11 @@ hipError_t launch_split(FewArgs a, const Groups &G, int rows, int row_blocks, co
     auto launch = [&](auto kernel) {
         return launch_few_shape(kernel, Split::kThreads, a, G, cols, rows, row_blocks, epi, what, stream);
     };
-    if constexpr (!Epi::kBlockWide) {
+    if constexpr (!Epi::kBlockWide)
         if (rows == 64)
             return launch(split_kernel<FP8, 4, F, Epi>);
-        if (rows == 32)
-            return launch(split_kernel<FP8, 2, F, Epi>);
-    }
+    if (rows == 32)
+        return launch(split_kernel<FP8, 2, F, Epi>);
     return launch(split_kernel<FP8, 1, F, Epi>);
 }
 
@@ -354,10 +360,11 @@ hipError_t launch_split(FewArgs a, const Groups &G, int rows, int row_blocks, co
 // 254 against 267, 16 rows, where a second run reads the weight again, 335 against
 // 275), and up to 64 in at most two rounds of blocks, where the weight comes from
 // the cache the second time (eight of 768 x 2048, 50 rows: 23.8 against 39.7 us; 64 of
-// 352 x 256, 51 rows, three rounds: 17 against 13); not so for gated FP8, whose
-// blocks take 16 rows (eight of 768 x 2048, 8 rows: 18.9 against 24.0 us, 12 rows: 27.9
-// against 24.0).  Blocks walk a group's rows: where one group could take more than
-// 16 runs, those of over 64 rows are left to tiles(G, most).
+// 352 x 256, 51 rows, three rounds: 17 against 13); gated FP8, whose blocks take at
+// most 32 rows, up to 22 and only where tiles would widen too (eight of 768 x 2048,
+// 10 rows: 20.9 against 28.8 us; of 2048 x 4096, 16 rows: 52.6 against 43.8).
+// Blocks walk a group's rows: where one group could take more than 16 runs, those
+// of over 64 rows are left to tiles(G, most).
 template <bool FP8, Form F, class Epi, class Tiles>
 hipError_t launch_groups(FewArgs a, Groups G, int64_t max_pairs, int64_t most_rows, const Epi &epi,
                          const char *what, hipStream_t stream, Tiles tiles)
@@ -369,7 +376,8 @@ hipError_t launch_groups(FewArgs a, Groups G, int64_t max_pairs, int64_t most_ro
     most_rows = most_rows < max_pairs ? most_rows : max_pairs;
     a.active = int(max_pairs < G.num ? max_pairs : G.num);
     const int64_t avg = max_pairs / a.active, blocks = int64_t((a.N + cols - 1) / cols) * a.active;
-    const bool few = avg <= 8 || (!Epi::kBlockWide && avg <= 64 && blocks <= 2 * compute_units());
+    const int border = !Epi::kBlockWide ? 64 : max_pairs * a.N < kFewActivations ? 22 : 8;
+    const bool few = avg <= 8 || (avg <= border && blocks <= 2 * compute_units());
     if (few && blocks <= kMaxTileBlocks) {
         // most groups in one run (eight bf16 experts of 768 x 2048, 12 rows: 19.4 us in
         // blocks of 32, 25.1 in blocks of 16; 24 rows: 20.2 in blocks of 32, 22.1 of 64)

@@ -227,13 +227,6 @@ __global__ __launch_bounds__(NT) void fp8_tile_kernel(FewArgs a, Groups G, Epi e
     });
 }
 
-// Activations of a batch below which one of them in a neighbouring 8-bit code
-// shows in the norm of the result: a large one, 10 times their mean square's root
-// and a sixteenth off, is 0.6 of that root, 1.7e-3 of the norm of 2^17 of them, as
-// much as the result's own rounding.  Those batches pay for widening (eight experts
-// of 768 x 2048, 16 rows each: 30 us instead of 24).
-constexpr int64_t kFewActivations = int64_t(1) << 17;
-
 template <Form F, class Epi>
 hipError_t launch_fp8_tiles(FewArgs a, const Groups &G, int64_t rows, int64_t max_tiles, const Epi &epi,
                             const char *what, hipStream_t stream)
