@@ -74,7 +74,8 @@ def test_low_latency_expert_ffn_fp8(T, H, I, E, R, K, mask):
 
 
 @pytest.mark.parametrize("T,H,I,E,R,K", [(60, 256, 128, 64, 8, 2), (100, 128, 256, 64, 8, 2), (64, 1024, 512, 64, 4, 4),
-                                         (300, 128, 128, 128, 8, 2), (20, 128, 128, 8, 2, 2)])
+                                         (300, 128, 128, 128, 8, 2), (20, 128, 128, 8, 2, 2),
+                                         (60, 128, 128, 8, 2, 2)])
 def test_low_latency_expert_ffn_fp8_skewed(monkeypatch, T, H, I, E, R, K):
     skewed(monkeypatch)
     base.test_low_latency_expert_ffn_fp8(T, H, I, E, R, K, 0.0)
