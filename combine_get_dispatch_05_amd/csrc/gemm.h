@@ -448,7 +448,8 @@ __device__ __forceinline__ int64_t share_of_xcd(unsigned n, unsigned x, unsigned
 // which cost at most half: in the order of the groups they would leave some blocks
 // with a round more of whole tiles than others (experts of about 1024 rows: 9
 // rounds of blocks for 8.5 rounds of work).  The order is laid over the tiles
-// that there are, not over the grid.  Every thread of the block takes part.
+// that there are, not over the grid.  Every thread of the block takes part; calls
+// need no barrier between them.
 template <int BM, int NT>
 __device__ __forceinline__ Tile find_tile(const Groups &G, unsigned b, unsigned nt)
 {
@@ -467,6 +468,10 @@ __device__ __forceinline__ Tile find_tile(const Groups &G, unsigned b, unsigned 
         __syncthreads();
         if (lane == 63)
             s[wave] = pre;
+        // behind the scan's first barrier, which no wave passes before all have read what
+        // an earlier call found, and before its second, which the match below comes after
+        if (threadIdx.x == 0)
+            found[0] = -1;
         __syncthreads();
         uint64_t before = 0;
         total = 0;
@@ -478,8 +483,6 @@ __device__ __forceinline__ Tile find_tile(const Groups &G, unsigned b, unsigned 
         }
         return before + pre - t;
     };
-    if (threadIdx.x == 0)
-        found[0] = -1;
     int rows = 0;
     uint64_t total = 0;
     uint64_t t = tiles_of(threadIdx.x, rows);
