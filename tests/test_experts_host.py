@@ -1,13 +1,16 @@
 """Device functions of the expert products run on the host, from their own source
 text in csrc/gemm.h: the search for a block's tile with a block's threads as
-fibers, one wave as far ahead of the others as the barriers let it."""
+fibers, one wave as far ahead of the others as the barriers let it, and the
+sigmoid over the whole range of its argument."""
 
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import subprocess
 
+import numpy as np
 import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "combine_get_dispatch_05_amd",
@@ -224,3 +227,45 @@ def test_every_tile_is_found_once_by_all_waves(tiles, rows, cells, bm, nt, desce
     for b, t in second.items():
         assert t == first.get(b, t), b
         assert t[0] < 0 or t in want
+
+
+# The hardware's 2^x and reciprocal, rounded from 64 bits; their results below the
+# normal numbers are zero there.
+SIGMOID = r"""
+#include <cmath>
+#define __device__
+#define __forceinline__ inline
+#define __builtin_amdgcn_exp2f emulated_exp2
+#define __builtin_amdgcn_rcpf emulated_rcp
+static float flushed(double v) { const float f = float(v); return std::fabs(f) < 1.17549435e-38f ? 0.0f : f; }
+static float emulated_exp2(float v) { return flushed(std::exp2(double(v))); }
+static float emulated_rcp(float v) { return flushed(1.0 / double(v)); }
+using std::fmaf;
+"""
+
+
+@pytest.fixture(scope="module")
+def sigmoid(tmp_path_factory):
+    body = source("// 1 / (1 + e^-v)", "__device__ __forceinline__ uint2 pack4")
+    lib = compiled(tmp_path_factory, "sigmoid", SIGMOID + body + 'extern "C" float sigmoid(float v) { return sigmoidf(v); }')
+    lib.sigmoid.restype, lib.sigmoid.argtypes = ctypes.c_float, [ctypes.c_float]
+    return lib.sigmoid
+
+
+def test_sigmoid_over_its_range(sigmoid):
+    v = np.concatenate([np.linspace(-87, 87, 4001), np.logspace(-20, 1.9, 300), -np.logspace(-20, 1.9, 300)])
+    for x in v.astype(np.float32):
+        want = 1 / (1 + math.exp(-float(x)))
+        # the exponential, the sum, the Newton step and the last product: at most a unit each
+        assert abs(sigmoid(x) - want) <= 4 * 2.0 ** -23 * want, x
+
+
+def test_sigmoid_at_its_ends(sigmoid):
+    """1 for large arguments and +inf, 0 below the normal results and at -inf, NaN for NaN."""
+    for x in (87.5, 88.8, 1e4, 2.3e38, 2.4e38, 3.4e38, math.inf):
+        assert sigmoid(x) == 1.0, x
+    for x in (-88.0, -89.0, -104.0, -1e4, -2.4e38, -3.4e38, -math.inf):
+        # what is left out there is below the smallest normal number and a half
+        assert 0.0 <= sigmoid(x) <= 1.7e-38, x
+        assert x >= -104 or sigmoid(x) == 0.0, x
+    assert math.isnan(sigmoid(math.nan))
