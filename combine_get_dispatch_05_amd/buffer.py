@@ -538,8 +538,10 @@ class Buffer:
         x is packed_x (bf16; w13 [E, 2 I, H] with the gate's rows first, w2 [E, H, I],
         bf16) or the FP8 pair of low_latency_dispatch(use_fp8=True) (w13 and w2 pairs
         of codes and scales [E, 2 I/128, H/128], [E, H/128, I/128]; the activation is
-        quantised the same way between the products).  Unused cells of out are left
-        as they were.  packed_count must be that of the handle's dispatch."""
+        quantised the same way between the products; an activation near a rounding border
+        of its code can get the neighbouring one in a batch of another size, whose gate and
+        up products take another kernel).  Unused cells of out are left as they were.
+        packed_count must be that of the handle's dispatch."""
         _need(packed_count, torch.int32, "packed_count", 2)
         epr, R, S, H = self.num_local_experts, self.num_ranks, handle.num_slots, handle.hidden
         _shape(packed_count, (epr, R), "packed_count")

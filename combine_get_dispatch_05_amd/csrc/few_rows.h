@@ -85,17 +85,21 @@ __device__ __forceinline__ f32x4 mfma_step_fp8(const Frag &a, const Frag &b)
                                                             0x7f7f7f7f);
 }
 
-// Activations of a batch below which one of them in a neighbouring 8-bit code
-// shows in the norm of the result: a large one, 10 times their mean square's root
-// and a sixteenth off, is 0.6 of that root, 1.7e-3 of the norm of 2^17 of them, as
-// much as the result's own rounding.  Those batches pay for widening (eight experts
-// of 768 x 2048, 16 rows each: 30 us instead of 24).
+// Gated products of fewer activations than this widen their operands; those of more
+// do so only where K is split.  Widening takes the alignment out of the activations,
+// where it can move one near a rounding border to the neighbouring 8-bit code.  It does
+// so in a batch of any size, and any order of an fp32 sum does it now and then: against 64 bits a row's output is off by 1.68e-3 of its norm
+// (median) and 0.9 to 1.8e-2 (the worst of 512 to 8192), widened by 1.66e-3 and 0.2 to
+// 1.0e-2.  The border is a choice of cost.  Below 2^17 a moved code, if it is a large
+// activation's, shows in the norm of the whole result (10 times the mean square's root
+// and a sixteenth off: 1.7e-3 of the norm of 2^17, as much as the result's own
+// rounding), and widening costs little: eight experts of 768 x 2048, 16 rows each, 30 us
+// instead of 24.  Above, the matrix cores set the time: 64 rows each 33.5 us instead of
+// 27.5, eight experts of 2048 x 4096 with 1024 rows each 632 instead of 238, 64 of 2048 x
+// 7168 with 128 rows each 966 instead of 758 (all three products).
 constexpr int64_t kFewActivations = int64_t(1) << 17;
 
-// The gated form's FP8 fragments are widened to bf16, exactly, and multiplied in
-// full fp32 sums: there the alignment would show, on a few rows, where it moves
-// an activation across a rounding border of its own 8-bit code, and the memory,
-// not the matrix cores, sets the time.
+// FP8 fragments widened to bf16, exactly, and multiplied in full fp32 sums.
 struct Wide {
     bf16x8 v[4];
 };

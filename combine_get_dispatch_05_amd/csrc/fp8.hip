@@ -233,7 +233,9 @@ hipError_t launch_fp8_tiles(FewArgs a, const Groups &G, int64_t rows, int64_t ma
 {
     const int cols = F == Form::kGated ? BN / 2 : BN;
     a.nt = unsigned((a.N + cols - 1) / cols);
-    const int bm = tile_rows(rows, max_tiles, a.nt);
+    // widened at 64 rows (so few activations take no other height on a whole card)
+    const bool wide = F == Form::kGated && rows * a.N < kFewActivations;
+    const int bm = wide ? 64 : tile_rows(rows, max_tiles, a.nt);
     const int64_t mt = rows / bm + (max_tiles < rows ? max_tiles : rows);
     if (mt * a.nt > kMaxTileBlocks)
         return hipErrorInvalidValue;
@@ -244,7 +246,7 @@ hipError_t launch_fp8_tiles(FewArgs a, const Groups &G, int64_t rows, int64_t ma
                    G.num, a.N, a.kbytes, bm, BN, (long long)mt * a.nt);
     const dim3 grid(unsigned(blocks_for_tiles(mt * a.nt)));
     if constexpr (F == Form::kGated)
-        if (bm == 64 && rows * a.N < kFewActivations) {
+        if (wide) {
             hipLaunchKernelGGL((fp8_tile_kernel<64, true, F, Epi>), grid, dim3(NT), 0, stream, a, G, epi);
             return hipGetLastError();
         }

@@ -421,9 +421,13 @@ int ep_ll_expert_ffn(const ep_dims *dims, int32_t num_slots, int32_t inter, cons
  * scale per 128 x 128 block: w13_scale [E][2 I/128][H/128], w2_scale
  * [E][H/128][I/128]).  Between the products the activation is quantised, from
  * its fp32 value, in the same format: act_q [E/R][R][num_slots][I] codes and
- * act_scale [..][I/128] are workspace.  The down product sums as ep_fp8_product does,
- * and so may the gate and up products (fp32 sums of exact products otherwise).  out
- * is bf16.  hidden % 128 == 0 and inter % 128 == 0 (EP_ERR_ALIGN).
+ * act_scale [..][I/128] are workspace.  The down product sums as ep_fp8_product does.
+ * The gate and up products of few activations (num_tokens * num_topk * inter below
+ * 2^17) are fp32 sums of exact products; those of more may be either, as their
+ * kernels go by the batch's shape.  So an activation near a rounding border of its
+ * code can get the neighbouring code in a batch of another size; in every batch it is
+ * the code of a value within that sum's bound of the exact one.  out is bf16.
+ * hidden % 128 == 0 and inter % 128 == 0 (EP_ERR_ALIGN).
  */
 int ep_ll_expert_ffn_fp8(const ep_dims *dims, int32_t num_slots, int32_t inter,
                          const void *packed_q, const float *packed_scale,

@@ -6,6 +6,7 @@ change of the rules cannot take these shapes elsewhere unseen."""
 
 from __future__ import annotations
 
+import ctypes
 import re
 import sys
 
@@ -102,3 +103,54 @@ def test_more_experts_than_threads(heights, tokens, experts, k, tile):
     assert heights().get("ll_expert_ffn gated") == tile
     base.test_low_latency_expert_ffn_fp8(tokens, 128, 128, experts, 8, k, 0.1)
     assert heights().get("ll_expert_ffn_fp8 gated tiles") == tile
+
+
+def quantised(buf, topk, x, w13, w2):
+    """Slots, codes and scales of the activation, and the outputs of an FP8 batch."""
+    tokens, H = x.shape
+    S, I, abi = tokens, w2[0].shape[2], base.abi
+    (q, sc), count, hdl, _, _ = buf.low_latency_dispatch(x, topk, S, use_fp8=True)
+    shape = q.shape[:3]
+    aq = torch.zeros((*shape, I), dtype=torch.uint8, device="cuda")
+    asc = torch.zeros((*shape, I // 128), device="cuda")
+    out = torch.zeros(q.shape, dtype=torch.bfloat16, device="cuda")
+    d = abi.dims(tokens, H, topk.shape[1], buf.num_experts, buf.num_ranks)
+    abi.check(abi.lib().ep_ll_expert_ffn_fp8(
+        ctypes.byref(d), S, I, *[abi.ptr(t) for t in (q, sc, count, *w13, *w2, aq, asc, out)],
+        abi.current_stream()), "ep_ll_expert_ffn_fp8")
+    return hdl.topk_slot.long(), aq.view(torch.float8_e4m3fn), asc, q, sc
+
+
+def test_fp8_codes_of_a_token_in_a_small_and_a_large_batch(heights):
+    """The gated products of few activations are fp32 sums, those of many are the 8-bit
+    instruction's: in each batch a token's codes are those of a value within its sum's
+    bound of the exact activation."""
+    few, tokens, experts, ranks, k, H, I = 6, 600, 8, 4, 3, 2048, 1024
+    g = base.gen(11)
+    topk, _ = base.routing(g, tokens, experts, k, 0.0)
+    x = base.normal(g, (tokens, H))
+    w13, w2 = base.fp8_weight(g, (experts, 2 * I, H)), base.fp8_weight(g, (experts, H, I))
+    v13, v2 = base.weight_value(w13), base.weight_value(w2)
+    buf = base.epm.Buffer(ranks, experts)
+    small = quantised(buf, topk[:few].contiguous(), x[:few].contiguous(), w13, w2)
+    assert heights() == {}  # K split
+    large = quantised(buf, topk, x, w13, w2)
+    assert "ll_expert_ffn_fp8 gated tiles" in heights()
+    epr = experts // ranks
+    for t in range(few):
+        for j in range(k):
+            e = int(topk[t, j])
+            le, r = e % epr, e // epr
+            values, bounds = [], []
+            for (slot, codes, scales, q, sc), fp8 in ((small, False), (large, True)):
+                at = (le, r, int(slot[t, j]))
+                row = base.rows_value((q[at][None], sc[at][None]))
+                _, _, _, act, _, _, eact = base.ffn_ref(row, v13[e], v2[e], fp8=fp8)
+                s = scales[at].double().repeat_interleave(128)[None]
+                value = codes[at].double()[None] * s
+                # half a step, the sum's own error, and the code's two fp32 roundings
+                tol = torch.maximum((act.abs() + eact) * 2.0 ** -4, s * 2.0 ** -10) + eact + 8 * base.U * act.abs()
+                base.close(value, act, tol, f"token {t}, expert {e}, {'large' if fp8 else 'small'} batch")
+                values.append(value)
+                bounds.append(tol)
+            base.close(values[0], values[1], bounds[0] + bounds[1], "between the batches")
