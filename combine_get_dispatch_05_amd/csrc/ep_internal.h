@@ -204,6 +204,23 @@ inline int tile_rows(int64_t rows, int64_t groups, int64_t column_tiles)
     return rows / groups > 64 && (rows / 256 + groups) * column_tiles * 2 > compute_units() ? 256 : 64;
 }
 
+// Row tiles of one launch: every group can end in a part tile, and no more tiles than
+// rows exist.
+inline int64_t row_tiles(int64_t rows, int64_t groups, int height)
+{
+    return rows / height + (groups < rows ? groups : rows);
+}
+// The most tiles that the rule above can give.  Where it takes 64 rows because 256
+// would leave the card idle there are less than four times the card's compute units;
+// kLeast stands for those.
+inline int64_t tiles_at_most(int64_t rows, int64_t groups, int64_t column_tiles)
+{
+    constexpr int64_t kLeast = 1 << 16;
+    groups = groups > 0 ? groups : 1;
+    const int64_t n = (rows / (rows / groups > 64 ? 256 : 64) + groups) * column_tiles;
+    return n > kLeast ? n : kLeast;
+}
+
 // Shared with the entry points outside ep_api.hip.
 int api_hip_error(hipError_t e);
 void api_trace_push(const char *name);

@@ -667,8 +667,7 @@ hipError_t launch_tiles(TileArgs a, const Groups &G, int64_t rows, int64_t group
     const int cols = F == Form::kGated ? BN / 2 : BN;
     a.nt = unsigned((a.N + cols - 1) / cols);
     const int bm = tile_rows(rows, groups, a.nt);
-    // every group can end in one part tile, and no more tiles than rows exist
-    const int64_t mt = rows / bm + (groups < rows ? groups : rows);
+    const int64_t mt = row_tiles(rows, groups, bm);
     if (mt * a.nt > kMaxTileBlocks)
         return hipErrorInvalidValue;
     if (mt == 0)

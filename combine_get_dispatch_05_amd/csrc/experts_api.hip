@@ -43,7 +43,7 @@ int check_expert_dims(const ep_dims *d, int32_t inter, int32_t unit)
 bool grids_fit(int64_t rows, int64_t groups, int64_t hidden, int64_t inter, bool grads)
 {
     const int64_t cols = (hidden > inter ? hidden : inter) / 128 + 1;
-    if ((rows / (rows / groups > 64 && rows > 4096 ? 256 : 64) + groups) * cols > kMaxTileBlocks)
+    if (tiles_at_most(rows, groups, cols) > kMaxTileBlocks)
         return false;
     return !grads || groups * (2 * inter / 256 + 1) * (hidden / 256 + 1) <= kMaxTileBlocks;
 }

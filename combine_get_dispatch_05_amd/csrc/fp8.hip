@@ -236,7 +236,7 @@ hipError_t launch_fp8_tiles(FewArgs a, const Groups &G, int64_t rows, int64_t ma
     // widened at 64 rows (so few activations take no other height on a whole card)
     const bool wide = F == Form::kGated && rows * a.N < kFewActivations;
     const int bm = wide ? 64 : tile_rows(rows, max_tiles, a.nt);
-    const int64_t mt = rows / bm + (max_tiles < rows ? max_tiles : rows);
+    const int64_t mt = row_tiles(rows, max_tiles, bm);
     if (mt * a.nt > kMaxTileBlocks)
         return hipErrorInvalidValue;
     if (mt == 0)

@@ -1,13 +1,14 @@
-"""Device functions of the expert products run on the host, from their own source
-text in csrc/gemm.h: the search for a block's tile with a block's threads as
-fibers, one wave as far ahead of the others as the barriers let it, and the
-sigmoid over the whole range of its argument."""
+"""Functions of the expert products run on the host, from their own source text in
+csrc/: the search for a block's tile with a block's threads as fibers, one wave as
+far ahead of the others as the barriers let it, the sigmoid over the whole range of
+its argument, and the rules that bound a launch."""
 
 from __future__ import annotations
 
 import ctypes
 import math
 import os
+import random
 import subprocess
 
 import numpy as np
@@ -17,8 +18,8 @@ CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                     "csrc")
 
 
-def source(start: str, end: str) -> str:
-    with open(os.path.join(CSRC, "gemm.h")) as f:
+def source(start: str, end: str, name: str = "gemm.h") -> str:
+    with open(os.path.join(CSRC, name)) as f:
         text = f.read()
     assert text.count(start) == 1 and text.count(end) >= 1, (start, end)
     return text[text.index(start):text.index(end, text.index(start))]
@@ -269,3 +270,49 @@ def test_sigmoid_at_its_ends(sigmoid):
         assert 0.0 <= sigmoid(x) <= 1.7e-38, x
         assert x >= -104 or sigmoid(x) == 0.0, x
     assert math.isnan(sigmoid(math.nan))
+
+
+RULES = """
+#include <stdint.h>
+static int units;
+static int compute_units() { return units; }
+"""
+RULES_OUT = """
+extern "C" int height(int64_t rows, int64_t groups, int64_t columns, int cus)
+{
+    units = cus;
+    return tile_rows(rows, groups, columns);
+}
+extern "C" int64_t needed(int64_t rows, int64_t groups, int64_t columns, int cus)
+{
+    return row_tiles(rows, groups, height(rows, groups, columns, cus)) * columns;
+}
+extern "C" int64_t at_most(int64_t rows, int64_t groups, int64_t columns)
+{
+    return tiles_at_most(rows, groups, columns);
+}
+"""
+
+
+def test_no_launch_needs_more_tiles_than_the_check_allows(tmp_path_factory):
+    """What the entry points check before the first launch bounds every launch, whatever
+    height it takes, also one that is left only the groups of more than 64 rows."""
+    body = source("inline int tile_rows", "// Shared with the entry points", "ep_internal.h")
+    lib = compiled(tmp_path_factory, "rules", RULES + body + RULES_OUT)
+    i64 = ctypes.c_int64
+    lib.height.argtypes = lib.needed.argtypes = [i64, i64, i64, ctypes.c_int]
+    lib.at_most.argtypes = [i64, i64, i64]
+    lib.needed.restype = lib.at_most.restype = i64
+    rng = random.Random(5)
+    seen = set()
+    for _ in range(20000):
+        rows = int(2 ** rng.uniform(0, 28))
+        groups = int(2 ** rng.uniform(0, 13))
+        columns = int(2 ** rng.uniform(0, 13))
+        cus = rng.choice([32, 256])
+        most = lib.at_most(rows, groups, columns)
+        assert lib.needed(rows, groups, columns, cus) <= most
+        left = min(rows // 65, groups)
+        assert lib.needed(rows, left, columns, cus) <= most
+        seen.add((lib.height(rows, groups, columns, cus), rows // groups > 64))
+    assert seen == {(64, False), (64, True), (256, True)}
