@@ -170,7 +170,7 @@ hipError_t launch_rms_norm(int64_t T, int H, float eps, const void *x, const voi
                            float *out_scale, float *rstd, hipStream_t stream);
 
 // Rows of fp32 partial sums of dweight that the backward pass writes.
-int rms_norm_parts(int64_t T, int H);
+int rms_norm_parts(int64_t T);
 
 hipError_t launch_rms_norm_backward(int64_t T, int H, const void *dout, const void *h,
                                     const void *weight, const float *rstd, const void *dresidual,

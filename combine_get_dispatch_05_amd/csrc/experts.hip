@@ -240,8 +240,8 @@ struct GatedBack {
     int tiles;
     // mbase: the wave's first row inside the tile of ROWS rows
     template <int MT, int NW, int WN, int ROWS>
-    __device__ __forceinline__ void store_block(const Tile &t, int64_t start, bool, int wn, int mbase, int n0,
-                                                int I, f32x4 (&acc)[MT][NW], int lane) const
+    __device__ __forceinline__ void store_block(const Tile &t, int64_t start, int wn, int mbase, int n0, int I,
+                                                f32x4 (&acc)[MT][NW], int lane) const
     {
         __shared__ float part[WN][ROWS];
         const int tid = threadIdx.x;
@@ -425,7 +425,7 @@ __global__ __launch_bounds__(NT) void tile_kernel(TileArgs a, Groups G, Epi epi)
             const int64_t start = group_start(G, c.group);
             const int n0 = c.n * (F == Form::kGated ? BN / 2 : BN) + wn * (F == Form::kGated ? 32 : 64);
             if constexpr (Epi::kBlockWide)
-                epi.template store_block<MT, 4, 4, R>(c, start, true, wn, wm * (R / 2), n0, a.N, acc, lane);
+                epi.template store_block<MT, 4, 4, R>(c, start, wn, wm * (R / 2), n0, a.N, acc, lane);
             else
                 epi.store(c, start, c.m0 + wm * (R / 2), n0, a.N, acc, lane);
         };

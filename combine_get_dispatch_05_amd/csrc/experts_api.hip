@@ -111,7 +111,7 @@ size_t ep_rms_norm_backward_workspace(int32_t num_tokens, int32_t hidden)
 {
     if (check_rows_dims(num_tokens, hidden) != EP_OK)
         return 0;
-    return size_t(rms_norm_parts(num_tokens, hidden)) * hidden * sizeof(float);
+    return size_t(rms_norm_parts(num_tokens)) * hidden * sizeof(float);
 }
 
 int ep_rms_norm_backward(int32_t num_tokens, int32_t hidden, const void *dout, const void *h,

@@ -299,7 +299,7 @@ split_kernel(FewArgs a, Groups G, Epi epi)
                     for (int w = 0; w < W; ++w)
                         sum[m][i] += sums[w * (kOwn / 16) + (m * NW + at) * kWave + lane];
                 }
-            epi.template store_block<MT, 4, W, 16 * MT>(t, start, true, wave, 0, n0 + wave * 32, a.N, sum, lane);
+            epi.template store_block<MT, 4, W, 16 * MT>(t, start, wave, 0, n0 + wave * 32, a.N, sum, lane);
         } else if (wave < 2 * MT) {  // two column tiles each: neighbours, or a gate and its up tile
             const int m = wave >> 1, h = wave & 1;
             const int i0 = F == Form::kGated ? h : 2 * h, i1 = F == Form::kGated ? h + 2 : i0 + 1;

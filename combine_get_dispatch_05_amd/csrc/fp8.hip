@@ -18,34 +18,29 @@ struct GatedFp8Out {
     float *scales;   // [.][I / 128]
     // mbase: this wave's first row inside the tile; ROWS: rows of the tile
     template <int MT, int NW, int WN, int ROWS>
-    __device__ __forceinline__ void store_block(const Tile &t, int64_t start, bool active, int wn,
-                                                int mbase, int n0, int I, f32x4 (&acc)[MT][NW],
-                                                int lane) const
+    __device__ __forceinline__ void store_block(const Tile &t, int64_t start, int wn, int mbase, int n0, int I,
+                                                f32x4 (&acc)[MT][NW], int lane) const
     {
         __shared__ float amaxs[WN][ROWS];
-        if (active) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                float big = 0.0f;
+        for (int m = 0; m < MT; ++m) {
+            float big = 0.0f;
 #pragma unroll
-                for (int i = 0; i < NW / 2; ++i) {
+            for (int i = 0; i < NW / 2; ++i) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float g = acc[m][i][k];
-                        const float v = g * sigmoidf(g) * acc[m][i + NW / 2][k];
-                        acc[m][i][k] = v;
-                        big = fmaxf(big, fabsf(v));
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    const float g = acc[m][i][k];
+                    const float v = g * sigmoidf(g) * acc[m][i + NW / 2][k];
+                    acc[m][i][k] = v;
+                    big = fmaxf(big, fabsf(v));
                 }
-                big = fmaxf(big, __shfl_xor(big, 16));
-                big = fmaxf(big, __shfl_xor(big, 32));
-                if (lane < 16)
-                    amaxs[wn][mbase + m * 16 + lane] = big;
             }
+            big = fmaxf(big, __shfl_xor(big, 16));
+            big = fmaxf(big, __shfl_xor(big, 32));
+            if (lane < 16)
+                amaxs[wn][mbase + m * 16 + lane] = big;
         }
         __syncthreads();
-        if (!active)
-            return;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             const int r = mbase + m * 16 + (lane & 15);
@@ -221,7 +216,7 @@ __global__ __launch_bounds__(NT) void fp8_tile_kernel(FewArgs a, Groups G, Epi e
         const int64_t start = group_start(G, cur.group);
         const int n0 = cur.n * (F == Form::kGated ? BN / 2 : BN) + wn * (F == Form::kGated ? 32 : 64);
         if constexpr (Epi::kBlockWide)
-            epi.template store_block<MT, 4, 4, R>(cur, start, true, wn, wm * (R / 2), n0, a.N, acc, lane);
+            epi.template store_block<MT, 4, 4, R>(cur, start, wn, wm * (R / 2), n0, a.N, acc, lane);
         else
             epi.store(cur, start, cur.m0 + wm * (R / 2), n0, a.N, acc, lane);
     });

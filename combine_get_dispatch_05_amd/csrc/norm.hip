@@ -361,17 +361,13 @@ hipError_t launch_rms_norm(int64_t T, int H, float eps, const void *x, const voi
 
 // Two blocks a compute unit (4096 rows of 7168: 35.6 us and 4.7 for their sum; of
 // 256 blocks 38.7 and 4.7, of 1024 39.5 and 5.8).
-int rms_norm_parts(int64_t T, int H)
-{
-    (void)H;
-    return int(T < 512 ? T : 512);
-}
+int rms_norm_parts(int64_t T) { return int(T < 512 ? T : 512); }
 
 hipError_t launch_rms_norm_backward(int64_t T, int H, const void *dout, const void *h,
                                     const void *weight, const float *rstd, const void *dresidual,
                                     void *dx, float *dweight, float *parts, hipStream_t stream)
 {
-    const int n = rms_norm_parts(T, H);
+    const int n = rms_norm_parts(T);
     NormBackArgs a{};
     a.dout = static_cast<const u32x4 *>(dout);
     a.h = static_cast<const u32x4 *>(h);
