@@ -251,6 +251,15 @@ class ExpertRows:
     pair_slot: torch.Tensor  # int32 [pairs], row * K + slot
     row_pair: torch.Tensor  # int32 [rows, K], -1 for a slot without a pair
 
+    def _check(self, num_experts: int) -> None:
+        # the kernels take all four as they are, so each is looked at in every call
+        i32 = torch.int32
+        _row(self.expert_offsets, i32, (num_experts + 1,), "the rows' expert_offsets")
+        _row(self.pair_row, i32, (self.pair_row.shape[0] if self.pair_row.dim() else 0,), "the rows' pair_row")
+        _row(self.pair_slot, i32, self.pair_row.shape, "the rows' pair_slot")
+        _need(self.row_pair, i32, "the rows' row_pair", 2)
+        _here(self.expert_offsets, self.pair_row, self.pair_slot, self.row_pair)
+
     def _raw(self) -> abi.ExpertGroups:
         return abi.ExpertGroups(self.row_pair.shape[0], self.pair_row.shape[0],
                                 self.expert_offsets.data_ptr(), self.pair_row.data_ptr(),
@@ -626,13 +635,12 @@ class Buffer:
         return rows
 
     def _expert_args(self, x, rows: ExpertRows, topk_weights, w13, w2):
+        rows._check(self.num_experts)
         _need(x, torch.bfloat16, "x", 2)
         N, H = x.shape
         K = rows.row_pair.shape[1]
         _shape(rows.row_pair, (N, K), "the rows' row_pair")
-        _shape(rows.expert_offsets, (self.num_experts + 1,), "the rows' expert_offsets")
-        _need(topk_weights, torch.float32, "topk_weights", 2)
-        _shape(topk_weights, (N, K), "topk_weights")
+        _row(topk_weights, torch.float32, (N, K), "topk_weights")
         return N, H, K, self._expert_weights(w13, w2, H)
 
     def expert_ffn(self, x: torch.Tensor, rows: ExpertRows, topk_weights: torch.Tensor,
