@@ -305,19 +305,19 @@ enum class Form { kPlain, kGated, kBack };
 // 1 / (1 + e^-v), good to a few units in the last place.  e^-v = 2^t (1 + r ln 2)
 // with t = -v / ln 2 rounded and r what the rounding lost; one Newton step on the
 // hardware reciprocal.  Past 87 the steps are taken at 87, where it is 1, so that
-// they stay finite; below -87 it would no longer be a normal number, and is 0.  NaN
-// stays NaN.  (The library's exponential and division took 13 us of a 254 us tile.)
+// they stay finite; below -87 it would no longer be a normal number, and is 0.  A NaN
+// gives some number: each use multiplies by v as well.  (The library's exponential and
+// division took 13 us of a 254 us tile.)
 __device__ __forceinline__ float sigmoidf(float v)
 {
     constexpr float kLog2e = 1.44269504f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.69314718f;
-    const bool none = v < -87.0f;
-    v = none ? -87.0f : v > 87.0f ? 87.0f : v;
-    const float t = -v * kLog2e;
-    const float r = fmaf(-v, kLog2e, -t) - v * kLog2eLow;
+    const float c = __builtin_amdgcn_fmed3f(v, -87.0f, 87.0f);
+    const float t = -c * kLog2e;
+    const float r = fmaf(-c, kLog2e, -t) - c * kLog2eLow;
     const float e = __builtin_amdgcn_exp2f(t);
     const float d = 1.0f + fmaf(e, r * kLn2, e);
     const float q = __builtin_amdgcn_rcpf(d);
-    return none ? 0.0f : fmaf(q, fmaf(-d, q, 1.0f), q);
+    return v < -87.0f ? 0.0f : fmaf(q, fmaf(-d, q, 1.0f), q);
 }
 
 __device__ __forceinline__ uint2 pack4(f32x4 v)

@@ -95,6 +95,32 @@ def test_large_gate(T, H, I, E, gate):
     assert ((dw2[:, :, 0].double() - want).abs() <= want * 2 * BF * 1.01).all()
 
 
+@pytest.mark.parametrize("T,H,I,E", SHAPES)
+def test_gate_that_is_not_a_number(T, H, I, E):
+    """Its row is NaN in the outputs and in its own gradient, every other row as it was."""
+    g = gen(T)
+    x, w13, w2 = normal(g, (T, H)), normal(g, (E, 2 * I, H), H ** -0.5), normal(g, (E, H, I), I ** -0.5)
+    buf = epm.Buffer(1, E)
+    ids = torch.arange(E, device="cuda").repeat(T, 1)
+    rows = buf.expert_rows(ids, torch.tensor([T], dtype=torch.int32, device="cuda"))
+    weights = torch.rand((T, E), generator=g, device="cuda")
+    dy = normal(g, x.shape)
+
+    def run():
+        packed, count, hdl, _, _ = buf.low_latency_dispatch(x, ids, T)
+        cells = buf.low_latency_expert_ffn(packed, count, hdl, w13, w2)
+        y, saved = buf.expert_ffn(x, rows, weights, w13, w2, save=True)
+        dx, dtw, dw13, dw2 = buf.expert_ffn_backward(dy, x, rows, weights, w13, w2, saved)
+        return cells[:, 0], y[None], dx[None], dtw[None, :, :], dw13, dw2
+    want = run()
+    x[1, 3] = float("nan")
+    got = run()
+    others = torch.arange(T, device="cuda") != 1
+    for a, b in zip(got[:4], want[:4]):
+        assert a[:, 1].isnan().all() and torch.equal(a[:, others], b[:, others]) and b.isfinite().all()
+    assert got[4].isnan().all() and got[5].isnan().all()  # sums over all rows
+
+
 # K split, 64-row tiles of few activations and of many, 256-row tiles
 @pytest.mark.parametrize("T,H,I,E", [(4, 128, 128, 2), (70, 128, 128, 4), (70, 256, 1024, 4), (300, 256, 2048, 16)])
 def test_large_gate_fp8(T, H, I, E):
