@@ -649,7 +649,9 @@ class Buffer:
         (bf16) y = sum over its slots of topk_weights * (silu(x Wg^T) * (x Wu^T)) W2^T,
         zero for a row without a slot.  w13 [E, 2 I, H] (the gate's rows first) and
         w2 [E, H, I] are bf16.  Returns (y [rows, H] bf16, saved): saved is what
-        expert_ffn_backward takes, the fp32 g and u of every pair, None without save."""
+        expert_ffn_backward takes, the fp32 g and u of every pair, None without save.
+        Workspace of a call: 4 H + 2 I bytes for every pair that rows has room for, so
+        give expert_rows the number of tokens where it takes a bare prefix."""
         N, H, K, inter = self._expert_args(x, rows, topk_weights, w13, w2)
         index = _here(x, rows.row_pair, topk_weights, w13, w2)
         dev, cap = x.device, rows.pair_row.shape[0]

@@ -314,10 +314,13 @@ struct GatedBack {
 // A block works through every gridDim.x-th tile: it looks up the next one while
 // the first stage of this one arrives, and sends off the next one's first stage
 // before it stores this one.  At 32 experts of 2048 x 7168 with about 1024 rows each
-// the gated product takes 1.75 ms (1100 TFLOP/s; the product of equal 8192 x 8192 x
+// the gated product takes 1.77 ms (1090 TFLOP/s; the product of equal 8192 x 8192 x
 // 8192 matrices reaches 1620 on the same card), the down product 1.05, the gate's
-// backward 1.27, dx 1.89: the matrix cores' clock under load and the wait for a
-// stage's loads, which two stages of 64 KB do not hide, are what is left.
+// backward 1.28, dx 1.89: the values themselves (on zeros 8 to 12 % less) and the wait
+// for a stage's loads, which two stages of 64 KB do not hide, are what is left.  At 256
+// rows the next tile is set up while 128 accumulators a lane wait to be stored, and
+// registers run out there: the gate's backward spills 141 vector registers (232 bytes a
+// lane), dx 6, and each of these kernels 54 to 144 scalar ones.  The K loops are free of it.
 template <int BM, bool PCOL, Form F, class Epi>
 __global__ __launch_bounds__(NT) void tile_kernel(TileArgs a, Groups G, Epi epi)
 {
@@ -473,9 +476,9 @@ __device__ __forceinline__ void weight_grad(const GradArgs &a, lds_char *lds, un
     using CS = ColStage<B, NT>;
     // Each wave keeps the stages' 64 picked rows to itself, three stages ahead,
     // loaded straight into LDS like the stages: held in registers their copies
-    // from stage to stage waited for the loads (46 us a tile of 1024 rows, 29
-    // without picking).  Slots 0 to 3 go round; a tile's first three stages have
-    // slots of their own, filled while the tile before is worked on, for which
+    // from stage to stage waited for the loads (46 us a tile of 1024 rows; this way
+    // 40, its stores among them).  Slots 0 to 3 go round; a tile's first three stages
+    // have slots of their own, filled while the tile before is worked on, for which
     // tiles take turns with two sets.
     constexpr int kSlot = kWave * 4;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -598,8 +601,9 @@ __device__ __forceinline__ void weight_grad(const GradArgs &a, lds_char *lds, un
 
 // Both weight gradients: dW2 (rows of dy picked), then dW13 (rows of x picked), so
 // that the second fills what the first leaves idle at its end.  Its tiles start
-// at the block after the first's last.  (The 32 experts above: 3.3 ms, 874 TFLOP/s;
-// K is a group's rows, and both operands come through the transposing read.)
+// at the block after the first's last.  (The 32 experts above: 3.4 ms, 860 TFLOP/s;
+// K is a group's rows, and both operands come through the transposing read.  16 vector
+// registers are spilled between tiles.)
 __global__ __launch_bounds__(NT) void weight_grads_kernel(GradArgs dw2, GradArgs dw13)
 {
     __shared__ __attribute__((aligned(128))) char smem[kGradLds];
@@ -615,7 +619,7 @@ __global__ __launch_bounds__(NT) void weight_grads_kernel(GradArgs dw2, GradArgs
 // Rows with no pair (zero) or several (their fp32 terms in slot order); rows of
 // one pair are already written.  With parts: also every slot's routing-weight
 // gradient, the sum of its pair's column tiles in order.  Bound by HBM (21 thousand
-// rows of 7168: 155 us).
+// rows of 7168: 158 us).
 __global__ __launch_bounds__(256) void rows_kernel(const int32_t *__restrict__ row_pair, int64_t rows, int K, int N,
                                                    const int32_t *__restrict__ pair_row,
                                                    const float *__restrict__ terms,

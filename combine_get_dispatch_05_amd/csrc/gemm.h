@@ -19,7 +19,7 @@
 // order, so the bank swizzle is applied to the global address instead.
 //
 // The eight waves of a block are two groups of four, one wave of each on every
-// SIMD, and take turns (take_turns): while one group's wave keeps the matrix
+// SIMD, and take turns (turns_on_ring, turns_on_pair): while one group's wave keeps the matrix
 // core busy, the other reads its next fragments from LDS and sends off loads.
 #pragma once
 
