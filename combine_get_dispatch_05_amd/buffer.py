@@ -258,7 +258,9 @@ class ExpertRows:
         _row(self.pair_row, i32, (self.pair_row.shape[0] if self.pair_row.dim() else 0,), "the rows' pair_row")
         _row(self.pair_slot, i32, self.pair_row.shape, "the rows' pair_slot")
         _need(self.row_pair, i32, "the rows' row_pair", 2)
-        _here(self.expert_offsets, self.pair_row, self.pair_slot, self.row_pair)
+
+    def _tensors(self):
+        return self.expert_offsets, self.pair_row, self.pair_slot, self.row_pair
 
     def _raw(self) -> abi.ExpertGroups:
         return abi.ExpertGroups(self.row_pair.shape[0], self.pair_row.shape[0],
@@ -653,7 +655,7 @@ class Buffer:
         Workspace of a call: 4 H + 2 I bytes for every pair that rows has room for, so
         give expert_rows the number of tokens where it takes a bare prefix."""
         N, H, K, inter = self._expert_args(x, rows, topk_weights, w13, w2)
-        index = _here(x, rows.row_pair, topk_weights, w13, w2)
+        index = _here(x, *rows._tensors(), topk_weights, w13, w2)
         dev, cap = x.device, rows.pair_row.shape[0]
         y = torch.empty_like(x)
         act = torch.empty((cap, inter), dtype=torch.bfloat16, device=dev)
@@ -678,7 +680,7 @@ class Buffer:
         cap, dev = rows.pair_row.shape[0], x.device
         _need(saved, torch.float32, "saved", 2)
         _shape(saved, (cap, 2 * inter), "saved")
-        index = _here(dy, x, rows.row_pair, topk_weights, w13, w2, saved)
+        index = _here(dy, x, *rows._tensors(), topk_weights, w13, w2, saved)
         bf = dict(dtype=torch.bfloat16, device=dev)
         f32 = dict(dtype=torch.float32, device=dev)
         dgu, act = torch.empty((cap, 2 * inter), **bf), torch.empty((cap, inter), **bf)

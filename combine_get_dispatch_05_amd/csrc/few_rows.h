@@ -88,9 +88,9 @@ __device__ __forceinline__ f32x4 mfma_step_fp8(const Frag &a, const Frag &b)
 // Gated products of fewer activations than this widen their operands; those of more
 // do so only where K is split.  Widening takes the alignment out of the activations,
 // where it can move one near a rounding border to the neighbouring 8-bit code.  It does
-// so in a batch of any size, and any order of an fp32 sum does it now and then: against 64 bits a row's output is off by 1.68e-3 of its norm
-// (median) and 0.9 to 1.8e-2 (the worst of 512 to 8192), widened by 1.66e-3 and 0.2 to
-// 1.0e-2.  The border is a choice of cost.  Below 2^17 a moved code, if it is a large
+// so in a batch of any size, and any order of an fp32 sum does it now and then: against
+// 64 bits a row's output is off by 1.68e-3 of its norm (median) and 0.9 to 1.8e-2 (the
+// worst of 512 to 8192), widened by 1.66e-3 and 0.2 to 1.0e-2.  The border is a choice of cost.  Below 2^17 a moved code, if it is a large
 // activation's, shows in the norm of the whole result (10 times the mean square's root
 // and a sixteenth off: 1.7e-3 of the norm of 2^17, as much as the result's own
 // rounding), and widening costs little: eight experts of 768 x 2048, 16 rows each, 30 us
