@@ -33,6 +33,7 @@ EXPORTS = (
     "ep_lb_reduce_grads", "ep_pool_stats", "ep_get_dispatch_layout_noalloc", "ep_rms_norm",
     "ep_rms_norm_backward_workspace", "ep_rms_norm_backward", "ep_fp8_product", "ep_ll_expert_ffn",
     "ep_ll_expert_ffn_fp8", "ep_expert_rows", "ep_expert_ffn", "ep_expert_ffn_backward",
+    "ep_route_workspace", "ep_route", "ep_route_backward",
 )
 
 
@@ -60,6 +61,11 @@ class ExpertGroups(ctypes.Structure):
                 ("pair_slot", ctypes.c_void_p), ("row_pair", ctypes.c_void_p)]
 
 
+class RouterRule(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("num_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("normalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 class EpError(RuntimeError):
     def __init__(self, code: int, fn: str):
         self.code = code
@@ -81,6 +87,7 @@ def _load():
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
     f32, sz, pgroups = ctypes.c_float, ctypes.c_size_t, ctypes.POINTER(ExpertGroups)
+    prouter = ctypes.POINTER(RouterRule)
     pdims, pout = ctypes.POINTER(Dims), ctypes.POINTER(LayoutOut)
     sig = {
         "ep_max_recv_rows": (i64, [pdims]),
@@ -107,6 +114,9 @@ def _load():
         "ep_expert_rows": (ctypes.c_int, [pdims, vp, vp, i64, i64] + [vp] * 6),
         "ep_expert_ffn": (ctypes.c_int, [pdims, i32, pgroups] + [vp] * 9),
         "ep_expert_ffn_backward": (ctypes.c_int, [pdims, i32, pgroups] + [vp] * 15),
+        "ep_route_workspace": (sz, [pdims]),
+        "ep_route": (ctypes.c_int, [pdims, prouter, vp, i32] + [vp] * 6 + [sz, vp]),
+        "ep_route_backward": (ctypes.c_int, [pdims, prouter, vp, vp, i32] + [vp] * 4),
         "ep_handle_copy_layout": (ctypes.c_int, [vp, pout, vp]),
         "ep_handle_num_recv": (ctypes.c_int, [vp, ctypes.POINTER(i64)]),
         "ep_handle_dims": (ctypes.c_int, [vp, pdims]),

@@ -158,6 +158,26 @@ def fp8_product(a, w) -> torch.Tensor:
     return out
 
 
+@dataclass(frozen=True)
+class Router:
+    """How experts are chosen from logits and weighted (include/ep.h, ep_router): num_topk of them
+    by softmax or sigmoid scores, from the topk_groups best of num_groups groups, the
+    weights divided by the chosen ones' sum (normalize) and multiplied by scale."""
+
+    num_topk: int
+    score: str = "softmax"
+    num_groups: int = 1
+    topk_groups: int = 1
+    normalize: bool = True
+    scale: float = 1.0
+
+    def _raw(self) -> abi.RouterRule:
+        if self.score not in ("softmax", "sigmoid"):
+            raise ValueError(f"score must be softmax or sigmoid, got {self.score!r}")
+        return abi.RouterRule(int(self.score == "sigmoid"), self.num_groups, self.topk_groups, bool(self.normalize),
+                              self.scale)
+
+
 @dataclass
 class Layout:
     """Device copies of a dispatch layout ("What the Handle Contains")."""
@@ -694,6 +714,59 @@ class Buffer:
             abi.address(act), abi.address(terms), abi.address(parts), abi.address(dx), abi.address(dweights),
             abi.address(dw13), abi.address(dw2), abi.raw_stream(index)), "ep_expert_ffn_backward")
         return dx, dweights, dw13, dw2
+
+    # -------------------------------------------------------------- router
+    def _logits(self, logits: torch.Tensor) -> int:
+        """Checks logits [T, E], fp32 or bf16; returns 1 for bf16."""
+        bf16 = logits.dtype == torch.bfloat16
+        _need(logits, torch.bfloat16 if bf16 else torch.float32, "logits", 2)
+        _shape(logits, (logits.shape[0], self.num_experts), "logits")
+        return int(bf16)
+
+    def route(self, logits: torch.Tensor, router: Router, bias: Optional[torch.Tensor] = None,
+              score_sums: bool = False):
+        """Chooses each token's experts from logits [T, E] (fp32 or bf16).  Returns (topk_idx [T, K]
+        int64, topk_weights [T, K] fp32, sums): what dispatch and combine take, -1 with weight 0 where
+        too few experts are left.  bias [E] fp32 is added to the scores for the choice alone.
+        With score_sums, sums [E] fp32 is each expert's summed share of the tokens' scores, for a
+        balancing loss.  Experts on ranks masked in the mask buffer, and those whose logit is -inf, are
+        not chosen."""
+        bf16 = self._logits(logits)
+        T, K = logits.shape[0], router.num_topk
+        if bias is not None:
+            _row(bias, torch.float32, (self.num_experts,), "bias")
+        dev = _here(logits, bias, self._mask)
+        rule, d = router._raw(), self._dims(T, 8, K)
+        idx = torch.empty((T, max(K, 0)), dtype=torch.int64, device=logits.device)
+        weights = torch.empty((T, max(K, 0)), dtype=torch.float32, device=logits.device)
+        sums, work, size = None, None, 0
+        if score_sums:
+            sums = torch.empty(self.num_experts, dtype=torch.float32, device=logits.device)
+            size = abi.lib().ep_route_workspace(ctypes.byref(d))
+            work = torch.empty(size, dtype=torch.uint8, device=logits.device)
+        at = abi.address
+        abi.check(abi.lib().ep_route(ctypes.byref(d), ctypes.byref(rule), at(logits), bf16, at(bias), at(self._mask),
+                                     at(idx), at(weights), at(sums), at(work), size, abi.raw_stream(dev)), "ep_route")
+        return idx, weights, sums
+
+    def route_backward(self, dtopk_weights: torch.Tensor, logits: torch.Tensor, topk_idx: torch.Tensor, router: Router,
+                       dscore_sums: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """The gradient of route's logits (their type and shape) given those of topk_weights [T, K]
+        fp32, as combine sums them back, and of the score sums [E] fp32.  topk_idx is route's."""
+        bf16 = self._logits(logits)
+        T, K = logits.shape[0], router.num_topk
+        _row(dtopk_weights, torch.float32, (T, K), "dtopk_weights")
+        _row(topk_idx, torch.int64, (T, K), "topk_idx")
+        if dscore_sums is not None:
+            _row(dscore_sums, torch.float32, (self.num_experts,), "dscore_sums")
+        dev = _here(dtopk_weights, logits, topk_idx, dscore_sums)
+        out = torch.empty_like(logits)
+        rule, d = router._raw(), self._dims(T, 8, K)
+        at = abi.address
+        abi.check(abi.lib().ep_route_backward(ctypes.byref(d), ctypes.byref(rule), at(dtopk_weights), at(logits), bf16,
+                                              at(topk_idx), at(dscore_sums), at(out), abi.raw_stream(dev)),
+                  "ep_route_backward")
+        return out
 
     # ------------------------------------------------------ load balancing
     @staticmethod

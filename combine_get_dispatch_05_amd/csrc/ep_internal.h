@@ -176,6 +176,22 @@ hipError_t launch_rms_norm_backward(int64_t T, int H, const void *dout, const vo
                                     const void *weight, const float *rstd, const void *dresidual,
                                     void *dx, float *dweight, float *parts, hipStream_t stream);
 
+// out[c] = the sum of parts[0 .. n - 1][c], in a fixed order.
+hipError_t launch_sum_parts(const float *parts, int n, int width, float *out, hipStream_t stream);
+
+// ----------------------------------------------------------------- router
+
+struct RouteRule;  // route.h
+
+// Rows of fp32 partial score sums that the router writes.
+int route_parts(int64_t T, int experts);
+
+hipError_t launch_route(const RouteRule &rule, int64_t T, const void *logits, bool bf16, int64_t *topk_idx,
+                        float *weights, float *score_sums, float *parts, hipStream_t stream);
+
+hipError_t launch_route_backward(const RouteRule &rule, int64_t T, const float *dweights, const void *logits, bool bf16,
+                                 const int64_t *topk_idx, const float *dsums, void *dlogits, hipStream_t stream);
+
 // A block for each row.  A dimension of a launch holds fewer than 2^32 threads,
 // so rows past 2^20 go into y; the kernel drops the excess.
 constexpr int64_t kRowGrid = int64_t(1) << 20;

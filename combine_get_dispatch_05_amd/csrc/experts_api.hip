@@ -2,7 +2,7 @@
 // argument checks, then the launches.  Nothing here allocates or waits.
 #include <cmath>
 
-#include "ep_internal.h"
+#include "route.h"
 
 using namespace ep;
 
@@ -79,9 +79,95 @@ ExpertFfn ffn_of(const ep_dims *d, int32_t inter, const ep_expert_groups *g, con
     return f;
 }
 
+// The dims' experts, ranks and choices under a router.
+int check_router(const ep_dims *d, const ep_router *r)
+{
+    if (d == nullptr || r == nullptr)
+        return EP_ERR_INVALID;
+    if (d->num_tokens < 0 || d->num_tokens > kMaxTokens || d->num_topk < 1 || d->num_topk > kMaxTopk ||
+        d->num_ranks < 1 || d->num_ranks > kMaxRanks || d->num_experts < 1 || d->num_experts > kMaxExperts ||
+        d->num_experts % d->num_ranks != 0)
+        return EP_ERR_INVALID;
+    if (r->score != EP_SCORE_SOFTMAX && r->score != EP_SCORE_SIGMOID)
+        return EP_ERR_INVALID;
+    if (r->num_groups < 1 || r->num_groups > kMaxRouteGroups || d->num_experts % r->num_groups != 0 ||
+        r->topk_groups < 1 || r->topk_groups > r->num_groups || !std::isfinite(r->scale))
+        return EP_ERR_INVALID;
+    return EP_OK;
+}
+
+RouteRule rule_of(const ep_dims *d, const ep_router *r, const float *bias, const int32_t *rank_mask)
+{
+    RouteRule q{};
+    q.experts = d->num_experts;
+    q.topk = d->num_topk;
+    q.groups = r->num_groups;
+    q.topk_groups = r->topk_groups;
+    q.epr = d->num_experts / d->num_ranks;
+    q.soft = r->score == EP_SCORE_SOFTMAX;
+    q.normalize = r->normalize != 0;
+    q.scale = r->scale;
+    q.bias = bias;
+    q.rank_mask = rank_mask;
+    return q;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t ep_route_workspace(const ep_dims *dims)
+{
+    if (dims == nullptr || dims->num_tokens < 0 || dims->num_tokens > kMaxTokens || dims->num_experts < 1 ||
+        dims->num_experts > kMaxExperts)
+        return 0;
+    return size_t(route_parts(dims->num_tokens, dims->num_experts)) * dims->num_experts * sizeof(float);
+}
+
+int ep_route(const ep_dims *dims, const ep_router *router, const void *logits, int32_t logits_bf16, const float *bias,
+             const int32_t *rank_mask, int64_t *topk_idx, float *topk_weights, float *score_sums, void *workspace,
+             size_t workspace_bytes, ep_stream_t stream)
+{
+    Traced trace("ep_route");
+    const int rc = check_router(dims, router);
+    if (rc != EP_OK)
+        return rc;
+    const bool any = dims->num_tokens > 0;
+    if (any && (logits == nullptr || topk_idx == nullptr || topk_weights == nullptr))
+        return EP_ERR_INVALID;
+    if (!al(logits, logits_bf16 != 0 ? 2 : 4) || !al(bias, 4) || !al(rank_mask, 4) || !al(topk_idx, 8) ||
+        !al(topk_weights, 4) || !al(score_sums, 4) || !al(workspace, 4))
+        return EP_ERR_ALIGN;
+    if (score_sums != nullptr) {
+        if (any && workspace == nullptr)
+            return EP_ERR_INVALID;
+        if (workspace_bytes < ep_route_workspace(dims))
+            return EP_ERR_CAPACITY;
+    }
+    return done(launch_route(rule_of(dims, router, bias, rank_mask), dims->num_tokens, logits, logits_bf16 != 0, topk_idx,
+                             topk_weights, score_sums, static_cast<float *>(workspace),
+                             static_cast<hipStream_t>(stream)));
+}
+
+int ep_route_backward(const ep_dims *dims, const ep_router *router, const float *dtopk_weights, const void *logits,
+                      int32_t logits_bf16, const int64_t *topk_idx, const float *dscore_sums, void *dlogits,
+                      ep_stream_t stream)
+{
+    Traced trace("ep_route_backward");
+    const int rc = check_router(dims, router);
+    if (rc != EP_OK)
+        return rc;
+    if (dims->num_tokens > 0 &&
+        (dtopk_weights == nullptr || logits == nullptr || topk_idx == nullptr || dlogits == nullptr))
+        return EP_ERR_INVALID;
+    const size_t size = logits_bf16 != 0 ? 2 : 4;
+    if (!al(dtopk_weights, 4) || !al(logits, size) || !al(topk_idx, 8) || !al(dscore_sums, 4) || !al(dlogits, size))
+        return EP_ERR_ALIGN;
+    return done(launch_route_backward(rule_of(dims, router, nullptr, nullptr), dims->num_tokens, dtopk_weights, logits,
+                                      logits_bf16 != 0, topk_idx, dscore_sums, dlogits,
+                                      static_cast<hipStream_t>(stream)));
+}
+
 
 int ep_rms_norm(int32_t num_tokens, int32_t hidden, float eps, const void *x, const void *residual,
                 const void *weight, void *residual_out, void *out, void *out_q, float *out_scale,

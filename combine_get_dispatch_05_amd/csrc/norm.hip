@@ -318,6 +318,12 @@ __global__ __launch_bounds__(1024) void sum_parts_kernel(const float *__restrict
 
 }  // namespace
 
+hipError_t launch_sum_parts(const float *parts, int n, int width, float *out, hipStream_t stream)
+{
+    hipLaunchKernelGGL(sum_parts_kernel, dim3((width + 63) / 64), dim3(1024), 0, stream, parts, n, width, out);
+    return hipGetLastError();
+}
+
 hipError_t launch_rms_norm(int64_t T, int H, float eps, const void *x, const void *residual,
                            const void *weight, void *residual_out, void *out, void *out_q,
                            float *out_scale, float *rstd, hipStream_t stream)
@@ -398,9 +404,7 @@ hipError_t launch_rms_norm_backward(int64_t T, int H, const void *dout, const vo
         if (e != hipSuccess)
             return e;
     }
-    hipLaunchKernelGGL(sum_parts_kernel, dim3((H + 63) / 64), dim3(1024), 0, stream, parts, n, H,
-                       dweight);
-    return hipGetLastError();
+    return launch_sum_parts(parts, n, H, dweight, stream);
 }
 
 }  // namespace ep

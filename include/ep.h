@@ -496,6 +496,57 @@ int ep_expert_ffn_backward(const ep_dims *dims, int32_t inter, const ep_expert_g
                            void *act, float *terms, float *parts, void *dx, float *dtopk_weights,
                            void *dw13, void *dw2, ep_stream_t stream);
 
+/*
+ * The router: the experts of each token and their weights, from its logits l[e].
+ *   s = softmax(l) over all E experts, or sigmoid(l)
+ *   key[e] = s[e] + bias[e]; without a bias key[e] = l[e] (s grows with l)
+ *   with groups of E / num_groups neighbouring experts, the topk_groups groups of the
+ *   largest scores stay: a group's score is its largest key, with a bias the sum of
+ *   its two largest (of its largest alone where there is no second)
+ *   topk_idx[t]: the K largest keys left, largest first; equal keys (and groups) go to the lowest index
+ *   weight of a chosen expert: scale * s, or with normalize
+ *     softmax: scale * the softmax over the chosen logits alone
+ *     sigmoid: scale * s / (the chosen ones' sum + 1e-20)
+ * An expert whose logit is -inf or NaN, or whose rank is masked, is not chosen.  Slots for which
+ * nothing is left get -1 and weight 0.  The choice is that of exact keys: gaps within fp32 rounding are
+ * decided in 64 bits.  Weights are fp32.  Scores are not changed by the mask.  A row of
+ * -inf alone has scores 0; a softmax row with +inf or NaN has NaN for scores and weights.
+ */
+#define EP_SCORE_SOFTMAX 0
+#define EP_SCORE_SIGMOID 1
+typedef struct ep_router {
+    int32_t score;       /* EP_SCORE_SOFTMAX or EP_SCORE_SIGMOID */
+    int32_t num_groups;  /* 1 to 64, divides E; 1: no groups */
+    int32_t topk_groups; /* 1 to num_groups */
+    int32_t normalize;   /* nonzero: weights are divided by the chosen ones' sum */
+    float scale;         /* finite */
+} ep_router;
+
+/*
+ * Routes logits [num_tokens][E], fp32 or (logits_bf16 nonzero) bf16.  Of dims, the hidden
+ * size and channels are not used.  bias fp32 [E] and rank_mask int32 [R] are nullable.
+ *   topk_idx     int64 [num_tokens][K], topk_weights fp32 [num_tokens][K]
+ *   score_sums   fp32 [E], nullable: sum over tokens of p, p = s for softmax and s / sum(s)
+ *                for sigmoid scores (in a fixed order): with the tokens' counts, what a balancing
+ *                loss is made of.  It needs workspace, ep_route_workspace() bytes
+ *                (EP_ERR_CAPACITY if workspace_bytes is less).
+ * No host sync.
+ */
+size_t ep_route_workspace(const ep_dims *dims);
+int ep_route(const ep_dims *dims, const ep_router *router, const void *logits, int32_t logits_bf16,
+             const float *bias, const int32_t *rank_mask, int64_t *topk_idx, float *topk_weights,
+             float *score_sums, void *workspace, size_t workspace_bytes, ep_stream_t stream);
+
+/*
+ * Gradient of ep_route: dlogits [num_tokens][E], of the logits' type, overwritten, given the gradients
+ * of topk_weights [num_tokens][K] fp32 and (nullable) of score_sums [E] fp32.  topk_idx is what
+ * ep_route wrote (ids outside [0, E) are taken as -1); the choice itself has no gradient.
+ * The weights' sums are those of ep_route.  No host sync.
+ */
+int ep_route_backward(const ep_dims *dims, const ep_router *router, const float *dtopk_weights,
+                      const void *logits, int32_t logits_bf16, const int64_t *topk_idx,
+                      const float *dscore_sums, void *dlogits, ep_stream_t stream);
+
 /* Copy the handle's layout into caller buffers (fields may be NULL); same
  * shapes and capacity rule as ep_get_dispatch_layout. */
 int ep_handle_copy_layout(ep_handle *handle, ep_layout_out *out, ep_stream_t stream);
