@@ -33,7 +33,7 @@ EXPORTS = (
     "ep_lb_reduce_grads", "ep_pool_stats", "ep_get_dispatch_layout_noalloc", "ep_rms_norm",
     "ep_rms_norm_backward_workspace", "ep_rms_norm_backward", "ep_fp8_product", "ep_ll_expert_ffn",
     "ep_ll_expert_ffn_fp8", "ep_expert_rows", "ep_expert_ffn", "ep_expert_ffn_backward",
-    "ep_route_workspace", "ep_route", "ep_route_backward",
+    "ep_route_workspace", "ep_route", "ep_route_backward", "ep_ll_moe_workspace", "ep_ll_moe",
 )
 
 
@@ -117,6 +117,8 @@ def _load():
         "ep_route_workspace": (sz, [pdims]),
         "ep_route": (ctypes.c_int, [pdims, prouter, vp, i32] + [vp] * 6 + [sz, vp]),
         "ep_route_backward": (ctypes.c_int, [pdims, prouter, vp, vp, i32] + [vp] * 4),
+        "ep_ll_moe_workspace": (sz, [pdims, i32]),
+        "ep_ll_moe": (ctypes.c_int, [pdims, i32, prouter, vp, vp, i32] + [vp] * 11 + [sz, vp]),
         "ep_handle_copy_layout": (ctypes.c_int, [vp, pout, vp]),
         "ep_handle_num_recv": (ctypes.c_int, [vp, ctypes.POINTER(i64)]),
         "ep_handle_dims": (ctypes.c_int, [vp, pdims]),

@@ -768,6 +768,47 @@ class Buffer:
                   "ep_route_backward")
         return out
 
+    # --------------------------------------------------------- whole layer
+    def low_latency_moe(self, x: torch.Tensor, w_router: torch.Tensor, router: Router, w13, w2,
+                        bias: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None):
+        """A whole mixture-of-experts layer for up to 64 tokens x [T, H] bf16 and 512 experts, without
+        dispatch and combine: logits x w_router^T (w_router [E, H] bf16 or fp32; summed in 64 bits),
+        route (bias [E] fp32 for the choice alone), the chosen experts' gated feed-forward and the
+        weighted sum, with residual [T, H] bf16 added.  w13 [E, 2 I, H] (the gate's rows first) and
+        w2 [E, H, I] are bf16, or pairs (codes, scales) as for low_latency_expert_ffn; beside those too, x and
+        the activation stay bf16.  Returns (y [T, H] bf16, topk_idx [T, K] int64, topk_weights
+        [T, K] fp32).  Ranks masked in the mask buffer have none of their experts chosen."""
+        E, K = self.num_experts, router.num_topk
+        _need(x, torch.bfloat16, "x", 2)
+        T, H = x.shape
+        f32 = w_router.dtype == torch.float32
+        _row(w_router, torch.float32 if f32 else torch.bfloat16, (E, H), "w_router")
+        if bias is not None:
+            _row(bias, torch.float32, (E,), "bias")
+        if residual is not None:
+            _row(residual, torch.bfloat16, (T, H), "residual")
+        if isinstance(w13, (tuple, list)) or isinstance(w2, (tuple, list)):
+            (w13, s13), (w2, s2) = _fp8_pair(w13, "w13", 3, True), _fp8_pair(w2, "w2", 3, True)
+            inter = w2.shape[2]
+            _shape(w13, (E, 2 * inter, H), "w13 codes")
+            _shape(w2, (E, H, inter), "w2 codes")
+        else:
+            s13 = s2 = None
+            inter = self._expert_weights(w13, w2, H)
+        dev = _here(x, w_router, bias, residual, w13, s13, w2, s2, self._mask)
+        rule, d = router._raw(), self._dims(T, H, K)
+        at, like = abi.address, dict(device=x.device)
+        y = torch.empty_like(x)
+        idx = torch.empty((T, max(K, 0)), dtype=torch.int64, **like)
+        weights = torch.empty((T, max(K, 0)), dtype=torch.float32, **like)
+        size = abi.lib().ep_ll_moe_workspace(ctypes.byref(d), inter)
+        work = torch.empty(size, dtype=torch.uint8, **like)
+        abi.check(abi.lib().ep_ll_moe(
+            ctypes.byref(d), inter, ctypes.byref(rule), at(x), at(w_router), int(f32), at(bias), at(self._mask), at(w13),
+            at(s13), at(w2), at(s2), at(residual), at(idx), at(weights), at(y), at(work), size, abi.raw_stream(dev)),
+            "ep_ll_moe")
+        return y, idx, weights
+
     # ------------------------------------------------------ load balancing
     @staticmethod
     def _lb_args(redundant: torch.Tensor, expert: torch.Tensor, mapping: torch.Tensor):

@@ -192,6 +192,23 @@ hipError_t launch_route(const RouteRule &rule, int64_t T, const void *logits, bo
 hipError_t launch_route_backward(const RouteRule &rule, int64_t T, const float *dweights, const void *logits, bool bf16,
                                  const int64_t *topk_idx, const float *dsums, void *dlogits, hipStream_t stream);
 
+// ------------------------------------------------------------ whole layer
+
+constexpr int kMoeTokens = 64;    // a bit each in an expert's mask
+constexpr int kMoeExperts = 512;  // what the router holds in one wave
+
+struct MoeCall {
+    int T, H, I;
+    const void *x, *w_router, *w13, *w2, *residual;  // residual nullable
+    bool router_f32;
+    const float *w13_scale, *w2_scale;               // FP8 weights, else null
+    int64_t *topk_idx;
+    float *topk_weights;
+    void *y, *workspace;
+};
+size_t moe_workspace(int T, int E, int K, int I);
+hipError_t launch_moe(const RouteRule &rule, const MoeCall &call, hipStream_t stream);
+
 // A block for each row.  A dimension of a launch holds fewer than 2^32 threads,
 // so rows past 2^20 go into y; the kernel drops the excess.
 constexpr int64_t kRowGrid = int64_t(1) << 20;

@@ -149,6 +149,59 @@ int ep_route(const ep_dims *dims, const ep_router *router, const void *logits, i
                              static_cast<hipStream_t>(stream)));
 }
 
+size_t ep_ll_moe_workspace(const ep_dims *dims, int32_t inter)
+{
+    if (check_expert_dims(dims, inter, 8) != EP_OK || dims->num_tokens > kMoeTokens || dims->num_experts > kMoeExperts)
+        return 0;
+    return moe_workspace(dims->num_tokens, dims->num_experts, dims->num_topk, inter);
+}
+
+int ep_ll_moe(const ep_dims *dims, int32_t inter, const ep_router *router, const void *x, const void *w_router,
+              int32_t w_router_fp32, const float *bias, const int32_t *rank_mask, const void *w13,
+              const float *w13_scale, const void *w2, const float *w2_scale, const void *residual, int64_t *topk_idx,
+              float *topk_weights, void *y, void *workspace, size_t workspace_bytes, ep_stream_t stream)
+{
+    Traced trace("ep_ll_moe");
+    if ((w13_scale != nullptr) != (w2_scale != nullptr))
+        return EP_ERR_INVALID;
+    int rc = check_expert_dims(dims, inter, w13_scale != nullptr ? 128 : 8);
+    if (rc == EP_OK)
+        rc = check_router(dims, router);
+    if (rc != EP_OK)
+        return rc;
+    if (dims->num_tokens > kMoeTokens || dims->num_experts > kMoeExperts)
+        return EP_ERR_TOO_LARGE;
+    if (w_router == nullptr || w13 == nullptr || w2 == nullptr ||
+        (dims->num_tokens > 0 && (x == nullptr || topk_idx == nullptr || topk_weights == nullptr || y == nullptr ||
+                                  workspace == nullptr)))
+        return EP_ERR_INVALID;
+    if (!al(x, 16) || !al(w_router, 16) || !al(w13, 16) || !al(w2, 16) || !al(residual, 16) || !al(y, 16) ||
+        !al(workspace, 256) || !al(bias, 4) || !al(rank_mask, 4) || !al(w13_scale, 4) || !al(w2_scale, 4) ||
+        !al(topk_idx, 8) || !al(topk_weights, 4))
+        return EP_ERR_ALIGN;
+    if (workspace_bytes < ep_ll_moe_workspace(dims, inter))
+        return EP_ERR_CAPACITY;
+    if (dims->num_tokens == 0)
+        return EP_OK;
+    MoeCall c{};
+    c.T = dims->num_tokens;
+    c.H = dims->hidden;
+    c.I = inter;
+    c.x = x;
+    c.w_router = w_router;
+    c.router_f32 = w_router_fp32 != 0;
+    c.w13 = w13;
+    c.w13_scale = w13_scale;
+    c.w2 = w2;
+    c.w2_scale = w2_scale;
+    c.residual = residual;
+    c.topk_idx = topk_idx;
+    c.topk_weights = topk_weights;
+    c.y = y;
+    c.workspace = workspace;
+    return done(launch_moe(rule_of(dims, router, bias, rank_mask), c, static_cast<hipStream_t>(stream)));
+}
+
 int ep_route_backward(const ep_dims *dims, const ep_router *router, const float *dtopk_weights, const void *logits,
                       int32_t logits_bf16, const int64_t *topk_idx, const float *dscore_sums, void *dlogits,
                       ep_stream_t stream)

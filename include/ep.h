@@ -71,7 +71,7 @@ typedef enum ep_status {
     EP_ERR_HANDLE = 4,   /* handle does not match the dims, or NULL handle */
     EP_ERR_HIP = 5,      /* a HIP runtime call failed (see ep_last_hip_error) */
     EP_ERR_NOMEM = 6,    /* device or host allocation failed */
-    EP_ERR_TOO_LARGE = 7 /* needs more than ep_get_dispatch_layout_noalloc's static scratch */
+    EP_ERR_TOO_LARGE = 7 /* larger than the call takes (ep_get_dispatch_layout_noalloc, ep_ll_moe) */
 } ep_status;
 
 /* Problem sizes.  Limits: 0 <= num_tokens <= 2^24; hidden > 0, hidden % 8 == 0,
@@ -546,6 +546,30 @@ int ep_route(const ep_dims *dims, const ep_router *router, const void *logits, i
 int ep_route_backward(const ep_dims *dims, const ep_router *router, const float *dtopk_weights,
                       const void *logits, int32_t logits_bf16, const int64_t *topk_idx,
                       const float *dscore_sums, void *dlogits, ep_stream_t stream);
+
+/*
+ * A whole mixture-of-experts layer for a few tokens: router, experts and combine in one call, no rows
+ * packed in between.
+ *   logits[t][e] = fp32(x[t] . w_router[e]), summed in 64 bits
+ *   topk_idx, topk_weights as ep_route gives them for these logits
+ *   y[t] = bf16_rne( residual[t] + sum over its experts, fp32, of weight * (act W2^T) ), act as for
+ *          ep_ll_expert_ffn, rounded to bf16 between the products
+ * x, residual (nullable), y [num_tokens][hidden] bf16; y may be the same memory as residual, not as x.
+ * w_router [E][hidden] bf16, or fp32 with w_router_fp32 nonzero.  bias [E], rank_mask [R] nullable.
+ * w13 [E][2 inter][hidden], w2 [E][hidden][inter]: bf16, or with w13_scale and w2_scale (both or neither)
+ * FP8 codes and scales as for ep_ll_expert_ffn_fp8.  Beside FP8 weights too, x and
+ * act stay bf16: every product is exact and summed in fp32, the scales applied once per 128 of K.
+ * A token's experts do not depend on the batch it comes in.
+ * num_tokens <= 64 and E <= 512 (EP_ERR_TOO_LARGE); hidden % 8 == 0 and inter % 8 == 0, with FP8
+ * % 128 (EP_ERR_ALIGN).  workspace: ep_ll_moe_workspace() bytes, 256-byte aligned
+ * (EP_ERR_CAPACITY if workspace_bytes is less).  No host sync.
+ */
+size_t ep_ll_moe_workspace(const ep_dims *dims, int32_t inter);
+int ep_ll_moe(const ep_dims *dims, int32_t inter, const ep_router *router, const void *x, const void *w_router,
+              int32_t w_router_fp32, const float *bias, const int32_t *rank_mask, const void *w13,
+              const float *w13_scale, const void *w2, const float *w2_scale, const void *residual,
+              int64_t *topk_idx, float *topk_weights, void *y, void *workspace, size_t workspace_bytes,
+              ep_stream_t stream);
 
 /* Copy the handle's layout into caller buffers (fields may be NULL); same
  * shapes and capacity rule as ep_get_dispatch_layout. */
