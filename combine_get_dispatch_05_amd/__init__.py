@@ -7,7 +7,8 @@ Importing it requires the built library -- there is no CPU fallback.
 
 from . import abi  # noqa: F401  (raises ImportError when libep.so is missing)
 from .buffer import (Buffer, ExpertRows, Handle, Layout, LowLatencyHandle, Router,  # noqa: F401
-                     fp8_product, rms_norm, rms_norm_backward)
+                     adapter_product, adapter_product_backward, fp8_product, rms_norm, rms_norm_backward)
 
-__all__ = ["Buffer", "ExpertRows", "Handle", "Layout", "LowLatencyHandle", "Router", "abi", "fp8_product",
+__all__ = ["Buffer", "ExpertRows", "Handle", "Layout", "LowLatencyHandle", "Router", "abi", "adapter_product",
+           "adapter_product_backward", "fp8_product",
            "rms_norm", "rms_norm_backward"]

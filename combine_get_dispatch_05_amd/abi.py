@@ -34,6 +34,7 @@ EXPORTS = (
     "ep_rms_norm_backward_workspace", "ep_rms_norm_backward", "ep_fp8_product", "ep_ll_expert_ffn",
     "ep_ll_expert_ffn_fp8", "ep_expert_rows", "ep_expert_ffn", "ep_expert_ffn_backward",
     "ep_route_workspace", "ep_route", "ep_route_backward", "ep_ll_moe_workspace", "ep_ll_moe",
+    "ep_adapter_workspace", "ep_adapter_product", "ep_adapter_product_backward",
 )
 
 
@@ -66,6 +67,11 @@ class RouterRule(ctypes.Structure):
                 ("normalize", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class AdapterDims(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32),
+                ("rank", ctypes.c_int32), ("num_adapters", ctypes.c_int32)]
+
+
 class EpError(RuntimeError):
     def __init__(self, code: int, fn: str):
         self.code = code
@@ -87,6 +93,7 @@ def _load():
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
     f32, sz, pgroups = ctypes.c_float, ctypes.c_size_t, ctypes.POINTER(ExpertGroups)
+    padapter = ctypes.POINTER(AdapterDims)
     prouter = ctypes.POINTER(RouterRule)
     pdims, pout = ctypes.POINTER(Dims), ctypes.POINTER(LayoutOut)
     sig = {
@@ -119,6 +126,9 @@ def _load():
         "ep_route_backward": (ctypes.c_int, [pdims, prouter, vp, vp, i32] + [vp] * 4),
         "ep_ll_moe_workspace": (sz, [pdims, i32]),
         "ep_ll_moe": (ctypes.c_int, [pdims, i32, prouter, vp, vp, i32] + [vp] * 11 + [sz, vp]),
+        "ep_adapter_workspace": (sz, [padapter, i32]),
+        "ep_adapter_product": (ctypes.c_int, [padapter] + [vp] * 9 + [sz, vp]),
+        "ep_adapter_product_backward": (ctypes.c_int, [padapter] + [vp] * 12 + [sz, vp]),
         "ep_handle_copy_layout": (ctypes.c_int, [vp, pout, vp]),
         "ep_handle_num_recv": (ctypes.c_int, [vp, ctypes.POINTER(i64)]),
         "ep_handle_dims": (ctypes.c_int, [vp, pdims]),

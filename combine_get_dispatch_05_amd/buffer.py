@@ -158,6 +158,66 @@ def fp8_product(a, w) -> torch.Tensor:
     return out
 
 
+def _adapter_args(x, adapter_ids, down, up, scales):
+    _need(x, torch.bfloat16, "x", 2)
+    T, K = x.shape
+    _row(adapter_ids, torch.int64, (T,), "adapter_ids")
+    _need(down, torch.bfloat16, "down", 3)
+    L, r = down.shape[:2]
+    _row(down, torch.bfloat16, (L, r, K), "down")
+    _need(up, torch.bfloat16, "up", 3)
+    N = up.shape[1]
+    _row(up, torch.bfloat16, (L, N, r), "up")
+    _row(scales, torch.float32, (L,), "scales")
+    return abi.AdapterDims(T, K, N, r, L)
+
+
+def adapter_product(x: torch.Tensor, adapter_ids: torch.Tensor, down: torch.Tensor, up: torch.Tensor,
+                    scales: torch.Tensor, base: Optional[torch.Tensor] = None, save: bool = False):
+    """Low-rank adapters of many requests beside a shared projection: out[t] = base[t] + scales[a]
+    (x[t] down_a^T) up_a^T with a = adapter_ids[t] (int64 [T]; outside [0, L): no adapter).  x [T, K] and
+    base [T, N] (the projection's output; None: zeros) bf16, down [L, r, K], up [L, N, r] bf16 with r up to
+    128, scales [L] fp32.  Returns (out [T, N] bf16, hidden): hidden [T, r] bf16 is what
+    adapter_product_backward takes, None without save."""
+    d = _adapter_args(x, adapter_ids, down, up, scales)
+    T, N = d.num_tokens, d.out_features
+    if base is not None:
+        _row(base, torch.bfloat16, (T, N), "base")
+    dev = _here(x, adapter_ids, down, up, scales, base)
+    out = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
+    hidden = torch.empty((T, d.rank), dtype=torch.bfloat16, device=x.device) if save else None
+    size = abi.lib().ep_adapter_workspace(ctypes.byref(d), 0)
+    work = torch.empty(size, dtype=torch.uint8, device=x.device)
+    at = abi.address
+    abi.check(abi.lib().ep_adapter_product(ctypes.byref(d), at(x), at(adapter_ids), at(down), at(up), at(scales), at(base),
+                                           at(out), at(hidden), at(work), size, abi.raw_stream(dev)),
+              "ep_adapter_product")
+    return out, hidden
+
+
+def adapter_product_backward(dy: torch.Tensor, x: torch.Tensor, adapter_ids: torch.Tensor, down: torch.Tensor,
+                             up: torch.Tensor, scales: torch.Tensor, hidden: torch.Tensor,
+                             dx_base: Optional[torch.Tensor] = None):
+    """Gradients of adapter_product given dy [T, N] bf16 (base's gradient is dy itself).  dx_base [T, K] bf16 is
+    the projection's own gradient of x, to which the adapters' is added.  Returns (dx [T, K], ddown, dup), bf16;
+    an adapter without tokens has zeros."""
+    d = _adapter_args(x, adapter_ids, down, up, scales)
+    T = d.num_tokens
+    _row(dy, torch.bfloat16, (T, d.out_features), "dy")
+    _row(hidden, torch.bfloat16, (T, d.rank), "hidden")
+    if dx_base is not None:
+        _row(dx_base, torch.bfloat16, (T, d.in_features), "dx_base")
+    dev = _here(dy, x, adapter_ids, down, up, scales, hidden, dx_base)
+    dx, ddown, dup = torch.empty_like(x), torch.empty_like(down), torch.empty_like(up)
+    size = abi.lib().ep_adapter_workspace(ctypes.byref(d), 1)
+    work = torch.empty(size, dtype=torch.uint8, device=x.device)
+    at = abi.address
+    abi.check(abi.lib().ep_adapter_product_backward(
+        ctypes.byref(d), at(dy), at(x), at(adapter_ids), at(down), at(up), at(scales), at(hidden), at(dx_base), at(dx),
+        at(ddown), at(dup), at(work), size, abi.raw_stream(dev)), "ep_adapter_product_backward")
+    return dx, ddown, dup
+
+
 @dataclass(frozen=True)
 class Router:
     """How experts are chosen from logits and weighted (include/ep.h, ep_router): num_topk of them

@@ -1270,7 +1270,7 @@ const char *ep_status_str(int status)
     case EP_ERR_HANDLE: return "handle missing or does not match the dims";
     case EP_ERR_HIP: return "HIP runtime error";
     case EP_ERR_NOMEM: return "out of memory";
-    case EP_ERR_TOO_LARGE: return "problem is larger than this call takes";
+    case EP_ERR_TOO_LARGE: return "problem needs more than this call offers";
     default: return "unknown status";
     }
 }

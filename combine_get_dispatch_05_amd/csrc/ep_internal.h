@@ -209,6 +209,23 @@ struct MoeCall {
 size_t moe_workspace(int T, int E, int K, int I);
 hipError_t launch_moe(const RouteRule &rule, const MoeCall &call, hipStream_t stream);
 
+// --------------------------------------------------------------- adapters
+
+constexpr int kMaxRank = 128;
+constexpr int kMaxAdapters = 8192;
+
+struct AdapterShape {
+    int T, K, N, r, L;
+    const int64_t *ids;   // [T]
+    const float *scales;  // [L]
+};
+size_t adapter_workspace(const AdapterShape &s, bool back);
+hipError_t launch_adapter(const AdapterShape &s, const void *x, const void *down, const void *up, const void *base, void *out,
+                          void *hidden, void *workspace, hipStream_t stream);
+hipError_t launch_adapter_backward(const AdapterShape &s, const void *dy, const void *x, const void *down, const void *up,
+                                   const void *hidden, const void *dx_base, void *dx, void *ddown, void *dup, void *workspace,
+                                   hipStream_t stream);
+
 // A block for each row.  A dimension of a launch holds fewer than 2^32 threads,
 // so rows past 2^20 go into y; the kernel drops the excess.
 constexpr int64_t kRowGrid = int64_t(1) << 20;

@@ -112,9 +112,79 @@ RouteRule rule_of(const ep_dims *d, const ep_router *r, const float *bias, const
     return q;
 }
 
+int check_adapters(const ep_adapter_dims *d)
+{
+    if (d == nullptr || d->num_tokens < 0 || d->num_tokens > kMaxTokens || d->in_features <= 0 ||
+        d->in_features > kMaxHidden || d->out_features <= 0 || d->out_features > kMaxHidden || d->rank <= 0 ||
+        d->rank > kMaxRank || d->num_adapters < 1 || d->num_adapters > kMaxAdapters)
+        return EP_ERR_INVALID;
+    return d->in_features % 8 != 0 || d->out_features % 8 != 0 || d->rank % 8 != 0 ? EP_ERR_ALIGN : EP_OK;
+}
+
+AdapterShape adapters_of(const ep_adapter_dims *d, const int64_t *ids, const float *scales)
+{
+    return {d->num_tokens, d->in_features, d->out_features, d->rank, d->num_adapters, ids, scales};
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t ep_adapter_workspace(const ep_adapter_dims *dims, int32_t backward)
+{
+    if (check_adapters(dims) != EP_OK)
+        return 0;
+    return adapter_workspace(adapters_of(dims, nullptr, nullptr), backward != 0);
+}
+
+int ep_adapter_product(const ep_adapter_dims *dims, const void *x, const int64_t *adapter_ids, const void *down,
+                       const void *up, const float *scales, const void *base, void *out, void *hidden, void *workspace,
+                       size_t workspace_bytes, ep_stream_t stream)
+{
+    Traced trace("ep_adapter_product");
+    const int rc = check_adapters(dims);
+    if (rc != EP_OK)
+        return rc;
+    if (down == nullptr || up == nullptr || scales == nullptr ||
+        (dims->num_tokens > 0 && (x == nullptr || adapter_ids == nullptr || out == nullptr || workspace == nullptr)))
+        return EP_ERR_INVALID;
+    if (!al(x, 16) || !al(down, 16) || !al(up, 16) || !al(base, 16) || !al(out, 16) || !al(hidden, 16) ||
+        !al(workspace, 256) || !al(adapter_ids, 8) || !al(scales, 4))
+        return EP_ERR_ALIGN;
+    if (workspace_bytes < ep_adapter_workspace(dims, 0))
+        return EP_ERR_CAPACITY;
+    if (dims->num_tokens == 0)
+        return EP_OK;
+    return done(launch_adapter(adapters_of(dims, adapter_ids, scales), x, down, up, base, out, hidden, workspace,
+                               static_cast<hipStream_t>(stream)));
+}
+
+int ep_adapter_product_backward(const ep_adapter_dims *dims, const void *dy, const void *x, const int64_t *adapter_ids,
+                                const void *down, const void *up, const float *scales, const void *hidden,
+                                const void *dx_base, void *dx, void *ddown, void *dup, void *workspace,
+                                size_t workspace_bytes, ep_stream_t stream)
+{
+    Traced trace("ep_adapter_product_backward");
+    const int rc = check_adapters(dims);
+    if (rc != EP_OK)
+        return rc;
+    if (down == nullptr || up == nullptr || scales == nullptr || ddown == nullptr || dup == nullptr ||
+        workspace == nullptr ||
+        (dims->num_tokens > 0 && (dy == nullptr || x == nullptr || adapter_ids == nullptr || hidden == nullptr ||
+                                  dx == nullptr)))
+        return EP_ERR_INVALID;
+    if (!al(dy, 16) || !al(x, 16) || !al(down, 16) || !al(up, 16) || !al(hidden, 16) || !al(dx_base, 16) || !al(dx, 16) ||
+        !al(ddown, 16) || !al(dup, 16) || !al(workspace, 256) || !al(adapter_ids, 8) || !al(scales, 4))
+        return EP_ERR_ALIGN;
+    // the gradients' blocks are one launch
+    const int64_t runs = (int64_t(dims->in_features) + 255) / 256 + (int64_t(dims->out_features) + 255) / 256;
+    if (dims->num_adapters * runs > kMaxTileBlocks)
+        return EP_ERR_INVALID;
+    if (workspace_bytes < ep_adapter_workspace(dims, 1))
+        return EP_ERR_CAPACITY;
+    return done(launch_adapter_backward(adapters_of(dims, adapter_ids, scales), dy, x, down, up, hidden, dx_base, dx,
+                                        ddown, dup, workspace, static_cast<hipStream_t>(stream)));
+}
 
 size_t ep_route_workspace(const ep_dims *dims)
 {

@@ -571,6 +571,43 @@ int ep_ll_moe(const ep_dims *dims, int32_t inter, const ep_router *router, const
               int64_t *topk_idx, float *topk_weights, void *y, void *workspace, size_t workspace_bytes,
               ep_stream_t stream);
 
+/*
+ * Low-rank adapters of many requests beside a shared projection (ep_fp8_product's, or any other): token t
+ * uses adapter a = adapter_ids[t], none if that is outside [0, num_adapters).
+ *   h[t] = bf16_rne( scales[a] * (x[t] down_a^T) ),  out[t] = bf16_rne( base[t] + h[t] up_a^T )
+ * with fp32 sums; a token without an adapter gets base[t] (zeros without a base).
+ *   x [T][in] bf16, adapter_ids int64 [T], down [L][rank][in], up [L][out][rank] bf16, scales fp32 [L]
+ *   base [T][out] bf16, nullable; out [T][out] may be the same memory as base
+ *   hidden [T][rank] bf16, nullable: h, which the backward pass takes (zeros without an adapter)
+ * in, out and rank % 8 == 0 (EP_ERR_ALIGN), rank <= 128, L <= 8192.  workspace: ep_adapter_workspace(dims, 0)
+ * bytes, 256-byte aligned (EP_ERR_CAPACITY if workspace_bytes is less).  No host sync.
+ */
+typedef struct ep_adapter_dims {
+    int32_t num_tokens;   /* T */
+    int32_t in_features;  /* x's width */
+    int32_t out_features; /* out's width */
+    int32_t rank;
+    int32_t num_adapters; /* L */
+} ep_adapter_dims;
+size_t ep_adapter_workspace(const ep_adapter_dims *dims, int32_t backward);
+int ep_adapter_product(const ep_adapter_dims *dims, const void *x, const int64_t *adapter_ids, const void *down,
+                       const void *up, const float *scales, const void *base, void *out, void *hidden,
+                       void *workspace, size_t workspace_bytes, ep_stream_t stream);
+
+/*
+ * Gradients of ep_adapter_product given dy [T][out] bf16 (base's gradient is dy itself; scales are constants):
+ *   dh[t] = bf16_rne( scales[a] * (dy[t] up_a) ),  dx[t] = bf16_rne( dx_base[t] + dh[t] down_a )
+ *   ddown_a = bf16_rne( sum_t dh[t]^T x[t] ),  dup_a = bf16_rne( sum_t dy[t]^T h[t] ),  in a fixed order
+ * dx_base [T][in] (nullable) is the projection's own gradient of x; dx may be the same memory.  ddown and
+ * dup are overwritten whole (zeros for adapters without tokens).  hidden is ep_adapter_product's.
+ * workspace: ep_adapter_workspace(dims, 1) bytes.  No host sync.
+ */
+int ep_adapter_product_backward(const ep_adapter_dims *dims, const void *dy, const void *x,
+                                const int64_t *adapter_ids, const void *down, const void *up,
+                                const float *scales, const void *hidden, const void *dx_base, void *dx,
+                                void *ddown, void *dup, void *workspace, size_t workspace_bytes,
+                                ep_stream_t stream);
+
 /* Copy the handle's layout into caller buffers (fields may be NULL); same
  * shapes and capacity rule as ep_get_dispatch_layout. */
 int ep_handle_copy_layout(ep_handle *handle, ep_layout_out *out, ep_stream_t stream);
