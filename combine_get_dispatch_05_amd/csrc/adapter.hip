@@ -182,7 +182,7 @@ __device__ __forceinline__ void shrink_tile(const AdapterArgs &a, const AdapterT
             const int row = j * 16 + (lane & 15);
             prow[j] = w + int64_t(row < a.r ? row : a.r - 1) * width * 2;
         }
-        stream<false, TAIL, (RT * MT > 4 ? 2 : 4)>(prow, none, qrow, s0, s1, width * 2, lane, acc);
+        stream<false, TAIL, (RT * MT > 4 ? 2 : 4), 1>(prow, none, qrow, s0, s1, width * 2, lane, acc);
     }
 #pragma unroll
     for (int j = 0; j < RT; ++j)

@@ -104,6 +104,11 @@ RouteRule rule_of(const ep_dims *d, const ep_router *r, const float *bias, const
     q.groups = r->num_groups;
     q.topk_groups = r->topk_groups;
     q.epr = d->num_experts / d->num_ranks;
+    q.size = q.experts / q.groups;
+    q.lanes = 64;
+    while (q.lanes * q.groups > 64)
+        q.lanes /= 2;
+    q.per_size = 1.0f / float(q.size);
     q.soft = r->score == EP_SCORE_SOFTMAX;
     q.normalize = r->normalize != 0;
     q.scale = r->scale;

@@ -13,67 +13,110 @@ namespace ep {
 
 namespace {
 
-constexpr int kAhead = 4;
-
-struct ActiveExpert {
+struct alignas(32) ActiveExpert {
     int32_t expert, start, count, unused;  // its pairs: [start, start + count)
+    uint64_t tokens;                       // bit t: token t
 };
+// The token of its i-th pair.
+__device__ __forceinline__ int token_of(uint64_t tokens, int i)
+{
+    for (; i > 0; --i)
+        tokens &= tokens - 1;
+    return __builtin_ctzll(tokens);
+}
+
+// K steps that a wave keeps in flight: as many as fit some 100 registers, at most four (a run's length is
+// rounded up to them).
+constexpr int ahead(bool fp8, int C, int RT, int MT)
+{
+    const int n = 100 / (4 * (RT * 2 / C + MT * (fp8 ? 4 : 2) / C));
+    return n < 2 ? 2 : n < 4 ? n : 4;
+}
+
+constexpr int kLogitSplits = 8;  // at most
 
 struct MoeWork {
-    float *logits;         // [T][E]
-    int32_t *active_count;
-    ActiveExpert *active;  // [min(P, E)]
-    int32_t *pair_token;   // [P], sorted by (expert, token)
-    float *pair_weight;    // [P]
+    double *logits;        // [splits][T][E] parts
+    int splits;
+    ActiveExpert *active;  // [min(P, E)], those that tokens chose first, the others with no pairs
+    float *pair_weight;    // [P], by (expert, token)
     uint16_t *act;         // [P][I]
 };
 
 // ----------------------------------------------------------------- router
 
-// One expert a block, up to TT tokens: logits[t][e] in 64 bits, so that a choice depends neither on the batch
-// nor on the order of a sum.
-template <int TT, bool F32>
-__global__ __launch_bounds__(256) void moe_logits_kernel(const u32x4 *x, const void *w_router, int T, int E, int V,
-                                                         float *logits)
+// logits[t][e] in 64 bits, so that a choice depends neither on the batch nor on the order of a sum.
+// Eight values of a router row as doubles.
+template <bool F32>
+__device__ __forceinline__ void router8(const void *w, int64_t v, double (&d)[8])
 {
-    __shared__ double red[4][TT];
-    const int e = blockIdx.x, t0 = blockIdx.y * TT;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    double acc[TT] = {};
+    if constexpr (F32) {
+        const float4 a = static_cast<const float4 *>(w)[2 * v], b = static_cast<const float4 *>(w)[2 * v + 1];
+        d[0] = a.x, d[1] = a.y, d[2] = a.z, d[3] = a.w, d[4] = b.x, d[5] = b.y, d[6] = b.z, d[7] = b.w;
+    } else {
+        const u32x4 a = static_cast<const u32x4 *>(w)[v];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            d[2 * q] = bf16_lo(a[q]), d[2 * q + 1] = bf16_hi(a[q]);
+    }
+}
+
+// One token: an expert a block.
+template <bool F32>
+__global__ __launch_bounds__(256) void moe_logits_kernel(const u32x4 *x, const void *w_router, int E, int V, double *logits)
+{
+    __shared__ double red[4];
+    const int e = blockIdx.x;
+    double acc = 0;
     for (int v = threadIdx.x; v < V; v += 256) {
         double w[8];
-        if constexpr (F32) {
-            const float4 *p = static_cast<const float4 *>(w_router) + (int64_t(e) * V + v) * 2;
-            const float4 a = p[0], b = p[1];
-            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-        } else {
-            const u32x4 a = static_cast<const u32x4 *>(w_router)[int64_t(e) * V + v];
+        router8<F32>(w_router, int64_t(e) * V + v, w);
+        const u32x4 b = x[v];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                w[2 * q] = bf16_lo(a[q]), w[2 * q + 1] = bf16_hi(a[q]);
-        }
-#pragma unroll
-        for (int i = 0; i < TT; ++i) {
-            const int t = t0 + i < T ? t0 + i : T - 1;
-            const u32x4 b = x[int64_t(t) * V + v];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                acc[i] = fma(w[2 * q], double(bf16_lo(b[q])), acc[i]);
-                acc[i] = fma(w[2 * q + 1], double(bf16_hi(b[q])), acc[i]);
-            }
+        for (int q = 0; q < 4; ++q) {
+            acc = fma(w[2 * q], double(bf16_lo(b[q])), acc);
+            acc = fma(w[2 * q + 1], double(bf16_hi(b[q])), acc);
         }
     }
-#pragma unroll
-    for (int i = 0; i < TT; ++i) {
-        acc[i] = wave_sum(acc[i]);
-        if (lane == 0)
-            red[wave][i] = acc[i];
-    }
+    acc = wave_sum(acc);
+    if ((threadIdx.x & 63) == 0)
+        red[threadIdx.x >> 6] = acc;
     __syncthreads();
-    if (threadIdx.x < TT && t0 + int(threadIdx.x) < T) {
-        const int i = threadIdx.x;
-        logits[int64_t(t0 + i) * E + e] = float(red[0][i] + red[1][i] + red[2][i] + red[3][i]);
+    if (threadIdx.x == 0)
+        logits[e] = red[0] + red[1] + red[2] + red[3];
+}
+
+// More: 16 experts by 16 tokens a block on the matrix cores, K shared out over its waves and gridDim.z blocks.
+template <bool F32>
+__global__ __launch_bounds__(256) void moe_logits_tile_kernel(const u32x4 *x, const void *w_router, int T, int E, int V,
+                                                              double *logits)
+{
+    typedef double f64x4 __attribute__((ext_vector_type(4)));
+    __shared__ double sums[4][16][16];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16;
+    const int e = e0 + (lane & 15) < E ? e0 + (lane & 15) : E - 1, t = t0 + (lane & 15) < T ? t0 + (lane & 15) : T - 1;
+    const int steps = (V + 3) / 4, part = int(blockIdx.z) * 4 + wave, of = int(gridDim.z) * 4;
+    f64x4 acc = {};
+    for (int s = steps * part / of; s < steps * (part + 1) / of; ++s) {
+        const int v = s * 4 + (lane >> 4);
+        double w[8] = {}, q[8] = {};
+        if (v < V) {
+            router8<F32>(w_router, int64_t(e) * V + v, w);
+            router8<false>(x, int64_t(t) * V + v, q);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            acc = __builtin_amdgcn_mfma_f64_16x16x4f64(w[i], q[i], acc, 0, 0, 0);
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // expert 4 i + l / 16, token l % 16
+        sums[wave][lane & 15][4 * i + (lane >> 4)] = acc[i];
+    __syncthreads();
+    const int i = threadIdx.x >> 4, j = threadIdx.x & 15;
+    if (t0 + i < T && e0 + j < E)
+        logits[(int64_t(blockIdx.z) * T + t0 + i) * E + e0 + j] =
+            sums[0][i][j] + sums[1][i][j] + sums[2][i][j] + sums[3][i][j];
 }
 
 // All tokens' choices, and the pairs by expert: bit t of an expert's mask is token t.
@@ -81,9 +124,12 @@ template <int V>
 __global__ __launch_bounds__(1024) void moe_select_kernel(RouteRule r, int T, MoeWork work, int64_t *topk_idx, float *topk_weights)
 {
     __shared__ double scratch[16][V * 64];
+    __shared__ float row[16][V * 64], weights[kMoeTokens * kMaxTopk];
+    __shared__ int16_t ids[kMoeTokens * kMaxTopk];
     __shared__ unsigned long long mask[kWaveExperts];
     __shared__ int start[kWaveExperts];
     __shared__ uint32_t totals[kWaveExperts / 64];
+    __shared__ int used;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     if (threadIdx.x < kWaveExperts)
         mask[threadIdx.x] = 0;
@@ -94,15 +140,27 @@ __global__ __launch_bounds__(1024) void moe_select_kernel(RouteRule r, int T, Mo
     for (int j = 0; j < V; ++j)
         bias[j] = r.bias != nullptr && j * 64 + lane < r.experts ? r.bias[j * 64 + lane] : 0.0f;
     for (int t = wave; t < T; t += 16) {
-        const float *row = work.logits + int64_t(t) * r.experts;
         float l[V], s[V] = {}, w;
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            l[j] = j * 64 + lane < r.experts ? row[j * 64 + lane] : -INFINITY;
-        const int e = route_row(r, l, bias, live, lane, scratch[wave], false, s, [&](int i) { return row[i]; }, w);
+        for (int j = 0; j < V; ++j) {
+            const int e = j * 64 + lane;
+            double part[kLogitSplits] = {};  // all loads in flight
+#pragma unroll
+            for (int i = 0; i < kLogitSplits; ++i)
+                if (i < work.splits && e < r.experts)
+                    part[i] = work.logits[(int64_t(i) * T + t) * r.experts + e];
+#pragma unroll
+            for (int i = 1; i < kLogitSplits; ++i)
+                part[0] += part[i];
+            l[j] = e < r.experts ? float(part[0]) : -INFINITY;
+            row[wave][e] = l[j];
+        }
+        const int e = route_row(r, l, bias, live, lane, scratch[wave], false, false, s, [&](int i) { return row[wave][i]; }, w);
         if (lane < r.topk) {
             topk_idx[t * r.topk + lane] = e;
             topk_weights[t * r.topk + lane] = w;
+            ids[t * r.topk + lane] = int16_t(e);
+            weights[t * r.topk + lane] = w;
             if (e >= 0)
                 atomicOr(&mask[e], 1ull << t);
         }
@@ -124,19 +182,20 @@ __global__ __launch_bounds__(1024) void moe_select_kernel(RouteRule r, int T, Mo
             before += totals[w];
         start[threadIdx.x] = int(before >> 16);
         if (own != 0)
-            work.active[before & 0xffff] = ActiveExpert{int(threadIdx.x), int(before >> 16), int(own >> 16), 0};
+            work.active[before & 0xffff] =
+                ActiveExpert{int(threadIdx.x), int(before >> 16), int(own >> 16), 0, mask[threadIdx.x]};
         if (threadIdx.x == kWaveExperts - 1)
-            *work.active_count = int((before + own) & 0xffff);
+            used = int((before + own) & 0xffff);
     }
     __syncthreads();
-    // (this block's own stores)
+    const int room = T * r.topk < r.experts ? T * r.topk : r.experts;
+    for (int i = used + int(threadIdx.x); i < room; i += 1024)
+        work.active[i] = ActiveExpert{};
     for (int i = threadIdx.x; i < T * r.topk; i += 1024) {
         const int t = i / r.topk;
-        const int e = int(topk_idx[i]);
+        const int e = ids[i];
         if (e >= 0) {
-            const int at = start[e] + __popcll(mask[e] & ((1ull << t) - 1));
-            work.pair_token[at] = t;
-            work.pair_weight[at] = topk_weights[i];
+            work.pair_weight[start[e] + __popcll(mask[e] & ((1ull << t) - 1))] = weights[i];
         }
     }
 }
@@ -152,121 +211,171 @@ struct MoeArgs {
     int kbytes;            // bytes of a weight row
 };
 
-// act of 16 gate and their 16 up columns for the tokens of one expert.
-constexpr int kGateWaves = 8;
-template <bool FP8, bool TAIL, int MT>
-__device__ __forceinline__ void gate_tile(const MoeArgs &a, const ActiveExpert &x, int n0, int m0, f32x4 *sums)
+// act of 16 G gate and their up columns for up to 16 / C * MT tokens of one expert.
+constexpr int kGateWaves = 8, kGateSums = 2 * 32 * 16;  // floats of a wave's sums
+template <bool FP8, bool TAIL, int G, int C, int MT>
+__device__ __forceinline__ void gate_tile(const MoeArgs &a, const ActiveExpert &x, int n0, int m0, float *sums)
 {
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int n = n0 + (lane & 15) < a.I ? n0 + (lane & 15) : a.I - 1;
+    constexpr int kRows = 16 / C, RG = C * G, RT = 2 * RG;  // of a tile; tiles: RG of the gate, RG of up
+    constexpr int kTokens = kRows * MT, kCols = 16 * G;
+    static_assert(2 * kTokens * kCols <= kGateSums, "the sums' place");
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), i0 = (lane & 15) / C;
     const char *w = a.p + int64_t(x.expert) * 2 * a.I * a.kbytes;
-    const char *prow[2] = {w + int64_t(n) * a.kbytes, w + int64_t(a.I + n) * a.kbytes};
     const int steps = (a.kbytes + kStepBytes - 1) / kStepBytes;
-    const float *scale[2] = {};
-    if constexpr (FP8) {
-        scale[0] = a.p_scale + (int64_t(x.expert) * 2 * (a.I >> 7) + (n0 >> 7)) * steps;
-        scale[1] = scale[0] + int64_t(a.I >> 7) * steps;
+    const char *prow[RT];
+    const float *scale[RT] = {};
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        const int n = n0 + r % RG * kRows + i0;
+        prow[r] = w + (int64_t(r / RG) * a.I + (n < a.I ? n : a.I - 1)) * a.kbytes;
+        if constexpr (FP8)  // (a block's columns lie in one scale block: they divide 128)
+            scale[r] = a.p_scale + ((int64_t(x.expert) * 2 + r / RG) * (a.I >> 7) + (n0 >> 7)) * steps;
     }
     const char *qrow[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-        const int i = m0 + m * 16 + (lane & 15);
-        qrow[m] = a.q + int64_t(a.work.pair_token[x.start + (i < x.count ? i : x.count - 1)]) * a.H * 2;
+        const int i = m0 + m * kRows + i0;
+        qrow[m] = a.q + int64_t(token_of(x.tokens, i < x.count ? i : x.count - 1)) * a.H * 2;
     }
-    f32x4 acc[2][MT] = {};
-    stream<FP8, TAIL, kAhead>(prow, scale, qrow, steps * wave / kGateWaves, steps * (wave + 1) / kGateWaves, a.kbytes, lane, acc);
+    f32x4 acc[RT][MT] = {};
+    stream<FP8, TAIL, ahead(FP8, C, RT, MT), C>(prow, scale, qrow, steps * wave / kGateWaves,
+                                                steps * (wave + 1) / kGateWaves, a.kbytes, lane, acc);
+    // the waves' sums, [wave][gate, up][token][columns]
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-            sums[(wave * 2 * MT + h * MT + m) * kWave + lane] = acc[h][m];
+        for (int m = 0; m < MT; ++m) {
+            float *to = sums + wave * kGateSums + (r / RG * kTokens + m * kRows + i0) * kCols + r % RG * kRows;
+            if constexpr (C == 1)
+                *reinterpret_cast<f32x4 *>(to + (lane >> 4) * 4) = acc[r][m];
+            else
+                to[(lane >> 4) * 2 + (lane & 1)] = fold(acc[r][m], lane);
+        }
     __syncthreads();
-    if (wave < MT) {
-        const int m = wave;
+    const int i = threadIdx.x / (kCols / 4), c = threadIdx.x % (kCols / 4) * 4;
+    if (i < kTokens) {
         f32x4 gate = {}, up = {};
 #pragma unroll
         for (int w8 = 0; w8 < kGateWaves; ++w8) {
-            gate += sums[(w8 * 2 * MT + m) * kWave + lane];
-            up += sums[(w8 * 2 * MT + MT + m) * kWave + lane];
+            gate += *reinterpret_cast<const f32x4 *>(sums + w8 * kGateSums + i * kCols + c);
+            up += *reinterpret_cast<const f32x4 *>(sums + w8 * kGateSums + (kTokens + i) * kCols + c);
         }
-        const int i = m0 + m * 16 + (lane & 15), c = n0 + (lane >> 4) * 4;
         f32x4 v;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             v[k] = gate[k] * sigmoidf(gate[k]) * up[k];
-        if (i < x.count && c < a.I)
-            *reinterpret_cast<uint2 *>(a.work.act + int64_t(x.start + i) * a.I + c) = pack4(v);
+        if (m0 + i < x.count && n0 + c < a.I)
+            *reinterpret_cast<uint2 *>(a.work.act + int64_t(x.start + m0 + i) * a.I + n0 + c) = pack4(v);
     }
     __syncthreads();
 }
 
-template <bool FP8, bool TAIL>
+template <bool FP8, bool TAIL, int G>
 __global__ __launch_bounds__(kGateWaves *kWave) void moe_gate_kernel(MoeArgs a)
 {
-    __shared__ f32x4 sums[kGateWaves * 2 * 2 * kWave];
-    if (int(blockIdx.y) >= *a.work.active_count)
-        return;
+    __shared__ __attribute__((aligned(16))) float sums[kGateWaves * kGateSums];
     const ActiveExpert x = a.work.active[blockIdx.y];
-    const int n0 = blockIdx.x * 16;
-    for (int m0 = 0; m0 < x.count; m0 += 32) {
-        if (x.count - m0 > 16)
-            gate_tile<FP8, TAIL, 2>(a, x, n0, m0, sums);
-        else
-            gate_tile<FP8, TAIL, 1>(a, x, n0, m0, sums);
+    const int n0 = blockIdx.x * 16 * G;
+    if (x.count <= 8) {
+        if (x.count > 0)
+            gate_tile<FP8, TAIL, G, 2, 1>(a, x, n0, 0, sums);
+        return;
     }
+    for (int g = 0; g < G && n0 + g * 16 < a.I; ++g)
+        for (int m0 = 0; m0 < x.count; m0 += 32) {
+            if (x.count - m0 > 16)
+                gate_tile<FP8, TAIL, 1, 1, 2>(a, x, n0 + g * 16, m0, sums);
+            else
+                gate_tile<FP8, TAIL, 1, 2, 2>(a, x, n0 + g * 16, m0, sums);
+        }
 }
 
 // 16 columns of y for every token: the block's waves share out the experts (each in `parts` pieces of
-// K), a wave adds each piece's weighted product to its own sums in LDS.
-template <bool FP8, bool TAIL, int MT>
-__device__ __forceinline__ void down_piece(const MoeArgs &a, const ActiveExpert &x, int n0, int m0, int s0, int s1, f32x4 *own)
+// K), a wave adds each piece's weighted product to its own sums [token][16] in LDS.
+template <bool FP8, bool TAIL, int C, int MT>
+__device__ __forceinline__ void down_piece(const MoeArgs &a, const ActiveExpert &x, int n0, int m0, int s0, int s1, float *own)
 {
-    const int lane = threadIdx.x & 63;
-    const int n = n0 + (lane & 15) < a.H ? n0 + (lane & 15) : a.H - 1;
-    const char *prow[1] = {a.p + (int64_t(x.expert) * a.H + n) * a.kbytes};
+    constexpr int kRows = 16 / C;
+    const int lane = threadIdx.x & 63, i0 = (lane & 15) / C;
     const int steps = (a.kbytes + kStepBytes - 1) / kStepBytes;
-    const float *scale[1] = {};
-    if constexpr (FP8)
-        scale[0] = a.p_scale + (int64_t(x.expert) * (a.H >> 7) + (n0 >> 7)) * steps;
+    const char *prow[C];
+    const float *scale[C] = {};
+#pragma unroll
+    for (int r = 0; r < C; ++r) {
+        const int n = n0 + r * kRows + i0;
+        prow[r] = a.p + (int64_t(x.expert) * a.H + (n < a.H ? n : a.H - 1)) * a.kbytes;
+        if constexpr (FP8)
+            scale[r] = a.p_scale + (int64_t(x.expert) * (a.H >> 7) + (n0 >> 7)) * steps;
+    }
     const char *qrow[MT];
     int token[MT];
     float weight[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-        const int i = m0 + m * 16 + (lane & 15), at = x.start + (i < x.count ? i : x.count - 1);
+        const int i = m0 + m * kRows + i0, at = x.start + (i < x.count ? i : x.count - 1);
         qrow[m] = a.q + int64_t(at) * a.I * 2;
-        token[m] = i < x.count ? a.work.pair_token[at] : -1;
+        token[m] = i < x.count ? token_of(x.tokens, i) : -1;
         weight[m] = a.work.pair_weight[at];
     }
-    f32x4 acc[1][MT] = {};
-    stream<FP8, TAIL, kAhead>(prow, scale, qrow, s0, s1, a.kbytes, lane, acc);
+    f32x4 acc[C][MT] = {};
+    stream<FP8, TAIL, ahead(FP8, C, C, MT), C>(prow, scale, qrow, s0, s1, a.kbytes, lane, acc);
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-        if (token[m] >= 0)
-            own[token[m] * 4 + (lane >> 4)] += acc[0][m] * weight[m];
+    for (int r = 0; r < C; ++r)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            if constexpr (C == 1) {
+                if (token[m] >= 0)
+                    *reinterpret_cast<f32x4 *>(own + token[m] * 16 + (lane >> 4) * 4) += acc[r][m] * weight[m];
+            } else {
+                const float v = fold(acc[r][m], lane) * weight[m];
+                if (token[m] >= 0)
+                    own[token[m] * 16 + r * kRows + (lane >> 4) * 2 + (lane & 1)] += v;
+            }
+        }
 }
 
 template <int W, bool FP8, bool TAIL>
-__global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs a, const uint16_t *residual, uint16_t *y)
+__global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs a, int room, const uint16_t *residual, uint16_t *y)
 {
     extern __shared__ f32x4 own[];  // [W][T][4]
+    __shared__ ActiveExpert list[kMoeExperts];
+    __shared__ int used[W];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int n0 = blockIdx.x * 16;
     const f32x4 zero = {};
     for (int i = lane; i < a.T * 4; i += 64)
         own[wave * a.T * 4 + i] = zero;
-    const int experts = uniform(*a.work.active_count);
+    int n = 0;
+    for (int i = threadIdx.x; i < room; i += W * kWave) {
+        list[i] = a.work.active[i];
+        n += list[i].count > 0;
+    }
+    n = int(wave_scan(uint32_t(n)));
+    if (lane == 63)
+        used[wave] = n;
+    __syncthreads();
+    int experts = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+        experts += used[w];
+    experts = uniform(experts);
     const int steps = (a.kbytes + kStepBytes - 1) / kStepBytes;
     int parts = experts > 0 ? (W + experts - 1) / experts : 1;
     parts = parts < steps ? parts : steps;
     for (int i = wave; i < experts * parts; i += W) {
-        const ActiveExpert x = a.work.active[i / parts];
+        ActiveExpert x = list[i / parts];
+        x.expert = uniform(x.expert);
+        x.start = uniform(x.start);
+        x.count = uniform(x.count);
         const int part = i % parts, s0 = steps * part / parts, s1 = steps * (part + 1) / parts;
         for (int m0 = 0; m0 < x.count; m0 += 32) {
+            float *sums = reinterpret_cast<float *>(own + wave * a.T * 4);
             if (x.count - m0 > 16)
-                down_piece<FP8, TAIL, 2>(a, x, n0, m0, s0, s1, own + wave * a.T * 4);
+                down_piece<FP8, TAIL, 1, 2>(a, x, n0, m0, s0, s1, sums);
+            else if (x.count - m0 > 8)
+                down_piece<FP8, TAIL, 2, 2>(a, x, n0, m0, s0, s1, sums);
             else
-                down_piece<FP8, TAIL, 1>(a, x, n0, m0, s0, s1, own + wave * a.T * 4);
+                down_piece<FP8, TAIL, 2, 1>(a, x, n0, m0, s0, s1, sums);
         }
     }
     __syncthreads();
@@ -287,7 +396,19 @@ __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs a, const uin
     }
 }
 
+constexpr int kGateRound = 256;  // blocks
+
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+
+// Lays the workspace out at base; returns its bytes.
+// Blocks that share a tile's K: some 256 in all.
+int logit_splits(int T, int E)
+{
+    if (T <= 1)
+        return 1;
+    const int n = 256 / ((E + 15) / 16 * ((T + 15) / 16));
+    return n < 1 ? 1 : n < kLogitSplits ? n : kLogitSplits;
+}
 
 // Lays the workspace out at base; returns its bytes.
 size_t moe_layout(int T, int E, int K, int I, char *base, MoeWork *w)
@@ -300,10 +421,9 @@ size_t moe_layout(int T, int E, int K, int I, char *base, MoeWork *w)
         return p;
     };
     MoeWork m;
-    m.logits = reinterpret_cast<float *>(take(size_t(T) * E * 4));
-    m.active_count = reinterpret_cast<int32_t *>(take(4));
+    m.splits = logit_splits(T, E);
+    m.logits = reinterpret_cast<double *>(take(size_t(m.splits) * T * E * 8));
     m.active = reinterpret_cast<ActiveExpert *>(take(n * sizeof(ActiveExpert)));
-    m.pair_token = reinterpret_cast<int32_t *>(take(P * 4));
     m.pair_weight = reinterpret_cast<float *>(take(P * 4));
     m.act = reinterpret_cast<uint16_t *>(take(P * I * 2));
     if (w != nullptr)
@@ -325,14 +445,13 @@ hipError_t launch_moe(const RouteRule &rule, const MoeCall &c, hipStream_t strea
     if (log_enabled())
         log_launch("ll_moe: T=%d H=%d I=%d E=%d K=%d%s", c.T, c.H, c.I, E, rule.topk, fp8 ? " fp8" : "");
     const u32x4 *x = static_cast<const u32x4 *>(c.x);
-    auto logits = [&](auto bf, auto f32, int tokens) {
-        hipLaunchKernelGGL(c.router_f32 ? f32 : bf, dim3(E, (c.T + tokens - 1) / tokens), dim3(256), 0, stream, x, c.w_router,
-                           c.T, E, V, a.work.logits);
-    };
     if (c.T == 1)
-        logits(moe_logits_kernel<1, false>, moe_logits_kernel<1, true>, 1);
+        hipLaunchKernelGGL((c.router_f32 ? moe_logits_kernel<true> : moe_logits_kernel<false>), dim3(E), dim3(256), 0, stream, x,
+                           c.w_router, E, V, a.work.logits);
     else
-        logits(moe_logits_kernel<8, false>, moe_logits_kernel<8, true>, 8);
+        hipLaunchKernelGGL((c.router_f32 ? moe_logits_tile_kernel<true> : moe_logits_tile_kernel<false>),
+                           dim3((E + 15) / 16, (c.T + 15) / 16, a.work.splits), dim3(256), 0, stream, x, c.w_router, c.T, E, V,
+                           a.work.logits);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
@@ -357,15 +476,19 @@ hipError_t launch_moe(const RouteRule &rule, const MoeCall &c, hipStream_t strea
     a.p_scale = c.w13_scale;
     a.q = static_cast<const char *>(c.x);
     a.kbytes = c.H * (fp8 ? 1 : 2);
-    auto gate = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3((c.I + 15) / 16, most), dim3(kGateWaves * kWave), 0, stream, a);
+    // 32 columns a block, whose tokens' loads then serve twice the weights, where 16 would make more than four
+    // blocks a compute unit (64 FP8 experts of 2048 x 7168: 314 against 326 us)
+    const bool wide = int64_t((c.I + 15) / 16) * most > 4 * kGateRound;
+    auto gate = [&](auto narrow, auto wider) {
+        hipLaunchKernelGGL(wide ? wider : narrow, dim3((c.I + (wide ? 31 : 15)) / (wide ? 32 : 16), most),
+                           dim3(kGateWaves * kWave), 0, stream, a);
     };
     if (fp8)
-        gate(moe_gate_kernel<true, false>);
+        gate(moe_gate_kernel<true, false, 1>, moe_gate_kernel<true, false, 2>);
     else if (a.kbytes % kStepBytes == 0)
-        gate(moe_gate_kernel<false, false>);
+        gate(moe_gate_kernel<false, false, 1>, moe_gate_kernel<false, false, 2>);
     else
-        gate(moe_gate_kernel<false, true>);
+        gate(moe_gate_kernel<false, true, 1>, moe_gate_kernel<false, true, 2>);
     e = hipGetLastError();
     if (e != hipSuccess)
         return e;
@@ -374,7 +497,7 @@ hipError_t launch_moe(const RouteRule &rule, const MoeCall &c, hipStream_t strea
     a.q = reinterpret_cast<const char *>(a.work.act);
     a.kbytes = c.I * (fp8 ? 1 : 2);
     auto down = [&](auto kernel, int waves) {
-        hipLaunchKernelGGL(kernel, dim3((c.H + 15) / 16), dim3(waves * kWave), size_t(waves) * c.T * 64, stream, a,
+        hipLaunchKernelGGL(kernel, dim3((c.H + 15) / 16), dim3(waves * kWave), size_t(waves) * c.T * 64, stream, a, most,
                            static_cast<const uint16_t *>(c.residual), static_cast<uint16_t *>(c.y));
     };
     if (fp8)

@@ -2,13 +2,13 @@
 // (route.hip) and the layer for a few tokens (moe.hip).  Device code.
 //
 // Lane l holds experts l, 64 + l, ...; the chosen ones end in lanes 0 to K - 1.
-// What is chosen never depends on a rounding: without a bias the logits themselves
-// are compared, and with one the 32-bit keys decide only where the gaps between them
-// are larger than what they can be off by; a token with a smaller gap (less than one in
-// a hundred) is chosen again with keys of 64 bits.
+// What is chosen never depends on a rounding: the 32-bit keys decide only where the gaps between
+// them are larger than what they can be off by (the bits that hold the index, and with a
+// bias the rounding of the scores); a token with a smaller gap (a few in a hundred) is chosen
+// again with keys of 64 bits.
 #pragma once
 
-#include "ep_internal.h"
+#include "gemm.h"
 
 namespace ep {
 
@@ -18,6 +18,8 @@ constexpr float kShareFloor = 1e-20f;  // beside the sum that sigmoid scores are
 
 struct RouteRule {
     int experts, topk, groups, topk_groups, epr;
+    int size, lanes;   // experts of a group; lanes that look at one: a power of two
+    float per_size;    // 1 / size
     int soft;       // softmax scores, else sigmoid
     int normalize;
     float scale;
@@ -55,6 +57,28 @@ __device__ __forceinline__ float wave_sum(float v)
     v += dpp_or<0x143, 0xC>(0.0f, v);
     return last_lane(v);
 }
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+    auto step = [&](uint32_t o) { v = o > v ? o : v; };
+    step(uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x111, 0xF, 0xF, true)));
+    step(uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x112, 0xF, 0xF, true)));
+    step(uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x114, 0xF, 0xF, true)));
+    step(uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x118, 0xF, 0xF, true)));
+    step(uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x142, 0xA, 0xF, false)));
+    step(uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x143, 0xC, 0xF, false)));
+    return uint32_t(__builtin_amdgcn_readlane(int(v), 63));
+}
+__device__ __forceinline__ float lane_of(float v, int lane)
+{
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+__device__ __forceinline__ double lane_of(double v, int lane)
+{
+    const uint64_t u = uint64_t(__double_as_longlong(v));
+    const uint32_t lo = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(u)), lane));
+    const uint32_t hi = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(u >> 32)), lane));
+    return __longlong_as_double(static_cast<long long>(uint64_t(hi) << 32 | lo));
+}
 __device__ __forceinline__ double wave_max(double v)
 {
 #pragma unroll
@@ -70,11 +94,22 @@ __device__ __forceinline__ double wave_sum(double v)
     return v;
 }
 
+// Floats as integers in the same order.
+__device__ __forceinline__ uint32_t ordered(float v)
+{
+    const uint32_t u = __float_as_uint(v + 0.0f);  // (-0 equals 0)
+    return int32_t(u) < 0 ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t u)
+{
+    return __uint_as_float(int32_t(u) < 0 ? u & 0x7fffffffu : ~u);
+}
+
 // e / size for e < 8192 and any size: half a step away from every border.
 __device__ __forceinline__ int group_of(int e, float per_size) { return int((float(e) + 0.5f) * per_size); }
 
-// Scores of a row, and keys of what may be chosen.  A row with nothing but -inf has no scores.
-template <int V, class T>
+// Scores of a row.  A row with nothing but -inf has no softmax.  FOR_KEYS: of a NaN, which has no key, any number.
+template <bool FOR_KEYS, int V, class T>
 __device__ __forceinline__ void scores_of(bool soft, const float (&l)[V], T (&s)[V])
 {
     if (soft) {
@@ -97,8 +132,12 @@ __device__ __forceinline__ void scores_of(bool soft, const float (&l)[V], T (&s)
             s[j] = sum > T(0) ? s[j] / sum : sum != sum ? sum : T(0);
     } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            s[j] = T(1) / (T(1) + exp(-T(l[j])));
+        for (int j = 0; j < V; ++j) {
+            if constexpr (FOR_KEYS && sizeof(T) == 4)
+                s[j] = sigmoidf(l[j]);
+            else
+                s[j] = T(1) / (T(1) + exp(-T(l[j])));
+        }
     }
 }
 
@@ -112,10 +151,7 @@ __device__ __forceinline__ bool keep_groups(const RouteRule &r, T (&key)[V], int
     for (int j = 0; j < V; ++j)
         scratch[j * 64 + lane] = key[j];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
-    const int size = r.experts / r.groups;
-    int lanes = 64;  // of a group: a power of two
-    while (lanes * r.groups > 64)
-        lanes >>= 1;
+    const int size = r.size, lanes = r.lanes;
     const int group = lane / lanes, part = lane & (lanes - 1);
     T one = none, two = none;
     if (group < r.groups)
@@ -134,57 +170,127 @@ __device__ __forceinline__ bool keep_groups(const RouteRule &r, T (&key)[V], int
     const T score = r.bias == nullptr || two == none ? one : one + two;
     int ahead = 0;
     for (int g = 0; g < r.groups; ++g) {
-        const T other = __shfl(score, g * lanes);
+        const T other = lane_of(score, g * lanes);
         ahead += other > score || (other == score && g < group);
     }
     const bool keep = group < r.groups && ahead < r.topk_groups;
     const uint64_t kept = wave_ballot(keep && part == 0);
-    const float per_size = 1.0f / float(size);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int e = j * 64 + lane;
-        if (e < r.experts && !(kept >> (group_of(e, per_size) * lanes) & 1))
+        if (e < r.experts && !(kept >> (group_of(e, r.per_size) * lanes) & 1))
             key[j] = none;
     }
     if (!(slack > T(0)))
         return false;
-    const T low = -wave_max(keep ? -score : none), high = wave_max(keep || group >= r.groups ? none : score);
-    return high > none && !(low - high > slack * (T(1) + (low < 0 ? -low : low)));
+    // (of the fp32 keys alone; the largest of the negated is the lowest)
+    const float low = -unordered(wave_max(keep ? ordered(-float(score)) : 0u));
+    const float high = unordered(wave_max(keep || group >= r.groups ? 0u : ordered(float(score))));
+    return high > -INFINITY && !(low - high > float(slack) * (1.0f + fabsf(low)));
 }
 
 // The K largest keys, largest first, ties to the lowest index: lane k returns the k-th, -1 where
-// nothing is left.  unsure: some gap on the way was within slack.
-template <int V, class T>
-__device__ __forceinline__ int pick(T (&key)[V], int K, int lane, T slack, bool &unsure)
+// nothing is left.  As integers in the same order, whose halves are compared one after the other.
+template <int V>
+__device__ __forceinline__ int pick(const double (&key)[V], int K, int lane)
 {
+    uint64_t u[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const uint64_t b = uint64_t(__double_as_longlong(key[j] + 0.0));  // (-0 equals 0)
+        u[j] = !(key[j] > -INFINITY) ? 0 : int64_t(b) < 0 ? ~b : b | 1ull << 63;
+    }
     int mine = -1;
-    T last = T(INFINITY);
-    for (int k = 0;; ++k) {
-        if (k == K && !(slack > T(0)))
-            break;
-        T m = key[0];
+    for (int k = 0; k < K; ++k) {
+        uint64_t m = u[0];
+        int tag = lane;
 #pragma unroll
-        for (int j = 1; j < V; ++j)
-            m = key[j] > m ? key[j] : m;
-        m = wave_max(m);
-        if (!(m > T(-INFINITY)))
-            break;
-        unsure |= slack > T(0) && !(last - m > slack * (T(1) + (m < 0 ? -m : m)));
-        if (k == K)
-            break;
-        last = m;
-        int at = 0;
-#pragma unroll
-        for (int j = V - 1; j >= 0; --j) {
-            const uint64_t b = wave_ballot(key[j] == m);
-            at = b != 0 ? j * 64 + __builtin_ctzll(b) : at;
+        for (int j = 1; j < V; ++j) {
+            tag = u[j] > m ? j * 64 + lane : tag;
+            m = u[j] > m ? u[j] : m;
         }
+        const uint32_t high = wave_max(uint32_t(m >> 32));
+        if (high == 0)
+            break;
+        const uint32_t low = wave_max(uint32_t(m >> 32) == high ? uint32_t(m) : 0u);
+        const int at = int(~wave_max(m == (uint64_t(high) << 32 | low) ? ~uint32_t(tag) : 0u));
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            key[j] = at == j * 64 + lane ? T(-INFINITY) : key[j];
+            u[j] = at == j * 64 + lane ? 0 : u[j];
         mine = lane == k ? at : mine;
     }
     return mine;
+}
+
+// The same from 32-bit keys, as integers that end in the index (its complement, so that ties go to the
+// lowest): a round is one maximum over the wave.  Each lane keeps its keys sorted and shows the largest.
+// The rest of the bits holds the key in steps of its range (so 2^-23 or less of it), or where 16 bits are
+// all of it (whole) the key itself.  unsure: a gap on the way, that to the K + 1st included, was
+// within slack, or keys fell on the same step.
+template <int V>
+__device__ __forceinline__ int pick(const float (&key)[V], int K, int lane, float slack, bool whole, bool &unsure)
+{
+    constexpr int kBits = V == 1 ? 6 : V == 2 ? 7 : V == 4 ? 8 : 9;
+    constexpr uint32_t kIndex = (1u << kBits) - 1, kSteps = 1u << (kBits < 8 ? 24 : 32 - kBits);
+    static_assert(64 * V == 1 << kBits, "an index a bit pattern");
+    uint32_t u[V];
+    float scale = 0.0f, most = 0.0f;
+    if (whole) {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            u[j] = ordered(key[j]) & ~kIndex;
+    } else {
+        uint32_t top = 0, down = 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const bool is = key[j] > -INFINITY;
+            const uint32_t a = is ? ordered(key[j]) : 0u, b = is ? ordered(-key[j]) : 0u;
+            top = a > top ? a : top;
+            down = b > down ? b : down;
+        }
+        const float high = unordered(wave_max(top)), low = -unordered(wave_max(down));
+        scale = high > low ? float(kSteps - 2) / (high - low) : 0.0f;
+        unsure |= !(high - low < INFINITY);
+        most = fmaxf(fabsf(high), fabsf(low));
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            u[j] = (uint32_t(fminf((key[j] - low) * scale, float(kSteps - 2))) + 1u) << kBits;
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        u[j] = key[j] > -INFINITY ? u[j] | (kIndex - uint32_t(j * 64 + lane)) : 0u;
+#pragma unroll
+    for (int i = 1; i < V; ++i)
+#pragma unroll
+        for (int j = i; j > 0; --j) {
+            const uint32_t a = u[j - 1], b = u[j];
+            u[j - 1] = a > b ? a : b;
+            u[j] = a > b ? b : a;
+        }
+    const bool exact = whole && !(slack > 0.0f);
+    const int rounds = exact ? K : K + 1;
+    uint32_t got = 0, next = 0;  // of lane k: the k-th, and the K + 1st
+    for (int k = 0; k < rounds; ++k) {
+        const uint32_t m = wave_max(u[0]);
+        if (m == 0)
+            break;
+        got = lane == k ? m : got;
+        next = m;
+        const bool taken = u[0] == m;
+#pragma unroll
+        for (int j = 0; j + 1 < V; ++j)
+            u[j] = taken ? u[j + 1] : u[j];
+        u[V - 1] = taken ? 0u : u[V - 1];
+    }
+    if (!exact) {
+        // (with 64 slots the K + 1st has no lane; where fewer are left it is the last one of them)
+        const uint32_t behind = uint32_t(__shfl_down(int(got), 1));  // (every lane takes part)
+        const uint32_t after = lane < 63 ? behind : K == 64 ? next : 0u;
+        const float gap = float((got >> kBits) - (after >> kBits));
+        const float least = slack > 0.0f ? slack * (1.0f + most) * scale + 2.0f : 0.0f;
+        unsure |= wave_ballot(lane < K && after != 0 && after != got && !(gap > least)) != 0;
+    }
+    return lane < K && got != 0 ? int(kIndex - (got & kIndex)) : -1;
 }
 
 // The keys of expert scores s (of the logits l without a bias), -inf for what may not be chosen: bit j of
@@ -206,13 +312,13 @@ template <int V>
 __device__ __forceinline__ int choose_exactly(const RouteRule &r, const float (&l)[V], const float (&bias)[V],
                                                         uint32_t live, int lane, double *scratch)
 {
-    double s[V], key[V];
-    scores_of(r.soft, l, s);
+    double s[V] = {}, key[V];
+    if (r.bias != nullptr)
+        scores_of<true>(r.soft, l, s);
     keys_of(r, l, s, bias, live, key);
     if (r.groups > 1)
         keep_groups(r, key, lane, scratch, 0.0);
-    bool unsure;
-    return pick(key, r.topk, lane, 0.0, unsure);
+    return pick(key, r.topk, lane);
 }
 
 // Which of this lane's experts may be chosen at all.
@@ -230,14 +336,17 @@ __device__ __forceinline__ uint32_t live_experts(const RouteRule &r, int lane)
 }
 
 // One token: the expert of slot k in lane k (-1 where there are too few, and past K) and its weight.
-// l: the logits, -inf past E; s: the scores, made where want_scores or the rule needs them.
+// l: the logits, -inf past E (whole: bf16 values without a bias); s: the scores, made where want_scores or the rule needs them.
 // at(e): the logit of expert e.
 template <int V, class At>
 __device__ __forceinline__ int route_row(const RouteRule &r, const float (&l)[V], const float (&bias)[V], uint32_t live,
-                                         int lane, double *scratch, bool want_scores, float (&s)[V], At at, float &weight)
+                                         int lane, double *scratch, bool want_scores, bool whole, float (&s)[V],
+                                         At at, float &weight)
 {
-    if (want_scores || r.bias != nullptr || (r.soft && !r.normalize))
-        scores_of(r.soft, l, s);
+    if (want_scores || (r.soft && !r.normalize))
+        scores_of<false>(r.soft, l, s);
+    else if (r.bias != nullptr)
+        scores_of<true>(r.soft, l, s);
     // a score is off by at most some 15 roundings of its sum (of its quotient), a key by one more
     const float slack = r.bias != nullptr ? 4e-6f : 0.0f;
     float key[V];
@@ -245,7 +354,7 @@ __device__ __forceinline__ int route_row(const RouteRule &r, const float (&l)[V]
     bool unsure = false;
     if (r.groups > 1)
         unsure = keep_groups(r, key, lane, reinterpret_cast<float *>(scratch), 2 * slack);
-    int e = pick(key, r.topk, lane, slack, unsure);
+    int e = pick(key, r.topk, lane, slack, whole && r.bias == nullptr, unsure);
     if (unsure)
         e = choose_exactly(r, l, bias, live, lane, scratch);
     const bool have = e >= 0;

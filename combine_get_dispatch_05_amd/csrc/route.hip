@@ -46,7 +46,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a)
 #pragma unroll
         for (int j = 0; j < V; ++j)
             l[j] = j * 64 + lane < r.experts ? logit_at<BF16>(a.logits, t * r.experts + j * 64 + lane) : -INFINITY;
-        const int e = route_row(r, l, bias, live, lane, scratch[wave], a.parts != nullptr, s,
+        const int e = route_row(r, l, bias, live, lane, scratch[wave], a.parts != nullptr, BF16, s,
                                 [&](int i) { return logit_at<BF16>(a.logits, t * r.experts + i); }, w);
         if (lane < r.topk) {
             a.topk_idx[t * r.topk + lane] = e;
@@ -138,7 +138,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_wide_kernel(RouteArgs a)
         }
         __syncthreads();
         if (r.groups > 1) {
-            const int size = r.experts / r.groups;
+            const int size = r.size;
             if (tid < r.groups) {
                 double one = none, two = none;
                 for (int i = 0; i < size; ++i) {
@@ -322,14 +322,23 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteBack
             inner += wave_sum(c * s);
         }
     }
+    // what the slots that chose an expert add
+    float adds[R] = {};
+    auto slots = [&](auto f) {
+        for (int k = 0; k < r.topk; ++k)
+            f(__builtin_amdgcn_readlane(e, k), lane_of(mine, k));
+    };
+    if constexpr (VREG > 0)
+        slots([&](int o, float m) {
+#pragma unroll
+            for (int j = 0; j < R; ++j)
+                adds[j] += o == j * 64 + lane ? m : 0.0f;
+        });
     each([&](int j, float l) {
         const int at = j * 64 + lane;
-        float add = 0.0f;  // of the slots that chose this expert
-        for (int k = 0; k < r.topk; ++k) {
-            const int o = __builtin_amdgcn_readlane(e, k);
-            const float m = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), k));
-            add += o == at ? m : 0.0f;
-        }
+        float add = VREG > 0 ? adds[VREG > 0 ? j : 0] : 0.0f;
+        if constexpr (VREG == 0)
+            slots([&](int o, float m) { add += o == at ? m : 0.0f; });
         if (at >= r.experts)
             return;
         float d;

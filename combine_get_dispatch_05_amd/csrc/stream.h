@@ -1,48 +1,66 @@
-// stream.h -- products of 16-row tiles of a weight with 16-row tiles of bf16 token rows, both
-// straight from memory into the matrix instruction's registers.  Device code; included by
-// moe.hip and adapter.hip.
+// stream.h -- products of a weight's rows with bf16 token rows, both straight from memory into the
+// matrix instruction's registers.  Device code; included by moe.hip and adapter.hip.
+//
+// The instruction takes 16 operand rows of four 16-byte chunks, lane l the chunk l / 16 of row l % 16, so with
+// one weight row an operand row the lanes of a load are 16 rows apart and the load takes as many
+// cycles as lanes.  With C = 2 an operand row is half of a weight row's 128 bytes: lane l holds chunk
+// 2 (l / 16) + l % 2 of row l % 16 / 2, on both sides, pairs of lanes read 32 neighbouring bytes, and the result
+// has what belongs together where the halves are the same (fold()).  It takes 8 rows by 8 tokens then.
 #pragma once
 
 #include "gemm.h"
 
 namespace ep {
 
-// One K step (128 bytes a weight row) of 16 weight rows: lane l holds row l % 16, chunks l / 16 and
-// 4 + l / 16 of eight.
-struct WeightStep {
-    i32x4 c[2];
-};
-// The same K values of 16 token rows: bf16 beside bf16 weights the same two chunks, beside FP8 ones the four that
-// hold the 32 values of the weight's two.
-template <bool FP8>
-struct TokenStep {
-    i32x4 c[FP8 ? 4 : 2];
-};
-
 __device__ __forceinline__ i32x4 load16(const char *p) { return *reinterpret_cast<const i32x4 *>(p); }
 
+// One K step, 128 bytes a weight row, of a tile of 16 / C weight rows.
+template <int C>
+struct WeightStep {
+    i32x4 c[2 / C];
+};
+// The same K values of 16 / C token rows: bf16 beside bf16 weights the same chunks, beside FP8 ones two for each.
+template <bool FP8, int C>
+struct TokenStep {
+    i32x4 c[(FP8 ? 4 : 2) / C];
+};
+
+// Byte of this lane's h-th chunk inside a step.
+template <int C>
+__device__ __forceinline__ int chunk_at(int h, int lane)
+{
+    return (h * 4 + (lane >> 4) * C + lane % C) * 16;
+}
+
 // TAIL: chunks at or past `end` (bytes of a weight row) are zeros.
-template <bool TAIL>
-__device__ __forceinline__ void load_step(WeightStep &f, const char *row, int at, int g, int end)
+template <bool TAIL, int C>
+__device__ __forceinline__ void load_step(WeightStep<C> &f, const char *row, int at, int lane, int end)
 {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int b = at + h * 64 + g * 16;
+    for (int h = 0; h < 2 / C; ++h) {
+        const int b = at + chunk_at<C>(h, lane);
         f.c[h] = load16(TAIL && b >= end ? reinterpret_cast<const char *>(kZero16) : row + b);
     }
 }
-template <bool TAIL, bool FP8>
-__device__ __forceinline__ void load_step(TokenStep<FP8> &f, const char *row, int at, int g, int end)
+template <bool TAIL, bool FP8, int C>
+__device__ __forceinline__ void load_step(TokenStep<FP8, C> &f, const char *row, int at, int lane, int end)
 {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int b = at + h * 64 + g * 16;
+    for (int h = 0; h < 2 / C; ++h) {
+        const int b = at + chunk_at<C>(h, lane);
         if constexpr (FP8) {
             f.c[2 * h] = load16(row + 2 * b);
             f.c[2 * h + 1] = load16(row + 2 * b + 16);
         } else
             f.c[h] = load16(TAIL && b >= end ? reinterpret_cast<const char *>(kZero16) : row + b);
     }
+}
+
+// C = 2: of an 8 x 8 tile, the sum of the halves: row 2 (l / 16) + l % 2, token l % 16 / 2.
+__device__ __forceinline__ float fold(const f32x4 &v, int lane)
+{
+    const bool odd = lane & 1;
+    return (odd ? v[3] : v[0]) + __shfl_xor(odd ? v[1] : v[2], 1);
 }
 
 // Eight FP8 values as bf16.
@@ -61,29 +79,28 @@ __device__ __forceinline__ bf16x8 widen8(int lo, int hi)
 }
 
 // acc[r][m] += weight rows of tile r times token tile m over steps [s0, s1).
-template <bool FP8, bool TAIL, int AHEAD, int RT, int MT>
+template <bool FP8, bool TAIL, int AHEAD, int C, int RT, int MT>
 __device__ __forceinline__ void stream(const char *const (&prow)[RT], const float *const (&scale)[RT],
                                        const char *const (&qrow)[MT], int s0, int s1, int kbytes, int lane,
                                        f32x4 (&acc)[RT][MT])
 {
-    const int g = lane >> 4;
     if (s0 >= s1)
         return;
-    WeightStep p[AHEAD][RT];
-    TokenStep<FP8> q[AHEAD][MT];
-    float c[AHEAD][RT];
+    WeightStep<C> p[AHEAD][RT];
+    TokenStep<FP8, C> q[AHEAD][MT];
+    float scales[AHEAD][RT];
     auto load = [&](int d, int s) {
         s = s < s1 ? s : s1 - 1;  // (past the end: loaded again, not used)
         const int at = s * kStepBytes;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-            load_step<TAIL>(p[d][r], prow[r], at, g, kbytes);
+            load_step<TAIL>(p[d][r], prow[r], at, lane, kbytes);
             if constexpr (FP8)
-                c[d][r] = scale[r][s];
+                scales[d][r] = scale[r][s];
         }
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-            load_step<TAIL, FP8>(q[d][m], qrow[m], at, g, kbytes);
+            load_step<TAIL>(q[d][m], qrow[m], at, lane, kbytes);
     };
     auto compute = [&](int d, int s) {
         if (s >= s1)
@@ -93,7 +110,7 @@ __device__ __forceinline__ void stream(const char *const (&prow)[RT], const floa
             if constexpr (FP8) {
                 f32x4 part[MT] = {};
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < 2 / C; ++h)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const bf16x8 w = widen8(p[d][r].c[h][2 * i], p[d][r].c[h][2 * i + 1]);
@@ -103,10 +120,10 @@ __device__ __forceinline__ void stream(const char *const (&prow)[RT], const floa
                     }
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
-                    acc[r][m] += part[m] * c[d][r];
+                    acc[r][m] += part[m] * scales[d][r];
             } else {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < 2 / C; ++h)
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
                         acc[r][m] = mfma_bf16(__builtin_bit_cast(bf16x8, p[d][r].c[h]),

@@ -182,7 +182,7 @@ def test_refusals_and_no_tokens():
             bad()
     with pytest.raises(TypeError):
         buf.low_latency_moe(x, wr, r, fp8_weight(gen(0), (8, 128, 256)), w2)
-    with pytest.raises(abi.EpError, match="TOO|large|scratch"):
+    with pytest.raises(abi.EpError, match="needs more"):
         buf.low_latency_moe(torch.zeros((65, 256), dtype=torch.bfloat16, device="cuda"), wr, r, w13, w2)
     with pytest.raises(abi.EpError):
         buf.low_latency_moe(x, wr, epm.Router(0), w13, w2)
