@@ -1,10 +1,10 @@
 // adapter.hip -- low-rank adapters of many requests beside a shared projection, and their gradients:
 //   h[t] = c_a (x[t] A_a^T),  out[t] = base[t] + h[t] B_a^T,   a = ids[t], A [r][K], B [N][r]
 //   dh[t] = c_a (dy[t] B_a),  dx[t] = dx_base[t] + dh[t] A_a,  dA_a = sum_t dh[t]^T x[t],  dB_a = sum_t dy[t]^T h[t]
-// Tokens are grouped by adapter first (a tile of up to 16 MT rows has one adapter).  The inner products to
-// the rank (shrink) split K over waves and blocks; the products back (expand) sum those parts, round h to
-// bf16, the matrix instruction's operand, and add the base.  All of it is bound by memory:
-// rows are read and written once in whole 128-byte lines.
+// A block takes a tile of tokens that share an adapter: of few tokens it looks for them itself, more are sorted by
+// adapter first.  The inner products to the rank (shrink) split K over waves and blocks; the products back
+// (expand) sum those parts, round h to bf16, the matrix instruction's operand, and add the
+// base.  All of it is bound by memory: each row is read and written once.
 #include "stream.h"
 
 namespace ep {
@@ -23,7 +23,7 @@ struct AdapterArgs {
     const char *q;     // shrink: token rows
     const char *p;     // shrink, expand: adapters
     int64_t width;     // of the rows that are shrunk or made
-    float *parts;      // [splits][T][RP], in `order`
+    float *parts;      // [splits][T][RP]
     int splits;
     const uint16_t *base;  // nullable
     uint16_t *out;
@@ -36,17 +36,23 @@ struct AdapterArgs {
 constexpr int kSortThreads = 1024;
 __global__ __launch_bounds__(kSortThreads) void adapter_group_kernel(AdapterArgs a)
 {
-    __shared__ int less_of[kSortThreads / kWave], here_of[kSortThreads / kWave];
+    __shared__ int less_of[kSortThreads / kWave], here_of[8 * (kSortThreads / kWave)];
     const int mine = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     auto group = [&](int t) {
-        if (t >= a.T)
-            return a.L + 1;
-        const int64_t id = a.ids[t];
-        return id >= 0 && id < a.L ? int(id) : a.L;
+        const int64_t id = a.ids[t < a.T ? t : a.T - 1];  // (a load that nothing waits for before the others)
+        return t >= a.T ? a.L + 1 : id >= 0 && id < a.L ? int(id) : a.L;
     };
+    constexpr int N = 8;  // tokens a thread at a time, their ids in flight together
     int less = 0;
-    for (int t = threadIdx.x; t < a.T; t += kSortThreads)
-        less += group(t) < mine;
+    for (int t0 = 0; t0 < a.T; t0 += N * kSortThreads) {
+        int g[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            g[i] = group(t0 + i * kSortThreads + int(threadIdx.x));
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            less += g[i] < mine;
+    }
     less = int(wave_scan(uint32_t(less)));
     if (lane == 63)
         less_of[wave] = less;
@@ -59,21 +65,33 @@ __global__ __launch_bounds__(kSortThreads) void adapter_group_kernel(AdapterArgs
         if (mine == a.L)
             a.offsets[a.L + 1] = a.T;
     }
-    for (int t0 = 0; t0 < a.T; t0 += kSortThreads) {
-        const int t = t0 + int(threadIdx.x);
-        const bool is = group(t) == mine;
-        const uint64_t m = wave_ballot(is);
-        __syncthreads();
-        if (lane == 0)
-            here_of[wave] = __popcll(m);
-        __syncthreads();
-        int before = at;
-        for (int w = 0; w < kSortThreads / kWave; ++w) {
-            before += w < wave ? here_of[w] : 0;
-            at += here_of[w];
+    for (int t0 = 0; t0 < a.T; t0 += N * kSortThreads) {
+        int g[N];
+        uint64_t m[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            g[i] = group(t0 + i * kSortThreads + int(threadIdx.x));
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            m[i] = wave_ballot(g[i] == mine);
+            if (lane == 0)
+                here_of[i * (kSortThreads / kWave) + wave] = __popcll(m[i]);
         }
-        if (is)
-            a.order[before + __popcll(m & lanemask_lt())] = t;
+        __syncthreads();
+        // 128 counts in token order; lane l holds those of 2 l and 2 l + 1 and what is before them
+        const int c0 = here_of[2 * lane], c1 = here_of[2 * lane + 1];
+        const int upto = int(wave_scan(uint32_t(c0 + c1)));
+        const int all = __builtin_amdgcn_readlane(upto, 63);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int k = i * (kSortThreads / kWave) + uniform(wave);
+            int before = at + __builtin_amdgcn_readlane(upto - c0 - c1, k >> 1);
+            before += k & 1 ? __builtin_amdgcn_readlane(c0, k >> 1) : 0;
+            if (g[i] == mine)
+                a.order[before + __popcll(m[i] & lanemask_lt())] = t0 + i * kSortThreads + int(threadIdx.x);
+        }
+        at += all;
+        __syncthreads();
     }
 }
 
@@ -102,6 +120,52 @@ __device__ __forceinline__ AdapterTile adapter_tile(const AdapterArgs &a, int b,
     return {-1, 0, 0};
 }
 
+// Few tokens are not sorted: block a of a launch takes adapter a (the last one those with none) and finds its
+// tokens, which it then goes through in tiles.
+constexpr int kScanTokens = kAdapterThreads, kScanAdapters = 128;
+__device__ __forceinline__ int scan_tokens(const AdapterArgs &a, int mine, int *list, int *count_of)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = threadIdx.x;
+    int64_t id = t < a.T ? a.ids[t] : -2;
+    id = t < a.T && !(id >= 0 && id < a.L) ? a.L : id;
+    const uint64_t m = wave_ballot(id == mine);
+    if (lane == 0)
+        count_of[wave] = __popcll(m);
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kAdapterWaves; ++w) {
+        before += w < wave ? count_of[w] : 0;
+        all += count_of[w];
+    }
+    if (id == mine)
+        list[before + __popcll(m & lanemask_lt())] = t;
+    __syncthreads();
+    return uniform(all);
+}
+
+// f(adapter, tokens in LDS, how many) for each tile of this block.
+template <bool SCAN, int HEIGHT, class F>
+__device__ __forceinline__ void each_tile(const AdapterArgs &a, F f)
+{
+    __shared__ int list[SCAN ? kScanTokens : HEIGHT], count_of[kAdapterWaves];
+    if constexpr (SCAN) {
+        const int all = scan_tokens(a, blockIdx.x, list, count_of);
+        for (int m0 = 0; m0 < all; m0 += HEIGHT) {
+            f(int(blockIdx.x), list + m0, all - m0 < HEIGHT ? all - m0 : HEIGHT);
+            __syncthreads();
+        }
+    } else {
+        const AdapterTile t = adapter_tile(a, blockIdx.x, HEIGHT, threadIdx.x & 63);
+        if (t.group < 0)
+            return;
+        for (int i = threadIdx.x; i < t.rows; i += kAdapterThreads)
+            list[i] = a.order[t.start + i];
+        __syncthreads();
+        f(t.group, static_cast<const int *>(list), t.rows);
+    }
+}
+
 // ------------------------------------------------------------------ shrink
 
 // 16 rows of a transposed operand out of LDS: rows k of `stride` bytes, lane l gets the column
@@ -117,72 +181,96 @@ __device__ __forceinline__ bf16x8 transposed(const lds_char *base, int stride, i
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// acc[j][m] += sum over k steps of 64: transposed weight rows [k][r] times token rows.
+// acc[j][m] += sum over steps of 64 of K: weight rows times token rows, a wave's own step of both staged in LDS (whole
+// lines a row) and the next one sent off as soon as it is in registers.  COL: the weight is [k][r].
 template <int RT, int MT>
-__device__ __forceinline__ void stream_transposed(const char *w, int r, const char *const (&qrow)[MT], int s0, int s1, int width,
-                                                  lds_char *own, int lane, f32x4 (&acc)[RT][MT])
+constexpr int kStageBytes = (RT + MT) * 16 * kStepBytes;
+template <int RT, int MT, bool COL, bool TAIL, class Token>
+__device__ __forceinline__ void stream_staged(const char *w, const AdapterArgs &a, Token token, int s0, int s1, int stride,
+                                              lds_char *own, int lane, f32x4 (&acc)[RT][MT])
 {
-    constexpr int CH = RT * 2, J = CH;  // 16-byte chunks of a staged row; loads a lane for 64 rows
-    const int g = lane >> 4;
-    for (int s = s0; s < s1; ++s) {
-        i32x4 q[MT][2];
+    using QS = RowStage<16 * MT, kWave>;
+    using PS = NearRowStage<16 * RT, kWave>;
+    constexpr int CH = RT * 2;
+    if (s0 >= s1)
+        return;
+    const int width = int(a.width);
+    lds_char *weights = own + QS::kBytes;
+    QS qs;
+    qs.init(lane, [&](int, int r) { return a.q + int64_t(token(r)) * width * 2; });
+    PS ps;
+    if constexpr (!COL)
+        ps.init(lane, w, [&](int, int r) { return uint32_t(r < a.r ? r : a.r - 1) * uint32_t(width) * 2; });
+    auto send = [&](int s) {
+        qs.template issue<TAIL>(own, lane, 0, int64_t(s) * kStepBytes, int64_t(width) * 2);
+        if constexpr (!COL)
+            ps.template issue<TAIL>(weights, lane, 0, int64_t(s) * kStepBytes, int64_t(width) * 2);
+        else {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+            for (int j = 0; j < CH; ++j) {
+                const int at = j * kWave + lane, k = s * 64 + at / CH, c = at % CH;
+                load_lds16(k < width && c * 8 < a.r ? w + (int64_t(k) * a.r + c * 8) * 2
+                                                    : reinterpret_cast<const char *>(kZero16),
+                           weights + j * kWave * 16);
+            }
+        }
+    };
+    send(s0);
+    for (int s = s0; s < s1; s += stride) {
+        landed<0>();
+        bf16x8 p[RT][2], q[MT][2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = s * 64 + h * 32 + g * 8;
-                q[m][h] = load16(k < width ? qrow[m] + k * 2 : reinterpret_cast<const char *>(kZero16));
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < RT; ++j) {
+                if constexpr (COL)
+                    p[j][h] = transposed(weights, RT * 32, h * 32, [&](int c) { return j * 16 + c * 4; }, lane);
+                else
+                    p[j][h] = PS::frag(weights, j * 16, h, lane);
             }
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int at = j * kWave + lane, k = s * 64 + at / CH, c = at % CH;
-            load_lds16(k < width && c * 8 < r ? w + (int64_t(k) * r + c * 8) * 2 : reinterpret_cast<const char *>(kZero16),
-                       own + j * kWave * 16);
+            for (int m = 0; m < MT; ++m)
+                q[m][h] = QS::frag(own, m * 16, h, lane);
         }
-        landed<0>();
+        // read before the same LDS is loaded again
+        asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+        if (s + stride < s1)
+            send(s + stride);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int j = 0; j < RT; ++j) {
-                const bf16x8 p = transposed(own, RT * 32, h * 32, [&](int c) { return j * 16 + c * 4; }, lane);
+            for (int j = 0; j < RT; ++j)
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
-                    acc[j][m] = mfma_bf16(p, __builtin_bit_cast(bf16x8, q[m][h]), acc[j][m]);
-            }
-        // read before the same LDS is loaded again
-        asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+                    acc[j][m] = mfma_bf16(p[j][h], q[m][h], acc[j][m]);
     }
 }
 
 template <int RT, int MT, bool COL, bool TAIL>
-__device__ __forceinline__ void shrink_tile(const AdapterArgs &a, const AdapterTile &t, f32x4 *sums)
+__device__ __forceinline__ void shrink_tile(const AdapterArgs &a, int adapter, const int *tokens, int rows, f32x4 *sums)
 {
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int width = int(a.width);
-    const char *qrow[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int i = m * 16 + (lane & 15);
-        qrow[m] = a.q + int64_t(a.order[t.start + (i < t.rows ? i : t.rows - 1)]) * width * 2;
-    }
-    const char *w = a.p + int64_t(t.group) * a.r * width * 2;
-    const int steps = (width + 63) / 64, split = int(blockIdx.y) * kAdapterWaves + wave;
-    const int of = a.splits * kAdapterWaves;
-    const int s0 = int(int64_t(steps) * split / of), s1 = int(int64_t(steps) * (split + 1) / of);
+    auto token = [&](int i) { return tokens[i < rows ? i : rows - 1]; };
+    const char *w = a.p + int64_t(adapter) * a.r * width * 2;
+    const int steps = (width + 63) / 64;
+    const int s0 = steps * int(blockIdx.y) / a.splits, s1 = steps * int(blockIdx.y + 1) / a.splits, own_steps = s1 - s0;
     f32x4 acc[RT][MT] = {};
-    if constexpr (COL) {
-        lds_char *own = (lds_char *)sums + wave * RT * 32 * 64;
-        stream_transposed<RT, MT>(w, a.r, qrow, s0, s1, width, own, lane, acc);
-        __syncthreads();
-    } else {
-        const char *prow[RT];
+    // one row tile of a Row weight has little to share: straight into registers, several steps in flight
+    if constexpr (!COL && MT == 1) {
+        const char *prow[RT], *qrow[1] = {a.q + int64_t(token(lane & 15)) * width * 2};
         const float *none[RT] = {};
 #pragma unroll
         for (int j = 0; j < RT; ++j) {
             const int row = j * 16 + (lane & 15);
             prow[j] = w + int64_t(row < a.r ? row : a.r - 1) * width * 2;
         }
-        stream<false, TAIL, (RT * MT > 4 ? 2 : 4), 1>(prow, none, qrow, s0, s1, width * 2, lane, acc);
+        stream<false, TAIL, (RT > 4 ? 2 : 4), 1>(prow, none, qrow, s0 + own_steps * wave / kAdapterWaves,
+                                                        s0 + own_steps * (wave + 1) / kAdapterWaves, width * 2, lane, acc);
+    } else {
+        // (the waves take turns along a row, so that its lines are read together)
+        stream_staged<RT, MT, COL, TAIL>(w, a, token, s0 + wave, s1, kAdapterWaves, (lds_char *)sums + wave * kStageBytes<RT, MT>, lane, acc);
+        __syncthreads();
     }
 #pragma unroll
     for (int j = 0; j < RT; ++j)
@@ -196,8 +284,8 @@ __device__ __forceinline__ void shrink_tile(const AdapterArgs &a, const AdapterT
         for (int w4 = 1; w4 < kAdapterWaves; ++w4)
             v += sums[(w4 * RT * MT + i) * kWave + lane];
         const int j = i / MT, m = (i % MT) * 16 + (lane & 15);
-        if (m < t.rows)
-            *reinterpret_cast<f32x4 *>(a.parts + (int64_t(blockIdx.y) * a.T + t.start + m) * (RT * 16) + j * 16 +
+        if (m < rows)
+            *reinterpret_cast<f32x4 *>(a.parts + (int64_t(blockIdx.y) * a.T + tokens[m]) * (RT * 16) + j * 16 +
                                        (lane >> 4) * 4) = v;
     }
 }
@@ -205,138 +293,197 @@ __device__ __forceinline__ void shrink_tile(const AdapterArgs &a, const AdapterT
 template <int RT>
 constexpr int kTokenTiles = RT <= 4 ? 4 : 2;  // 16-row tiles of tokens a block
 
-template <int RT, bool COL, bool TAIL>
+template <int RT, bool COL, bool TAIL, bool SCAN>
 __global__ __launch_bounds__(kAdapterThreads) void adapter_shrink_kernel(AdapterArgs a)
 {
     constexpr int MT = kTokenTiles<RT>;
-    __shared__ f32x4 sums[kAdapterWaves * RT * MT * kWave];
-    const AdapterTile t = adapter_tile(a, blockIdx.x, MT * 16, threadIdx.x & 63);
-    if (t.group < 0 || t.group == a.L)
-        return;
-    if (t.rows <= 16)
-        shrink_tile<RT, 1, COL, TAIL>(a, t, sums);
-    else
-        shrink_tile<RT, MT, COL, TAIL>(a, t, sums);
+    constexpr int kSums = kAdapterWaves * RT * MT * kWave * 16, kStages = kAdapterWaves * kStageBytes<RT, MT>;
+    __shared__ __attribute__((aligned(128))) char lds[kSums > kStages ? kSums : kStages];
+    f32x4 *sums = reinterpret_cast<f32x4 *>(lds);
+    each_tile<SCAN, MT * 16>(a, [&](int adapter, const int *tokens, int rows) {
+        if (adapter == a.L)
+            return;
+        if (rows <= 16)
+            shrink_tile<RT, 1, COL, TAIL>(a, adapter, tokens, rows, sums);
+        else
+            shrink_tile<RT, MT, COL, TAIL>(a, adapter, tokens, rows, sums);
+    });
 }
 
 // ------------------------------------------------------------------ expand
 
-// out rows of one tile, columns [n0, n1) in steps of 64 a wave.  The weight row of a tile's i-th operand row is
-// permuted, so that a lane ends with 16 neighbouring columns of its token and four lanes with a whole line.
-template <int RT, int MT, bool COL>
-__device__ __forceinline__ void expand_tile(const AdapterArgs &a, const AdapterTile &t, const uint16_t *hs, lds_char *own, int n0,
-                                            int n1)
+// out rows of one tile, columns [n0, n1) in steps of 64 a wave.  A wave stages its own weights in LDS; its results turn
+// there, 16 tokens at a time, so that eight lanes read and write a whole line of a row.
+constexpr int kTurnRow = 68;  // floats: 16 rows of 64, four apart in the banks
+template <int RT, bool COL>
+struct ExpandLds {
+    static constexpr int KS = (RT + 1) / 2;  // matrix steps of 32
+    static constexpr int kHidden = kTokenTiles<RT> * 16 * KS * 32;  // bf16 values
+    char weights[kAdapterWaves][COL ? KS * 32 * 128 : (RT + 3) / 4 * 64 * kStepBytes];
+    union {  // h is in registers before the first results turn
+        uint16_t hidden[kHidden];
+        float turn[kAdapterWaves][16 * kTurnRow];
+    };
+};
+
+template <int RT, int MT, bool COL, class MakeH>
+__device__ __forceinline__ void expand_tile(const AdapterArgs &a, int adapter, const int *tokens, int rows, ExpandLds<RT, COL> &lds,
+                                            int n0, int n1, MakeH make_h)
 {
-    constexpr int KS = (RT + 1) / 2;  // matrix steps of 32
+    constexpr int KS = (RT + 1) / 2;
+    using PS = NearRowStage<64, kWave>;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), g = lane >> 4;
     const int width = int(a.width);
-    const bool adapted = t.group < a.L;
+    const bool adapted = adapter < a.L;
+    lds_char *own = (lds_char *)lds.weights[wave];
+    float *turn = lds.turn[wave];
     bf16x8 h[MT][KS];
-    int64_t row[MT];
-    bool live[MT];
+    int64_t row[MT][2];  // of the line that this lane reads and writes a chunk of; -1: none
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int i = m * 16 + (lane & 15);
-        live[m] = i < t.rows;
-        row[m] = int64_t(a.order[t.start + (live[m] ? i : t.rows - 1)]) * width;
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
-            h[m][s] = *reinterpret_cast<const bf16x8 *>(hs + i * (KS * 32) + s * 32 + g * 8);
-    }
-    const char *w = a.p + int64_t(t.group) * a.r * width * 2;
-    for (int n = n0 + wave * 64; n < n1; n += kAdapterWaves * 64) {
-        const int c = n + g * 16;  // this lane's columns
-        u32x4 b[MT][2] = {};
-        if (a.base != nullptr) {
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (live[m] && c + i * 8 < width)
-                        b[m][i] = *reinterpret_cast<const u32x4 *>(a.base + row[m] + c + i * 8);
+        for (int i = 0; i < 2; ++i) {
+            const int at = m * 16 + i * 8 + (lane >> 3);
+            row[m][i] = at < rows ? int64_t(tokens[at]) * width + (lane & 7) * 8 : -1;
         }
-        f32x4 acc[4][MT] = {};
+    const char *w = a.p + int64_t(adapter) * a.r * width * 2;
+    u32x4 b[MT][2] = {};
+    auto send = [&](int n) {
         if (adapted) {
-            if constexpr (COL) {  // A [r][width]: r rows of 64 columns in LDS
-                constexpr int J = KS * 32 * 8 / kWave;
+            if constexpr (COL) {  // A [r][width]: r rows of 64 columns
 #pragma unroll
-                for (int j = 0; j < J; ++j) {
+                for (int j = 0; j < KS * 4; ++j) {
                     const int at = j * kWave + lane, k = at >> 3, col = n + (at & 7) * 8;
                     load_lds16(k < a.r && col < width ? w + (int64_t(k) * width + col) * 2
                                                       : reinterpret_cast<const char *>(kZero16),
                                own + j * kWave * 16);
                 }
-                landed<0>();
+            } else {  // B [width][r]: 64 rows
+                PS ps;
+                ps.init(lane, w + int64_t(n) * a.r * 2,
+                        [&](int, int r) { return uint32_t(n + r < width ? r : width - 1 - n) * uint32_t(a.r) * 2; });
+#pragma unroll
+                for (int k = 0; k < (RT + 3) / 4; ++k)
+                    ps.template issue<true>(own + k * PS::kBytes, lane, 0, k * kStepBytes, a.r * 2);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    bf16x8 p;
-                    if constexpr (COL)
-                        p = transposed(own, 128, s * 32, [&](int q) { return q * 16 + j * 4; }, lane);
-                    else {  // B [width][r]
-                        const int i = lane & 15, col = n + (i >> 2) * 16 + j * 4 + (i & 3), k = s * 32 + g * 8;
-                        p = __builtin_bit_cast(bf16x8,
-                                               load16(k < a.r ? w + (int64_t(col < width ? col : width - 1) * a.r + k) * 2
-                                                              : reinterpret_cast<const char *>(kZero16)));
-                    }
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-                        acc[j][m] = mfma_bf16(p, h[m][s], acc[j][m]);
-                }
-            if constexpr (COL)
-                asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
         }
+        if (a.base != nullptr) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (row[m][i] >= 0 && n + (lane & 7) * 8 < width)
+                        b[m][i] = *reinterpret_cast<const u32x4 *>(a.base + row[m][i] + n);
+        }
+    };
+    int n = n0 + wave * 64;
+    if (n < n1)
+        send(n);
+    make_h();  // while the first loads are on their way
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+            h[m][s] = *reinterpret_cast<const bf16x8 *>(lds.hidden + (m * 16 + (lane & 15)) * (KS * 32) + s * 32 + g * 8);
+    __syncthreads();
+    for (; n < n1; n += kAdapterWaves * 64) {
+        landed<0>();
+        u32x4 now[MT][2];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                u32x4 v;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int at = i * 8 + k * 2;
-                    v[k] = cvt_bf16x2(acc[at >> 2][m][at & 3] + bf16_lo(b[m][i][k]),
-                                      acc[at >> 2][m][(at & 3) + 1] + bf16_hi(b[m][i][k]));
-                }
-                if (live[m] && c + i * 8 < width)
-                    *reinterpret_cast<u32x4 *>(a.out + row[m] + c + i * 8) = v;
+                now[m][i] = b[m][i];
+                hold(now[m][i]);  // here: behind send() it would wait for the next loads
             }
+        f32x4 acc[4][MT] = {};
+        bf16x8 p[4][KS];
+        if (adapted) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    if constexpr (COL)
+                        p[j][s] = transposed(own, 128, s * 32, [&](int q) { return j * 16 + q * 4; }, lane);
+                    else
+                        p[j][s] = PS::frag(own + (s >> 1) * PS::kBytes, j * 16, s & 1, lane);
+                }
+        }
+        // read before the same LDS is loaded again
+        asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+        if (n + kAdapterWaves * 64 < n1)
+            send(n + kAdapterWaves * 64);
+        if (adapted) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+                        acc[j][m] = mfma_bf16(p[j][s], h[m][s], acc[j][m]);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<f32x4 *>(turn + (lane & 15) * kTurnRow + j * 16 + g * 4) = acc[j][m];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float *from = turn + (i * 8 + (lane >> 3)) * kTurnRow + (lane & 7) * 8;
+                const f32x4 lo = *reinterpret_cast<const f32x4 *>(from), hi = *reinterpret_cast<const f32x4 *>(from + 4);
+                const u32x4 &c = now[m][i];
+                const u32x4 v = {cvt_bf16x2(lo[0] + bf16_lo(c[0]), lo[1] + bf16_hi(c[0])),
+                                 cvt_bf16x2(lo[2] + bf16_lo(c[1]), lo[3] + bf16_hi(c[1])),
+                                 cvt_bf16x2(hi[0] + bf16_lo(c[2]), hi[1] + bf16_hi(c[2])),
+                                 cvt_bf16x2(hi[2] + bf16_lo(c[3]), hi[3] + bf16_hi(c[3]))};
+                if (row[m][i] >= 0 && n + (lane & 7) * 8 < width)
+                    __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(a.out + row[m][i] + n));
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
     }
 }
 
-template <int RT, bool COL>
+template <int RT, bool COL, bool SCAN>
 __global__ __launch_bounds__(kAdapterThreads) void adapter_expand_kernel(AdapterArgs a, int columns)
 {
     constexpr int MT = kTokenTiles<RT>, KS = (RT + 1) / 2, RP = RT * 16;
-    __shared__ __attribute__((aligned(128))) uint16_t hs[MT * 16 * KS * 32];
-    __shared__ __attribute__((aligned(128))) char stage[COL ? kAdapterWaves * KS * 32 * 128 : 16];
-    const AdapterTile t = adapter_tile(a, blockIdx.x, MT * 16, threadIdx.x & 63);
-    if (t.group < 0)
-        return;
-    // h: the parts' sum, scaled, in bf16; zeros past the rank and the rows
-    const float scale = t.group < a.L ? a.scales[t.group] : 0.0f;
-    for (int i = threadIdx.x; i < MT * 16 * KS * 8; i += kAdapterThreads) {
-        const int m = i / (KS * 8), k = i % (KS * 8) * 4;
-        f32x4 v = {};
-        if (t.group < a.L && m < t.rows && k < a.r) {
-            const float *from = a.parts + int64_t(t.start + m) * RP + k;
-            for (int s = 0; s < a.splits; ++s)
-                v += *reinterpret_cast<const f32x4 *>(from + int64_t(s) * a.T * RP);
-            v *= scale;
-        }
-        const uint2 b = pack4(v);
-        *reinterpret_cast<uint2 *>(hs + m * KS * 32 + k) = b;
-        if (a.hidden != nullptr && blockIdx.y == 0 && m < t.rows && k < a.r)
-            *reinterpret_cast<uint2 *>(a.hidden + int64_t(a.order[t.start + m]) * a.r + k) = b;
-    }
-    __syncthreads();
+    __shared__ __attribute__((aligned(128))) ExpandLds<RT, COL> lds;
     const int n0 = int(blockIdx.y) * columns, n1 = n0 + columns < a.width ? n0 + columns : int(a.width);
-    lds_char *own = (lds_char *)stage + (COL ? (threadIdx.x >> 6) * KS * 32 * 128 : 0);
-    if (t.rows <= 16)
-        expand_tile<RT, 1, COL>(a, t, hs, own, n0, n1);
-    else
-        expand_tile<RT, MT, COL>(a, t, hs, own, n0, n1);
+    each_tile<SCAN, MT * 16>(a, [&](int adapter, const int *tokens, int rows) {
+        // h: the parts' sum, scaled, in bf16; zeros past the rank and the rows
+        auto make_h = [&] {
+            const float scale = adapter < a.L ? a.scales[adapter] : 0.0f;
+            for (int i = threadIdx.x; i < MT * 16 * KS * 8; i += kAdapterThreads) {
+                const int m = i / (KS * 8), k = i % (KS * 8) * 4;
+                f32x4 v = {};
+                if (adapter < a.L && m < rows && k < a.r) {
+                    const float *from = a.parts + int64_t(tokens[m]) * RP + k;
+                    const int64_t apart = int64_t(a.T) * RP;
+                    for (int s = 0; s < a.splits; s += 8) {  // eight loads in flight
+                        f32x4 l[8];
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            l[u] = s + u < a.splits ? *reinterpret_cast<const f32x4 *>(from + (s + u) * apart) : f32x4{};
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            v += l[u];
+                    }
+                    v *= scale;
+                }
+                const uint2 b = pack4(v);
+                *reinterpret_cast<uint2 *>(lds.hidden + m * KS * 32 + k) = b;
+                if (a.hidden != nullptr && blockIdx.y == 0 && m < rows && k < a.r)
+                    *reinterpret_cast<uint2 *>(a.hidden + int64_t(tokens[m]) * a.r + k) = b;
+            }
+            __syncthreads();
+        };
+        if (rows <= 16)
+            expand_tile<RT, 1, COL>(a, adapter, tokens, rows, lds, n0, n1, make_h);
+        else
+            expand_tile<RT, MT, COL>(a, adapter, tokens, rows, lds, n0, n1, make_h);
+    });
 }
 
 // --------------------------------------------------------- adapters' gradients
@@ -350,99 +497,128 @@ struct AdapterGradArgs {
     int blocks;             // of the first
 };
 
-// 64 columns a wave of one adapter: sum over its tokens of wide[t][c] * narrow[t][j], 64 tokens a step,
-// both out of LDS transposed.
+// 64 columns of one adapter: sum over its tokens of wide[t][c] * narrow[t][j].  The waves share out the tokens, 64 a
+// step, both operands out of LDS transposed, the next step sent off as soon as this one is in
+// registers; the waves' sums meet in LDS.
+template <int RT>
+constexpr int kGradStage = 64 * 128 + 64 * RT * 32;
 template <int RT, bool DOWN>
-__device__ __forceinline__ void adapter_grad(const AdapterGradArgs &g, int block, lds_char *own)
+__device__ __forceinline__ void adapter_grad(const AdapterGradArgs &g, int block, char *lds)
 {
     const AdapterArgs &a = g.a;
-    constexpr int CH = RT * 2, J = CH;
+    constexpr int CH = RT * 2;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int width = g.width[DOWN ? 0 : 1], chunks = (width + kAdapterWaves * 64 - 1) / (kAdapterWaves * 64);
-    const int l = block / chunks, n = (block % chunks) * (kAdapterWaves * 64) + wave * 64;
-    if (n >= width)
-        return;
+    const int width = g.width[DOWN ? 0 : 1], chunks = (width + 63) / 64;
+    const int l = block / chunks, n = block % chunks * 64;
     const int from = a.offsets[l], count = a.offsets[l + 1] - from;
     const char *wide = g.wide[DOWN ? 0 : 1], *narrow = g.narrow[DOWN ? 0 : 1];
-    lds_char *small = own + 64 * 128;
-    f32x4 acc[4][RT] = {};
-    for (int t0 = 0; t0 < count; t0 += 64) {
+    lds_char *own = (lds_char *)lds + wave * kGradStage<RT>, *small = own + 64 * 128;
+    auto send = [&](int t0, int mine) {  // mine: the token of step row `lane`
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int t = t0 + j * 8 + (lane >> 3), c = n + (lane & 7) * 8;
-            load_lds16(t < count && c < width ? wide + (int64_t(a.order[from + t]) * width + c) * 2
-                                              : reinterpret_cast<const char *>(kZero16),
+            const int i = j * 8 + (lane >> 3), c = n + (lane & 7) * 8, t = __shfl(mine, i);
+            load_lds16(t0 + i < count && c < width ? wide + (int64_t(t) * width + c) * 2
+                                                   : reinterpret_cast<const char *>(kZero16),
                        own + j * kWave * 16);
         }
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int at = j * kWave + lane, t = t0 + at / CH, c = at % CH;
-            load_lds16(t < count && c * 8 < a.r ? narrow + (int64_t(a.order[from + t]) * a.r + c * 8) * 2
-                                                : reinterpret_cast<const char *>(kZero16),
+        for (int j = 0; j < CH; ++j) {
+            const int at = j * kWave + lane, i = at / CH, c = at % CH, t = __shfl(mine, i);
+            load_lds16(t0 + i < count && c * 8 < a.r ? narrow + (int64_t(t) * a.r + c * 8) * 2
+                                                     : reinterpret_cast<const char *>(kZero16),
                        small + j * kWave * 16);
         }
+    };
+    auto tokens = [&](int t0) { return t0 + lane < count ? a.order[from + t0 + lane] : 0; };
+    constexpr int kRound = kAdapterWaves * 64;
+    f32x4 acc[4][RT] = {};
+    int t0 = wave * 64;
+    if (t0 < count)
+        send(t0, tokens(t0));
+    int next = tokens(t0 + kRound);
+    for (; t0 < count; t0 += kRound) {
         landed<0>();
+        bf16x8 w[4][2], v[RT][2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            bf16x8 w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                w[i] = transposed(own, 128, s * 32, [&](int q) { return DOWN ? q * 16 + i * 4 : i * 16 + q * 4; }, lane);
+                w[i][s] = transposed(
+                    own, 128, s * 32, [&](int q) { return DOWN ? (i >> 1) * 32 + q * 8 + (i & 1) * 4 : i * 16 + q * 4; }, lane);
 #pragma unroll
-            for (int j = 0; j < RT; ++j) {
-                const bf16x8 v = transposed(small, RT * 32, s * 32, [&](int q) { return j * 16 + q * 4; }, lane);
+            for (int j = 0; j < RT; ++j)
+                v[j][s] = transposed(small, RT * 32, s * 32, [&](int q) { return j * 16 + q * 4; }, lane);
+        }
+        // read before the same LDS is loaded again
+        asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+        if (t0 + kRound < count) {
+            send(t0 + kRound, next);
+            next = tokens(t0 + 2 * kRound);
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int j = 0; j < RT; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    acc[i][j] = DOWN ? mfma_bf16(w[i], v, acc[i][j]) : mfma_bf16(v, w[i], acc[i][j]);
-            }
-        }
-        asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+                    acc[i][j] = DOWN ? mfma_bf16(w[i][s], v[j][s], acc[i][j]) : mfma_bf16(v[j][s], w[i][s], acc[i][j]);
     }
-    const int i16 = lane & 15, g16 = lane >> 4;
-    if constexpr (DOWN) {  // lane: rank j * 16 + l % 16, columns n + l / 16 * 16 ..
+    f32x4 *sums = reinterpret_cast<f32x4 *>(lds);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < RT; ++j)
+            sums[(wave * RT * 4 + j * 4 + i) * kWave + lane] = acc[i][j];
+    __syncthreads();
+    auto sum = [&](int tile) {
+        f32x4 v = sums[tile * kWave + lane];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int rank = j * 16 + i16, c = n + g16 * 16 + h * 8;
-                const uint2 lo = pack4(acc[2 * h][j]), hi = pack4(acc[2 * h + 1][j]);
-                if (rank < a.r && c < width)
-                    *reinterpret_cast<u32x4 *>(g.out[0] + (int64_t(l) * a.r + rank) * width + c) =
-                        u32x4{lo.x, lo.y, hi.x, hi.y};
-            }
-    } else {  // lane: column n + i * 16 + l % 16, ranks j * 16 + l / 16 * 4 ..
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < RT; ++j) {
-                const int c = n + i * 16 + i16, rank = j * 16 + g16 * 4;
-                if (rank < a.r && c < width)
-                    *reinterpret_cast<uint2 *>(g.out[1] + (int64_t(l) * width + c) * a.r + rank) = pack4(acc[i][j]);
-            }
+        for (int w = 1; w < kAdapterWaves; ++w)
+            v += sums[(w * RT * 4 + tile) * kWave + lane];
+        return pack4(v);
+    };
+    const int i16 = lane & 15, g16 = lane >> 4;
+    for (int p = wave; p < RT * 2; p += kAdapterWaves) {  // two tiles: rank tile p / 2
+        const int j = p >> 1, h = p & 1;
+        const uint2 lo = sum(j * 4 + 2 * h), hi = sum(j * 4 + 2 * h + 1);
+        if constexpr (DOWN) {  // lane: rank j * 16 + l % 16, eight columns
+            const int rank = j * 16 + i16, c = n + h * 32 + g16 * 8;
+            if (rank < a.r && c < width)
+                *reinterpret_cast<u32x4 *>(g.out[0] + (int64_t(l) * a.r + rank) * width + c) = u32x4{lo.x, lo.y, hi.x, hi.y};
+        } else {  // lane: ranks j * 16 + l / 16 * 4 .., columns h * 32 + l % 16 and 16 further on
+            const int rank = j * 16 + g16 * 4, c = n + h * 32 + i16;
+            if (rank < a.r && c < width)
+                *reinterpret_cast<uint2 *>(g.out[1] + (int64_t(l) * width + c) * a.r + rank) = lo;
+            if (rank < a.r && c + 16 < width)
+                *reinterpret_cast<uint2 *>(g.out[1] + (int64_t(l) * width + c + 16) * a.r + rank) = hi;
+        }
     }
 }
 
 template <int RT>
 __global__ __launch_bounds__(kAdapterThreads) void adapter_grads_kernel(AdapterGradArgs g)
 {
-    constexpr int kOwn = 64 * 128 + 64 * RT * 32;
-    __shared__ __attribute__((aligned(128))) char stage[kAdapterWaves * kOwn];
-    lds_char *own = (lds_char *)stage + (threadIdx.x >> 6) * kOwn;
+    constexpr int kStages = kAdapterWaves * kGradStage<RT>, kSums = kAdapterWaves * RT * 4 * kWave * 16;
+    __shared__ __attribute__((aligned(128))) char lds[kStages > kSums ? kStages : kSums];
     if (int(blockIdx.x) < g.blocks)
-        adapter_grad<RT, true>(g, blockIdx.x, own);
+        adapter_grad<RT, true>(g, blockIdx.x, lds);
     else
-        adapter_grad<RT, false>(g, int(blockIdx.x) - g.blocks, own);
+        adapter_grad<RT, false>(g, int(blockIdx.x) - g.blocks, lds);
 }
 
 // ---------------------------------------------------------------- launches
 
 int rank_tiles(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : 8; }
 int tile_tokens(int r) { return r <= 64 ? 64 : 32; }
+bool scans(int64_t T, int L) { return T <= kScanTokens && L < kScanAdapters; }
 int64_t most_tiles(int64_t T, int L, int r)
 {
     const int64_t groups = L + 1 < T ? L + 1 : T;
     return T / tile_tokens(r) + groups;
 }
+// Blocks of a launch that go by tile, or by adapter.
+unsigned tile_blocks(int64_t T, int L, int r) { return unsigned(scans(T, L) ? L + 1 : most_tiles(T, L, r)); }
 // Blocks that share a tile's K: so many that the card is full twice, each wave at least one step.
 int shrink_splits(int64_t T, int L, int r, int width)
 {
@@ -518,11 +694,13 @@ hipError_t shrink(AdapterArgs &a, const void *q, const void *w, int width, hipSt
     a.splits = shrink_splits(a.T, a.L, a.r, width);
     return by_rank(a.r, [&](auto rt) {
         constexpr int RT = decltype(rt)::value;
-        const dim3 grid(unsigned(most_tiles(a.T, a.L, a.r)), unsigned(a.splits));
-        if (!COL && width % 64 != 0)
-            hipLaunchKernelGGL((adapter_shrink_kernel<RT, COL, !COL>), grid, dim3(kAdapterThreads), 0, stream, a);
+        const dim3 grid(tile_blocks(a.T, a.L, a.r), unsigned(a.splits));
+        auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kAdapterThreads), 0, stream, a); };
+        const bool tail = width % 64 != 0;
+        if (scans(a.T, a.L))
+            go(tail ? adapter_shrink_kernel<RT, COL, true, true> : adapter_shrink_kernel<RT, COL, false, true>);
         else
-            hipLaunchKernelGGL((adapter_shrink_kernel<RT, COL, false>), grid, dim3(kAdapterThreads), 0, stream, a);
+            go(tail ? adapter_shrink_kernel<RT, COL, true, false> : adapter_shrink_kernel<RT, COL, false, false>);
         return hipGetLastError();
     });
 }
@@ -538,11 +716,16 @@ hipError_t expand(AdapterArgs &a, const void *w, int width, const void *base, vo
     return by_rank(a.r, [&](auto rt) {
         constexpr int RT = decltype(rt)::value;
         constexpr int kRun = kAdapterWaves * 64;
+        const bool scan = scans(a.T, a.L);
         const int64_t tiles = most_tiles(a.T, a.L, a.r), runs = (width + kRun - 1) / kRun;
-        int64_t n = 4 * kCard / tiles;  // blocks that share a tile's columns
+        // Blocks that share a tile's columns: two a compute unit, each then has several steps behind its start (8192 rows
+        // of 7168, rank 64: 64.0 us, with four 68.3); four where each finds its tokens itself, many of them none
+        // (128 tokens on 64 adapters: 6.9 us, with two 7.4).
+        int64_t n = (scan ? 4 : 2) * kCard / tiles;
         n = n < 1 ? 1 : n < runs ? n : runs;
         const int columns = int((runs + n - 1) / n) * kRun;
-        hipLaunchKernelGGL((adapter_expand_kernel<RT, COL>), dim3(unsigned(tiles), unsigned((width + columns - 1) / columns)),
+        hipLaunchKernelGGL((scan ? adapter_expand_kernel<RT, COL, true> : adapter_expand_kernel<RT, COL, false>),
+                           dim3(tile_blocks(a.T, a.L, a.r), unsigned((width + columns - 1) / columns)),
                            dim3(kAdapterThreads), 0, stream, a, columns);
         return hipGetLastError();
     });
@@ -561,7 +744,7 @@ hipError_t launch_adapter(const AdapterShape &s, const void *x, const void *down
     if (log_enabled())
         log_launch("adapter_product: T=%d K=%d N=%d r=%d L=%d splits=%d", s.T, s.K, s.N, s.r, s.L,
                    shrink_splits(s.T, s.L, s.r, s.K));
-    hipError_t e = group_tokens(a, stream);
+    hipError_t e = scans(s.T, s.L) ? hipSuccess : group_tokens(a, stream);
     if (e == hipSuccess)
         e = shrink<false>(a, x, down, s.K, stream);
     return e == hipSuccess ? expand<false>(a, up, s.N, base, out, hidden, stream) : e;
@@ -593,9 +776,8 @@ hipError_t launch_adapter_backward(const AdapterShape &s, const void *dy, const 
     g.out[1] = static_cast<uint16_t *>(dup);
     g.width[0] = s.K;
     g.width[1] = s.N;
-    constexpr int kRun = kAdapterWaves * 64;
-    g.blocks = s.L * ((s.K + kRun - 1) / kRun);
-    const unsigned all = unsigned(g.blocks + s.L * ((s.N + kRun - 1) / kRun));
+    g.blocks = s.L * ((s.K + 63) / 64);
+    const unsigned all = unsigned(g.blocks + s.L * ((s.N + 63) / 64));
     return by_rank(s.r, [&](auto rt) {
         hipLaunchKernelGGL((adapter_grads_kernel<decltype(rt)::value>), dim3(all), dim3(kAdapterThreads), 0, stream, g);
         return hipGetLastError();

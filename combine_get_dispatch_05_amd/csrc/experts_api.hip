@@ -182,7 +182,7 @@ int ep_adapter_product_backward(const ep_adapter_dims *dims, const void *dy, con
         !al(ddown, 16) || !al(dup, 16) || !al(workspace, 256) || !al(adapter_ids, 8) || !al(scales, 4))
         return EP_ERR_ALIGN;
     // the gradients' blocks are one launch
-    const int64_t runs = (int64_t(dims->in_features) + 255) / 256 + (int64_t(dims->out_features) + 255) / 256;
+    const int64_t runs = (int64_t(dims->in_features) + 63) / 64 + (int64_t(dims->out_features) + 63) / 64;
     if (dims->num_adapters * runs > kMaxTileBlocks)
         return EP_ERR_INVALID;
     if (workspace_bytes < ep_adapter_workspace(dims, 1))
