@@ -184,8 +184,8 @@ def adapter_product(x: torch.Tensor, adapter_ids: torch.Tensor, down: torch.Tens
     if base is not None:
         _row(base, torch.bfloat16, (T, N), "base")
     dev = _here(x, adapter_ids, down, up, scales, base)
-    out = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
-    hidden = torch.empty((T, d.rank), dtype=torch.bfloat16, device=x.device) if save else None
+    out = torch.empty(T, N, dtype=torch.bfloat16, device=x.device)
+    hidden = torch.empty(T, d.rank, dtype=torch.bfloat16, device=x.device) if save else None
     size = abi.lib().ep_adapter_workspace(ctypes.byref(d), 0)
     work = torch.empty(size, dtype=torch.uint8, device=x.device)
     at = abi.address
@@ -797,8 +797,8 @@ class Buffer:
             _row(bias, torch.float32, (self.num_experts,), "bias")
         dev = _here(logits, bias, self._mask)
         rule, d = router._raw(), self._dims(T, 8, K)
-        idx = torch.empty((T, max(K, 0)), dtype=torch.int64, device=logits.device)
-        weights = torch.empty((T, max(K, 0)), dtype=torch.float32, device=logits.device)
+        idx = torch.empty(T, max(K, 0), dtype=torch.int64, device=logits.device)
+        weights = torch.empty(T, max(K, 0), dtype=torch.float32, device=logits.device)
         sums, work, size = None, None, 0
         if score_sums:
             sums = torch.empty(self.num_experts, dtype=torch.float32, device=logits.device)
@@ -859,8 +859,8 @@ class Buffer:
         rule, d = router._raw(), self._dims(T, H, K)
         at, like = abi.address, dict(device=x.device)
         y = torch.empty_like(x)
-        idx = torch.empty((T, max(K, 0)), dtype=torch.int64, **like)
-        weights = torch.empty((T, max(K, 0)), dtype=torch.float32, **like)
+        idx = torch.empty(T, max(K, 0), dtype=torch.int64, **like)
+        weights = torch.empty(T, max(K, 0), dtype=torch.float32, **like)
         size = abi.lib().ep_ll_moe_workspace(ctypes.byref(d), inter)
         work = torch.empty(size, dtype=torch.uint8, **like)
         abi.check(abi.lib().ep_ll_moe(

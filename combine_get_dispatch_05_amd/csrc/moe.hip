@@ -270,12 +270,58 @@ __device__ __forceinline__ void gate_tile(const MoeArgs &a, const ActiveExpert &
     __syncthreads();
 }
 
-template <bool FP8, bool TAIL, int G>
-__global__ __launch_bounds__(kGateWaves *kWave) void moe_gate_kernel(MoeArgs a)
+// One token (V > 0): each block chooses for itself, which takes less than a launch in between; block 0 writes the
+// choice down.
+struct MoeChoice {
+    RouteRule rule;
+    int64_t *topk_idx;
+    float *topk_weights;
+};
+template <int V>
+__device__ __forceinline__ ActiveExpert choose_one(const MoeArgs &a, const MoeChoice &c, float *lds)
+{
+    __shared__ int chosen[kMaxTopk];
+    const RouteRule &r = c.rule;
+    const int lane = threadIdx.x & 63;
+    if (threadIdx.x < 64) {
+        float l[V], s[V] = {}, bias[V], w;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int e = j * 64 + lane;
+            l[j] = e < r.experts ? float(a.work.logits[e]) : -INFINITY;
+            bias[j] = r.bias != nullptr && e < r.experts ? r.bias[e] : 0.0f;
+        }
+        const int e = route_row(r, l, bias, live_experts<V>(r, lane), lane, reinterpret_cast<double *>(lds), false, false, s,
+                                [&](int i) { return float(a.work.logits[i]); }, w);
+        chosen[lane] = e;
+        if (blockIdx.x == 0 && blockIdx.y == 0 && lane < r.topk) {
+            c.topk_idx[lane] = e;
+            c.topk_weights[lane] = w;
+            if (lane < int(gridDim.y)) {
+                a.work.active[lane] = ActiveExpert{e, lane, e >= 0, 0, 1};
+                a.work.pair_weight[lane] = w;
+            }
+        }
+    }
+    __syncthreads();
+    const int e = uniform(chosen[blockIdx.y]);
+    return ActiveExpert{e, int(blockIdx.y), e >= 0, 0, 1};
+}
+
+// 32 columns a block, so that the tokens' loads serve twice the weights, where an expert's tokens are few.
+template <bool FP8, bool TAIL, int V>
+__global__ __launch_bounds__(kGateWaves *kWave) void moe_gate_kernel(MoeArgs a, MoeChoice c)
 {
     __shared__ __attribute__((aligned(16))) float sums[kGateWaves * kGateSums];
-    const ActiveExpert x = a.work.active[blockIdx.y];
+    constexpr int G = 2;
     const int n0 = blockIdx.x * 16 * G;
+    if constexpr (V > 0) {
+        const ActiveExpert x = choose_one<V>(a, c, sums);
+        if (x.count > 0)
+            gate_tile<FP8, TAIL, G, 2, 1>(a, x, n0, 0, sums);
+        return;
+    }
+    const ActiveExpert x = a.work.active[blockIdx.y];
     if (x.count <= 8) {
         if (x.count > 0)
             gate_tile<FP8, TAIL, G, 2, 1>(a, x, n0, 0, sums);
@@ -290,18 +336,18 @@ __global__ __launch_bounds__(kGateWaves *kWave) void moe_gate_kernel(MoeArgs a)
         }
 }
 
-// 16 columns of y for every token: the block's waves share out the experts (each in `parts` pieces of
-// K), a wave adds each piece's weighted product to its own sums [token][16] in LDS.
-template <bool FP8, bool TAIL, int C, int MT>
+// COLS columns of y for every token: the block's waves share out the experts (each in `parts` pieces of
+// K), a wave adds each piece's weighted product to its own sums [token][COLS] in LDS.
+template <bool FP8, bool TAIL, int COLS, int C, int MT>
 __device__ __forceinline__ void down_piece(const MoeArgs &a, const ActiveExpert &x, int n0, int m0, int s0, int s1, float *own)
 {
-    constexpr int kRows = 16 / C;
+    constexpr int kRows = 16 / C, RT = COLS / kRows;
     const int lane = threadIdx.x & 63, i0 = (lane & 15) / C;
     const int steps = (a.kbytes + kStepBytes - 1) / kStepBytes;
-    const char *prow[C];
-    const float *scale[C] = {};
+    const char *prow[RT];
+    const float *scale[RT] = {};
 #pragma unroll
-    for (int r = 0; r < C; ++r) {
+    for (int r = 0; r < RT; ++r) {
         const int n = n0 + r * kRows + i0;
         prow[r] = a.p + (int64_t(x.expert) * a.H + (n < a.H ? n : a.H - 1)) * a.kbytes;
         if constexpr (FP8)
@@ -317,34 +363,36 @@ __device__ __forceinline__ void down_piece(const MoeArgs &a, const ActiveExpert 
         token[m] = i < x.count ? token_of(x.tokens, i) : -1;
         weight[m] = a.work.pair_weight[at];
     }
-    f32x4 acc[C][MT] = {};
-    stream<FP8, TAIL, ahead(FP8, C, C, MT), C>(prow, scale, qrow, s0, s1, a.kbytes, lane, acc);
+    f32x4 acc[RT][MT] = {};
+    stream<FP8, TAIL, ahead(FP8, C, RT, MT), C>(prow, scale, qrow, s0, s1, a.kbytes, lane, acc);
 #pragma unroll
-    for (int r = 0; r < C; ++r)
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             if constexpr (C == 1) {
                 if (token[m] >= 0)
-                    *reinterpret_cast<f32x4 *>(own + token[m] * 16 + (lane >> 4) * 4) += acc[r][m] * weight[m];
+                    *reinterpret_cast<f32x4 *>(own + token[m] * COLS + r * kRows + (lane >> 4) * 4) += acc[r][m] * weight[m];
             } else {
                 const float v = fold(acc[r][m], lane) * weight[m];
                 if (token[m] >= 0)
-                    own[token[m] * 16 + r * kRows + (lane >> 4) * 2 + (lane & 1)] += v;
+                    own[token[m] * COLS + r * kRows + (lane >> 4) * 2 + (lane & 1)] += v;
             }
         }
 }
 
-template <int W, bool FP8, bool TAIL>
-__global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs a, int room, const uint16_t *residual, uint16_t *y)
+constexpr int kDownWaves = 8;
+template <bool FP8, bool TAIL, int COLS>
+__global__ __launch_bounds__(kDownWaves *kWave) void moe_down_kernel(MoeArgs a, int room, const uint16_t *residual, uint16_t *y)
 {
-    extern __shared__ f32x4 own[];  // [W][T][4]
+    constexpr int W = kDownWaves, Q = COLS / 4;  // Q: vectors of a token's columns
+    extern __shared__ f32x4 own[];               // [W][T][Q]
     __shared__ ActiveExpert list[kMoeExperts];
     __shared__ int used[W];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int n0 = blockIdx.x * 16;
+    const int n0 = blockIdx.x * COLS;
     const f32x4 zero = {};
-    for (int i = lane; i < a.T * 4; i += 64)
-        own[wave * a.T * 4 + i] = zero;
+    for (int i = lane; i < a.T * Q; i += 64)
+        own[wave * a.T * Q + i] = zero;
     int n = 0;
     for (int i = threadIdx.x; i < room; i += W * kWave) {
         list[i] = a.work.active[i];
@@ -362,6 +410,7 @@ __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs a, int room,
     const int steps = (a.kbytes + kStepBytes - 1) / kStepBytes;
     int parts = experts > 0 ? (W + experts - 1) / experts : 1;
     parts = parts < steps ? parts : steps;
+    float *sums = reinterpret_cast<float *>(own + wave * a.T * Q);
     for (int i = wave; i < experts * parts; i += W) {
         ActiveExpert x = list[i / parts];
         x.expert = uniform(x.expert);
@@ -369,25 +418,27 @@ __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs a, int room,
         x.count = uniform(x.count);
         const int part = i % parts, s0 = steps * part / parts, s1 = steps * (part + 1) / parts;
         for (int m0 = 0; m0 < x.count; m0 += 32) {
-            float *sums = reinterpret_cast<float *>(own + wave * a.T * 4);
-            if (x.count - m0 > 16)
-                down_piece<FP8, TAIL, 1, 2>(a, x, n0, m0, s0, s1, sums);
-            else if (x.count - m0 > 8)
-                down_piece<FP8, TAIL, 2, 2>(a, x, n0, m0, s0, s1, sums);
+            if (x.count - m0 > 16) {
+                if constexpr (COLS == 16)
+                    down_piece<FP8, TAIL, COLS, 1, 2>(a, x, n0, m0, s0, s1, sums);
+                else
+                    down_piece<FP8, TAIL, COLS, 2, 4>(a, x, n0, m0, s0, s1, sums);
+            } else if (x.count - m0 > 8)
+                down_piece<FP8, TAIL, COLS, 2, 2>(a, x, n0, m0, s0, s1, sums);
             else
-                down_piece<FP8, TAIL, 2, 1>(a, x, n0, m0, s0, s1, sums);
+                down_piece<FP8, TAIL, COLS, 2, 1>(a, x, n0, m0, s0, s1, sums);
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < a.T * 4; i += W * kWave) {
-        const int n = n0 + (i & 3) * 4;
-        if (n >= a.H)
+    for (int i = threadIdx.x; i < a.T * Q; i += W * kWave) {
+        const int c = n0 + i % Q * 4;
+        if (c >= a.H)
             continue;
         f32x4 v = own[i];
 #pragma unroll
         for (int w = 1; w < W; ++w)
-            v += own[w * a.T * 4 + i];
-        const int64_t at = int64_t(i >> 2) * a.H + n;
+            v += own[w * a.T * Q + i];
+        const int64_t at = int64_t(i / Q) * a.H + c;
         if (residual != nullptr) {
             const uint2 b = *reinterpret_cast<const uint2 *>(residual + at);
             v[0] += bf16_lo(b.x), v[1] += bf16_hi(b.x), v[2] += bf16_lo(b.y), v[3] += bf16_hi(b.y);
@@ -395,8 +446,6 @@ __global__ __launch_bounds__(W *kWave) void moe_down_kernel(MoeArgs a, int room,
         *reinterpret_cast<uint2 *>(y + at) = pack4(v);
     }
 }
-
-constexpr int kGateRound = 256;  // blocks
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
@@ -455,20 +504,22 @@ hipError_t launch_moe(const RouteRule &rule, const MoeCall &c, hipStream_t strea
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    auto select = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3(1), dim3(1024), 0, stream, rule, c.T, a.work, c.topk_idx, c.topk_weights);
-    };
-    if (E <= 64)
-        select(moe_select_kernel<1>);
-    else if (E <= 128)
-        select(moe_select_kernel<2>);
-    else if (E <= 256)
-        select(moe_select_kernel<4>);
-    else
-        select(moe_select_kernel<8>);
-    e = hipGetLastError();
-    if (e != hipSuccess)
-        return e;
+    if (c.T > 1) {
+        auto select = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, dim3(1), dim3(1024), 0, stream, rule, c.T, a.work, c.topk_idx, c.topk_weights);
+        };
+        if (E <= 64)
+            select(moe_select_kernel<1>);
+        else if (E <= 128)
+            select(moe_select_kernel<2>);
+        else if (E <= 256)
+            select(moe_select_kernel<4>);
+        else
+            select(moe_select_kernel<8>);
+        e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
     a.I = c.I;
     a.H = c.H;
     a.T = c.T;
@@ -476,19 +527,27 @@ hipError_t launch_moe(const RouteRule &rule, const MoeCall &c, hipStream_t strea
     a.p_scale = c.w13_scale;
     a.q = static_cast<const char *>(c.x);
     a.kbytes = c.H * (fp8 ? 1 : 2);
-    // 32 columns a block, whose tokens' loads then serve twice the weights, where 16 would make more than four
-    // blocks a compute unit (64 FP8 experts of 2048 x 7168: 314 against 326 us)
-    const bool wide = int64_t((c.I + 15) / 16) * most > 4 * kGateRound;
-    auto gate = [&](auto narrow, auto wider) {
-        hipLaunchKernelGGL(wide ? wider : narrow, dim3((c.I + (wide ? 31 : 15)) / (wide ? 32 : 16), most),
-                           dim3(kGateWaves * kWave), 0, stream, a);
+    const MoeChoice choice{rule, c.topk_idx, c.topk_weights};
+    auto gate = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((c.I + 31) / 32, most), dim3(kGateWaves * kWave), 0, stream, a, choice);
     };
-    if (fp8)
-        gate(moe_gate_kernel<true, false, 1>, moe_gate_kernel<true, false, 2>);
-    else if (a.kbytes % kStepBytes == 0)
-        gate(moe_gate_kernel<false, false, 1>, moe_gate_kernel<false, false, 2>);
+    auto gates = [&](auto experts) {
+        constexpr int V = decltype(experts)::value;
+        if (fp8)
+            gate(moe_gate_kernel<true, false, V>);
+        else if (a.kbytes % kStepBytes == 0)
+            gate(moe_gate_kernel<false, false, V>);
+        else
+            gate(moe_gate_kernel<false, true, V>);
+    };
+    if (c.T > 1)
+        gates(std::integral_constant<int, 0>());
+    else if (E <= 64)
+        gates(std::integral_constant<int, 1>());
+    else if (E <= 256)
+        gates(std::integral_constant<int, 4>());
     else
-        gate(moe_gate_kernel<false, true, 1>, moe_gate_kernel<false, true, 2>);
+        gates(std::integral_constant<int, 8>());
     e = hipGetLastError();
     if (e != hipSuccess)
         return e;
@@ -496,16 +555,26 @@ hipError_t launch_moe(const RouteRule &rule, const MoeCall &c, hipStream_t strea
     a.p_scale = c.w2_scale;
     a.q = reinterpret_cast<const char *>(a.work.act);
     a.kbytes = c.I * (fp8 ? 1 : 2);
-    auto down = [&](auto kernel, int waves) {
-        hipLaunchKernelGGL(kernel, dim3((c.H + 15) / 16), dim3(waves * kWave), size_t(waves) * c.T * 64, stream, a, most,
-                           static_cast<const uint16_t *>(c.residual), static_cast<uint16_t *>(c.y));
+    auto down = [&](auto cols) {
+        constexpr int COLS = decltype(cols)::value;
+        auto go = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, dim3((c.H + COLS - 1) / COLS), dim3(kDownWaves * kWave),
+                               size_t(kDownWaves) * c.T * COLS * 4, stream, a, most, static_cast<const uint16_t *>(c.residual),
+                               static_cast<uint16_t *>(c.y));
+        };
+        if (fp8)
+            go(moe_down_kernel<true, false, COLS>);
+        else if (a.kbytes % kStepBytes == 0)
+            go(moe_down_kernel<false, false, COLS>);
+        else
+            go(moe_down_kernel<false, true, COLS>);
     };
-    if (fp8)
-        down(moe_down_kernel<8, true, false>, 8);
-    else if (a.kbytes % kStepBytes == 0)
-        down(moe_down_kernel<8, false, false>, 8);
+    // 8 columns a block where blocks of 16 would be fewer than the compute units (H = 2048, eight experts of 768: 6.6
+    // against 8.2 us; where they are not, 16 share the activations' loads: H = 7168, FP8, 24.9 against 32)
+    if (c.H < 16 * compute_units())
+        down(std::integral_constant<int, 8>());
     else
-        down(moe_down_kernel<8, false, true>, 8);
+        down(std::integral_constant<int, 16>());
     return hipGetLastError();
 }
 

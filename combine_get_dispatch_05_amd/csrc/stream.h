@@ -80,9 +80,9 @@ __device__ __forceinline__ bf16x8 widen8(int lo, int hi)
 
 // acc[r][m] += weight rows of tile r times token tile m over steps [s0, s1).
 template <bool FP8, bool TAIL, int AHEAD, int C, int RT, int MT>
-__device__ __forceinline__ void stream(const char *const (&prow)[RT], const float *const (&scale)[RT],
-                                       const char *const (&qrow)[MT], int s0, int s1, int kbytes, int lane,
-                                       f32x4 (&acc)[RT][MT])
+__device__ __forceinline__ void stream_run(const char *const (&prow)[RT], const float *const (&scale)[RT],
+                                           const char *const (&qrow)[MT], int s0, int s1, int kbytes, int lane,
+                                           f32x4 (&acc)[RT][MT])
 {
     if (s0 >= s1)
         return;
@@ -145,6 +145,17 @@ __device__ __forceinline__ void stream(const char *const (&prow)[RT], const floa
 #pragma unroll
     for (int d = 0; d < AHEAD; ++d)
         compute(d, s + d);
+}
+
+// A run is rounded up to the steps in flight, so a short one has fewer.
+template <bool FP8, bool TAIL, int AHEAD, int C, int RT, int MT>
+__device__ __forceinline__ void stream(const char *const (&prow)[RT], const float *const (&scale)[RT],
+                                       const char *const (&qrow)[MT], int s0, int s1, int kbytes, int lane, f32x4 (&acc)[RT][MT])
+{
+    if (AHEAD > 2 && s1 - s0 <= 2)
+        stream_run<FP8, TAIL, 2, C>(prow, scale, qrow, s0, s1, kbytes, lane, acc);
+    else
+        stream_run<FP8, TAIL, AHEAD, C>(prow, scale, qrow, s0, s1, kbytes, lane, acc);
 }
 
 }  // namespace ep
