@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass
+from functools import lru_cache
 from typing import Optional
 
 import torch
@@ -158,18 +159,27 @@ def fp8_product(a, w) -> torch.Tensor:
     return out
 
 
+# The small calls' host time counts: the library is asked once for each size.
+@lru_cache(maxsize=4096)
+def _workspace(name: str, dims, *rest) -> int:
+    return getattr(abi.lib(), name)(ctypes.byref(abi.Dims(*dims)), *rest)
+
+
+@lru_cache(maxsize=4096)
+def _adapter_workspace(T: int, K: int, N: int, r: int, L: int, back: int) -> int:
+    return abi.lib().ep_adapter_workspace(ctypes.byref(abi.AdapterDims(T, K, N, r, L)), back)
+
+
 def _adapter_args(x, adapter_ids, down, up, scales):
     _need(x, torch.bfloat16, "x", 2)
-    T, K = x.shape
-    _row(adapter_ids, torch.int64, (T,), "adapter_ids")
     _need(down, torch.bfloat16, "down", 3)
-    L, r = down.shape[:2]
-    _row(down, torch.bfloat16, (L, r, K), "down")
     _need(up, torch.bfloat16, "up", 3)
-    N = up.shape[1]
-    _row(up, torch.bfloat16, (L, N, r), "up")
+    (T, K), (L, r, _), N = x.shape, down.shape, up.shape[1]
+    _row(adapter_ids, torch.int64, (T,), "adapter_ids")
+    _shape(down, (L, r, K), "down")
+    _shape(up, (L, N, r), "up")
     _row(scales, torch.float32, (L,), "scales")
-    return abi.AdapterDims(T, K, N, r, L)
+    return T, K, N, r, L
 
 
 def adapter_product(x: torch.Tensor, adapter_ids: torch.Tensor, down: torch.Tensor, up: torch.Tensor,
@@ -179,19 +189,18 @@ def adapter_product(x: torch.Tensor, adapter_ids: torch.Tensor, down: torch.Tens
     base [T, N] (the projection's output; None: zeros) bf16, down [L, r, K], up [L, N, r] bf16 with r up to
     128, scales [L] fp32.  Returns (out [T, N] bf16, hidden): hidden [T, r] bf16 is what
     adapter_product_backward takes, None without save."""
-    d = _adapter_args(x, adapter_ids, down, up, scales)
-    T, N = d.num_tokens, d.out_features
+    d = T, K, N, r, L = _adapter_args(x, adapter_ids, down, up, scales)
     if base is not None:
         _row(base, torch.bfloat16, (T, N), "base")
-    dev = _here(x, adapter_ids, down, up, scales, base)
-    out = torch.empty(T, N, dtype=torch.bfloat16, device=x.device)
-    hidden = torch.empty(T, d.rank, dtype=torch.bfloat16, device=x.device) if save else None
-    size = abi.lib().ep_adapter_workspace(ctypes.byref(d), 0)
-    work = torch.empty(size, dtype=torch.uint8, device=x.device)
-    at = abi.address
-    abi.check(abi.lib().ep_adapter_product(ctypes.byref(d), at(x), at(adapter_ids), at(down), at(up), at(scales), at(base),
-                                           at(out), at(hidden), at(work), size, abi.raw_stream(dev)),
-              "ep_adapter_product")
+    dev, at = _here(x, adapter_ids, down, up, scales, base), x.device
+    out = torch.empty(T, N, dtype=torch.bfloat16, device=at)
+    hidden = torch.empty(T, r, dtype=torch.bfloat16, device=at) if save else None
+    size = _adapter_workspace(*d, 0)
+    work = torch.empty(size, dtype=torch.uint8, device=at)
+    abi.check(abi.lib().ep_adapter_product(
+        ctypes.byref(abi.AdapterDims(*d)), x.data_ptr(), adapter_ids.data_ptr(), down.data_ptr(), up.data_ptr(),
+        scales.data_ptr(), abi.address(base), out.data_ptr(), abi.address(hidden), work.data_ptr(), size,
+        abi.raw_stream(dev)), "ep_adapter_product")
     return out, hidden
 
 
@@ -201,20 +210,19 @@ def adapter_product_backward(dy: torch.Tensor, x: torch.Tensor, adapter_ids: tor
     """Gradients of adapter_product given dy [T, N] bf16 (base's gradient is dy itself).  dx_base [T, K] bf16 is
     the projection's own gradient of x, to which the adapters' is added.  Returns (dx [T, K], ddown, dup), bf16;
     an adapter without tokens has zeros."""
-    d = _adapter_args(x, adapter_ids, down, up, scales)
-    T = d.num_tokens
-    _row(dy, torch.bfloat16, (T, d.out_features), "dy")
-    _row(hidden, torch.bfloat16, (T, d.rank), "hidden")
+    d = T, K, N, r, L = _adapter_args(x, adapter_ids, down, up, scales)
+    _row(dy, torch.bfloat16, (T, N), "dy")
+    _row(hidden, torch.bfloat16, (T, r), "hidden")
     if dx_base is not None:
-        _row(dx_base, torch.bfloat16, (T, d.in_features), "dx_base")
+        _row(dx_base, torch.bfloat16, (T, K), "dx_base")
     dev = _here(dy, x, adapter_ids, down, up, scales, hidden, dx_base)
     dx, ddown, dup = torch.empty_like(x), torch.empty_like(down), torch.empty_like(up)
-    size = abi.lib().ep_adapter_workspace(ctypes.byref(d), 1)
+    size = _adapter_workspace(*d, 1)
     work = torch.empty(size, dtype=torch.uint8, device=x.device)
-    at = abi.address
     abi.check(abi.lib().ep_adapter_product_backward(
-        ctypes.byref(d), at(dy), at(x), at(adapter_ids), at(down), at(up), at(scales), at(hidden), at(dx_base), at(dx),
-        at(ddown), at(dup), at(work), size, abi.raw_stream(dev)), "ep_adapter_product_backward")
+        ctypes.byref(abi.AdapterDims(*d)), dy.data_ptr(), x.data_ptr(), adapter_ids.data_ptr(), down.data_ptr(),
+        up.data_ptr(), scales.data_ptr(), hidden.data_ptr(), abi.address(dx_base), dx.data_ptr(), ddown.data_ptr(),
+        dup.data_ptr(), work.data_ptr(), size, abi.raw_stream(dev)), "ep_adapter_product_backward")
     return dx, ddown, dup
 
 
@@ -231,11 +239,11 @@ class Router:
     normalize: bool = True
     scale: float = 1.0
 
-    def _raw(self) -> abi.RouterRule:
+    def __post_init__(self):
         if self.score not in ("softmax", "sigmoid"):
             raise ValueError(f"score must be softmax or sigmoid, got {self.score!r}")
-        return abi.RouterRule(int(self.score == "sigmoid"), self.num_groups, self.topk_groups, bool(self.normalize),
-                              self.scale)
+        rule = abi.RouterRule(self.score == "sigmoid", self.num_groups, self.topk_groups, bool(self.normalize), self.scale)
+        object.__setattr__(self, "_raw", ctypes.byref(rule))  # (which keeps it alive)
 
 
 @dataclass
@@ -779,8 +787,9 @@ class Buffer:
     def _logits(self, logits: torch.Tensor) -> int:
         """Checks logits [T, E], fp32 or bf16; returns 1 for bf16."""
         bf16 = logits.dtype == torch.bfloat16
-        _need(logits, torch.bfloat16 if bf16 else torch.float32, "logits", 2)
-        _shape(logits, (logits.shape[0], self.num_experts), "logits")
+        if logits.dim() != 2:
+            _need(logits, logits.dtype, "logits", 2)
+        _row(logits, torch.bfloat16 if bf16 else torch.float32, (logits.shape[0], self.num_experts), "logits")
         return int(bf16)
 
     def route(self, logits: torch.Tensor, router: Router, bias: Optional[torch.Tensor] = None,
@@ -792,21 +801,22 @@ class Buffer:
         balancing loss.  Experts on ranks masked in the mask buffer, and those whose logit is -inf, are
         not chosen."""
         bf16 = self._logits(logits)
-        T, K = logits.shape[0], router.num_topk
+        T, K, E = logits.shape[0], router.num_topk, self.num_experts
         if bias is not None:
-            _row(bias, torch.float32, (self.num_experts,), "bias")
-        dev = _here(logits, bias, self._mask)
-        rule, d = router._raw(), self._dims(T, 8, K)
-        idx = torch.empty(T, max(K, 0), dtype=torch.int64, device=logits.device)
-        weights = torch.empty(T, max(K, 0), dtype=torch.float32, device=logits.device)
+            _row(bias, torch.float32, (E,), "bias")
+        dev, at, f32 = _here(logits, bias, self._mask), logits.device, torch.float32
+        d = (T, 8, K, E, self.num_ranks, 1)
+        idx = torch.empty(T, max(K, 0), dtype=torch.int64, device=at)
+        weights = torch.empty(T, max(K, 0), dtype=f32, device=at)
         sums, work, size = None, None, 0
         if score_sums:
-            sums = torch.empty(self.num_experts, dtype=torch.float32, device=logits.device)
-            size = abi.lib().ep_route_workspace(ctypes.byref(d))
-            work = torch.empty(size, dtype=torch.uint8, device=logits.device)
-        at = abi.address
-        abi.check(abi.lib().ep_route(ctypes.byref(d), ctypes.byref(rule), at(logits), bf16, at(bias), at(self._mask),
-                                     at(idx), at(weights), at(sums), at(work), size, abi.raw_stream(dev)), "ep_route")
+            sums = torch.empty(E, dtype=f32, device=at)
+            size = _workspace("ep_route_workspace", d)
+            work = torch.empty(size, dtype=torch.uint8, device=at)
+        ptr = abi.address
+        abi.check(abi.lib().ep_route(ctypes.byref(abi.Dims(*d)), router._raw, logits.data_ptr(), bf16, ptr(bias),
+                                     ptr(self._mask), idx.data_ptr(), weights.data_ptr(), ptr(sums), ptr(work), size,
+                                     abi.raw_stream(dev)), "ep_route")
         return idx, weights, sums
 
     def route_backward(self, dtopk_weights: torch.Tensor, logits: torch.Tensor, topk_idx: torch.Tensor, router: Router,
@@ -821,11 +831,10 @@ class Buffer:
             _row(dscore_sums, torch.float32, (self.num_experts,), "dscore_sums")
         dev = _here(dtopk_weights, logits, topk_idx, dscore_sums)
         out = torch.empty_like(logits)
-        rule, d = router._raw(), self._dims(T, 8, K)
-        at = abi.address
-        abi.check(abi.lib().ep_route_backward(ctypes.byref(d), ctypes.byref(rule), at(dtopk_weights), at(logits), bf16,
-                                              at(topk_idx), at(dscore_sums), at(out), abi.raw_stream(dev)),
-                  "ep_route_backward")
+        abi.check(abi.lib().ep_route_backward(
+            ctypes.byref(abi.Dims(T, 8, K, self.num_experts, self.num_ranks, 1)), router._raw, dtopk_weights.data_ptr(),
+            logits.data_ptr(), bf16, topk_idx.data_ptr(), abi.address(dscore_sums), out.data_ptr(), abi.raw_stream(dev)),
+            "ep_route_backward")
         return out
 
     # --------------------------------------------------------- whole layer
@@ -856,17 +865,16 @@ class Buffer:
             s13 = s2 = None
             inter = self._expert_weights(w13, w2, H)
         dev = _here(x, w_router, bias, residual, w13, s13, w2, s2, self._mask)
-        rule, d = router._raw(), self._dims(T, H, K)
-        at, like = abi.address, dict(device=x.device)
+        ptr, at, d = abi.address, x.device, (T, H, K, E, self.num_ranks, 1)
         y = torch.empty_like(x)
-        idx = torch.empty(T, max(K, 0), dtype=torch.int64, **like)
-        weights = torch.empty(T, max(K, 0), dtype=torch.float32, **like)
-        size = abi.lib().ep_ll_moe_workspace(ctypes.byref(d), inter)
-        work = torch.empty(size, dtype=torch.uint8, **like)
+        idx = torch.empty(T, max(K, 0), dtype=torch.int64, device=at)
+        weights = torch.empty(T, max(K, 0), dtype=torch.float32, device=at)
+        size = _workspace("ep_ll_moe_workspace", d, inter)
+        work = torch.empty(size, dtype=torch.uint8, device=at)
         abi.check(abi.lib().ep_ll_moe(
-            ctypes.byref(d), inter, ctypes.byref(rule), at(x), at(w_router), int(f32), at(bias), at(self._mask), at(w13),
-            at(s13), at(w2), at(s2), at(residual), at(idx), at(weights), at(y), at(work), size, abi.raw_stream(dev)),
-            "ep_ll_moe")
+            ctypes.byref(abi.Dims(*d)), inter, router._raw, x.data_ptr(), w_router.data_ptr(), f32, ptr(bias),
+            ptr(self._mask), w13.data_ptr(), ptr(s13), w2.data_ptr(), ptr(s2), ptr(residual), idx.data_ptr(),
+            weights.data_ptr(), y.data_ptr(), work.data_ptr(), size, abi.raw_stream(dev)), "ep_ll_moe")
         return y, idx, weights
 
     # ------------------------------------------------------ load balancing

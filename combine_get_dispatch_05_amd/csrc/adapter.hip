@@ -123,6 +123,7 @@ __device__ __forceinline__ AdapterTile adapter_tile(const AdapterArgs &a, int b,
 // Few tokens are not sorted: block a of a launch takes adapter a (the last one those with none) and finds its
 // tokens, which it then goes through in tiles.
 constexpr int kScanTokens = kAdapterThreads, kScanAdapters = 128;
+template <int W>
 __device__ __forceinline__ int scan_tokens(const AdapterArgs &a, int mine, int *list, int *count_of)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = threadIdx.x;
@@ -134,7 +135,7 @@ __device__ __forceinline__ int scan_tokens(const AdapterArgs &a, int mine, int *
     __syncthreads();
     int before = 0, all = 0;
 #pragma unroll
-    for (int w = 0; w < kAdapterWaves; ++w) {
+    for (int w = 0; w < W; ++w) {
         before += w < wave ? count_of[w] : 0;
         all += count_of[w];
     }
@@ -150,7 +151,7 @@ __device__ __forceinline__ void each_tile(const AdapterArgs &a, F f)
 {
     __shared__ int list[SCAN ? kScanTokens : HEIGHT], count_of[kAdapterWaves];
     if constexpr (SCAN) {
-        const int all = scan_tokens(a, blockIdx.x, list, count_of);
+        const int all = scan_tokens<kAdapterWaves>(a, blockIdx.x, list, count_of);
         for (int m0 = 0; m0 < all; m0 += HEIGHT) {
             f(int(blockIdx.x), list + m0, all - m0 < HEIGHT ? all - m0 : HEIGHT);
             __syncthreads();
@@ -315,20 +316,20 @@ __global__ __launch_bounds__(kAdapterThreads) void adapter_shrink_kernel(Adapter
 // out rows of one tile, columns [n0, n1) in steps of 64 a wave.  A wave stages its own weights in LDS; its results turn
 // there, 16 tokens at a time, so that eight lanes read and write a whole line of a row.
 constexpr int kTurnRow = 68;  // floats: 16 rows of 64, four apart in the banks
-template <int RT, bool COL>
+template <int RT, bool COL, int W>
 struct ExpandLds {
     static constexpr int KS = (RT + 1) / 2;  // matrix steps of 32
     static constexpr int kHidden = kTokenTiles<RT> * 16 * KS * 32;  // bf16 values
-    char weights[kAdapterWaves][COL ? KS * 32 * 128 : (RT + 3) / 4 * 64 * kStepBytes];
+    char weights[W][COL ? KS * 32 * 128 : (RT + 3) / 4 * 64 * kStepBytes];
     union {  // h is in registers before the first results turn
         uint16_t hidden[kHidden];
-        float turn[kAdapterWaves][16 * kTurnRow];
+        float turn[W][16 * kTurnRow];
     };
 };
 
-template <int RT, int MT, bool COL, class MakeH>
-__device__ __forceinline__ void expand_tile(const AdapterArgs &a, int adapter, const int *tokens, int rows, ExpandLds<RT, COL> &lds,
-                                            int n0, int n1, MakeH make_h)
+template <int RT, int MT, bool COL, int W, class MakeH>
+__device__ __forceinline__ void expand_tile(const AdapterArgs &a, int adapter, const int *tokens, int rows,
+                                            ExpandLds<RT, COL, W> &lds, int n0, int n1, MakeH make_h)
 {
     constexpr int KS = (RT + 1) / 2;
     using PS = NearRowStage<64, kWave>;
@@ -386,7 +387,7 @@ __device__ __forceinline__ void expand_tile(const AdapterArgs &a, int adapter, c
         for (int s = 0; s < KS; ++s)
             h[m][s] = *reinterpret_cast<const bf16x8 *>(lds.hidden + (m * 16 + (lane & 15)) * (KS * 32) + s * 32 + g * 8);
     __syncthreads();
-    for (; n < n1; n += kAdapterWaves * 64) {
+    for (; n < n1; n += W * 64) {
         landed<0>();
         u32x4 now[MT][2];
 #pragma unroll
@@ -411,8 +412,8 @@ __device__ __forceinline__ void expand_tile(const AdapterArgs &a, int adapter, c
         }
         // read before the same LDS is loaded again
         asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
-        if (n + kAdapterWaves * 64 < n1)
-            send(n + kAdapterWaves * 64);
+        if (n + W * 64 < n1)
+            send(n + W * 64);
         if (adapted) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -449,7 +450,7 @@ template <int RT, bool COL, bool SCAN>
 __global__ __launch_bounds__(kAdapterThreads) void adapter_expand_kernel(AdapterArgs a, int columns)
 {
     constexpr int MT = kTokenTiles<RT>, KS = (RT + 1) / 2, RP = RT * 16;
-    __shared__ __attribute__((aligned(128))) ExpandLds<RT, COL> lds;
+    __shared__ __attribute__((aligned(128))) ExpandLds<RT, COL, kAdapterWaves> lds;
     const int n0 = int(blockIdx.y) * columns, n1 = n0 + columns < a.width ? n0 + columns : int(a.width);
     each_tile<SCAN, MT * 16>(a, [&](int adapter, const int *tokens, int rows) {
         // h: the parts' sum, scaled, in bf16; zeros past the rank and the rows
@@ -484,6 +485,85 @@ __global__ __launch_bounds__(kAdapterThreads) void adapter_expand_kernel(Adapter
         else
             expand_tile<RT, MT, COL>(a, adapter, tokens, rows, lds, n0, n1, make_h);
     });
+}
+
+// --------------------------------------------------------------- few tokens
+
+// Both products in one launch: each block makes h of its adapter's tokens itself, 16 at a time, its waves sharing
+// out K, and then its columns of out.
+constexpr int kFewWaves = 8, kFewTokens = 16, kFewRank = 64;
+
+// The waves' parts of h, [wave][token][RT * 16 ranks], for 16 / C tokens from `tokens` (C: stream.h).
+template <int RT, int C, bool TAIL>
+__device__ __forceinline__ void few_parts(const AdapterArgs &a, int adapter, const int *tokens, int rows, float *parts)
+{
+    constexpr int kRows = 16 / C, TILES = RT * C;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), i0 = (lane & 15) / C;
+    const int width = int(a.width), steps = (width + 63) / 64;
+    const char *w = a.p + int64_t(adapter) * a.r * width * 2, *prow[TILES];
+    const char *qrow[1] = {a.q + int64_t(tokens[i0 < rows ? i0 : rows - 1]) * width * 2};
+    const float *none[TILES] = {};
+#pragma unroll
+    for (int j = 0; j < TILES; ++j) {
+        const int row = j * kRows + i0;
+        prow[j] = w + int64_t(row < a.r ? row : a.r - 1) * width * 2;
+    }
+    f32x4 acc[TILES][1] = {};
+    // (a run of 14 steps, K = 7168, goes in two rounds)
+    stream<false, TAIL, (RT == 1 ? 7 : RT == 2 ? 5 : 3), C>(prow, none, qrow, steps * wave / kFewWaves,
+                                                           steps * (wave + 1) / kFewWaves, width * 2, lane, acc);
+#pragma unroll
+    for (int j = 0; j < TILES; ++j) {
+        float *to = parts + (wave * 16 + i0) * (RT * 16) + j * kRows;
+        if constexpr (C == 1)
+            *reinterpret_cast<f32x4 *>(to + (lane >> 4) * 4) = acc[j][0];
+        else
+            to[(lane >> 4) * 2 + (lane & 1)] = fold(acc[j][0], lane);
+    }
+}
+
+template <int RT, bool TAIL>
+__global__ __launch_bounds__(kFewWaves *kWave) void adapter_few_kernel(AdapterArgs a, const char *up, int N)
+{
+    constexpr int KS = (RT + 1) / 2;
+    __shared__ __attribute__((aligned(128))) ExpandLds<RT, false, kFewWaves> lds;
+    __shared__ __attribute__((aligned(16))) float parts[kFewWaves * 16 * RT * 16];
+    __shared__ int list[kFewTokens], count_of[kFewWaves];
+    const int adapter = blockIdx.x;
+    const int all = scan_tokens<kFewWaves>(a, adapter, list, count_of);
+    const int n0 = int(blockIdx.y) * kFewWaves * 64, n1 = n0 + kFewWaves * 64 < N ? n0 + kFewWaves * 64 : N;
+    AdapterArgs e = a;  // of the second product
+    e.p = up;
+    e.width = N;
+    for (int m0 = 0; m0 < all; m0 += 16) {
+        const int rows = all - m0 < 16 ? all - m0 : 16, *tokens = list + m0;
+        auto make_h = [&] {
+            if (adapter < a.L) {
+                if (rows <= 8)
+                    few_parts<RT, 2, TAIL>(a, adapter, tokens, rows, parts);
+                else
+                    few_parts<RT, 1, TAIL>(a, adapter, tokens, rows, parts);
+            }
+            __syncthreads();
+            for (int i = threadIdx.x; i < 16 * KS * 8; i += kFewWaves * kWave) {
+                const int m = i / (KS * 8), k = i % (KS * 8) * 4;
+                f32x4 v = {};
+                if (m < rows && k < a.r && adapter < a.L) {
+#pragma unroll
+                    for (int w = 0; w < kFewWaves; ++w)
+                        v += *reinterpret_cast<const f32x4 *>(parts + (w * 16 + m) * (RT * 16) + k);
+                    v *= a.scales[adapter];
+                }
+                const uint2 b = pack4(v);
+                *reinterpret_cast<uint2 *>(lds.hidden + m * KS * 32 + k) = b;
+                if (a.hidden != nullptr && blockIdx.y == 0 && m < rows && k < a.r)
+                    *reinterpret_cast<uint2 *>(a.hidden + int64_t(tokens[m]) * a.r + k) = b;
+            }
+            __syncthreads();
+        };
+        expand_tile<RT, 1, false>(e, adapter, tokens, rows, lds, n0, n1, make_h);
+        __syncthreads();
+    }
 }
 
 // --------------------------------------------------------- adapters' gradients
@@ -627,6 +707,17 @@ int shrink_splits(int64_t T, int L, int r, int width)
     return int(n < 1 ? 1 : n < most ? n : most);
 }
 
+// One launch for few tokens, as long as every block that makes h again has a compute unit to itself and
+// little to read: 8 tokens, K = 7168, rank 16, a call 10.8 us against 13.4 in two launches (the host's time); rank 64 27.8
+// in two, 36.9 in one.
+bool few(const AdapterShape &s)
+{
+    const int64_t runs = (s.N + kFewWaves * 64 - 1) / (kFewWaves * 64);
+    const int64_t groups = s.L + 1 < s.T ? s.L + 1 : s.T;
+    return s.T <= kFewTokens && s.L < kScanAdapters && s.r <= kFewRank && int64_t(s.r) * s.K <= (1 << 17) &&
+           groups * runs <= kCard;
+}
+
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 struct AdapterWork {
@@ -744,6 +835,21 @@ hipError_t launch_adapter(const AdapterShape &s, const void *x, const void *down
     if (log_enabled())
         log_launch("adapter_product: T=%d K=%d N=%d r=%d L=%d splits=%d", s.T, s.K, s.N, s.r, s.L,
                    shrink_splits(s.T, s.L, s.r, s.K));
+    if (few(s)) {
+        a.q = static_cast<const char *>(x);
+        a.p = static_cast<const char *>(down);
+        a.width = s.K;
+        a.base = static_cast<const uint16_t *>(base);
+        a.out = static_cast<uint16_t *>(out);
+        a.hidden = static_cast<uint16_t *>(hidden);
+        return by_rank(s.r, [&](auto rt) {
+            constexpr int RT = decltype(rt)::value < 4 ? decltype(rt)::value : 4;
+            hipLaunchKernelGGL((s.K % 64 != 0 ? adapter_few_kernel<RT, true> : adapter_few_kernel<RT, false>),
+                               dim3(s.L + 1, (s.N + kFewWaves * 64 - 1) / (kFewWaves * 64)), dim3(kFewWaves * kWave), 0, stream, a,
+                               static_cast<const char *>(up), s.N);
+            return hipGetLastError();
+        });
+    }
     hipError_t e = scans(s.T, s.L) ? hipSuccess : group_tokens(a, stream);
     if (e == hipSuccess)
         e = shrink<false>(a, x, down, s.K, stream);

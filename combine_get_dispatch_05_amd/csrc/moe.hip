@@ -119,6 +119,20 @@ __global__ __launch_bounds__(256) void moe_logits_tile_kernel(const u32x4 *x, co
             sums[0][i][j] + sums[1][i][j] + sums[2][i][j] + sums[3][i][j];
 }
 
+// The sum of the parts, all loads in flight; -inf past the last expert.
+__device__ __forceinline__ float logit_of(const MoeWork &work, int T, int E, int t, int e)
+{
+    double part[kLogitSplits] = {};
+#pragma unroll
+    for (int i = 0; i < kLogitSplits; ++i)
+        if (i < work.splits && e < E)
+            part[i] = work.logits[(int64_t(i) * T + t) * E + e];
+#pragma unroll
+    for (int i = 1; i < kLogitSplits; ++i)
+        part[0] += part[i];
+    return e < E ? float(part[0]) : -INFINITY;
+}
+
 // All tokens' choices, and the pairs by expert: bit t of an expert's mask is token t.
 template <int V>
 __global__ __launch_bounds__(1024) void moe_select_kernel(RouteRule r, int T, MoeWork work, int64_t *topk_idx, float *topk_weights)
@@ -144,15 +158,7 @@ __global__ __launch_bounds__(1024) void moe_select_kernel(RouteRule r, int T, Mo
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int e = j * 64 + lane;
-            double part[kLogitSplits] = {};  // all loads in flight
-#pragma unroll
-            for (int i = 0; i < kLogitSplits; ++i)
-                if (i < work.splits && e < r.experts)
-                    part[i] = work.logits[(int64_t(i) * T + t) * r.experts + e];
-#pragma unroll
-            for (int i = 1; i < kLogitSplits; ++i)
-                part[0] += part[i];
-            l[j] = e < r.experts ? float(part[0]) : -INFINITY;
+            l[j] = logit_of(work, T, r.experts, t, e);
             row[wave][e] = l[j];
         }
         const int e = route_row(r, l, bias, live, lane, scratch[wave], false, false, s, [&](int i) { return row[wave][i]; }, w);
@@ -270,8 +276,8 @@ __device__ __forceinline__ void gate_tile(const MoeArgs &a, const ActiveExpert &
     __syncthreads();
 }
 
-// One token (V > 0): each block chooses for itself, which takes less than a launch in between; block 0 writes the
-// choice down.
+// Few tokens (V > 0): each block chooses for itself, which takes less than a launch in between; the first block
+// writes the choice down.  One token:
 struct MoeChoice {
     RouteRule rule;
     int64_t *topk_idx;
@@ -288,7 +294,7 @@ __device__ __forceinline__ ActiveExpert choose_one(const MoeArgs &a, const MoeCh
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int e = j * 64 + lane;
-            l[j] = e < r.experts ? float(a.work.logits[e]) : -INFINITY;
+            l[j] = logit_of(a.work, 1, r.experts, 0, e);
             bias[j] = r.bias != nullptr && e < r.experts ? r.bias[e] : 0.0f;
         }
         const int e = route_row(r, l, bias, live_experts<V>(r, lane), lane, reinterpret_cast<double *>(lds), false, false, s,
@@ -309,14 +315,91 @@ __device__ __forceinline__ ActiveExpert choose_one(const MoeArgs &a, const MoeCh
 }
 
 // 32 columns a block, so that the tokens' loads serve twice the weights, where an expert's tokens are few.
-template <bool FP8, bool TAIL, int V>
+// Up to a token a wave (ONE: one): the same, and the blockIdx.y-th of the experts that some token chose.
+constexpr int kChooseTokens = kGateWaves;
+template <int V>
+__device__ __forceinline__ ActiveExpert choose_few(const MoeArgs &a, const MoeChoice &c, float *lds)
+{
+    __shared__ uint32_t mask[kWaveExperts], totals[kGateWaves];
+    __shared__ int16_t ids[kChooseTokens * kMaxTopk], start[kWaveExperts];
+    __shared__ float weights[kChooseTokens * kMaxTopk];
+    __shared__ ActiveExpert found;
+    const RouteRule &r = c.rule;
+    const int lane = threadIdx.x & 63, t = uniform(threadIdx.x >> 6), me = threadIdx.x;
+    static_assert(kGateWaves * kWave == kWaveExperts, "a thread an expert");
+    mask[me] = 0;
+    if (me == 0)
+        found = ActiveExpert{};
+    __syncthreads();
+    if (t < a.T) {
+        float l[V], s[V] = {}, bias[V], w;
+        auto logit = [&](int e) { return logit_of(a.work, a.T, r.experts, t, e); };
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int e = j * 64 + lane;
+            l[j] = logit(e);
+            bias[j] = r.bias != nullptr && e < r.experts ? r.bias[e] : 0.0f;
+        }
+        double *scratch = reinterpret_cast<double *>(lds) + t * V * 64;
+        const int e = route_row(r, l, bias, live_experts<V>(r, lane), lane, scratch, false, false, s, logit, w);
+        if (lane < r.topk) {
+            ids[t * r.topk + lane] = int16_t(e);
+            weights[t * r.topk + lane] = w;
+            if (e >= 0)
+                atomicOr(&mask[e], 1u << t);
+        }
+    }
+    __syncthreads();
+    const uint32_t n = __popc(mask[me]), own = n << 16 | (n > 0);
+    uint32_t before = wave_scan(own);
+    if (lane == 63)
+        totals[t] = before;
+    __syncthreads();
+    before -= own;
+    uint32_t all = 0;
+#pragma unroll
+    for (int w = 0; w < kGateWaves; ++w) {
+        before += w < t ? totals[w] : 0;
+        all += totals[w];
+    }
+    const ActiveExpert mine{me, int(before >> 16), int(n), 0, mask[me]};
+    if (n > 0 && (before & 0xffff) == blockIdx.y)
+        found = mine;
+    if (blockIdx.x == 0 && blockIdx.y == 0) {  // the records, for the next launch and the caller
+        start[me] = int16_t(before >> 16);
+        if (n > 0)
+            a.work.active[before & 0xffff] = mine;
+        for (int i = int(all & 0xffff) + me; i < int(gridDim.y); i += kGateWaves * kWave)
+            a.work.active[i] = ActiveExpert{};
+        __syncthreads();
+        for (int i = me; i < a.T * r.topk; i += kGateWaves * kWave) {
+            const int e = ids[i];
+            c.topk_idx[i] = e;
+            c.topk_weights[i] = weights[i];
+            if (e >= 0)
+                a.work.pair_weight[start[e] + __popc(mask[e] & ((1u << i / r.topk) - 1))] = weights[i];
+        }
+    }
+    __syncthreads();
+    ActiveExpert x = found;
+    x.expert = uniform(x.expert);
+    x.start = uniform(x.start);
+    x.count = uniform(x.count);
+    return x;
+}
+
+template <bool FP8, bool TAIL, int V, bool ONE>
 __global__ __launch_bounds__(kGateWaves *kWave) void moe_gate_kernel(MoeArgs a, MoeChoice c)
 {
     __shared__ __attribute__((aligned(16))) float sums[kGateWaves * kGateSums];
     constexpr int G = 2;
     const int n0 = blockIdx.x * 16 * G;
     if constexpr (V > 0) {
-        const ActiveExpert x = choose_one<V>(a, c, sums);
+        ActiveExpert x;
+        if constexpr (ONE)
+            x = choose_one<V>(a, c, sums);
+        else
+            x = choose_few<V>(a, c, sums);
         if (x.count > 0)
             gate_tile<FP8, TAIL, G, 2, 1>(a, x, n0, 0, sums);
         return;
@@ -504,7 +587,7 @@ hipError_t launch_moe(const RouteRule &rule, const MoeCall &c, hipStream_t strea
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    if (c.T > 1) {
+    if (c.T > kChooseTokens) {
         auto select = [&](auto kernel) {
             hipLaunchKernelGGL(kernel, dim3(1), dim3(1024), 0, stream, rule, c.T, a.work, c.topk_idx, c.topk_weights);
         };
@@ -531,23 +614,30 @@ hipError_t launch_moe(const RouteRule &rule, const MoeCall &c, hipStream_t strea
     auto gate = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, dim3((c.I + 31) / 32, most), dim3(kGateWaves * kWave), 0, stream, a, choice);
     };
-    auto gates = [&](auto experts) {
+    auto gates = [&](auto experts, auto one) {
         constexpr int V = decltype(experts)::value;
+        constexpr bool ONE = decltype(one)::value;
         if (fp8)
-            gate(moe_gate_kernel<true, false, V>);
+            gate(moe_gate_kernel<true, false, V, ONE>);
         else if (a.kbytes % kStepBytes == 0)
-            gate(moe_gate_kernel<false, false, V>);
+            gate(moe_gate_kernel<false, false, V, ONE>);
         else
-            gate(moe_gate_kernel<false, true, V>);
+            gate(moe_gate_kernel<false, true, V, ONE>);
     };
-    if (c.T > 1)
-        gates(std::integral_constant<int, 0>());
-    else if (E <= 64)
-        gates(std::integral_constant<int, 1>());
-    else if (E <= 256)
-        gates(std::integral_constant<int, 4>());
+    auto by_experts = [&](auto one) {
+        if (E <= 64)
+            gates(std::integral_constant<int, 1>(), one);
+        else if (E <= 256)
+            gates(std::integral_constant<int, 4>(), one);
+        else
+            gates(std::integral_constant<int, 8>(), one);
+    };
+    if (c.T > kChooseTokens)
+        gates(std::integral_constant<int, 0>(), std::false_type());
+    else if (c.T > 1)
+        by_experts(std::false_type());
     else
-        gates(std::integral_constant<int, 8>());
+        by_experts(std::true_type());
     e = hipGetLastError();
     if (e != hipSuccess)
         return e;

@@ -81,4 +81,4 @@ def test_binding_refuses_before_the_library():
     with pytest.raises(ValueError, match="logits must"):
         buf.route(torch.zeros((4, 8)), r)  # not on the device
     with pytest.raises(ValueError, match="score must be"):
-        epm.Router(2, score="tanh")._raw()
+        epm.Router(2, score="tanh")
