@@ -187,14 +187,14 @@ def adapter_product(x: torch.Tensor, adapter_ids: torch.Tensor, down: torch.Tens
     """Low-rank adapters of many requests beside a shared projection: out[t] = base[t] + scales[a]
     (x[t] down_a^T) up_a^T with a = adapter_ids[t] (int64 [T]; outside [0, L): no adapter).  x [T, K] and
     base [T, N] (the projection's output; None: zeros) bf16, down [L, r, K], up [L, N, r] bf16 with r up to
-    128, scales [L] fp32.  Returns (out [T, N] bf16, hidden): hidden [T, r] bf16 is what
-    adapter_product_backward takes, None without save."""
+    128, scales [L] fp32.  Returns (out [T, N] bf16, hidden): hidden [2, T, r] bf16, the rows' r values as
+    sums of two, is what adapter_product_backward takes, None without save."""
     d = T, K, N, r, L = _adapter_args(x, adapter_ids, down, up, scales)
     if base is not None:
         _row(base, torch.bfloat16, (T, N), "base")
     dev, at = _here(x, adapter_ids, down, up, scales, base), x.device
     out = torch.empty(T, N, dtype=torch.bfloat16, device=at)
-    hidden = torch.empty(T, r, dtype=torch.bfloat16, device=at) if save else None
+    hidden = torch.empty(2, T, r, dtype=torch.bfloat16, device=at) if save else None
     size = _adapter_workspace(*d, 0)
     work = torch.empty(size, dtype=torch.uint8, device=at)
     abi.check(abi.lib().ep_adapter_product(
@@ -212,7 +212,7 @@ def adapter_product_backward(dy: torch.Tensor, x: torch.Tensor, adapter_ids: tor
     an adapter without tokens has zeros."""
     d = T, K, N, r, L = _adapter_args(x, adapter_ids, down, up, scales)
     _row(dy, torch.bfloat16, (T, N), "dy")
-    _row(hidden, torch.bfloat16, (T, r), "hidden")
+    _row(hidden, torch.bfloat16, (2, T, r), "hidden")
     if dx_base is not None:
         _row(dx_base, torch.bfloat16, (T, K), "dx_base")
     dev = _here(dy, x, adapter_ids, down, up, scales, hidden, dx_base)

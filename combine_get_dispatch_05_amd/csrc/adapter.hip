@@ -27,7 +27,7 @@ struct AdapterArgs {
     int splits;
     const uint16_t *base;  // nullable
     uint16_t *out;
-    uint16_t *hidden;  // nullable [T][r]
+    uint16_t *hidden;  // nullable [2][T][r]: h in bf16, and what that rounding lost in bf16 again
 };
 
 // ---------------------------------------------------------------- grouping
@@ -313,6 +313,15 @@ __global__ __launch_bounds__(kAdapterThreads) void adapter_shrink_kernel(Adapter
 
 // ------------------------------------------------------------------ expand
 
+// Four values of a token's h for the gradients, which are sums of its products: one rounding there would be as much
+// as the gradients' own.
+__device__ __forceinline__ void keep_hidden(const AdapterArgs &a, int token, int k, const f32x4 &v, const uint2 &b)
+{
+    uint16_t *to = a.hidden + int64_t(token) * a.r + k;
+    *reinterpret_cast<uint2 *>(to) = b;
+    *reinterpret_cast<uint2 *>(to + int64_t(a.T) * a.r) = pack4(lost(v, b));
+}
+
 // out rows of one tile, columns [n0, n1) in steps of 64 a wave.  A wave stages its own weights in LDS; its results turn
 // there, 16 tokens at a time, so that eight lanes read and write a whole line of a row.
 constexpr int kTurnRow = 68;  // floats: 16 rows of 64, four apart in the banks
@@ -476,7 +485,7 @@ __global__ __launch_bounds__(kAdapterThreads) void adapter_expand_kernel(Adapter
                 const uint2 b = pack4(v);
                 *reinterpret_cast<uint2 *>(lds.hidden + m * KS * 32 + k) = b;
                 if (a.hidden != nullptr && blockIdx.y == 0 && m < rows && k < a.r)
-                    *reinterpret_cast<uint2 *>(a.hidden + int64_t(tokens[m]) * a.r + k) = b;
+                    keep_hidden(a, tokens[m], k, v, b);
             }
             __syncthreads();
         };
@@ -557,7 +566,7 @@ __global__ __launch_bounds__(kFewWaves *kWave) void adapter_few_kernel(AdapterAr
                 const uint2 b = pack4(v);
                 *reinterpret_cast<uint2 *>(lds.hidden + m * KS * 32 + k) = b;
                 if (a.hidden != nullptr && blockIdx.y == 0 && m < rows && k < a.r)
-                    *reinterpret_cast<uint2 *>(a.hidden + int64_t(tokens[m]) * a.r + k) = b;
+                    keep_hidden(a, tokens[m], k, v, b);
             }
             __syncthreads();
         };
@@ -571,7 +580,7 @@ __global__ __launch_bounds__(kFewWaves *kWave) void adapter_few_kernel(AdapterAr
 struct AdapterGradArgs {
     AdapterArgs a;
     const char *wide[2];    // x (of K), dy (of N)
-    const char *narrow[2];  // dh, h: bf16 [T][r]
+    const char *narrow[2];  // dh, h: [2][T][r], sums of two bf16 values
     uint16_t *out[2];       // dA [L][r][K], dB [L][N][r]
     int width[2];
     int blocks;             // of the first
@@ -581,7 +590,7 @@ struct AdapterGradArgs {
 // step, both operands out of LDS transposed, the next step sent off as soon as this one is in
 // registers; the waves' sums meet in LDS.
 template <int RT>
-constexpr int kGradStage = 64 * 128 + 64 * RT * 32;
+constexpr int kGradStage = 64 * 128 + 2 * 64 * RT * 32;
 template <int RT, bool DOWN>
 __device__ __forceinline__ void adapter_grad(const AdapterGradArgs &g, int block, char *lds)
 {
@@ -604,9 +613,12 @@ __device__ __forceinline__ void adapter_grad(const AdapterGradArgs &g, int block
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
             const int at = j * kWave + lane, i = at / CH, c = at % CH, t = __shfl(mine, i);
-            load_lds16(t0 + i < count && c * 8 < a.r ? narrow + (int64_t(t) * a.r + c * 8) * 2
-                                                     : reinterpret_cast<const char *>(kZero16),
-                       small + j * kWave * 16);
+            const char *p = narrow + (int64_t(t) * a.r + c * 8) * 2;
+            const bool is = t0 + i < count && c * 8 < a.r;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                load_lds16(is ? p + u * int64_t(a.T) * a.r * 2 : reinterpret_cast<const char *>(kZero16),
+                           small + (u * CH + j) * kWave * 16);
         }
     };
     auto tokens = [&](int t0) { return t0 + lane < count ? a.order[from + t0 + lane] : 0; };
@@ -618,7 +630,7 @@ __device__ __forceinline__ void adapter_grad(const AdapterGradArgs &g, int block
     int next = tokens(t0 + kRound);
     for (; t0 < count; t0 += kRound) {
         landed<0>();
-        bf16x8 w[4][2], v[RT][2];
+        bf16x8 w[4][2], v[RT][2][2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
 #pragma unroll
@@ -627,7 +639,10 @@ __device__ __forceinline__ void adapter_grad(const AdapterGradArgs &g, int block
                     own, 128, s * 32, [&](int q) { return DOWN ? (i >> 1) * 32 + q * 8 + (i & 1) * 4 : i * 16 + q * 4; }, lane);
 #pragma unroll
             for (int j = 0; j < RT; ++j)
-                v[j][s] = transposed(small, RT * 32, s * 32, [&](int q) { return j * 16 + q * 4; }, lane);
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    v[j][s][u] = transposed(small + u * CH * kWave * 16, RT * 32, s * 32, [&](int q) { return j * 16 + q * 4; },
+                                            lane);
         }
         // read before the same LDS is loaded again
         asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
@@ -641,7 +656,10 @@ __device__ __forceinline__ void adapter_grad(const AdapterGradArgs &g, int block
             for (int j = 0; j < RT; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    acc[i][j] = DOWN ? mfma_bf16(w[i][s], v[j][s], acc[i][j]) : mfma_bf16(v[j][s], w[i][s], acc[i][j]);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        acc[i][j] = DOWN ? mfma_bf16(w[i][s], v[j][s][u], acc[i][j])
+                                         : mfma_bf16(v[j][s][u], w[i][s], acc[i][j]);
     }
     f32x4 *sums = reinterpret_cast<f32x4 *>(lds);
     __syncthreads();
@@ -736,7 +754,7 @@ size_t adapter_layout(const AdapterShape &s, bool back, char *base, AdapterWork 
     AdapterWork m;
     m.offsets = reinterpret_cast<int32_t *>(take(size_t(s.L + 2) * 4));
     m.order = reinterpret_cast<int32_t *>(take(size_t(s.T) * 4));
-    m.dh = reinterpret_cast<uint16_t *>(take(back ? size_t(s.T) * s.r * 2 : 0));
+    m.dh = reinterpret_cast<uint16_t *>(take(back ? size_t(s.T) * s.r * 4 : 0));
     const size_t splits = s.T > 0 ? shrink_splits(s.T, s.L, s.r, back ? s.N : s.K) : 0;
     m.parts = reinterpret_cast<float *>(take(splits * size_t(s.T) * rank_tiles(s.r) * 64));
     if (w != nullptr)

@@ -27,20 +27,29 @@ __device__ __forceinline__ int token_of(uint64_t tokens, int i)
 
 // K steps that a wave keeps in flight: as many as fit some 100 registers, at most four (a run's length is
 // rounded up to them).
-constexpr int ahead(bool fp8, int C, int RT, int MT)
+constexpr int ahead(bool fp8, int C, int RT, int MT, int planes = 1)
 {
-    const int n = 100 / (4 * (RT * 2 / C + MT * (fp8 ? 4 : 2) / C));
+    const int n = 100 / (4 * (RT * 2 / C + MT * planes * (fp8 ? 4 : 2) / C));
     return n < 2 ? 2 : n < 4 ? n : 4;
 }
 
 constexpr int kLogitSplits = 8;  // at most
+
+// The activation between the products is the matrix instruction's operand.  One rounding to bf16 makes the result's
+// error against 64 bits 1.4 times what its own rounding is (2.4e-3 of the norm instead of 1.7e-3).  Beside bf16
+// weights it is kept as a sum of two bf16 values, which costs 0.7 us of 22 (one token, eight experts of 768 x 2048).
+// Beside FP8 weights, whose codes are off by up to 2^-4, it is rounded once: the second load of
+// tokens would take 45 us of 470 (32 tokens, 64 experts of 2048 x 7168).
+template <bool FP8>
+constexpr int kActPlanes = FP8 ? 1 : 2;
 
 struct MoeWork {
     double *logits;        // [splits][T][E] parts
     int splits;
     ActiveExpert *active;  // [min(P, E)], those that tokens chose first, the others with no pairs
     float *pair_weight;    // [P], by (expert, token)
-    uint16_t *act;         // [P][I]
+    uint16_t *act;         // [planes][P][I]: bf16, and (kActPlanes) what that rounding lost in bf16 again
+    int64_t act_plane;     // bytes of one
 };
 
 // ----------------------------------------------------------------- router
@@ -270,8 +279,14 @@ __device__ __forceinline__ void gate_tile(const MoeArgs &a, const ActiveExpert &
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             v[k] = gate[k] * sigmoidf(gate[k]) * up[k];
-        if (m0 + i < x.count && n0 + c < a.I)
-            *reinterpret_cast<uint2 *>(a.work.act + int64_t(x.start + m0 + i) * a.I + n0 + c) = pack4(v);
+        if (m0 + i < x.count && n0 + c < a.I) {
+            const int64_t at = int64_t(x.start + m0 + i) * a.I + n0 + c;
+            const uint2 b = pack4(v);
+            *reinterpret_cast<uint2 *>(a.work.act + at) = b;
+            if constexpr (kActPlanes<FP8> == 2) {
+                *reinterpret_cast<uint2 *>(a.work.act + a.work.act_plane / 2 + at) = pack4(lost(v, b));
+            }
+        }
     }
     __syncthreads();
 }
@@ -447,7 +462,9 @@ __device__ __forceinline__ void down_piece(const MoeArgs &a, const ActiveExpert 
         weight[m] = a.work.pair_weight[at];
     }
     f32x4 acc[RT][MT] = {};
-    stream<FP8, TAIL, ahead(FP8, C, RT, MT), C>(prow, scale, qrow, s0, s1, a.kbytes, lane, acc);
+    constexpr int PLANES = kActPlanes<FP8>;
+    stream<FP8, TAIL, ahead(FP8, C, RT, MT, PLANES), C, PLANES>(prow, scale, qrow, s0, s1, a.kbytes, lane, acc,
+                                                                a.work.act_plane);
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -557,7 +574,8 @@ size_t moe_layout(int T, int E, int K, int I, char *base, MoeWork *w)
     m.logits = reinterpret_cast<double *>(take(size_t(m.splits) * T * E * 8));
     m.active = reinterpret_cast<ActiveExpert *>(take(n * sizeof(ActiveExpert)));
     m.pair_weight = reinterpret_cast<float *>(take(P * 4));
-    m.act = reinterpret_cast<uint16_t *>(take(P * I * 2));
+    m.act_plane = int64_t(up256(P * I * 2));
+    m.act = reinterpret_cast<uint16_t *>(take(2 * m.act_plane));
     if (w != nullptr)
         *w = m;
     return at;

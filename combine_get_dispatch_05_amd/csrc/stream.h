@@ -12,6 +12,17 @@
 
 namespace ep {
 
+// What rounding v to the bf16 values b lost (nothing where those are not finite).
+__device__ __forceinline__ f32x4 lost(const f32x4 &v, const uint2 &b)
+{
+    const f32x4 kept = {bf16_lo(b.x), bf16_hi(b.x), bf16_lo(b.y), bf16_hi(b.y)};
+    f32x4 rest;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        rest[k] = fabsf(kept[k]) < INFINITY ? v[k] - kept[k] : 0.0f;
+    return rest;
+}
+
 __device__ __forceinline__ i32x4 load16(const char *p) { return *reinterpret_cast<const i32x4 *>(p); }
 
 // One K step, 128 bytes a weight row, of a tile of 16 / C weight rows.
@@ -78,16 +89,17 @@ __device__ __forceinline__ bf16x8 widen8(int lo, int hi)
     return v;
 }
 
-// acc[r][m] += weight rows of tile r times token tile m over steps [s0, s1).
-template <bool FP8, bool TAIL, int AHEAD, int C, int RT, int MT>
+// acc[r][m] += weight rows of tile r times token tile m over steps [s0, s1).  PLANES: the token rows are a sum of that many
+// bf16 rows, `plane` bytes apart.
+template <bool FP8, bool TAIL, int AHEAD, int C, int PLANES, int RT, int MT>
 __device__ __forceinline__ void stream_run(const char *const (&prow)[RT], const float *const (&scale)[RT],
-                                           const char *const (&qrow)[MT], int s0, int s1, int kbytes, int lane,
+                                           const char *const (&qrow)[MT], int64_t plane, int s0, int s1, int kbytes, int lane,
                                            f32x4 (&acc)[RT][MT])
 {
     if (s0 >= s1)
         return;
     WeightStep<C> p[AHEAD][RT];
-    TokenStep<FP8, C> q[AHEAD][MT];
+    TokenStep<FP8, C> q[AHEAD][MT][PLANES];
     float scales[AHEAD][RT];
     auto load = [&](int d, int s) {
         s = s < s1 ? s : s1 - 1;  // (past the end: loaded again, not used)
@@ -100,7 +112,9 @@ __device__ __forceinline__ void stream_run(const char *const (&prow)[RT], const 
         }
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-            load_step<TAIL>(q[d][m], qrow[m], at, lane, kbytes);
+#pragma unroll
+            for (int u = 0; u < PLANES; ++u)
+                load_step<TAIL>(q[d][m][u], qrow[m] + u * plane, at, lane, kbytes);
     };
     auto compute = [&](int d, int s) {
         if (s >= s1)
@@ -116,7 +130,9 @@ __device__ __forceinline__ void stream_run(const char *const (&prow)[RT], const 
                         const bf16x8 w = widen8(p[d][r].c[h][2 * i], p[d][r].c[h][2 * i + 1]);
 #pragma unroll
                         for (int m = 0; m < MT; ++m)
-                            part[m] = mfma_bf16(w, __builtin_bit_cast(bf16x8, q[d][m].c[2 * h + i]), part[m]);
+#pragma unroll
+                            for (int u = 0; u < PLANES; ++u)
+                                part[m] = mfma_bf16(w, __builtin_bit_cast(bf16x8, q[d][m][u].c[2 * h + i]), part[m]);
                     }
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
@@ -126,8 +142,10 @@ __device__ __forceinline__ void stream_run(const char *const (&prow)[RT], const 
                 for (int h = 0; h < 2 / C; ++h)
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
-                        acc[r][m] = mfma_bf16(__builtin_bit_cast(bf16x8, p[d][r].c[h]),
-                                              __builtin_bit_cast(bf16x8, q[d][m].c[h]), acc[r][m]);
+#pragma unroll
+                        for (int u = 0; u < PLANES; ++u)
+                            acc[r][m] = mfma_bf16(__builtin_bit_cast(bf16x8, p[d][r].c[h]),
+                                                  __builtin_bit_cast(bf16x8, q[d][m][u].c[h]), acc[r][m]);
             }
         }
     };
@@ -148,14 +166,15 @@ __device__ __forceinline__ void stream_run(const char *const (&prow)[RT], const 
 }
 
 // A run is rounded up to the steps in flight, so a short one has fewer.
-template <bool FP8, bool TAIL, int AHEAD, int C, int RT, int MT>
+template <bool FP8, bool TAIL, int AHEAD, int C, int PLANES = 1, int RT, int MT>
 __device__ __forceinline__ void stream(const char *const (&prow)[RT], const float *const (&scale)[RT],
-                                       const char *const (&qrow)[MT], int s0, int s1, int kbytes, int lane, f32x4 (&acc)[RT][MT])
+                                       const char *const (&qrow)[MT], int s0, int s1, int kbytes, int lane, f32x4 (&acc)[RT][MT],
+                                       int64_t plane = 0)
 {
     if (AHEAD > 2 && s1 - s0 <= 2)
-        stream_run<FP8, TAIL, 2, C>(prow, scale, qrow, s0, s1, kbytes, lane, acc);
+        stream_run<FP8, TAIL, 2, C, PLANES>(prow, scale, qrow, plane, s0, s1, kbytes, lane, acc);
     else
-        stream_run<FP8, TAIL, AHEAD, C>(prow, scale, qrow, s0, s1, kbytes, lane, acc);
+        stream_run<FP8, TAIL, AHEAD, C, PLANES>(prow, scale, qrow, plane, s0, s1, kbytes, lane, acc);
 }
 
 }  // namespace ep

@@ -553,12 +553,13 @@ int ep_route_backward(const ep_dims *dims, const ep_router *router, const float 
  *   logits[t][e] = fp32(x[t] . w_router[e]), summed in 64 bits
  *   topk_idx, topk_weights as ep_route gives them for these logits
  *   y[t] = bf16_rne( residual[t] + sum over its experts, fp32, of weight * (act W2^T) ), act as for
- *          ep_ll_expert_ffn, rounded to bf16 between the products
+ *          ep_ll_expert_ffn, kept to 2^-16 of itself between the products beside bf16 weights and
+ *          rounded to bf16 beside FP8 ones (an infinite W2 gives infinities or NaN)
  * x, residual (nullable), y [num_tokens][hidden] bf16; y may be the same memory as residual, not as x.
  * w_router [E][hidden] bf16, or fp32 with w_router_fp32 nonzero.  bias [E], rank_mask [R] nullable.
  * w13 [E][2 inter][hidden], w2 [E][hidden][inter]: bf16, or with w13_scale and w2_scale (both or neither)
  * FP8 codes and scales as for ep_ll_expert_ffn_fp8.  Beside FP8 weights too, x and
- * act stay bf16: every product is exact and summed in fp32, the scales applied once per 128 of K.
+ * act are bf16: every product is exact and summed in fp32, the scales applied once per 128 of K.
  * A token's experts do not depend on the batch it comes in.
  * num_tokens <= 64 and E <= 512 (EP_ERR_TOO_LARGE); hidden % 8 == 0 and inter % 8 == 0, with FP8
  * % 128 (EP_ERR_ALIGN).  workspace: ep_ll_moe_workspace() bytes, 256-byte aligned
@@ -574,11 +575,12 @@ int ep_ll_moe(const ep_dims *dims, int32_t inter, const ep_router *router, const
 /*
  * Low-rank adapters of many requests beside a shared projection (ep_fp8_product's, or any other): token t
  * uses adapter a = adapter_ids[t], none if that is outside [0, num_adapters).
- *   h[t] = bf16_rne( scales[a] * (x[t] down_a^T) ),  out[t] = bf16_rne( base[t] + h[t] up_a^T )
+ *   h[t] = scales[a] * (x[t] down_a^T),  out[t] = bf16_rne( base[t] + bf16_rne(h[t]) up_a^T )
  * with fp32 sums; a token without an adapter gets base[t] (zeros without a base).
  *   x [T][in] bf16, adapter_ids int64 [T], down [L][rank][in], up [L][out][rank] bf16, scales fp32 [L]
  *   base [T][out] bf16, nullable; out [T][out] may be the same memory as base
- *   hidden [T][rank] bf16, nullable: h, which the backward pass takes (zeros without an adapter)
+ *   hidden [2][T][rank] bf16, nullable: h, which the backward pass takes, as the sum of its bf16 value
+ *     and of what that rounding lost (zeros without an adapter)
  * in, out and rank % 8 == 0 (EP_ERR_ALIGN), rank <= 128, L <= 8192.  workspace: ep_adapter_workspace(dims, 0)
  * bytes, 256-byte aligned (EP_ERR_CAPACITY if workspace_bytes is less).  No host sync.
  */
@@ -596,8 +598,9 @@ int ep_adapter_product(const ep_adapter_dims *dims, const void *x, const int64_t
 
 /*
  * Gradients of ep_adapter_product given dy [T][out] bf16 (base's gradient is dy itself; scales are constants):
- *   dh[t] = bf16_rne( scales[a] * (dy[t] up_a) ),  dx[t] = bf16_rne( dx_base[t] + dh[t] down_a )
- *   ddown_a = bf16_rne( sum_t dh[t]^T x[t] ),  dup_a = bf16_rne( sum_t dy[t]^T h[t] ),  in a fixed order
+ *   dh[t] = scales[a] * (dy[t] up_a),  dx[t] = bf16_rne( dx_base[t] + bf16_rne(dh[t]) down_a )
+ *   ddown_a = bf16_rne( sum_t dh[t]^T x[t] ),  dup_a = bf16_rne( sum_t dy[t]^T h[t] ),  in a fixed order,
+ * h and dh there to 2^-16 of themselves (an infinite dy or x gives infinities or NaN)
  * dx_base [T][in] (nullable) is the projection's own gradient of x; dx may be the same memory.  ddown and
  * dup are overwritten whole (zeros for adapters without tokens).  hidden is ep_adapter_product's.
  * workspace: ep_adapter_workspace(dims, 1) bytes.  No host sync.

@@ -65,7 +65,7 @@ def test_workspace_holds_what_the_launches_write():
             tiles = T // height + min(ad + 1, T)
             steps = -(-(N if back else K) // 64)
             splits = max(1, min(512 // tiles, -(-steps // 4)))
-            assert n >= (ad + 2) * 4 + T * 4 + splits * T * padded * 4 + back * T * r * 2
+            assert n >= (ad + 2) * 4 + T * 4 + splits * T * padded * 4 + back * T * r * 4
 
 
 def test_binding_refuses_before_the_library():

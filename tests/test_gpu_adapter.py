@@ -68,12 +68,13 @@ def check(ids, x, down, up, scales, base, dy, dx_base):
     ro = base.double().clone() if base is not None else torch.zeros((T, N), **f64)
     rx = dx_base.double().clone() if dx_base is not None else torch.zeros((T, K), **f64)
     eo, ex = ro.abs() * U, rx.abs() * U
-    rh, eh = torch.zeros((T, r), **f64), torch.zeros((T, r), **f64)
+    rh, eh, es = (torch.zeros((T, r), **f64) for _ in range(3))
     for a in range(L):
         t = (ids == a).nonzero()[:, 0]
         c, A, B = scales[a].double(), down[a].double(), up[a].double()
         xa, ya = x[t].double(), dy[t].double()
         h, eh_ = c * (xa @ A.t()), c * (xa.abs() @ A.abs().t()) * (err(K) + 2 * U)
+        es[t] = eh_ * (1 + BF)
         eh_ = eh_ + BF * (h.abs() + eh_)
         rh[t], eh[t] = h, eh_
         ro[t] += h @ B.t()
@@ -82,10 +83,15 @@ def check(ids, x, down, up, scales, base, dy, dx_base):
         ed = ed + BF * (dh.abs() + ed)
         rx[t] += dh @ A
         ex[t] += (ed + err(r) * (dh.abs() + ed)) @ A.abs()
-        rd, ref = dh.t() @ xa, ya.t() @ hidden[t].double()  # (h as it was kept)
-        close(ddown[a], rd, rd.abs() * BF + (ed + err(len(t)) * (dh.abs() + ed)).t() @ xa.abs() * (1 + BF) + TINY, f"ddown {a}")
-        close(dup[a], ref, ref.abs() * BF + err(len(t)) * (ya.abs().t() @ hidden[t].double().abs()) + TINY, f"dup {a}")
-    close(hidden, rh, eh + TINY, "hidden")
+        kept = hidden[0, t].double() + hidden[1, t].double()
+        rd, ref = dh.t() @ xa, ya.t() @ kept
+        # (dh is kept to 2^-16 of itself there, hidden is as it was kept)
+        ek = c * (ya.abs() @ B.abs()) * (err(N) + 2 * U) + BF * BF * dh.abs()
+        close(ddown[a], rd, rd.abs() * BF + (ek + err(len(t)) * (dh.abs() + ek)).t() @ xa.abs() * (1 + BF) + TINY, f"ddown {a}")
+        close(dup[a], ref, ref.abs() * BF + err(len(t)) * (ya.abs().t() @ hidden[:, t].double().abs().sum(0)) + TINY, f"dup {a}")
+    close(hidden[0], rh, eh + TINY, "hidden")
+    # the two together are h to 2^-16 of it, besides its sums
+    close(hidden[0].double() + hidden[1].double(), rh, es + BF * BF * rh.abs() + TINY, "hidden as a sum")
     close(out, ro, ro.abs() * BF + eo * (1 + BF) + TINY, "out")
     close(dx, rx, rx.abs() * BF + ex * (1 + BF) + TINY, "dx")
     return out, hidden, dx, ddown, dup
@@ -158,7 +164,7 @@ def test_no_tokens_and_refusals():
     x, down, up, scales, base, dy, dxb = made(6, 64, 72, 16, 3)
     ids = torch.zeros(6, dtype=torch.int64, device="cuda")
     out, hidden = epm.adapter_product(x[:0], ids[:0], down, up, scales, base=base[:0], save=True)
-    assert out.shape == (0, 72) and hidden.shape == (0, 16)
+    assert out.shape == (0, 72) and hidden.shape == (2, 0, 16)
     dx, ddown, dup = epm.adapter_product_backward(dy[:0], x[:0], ids[:0], down, up, scales, hidden)
     assert dx.shape == (0, 64) and (ddown == 0).all() and (dup == 0).all()
     out, hidden = epm.adapter_product(x, ids, down, up, scales, save=True)
@@ -170,7 +176,7 @@ def test_no_tokens_and_refusals():
                 lambda: epm.adapter_product(x, ids, down, up, scales[:2]),
                 lambda: epm.adapter_product(x, ids, down, up, scales, base=x),
                 lambda: epm.adapter_product(x.t(), ids, down, up, scales),
-                lambda: back(x, x, ids, down, up, scales, hidden), lambda: back(dy, x, ids, down, up, scales, hidden[:3]),
+                lambda: back(x, x, ids, down, up, scales, hidden), lambda: back(dy, x, ids, down, up, scales, hidden[0]),
                 lambda: back(dy, x, ids, down, up, scales, hidden, dx_base=dy)):
         with pytest.raises(ValueError):
             bad()
@@ -225,7 +231,7 @@ def test_gradient_against_differences():
     dh = dh * scales.double()[ids][:, None]
     mags = [torch.bmm(dh[:, None, :], down.double()[ids].abs())[:, 0],
             torch.stack([(dh * m[:, None]).t() @ x.double().abs() for m in mine.t()]),
-            torch.stack([(dy.double().abs() * m[:, None]).t() @ hidden.double().abs() for m in mine.t()])]
+            torch.stack([(dy.double().abs() * m[:, None]).t() @ hidden[0].double().abs() for m in mine.t()])]
     for i, g in enumerate(grads):
         d = torch.randn(g.shape, generator=gen(30 + i), device="cuda", dtype=torch.float64)
         step = 1e-4

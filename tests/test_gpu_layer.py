@@ -1,8 +1,9 @@
 """The mixture-of-experts layer for a few tokens against its definition in 64 bits.
 
 Bounds, per element: sums of n terms 2 (n + 8) U of the summed magnitudes (matrix instructions need
-not round to nearest inside), the activation's rounding to bf16 half a step of 2^-8, and the
-result's.  The FP8 products are exact here (codes widened to bf16), so the same bounds hold."""
+not round to nearest inside), the activation's rounding (to bf16, half a step of 2^-8, beside FP8 weights; to the
+sum of two such values beside bf16 ones) and the result's.  The FP8 products are exact here (codes
+widened to bf16), so the same bounds hold."""
 
 from __future__ import annotations
 
@@ -66,7 +67,8 @@ def reference(x, wr, r, w13, w2, bias=None, residual=None, masked=()):
         g, u = gu[:, :I], gu[:, I:]
         s = torch.sigmoid(g)
         act = g * s * u
-        ea = 1.1 * mag[:, :I] * (u.abs() + mag[:, I:]) + (g * s).abs() * mag[:, I:] + act.abs() * (BF + 16 * U)
+        kept = BF if isinstance(w13, tuple) else BF * BF
+        ea = 1.1 * mag[:, :I] * (u.abs() + mag[:, I:]) + (g * s).abs() * mag[:, I:] + act.abs() * (kept + 16 * U)
         y.index_add_(0, t, p * (act @ b.t()))
         most = (act.abs() + ea) @ b.abs().t()
         err.index_add_(0, t, p * (ea @ b.abs().t() + most * (2 * (I + 8) * U + 200 * U)))
@@ -166,6 +168,23 @@ def test_experts_that_nobody_chose_may_hold_anything():
     w13[unused], w2[unused] = math.nan, math.inf
     again, _, _ = buf.low_latency_moe(x, wr, r, w13, w2)
     assert torch.equal(y, again)
+
+
+@pytest.mark.parametrize("T", [1, 5, 12])
+def test_an_activation_past_the_largest_number_is_infinite_and_alone(T):
+    x, wr, w13, w2 = made(T, 256, 64, 16, seed=8)
+    wr[:, 0] = 0
+    w13[:], w13[:, 0, 0], w13[:, 64, 0] = 0, 1, 1  # act is (x0 silu(x0), 0, 0, ..)
+    w2[:, :128, 0], w2[:, 128:, 0] = 1, -1
+    buf, r = epm.Buffer(1, 16), epm.Router(2, normalize=True)
+    x[:, 0] = 2.0 ** 10
+    one, idx, _ = buf.low_latency_moe(x, wr, r, w13, w2)
+    x[T - 1, 0] = 2.0 ** 70
+    y, again, _ = buf.low_latency_moe(x, wr, r, w13, w2)
+    assert torch.equal(idx, again) and torch.equal(y[:T - 1], one[:T - 1])
+    want = torch.full((256,), math.inf, device="cuda", dtype=torch.bfloat16)
+    want[128:] = -math.inf
+    assert torch.equal(y[T - 1], want)
 
 
 def test_refusals_and_no_tokens():
