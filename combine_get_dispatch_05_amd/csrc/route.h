@@ -4,7 +4,7 @@
 // Lane l holds experts l, 64 + l, ...; the chosen ones end in lanes 0 to K - 1.
 // What is chosen never depends on a rounding: the 32-bit keys decide only where the gaps between
 // them are larger than what they can be off by (the bits that hold the index, and with a
-// bias the rounding of the scores); a token with a smaller gap (a few in a hundred) is chosen
+// bias the rounding of the scores); a token with a smaller gap (4 of 1000 of normal logits) is chosen
 // again with keys of 64 bits.
 #pragma once
 
@@ -127,9 +127,11 @@ __device__ __forceinline__ void scores_of(bool soft, const float (&l)[V], T (&s)
             sum += s[j];
         }
         sum = wave_sum(sum);
+        // (a quotient of two roundings: one division a lane; without a score or with a NaN it is 0 or NaN times 0)
+        const T per = sum > T(0) ? T(1) / sum : sum;
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            s[j] = sum > T(0) ? s[j] / sum : sum != sum ? sum : T(0);
+            s[j] *= per;
     } else {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -271,16 +273,13 @@ __device__ __forceinline__ int pick(const float (&key)[V], int K, int lane, floa
     const int rounds = exact ? K : K + 1;
     uint32_t got = 0, next = 0;  // of lane k: the k-th, and the K + 1st
     for (int k = 0; k < rounds; ++k) {
-        const uint32_t m = wave_max(u[0]);
-        if (m == 0)
-            break;
-        got = lane == k ? m : got;
-        next = m;
-        const bool taken = u[0] == m;
+        next = wave_max(u[0]);
+        got = lane == k ? next : got;
+        const uint32_t taken = u[0] == next ? ~0u : 0u;
 #pragma unroll
         for (int j = 0; j + 1 < V; ++j)
-            u[j] = taken ? u[j + 1] : u[j];
-        u[V - 1] = taken ? 0u : u[V - 1];
+            u[j] = (u[j + 1] & taken) | (u[j] & ~taken);
+        u[V - 1] &= ~taken;
     }
     if (!exact) {
         // (with 64 slots the K + 1st has no lane; where fewer are left it is the last one of them)
