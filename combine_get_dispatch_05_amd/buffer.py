@@ -17,7 +17,7 @@ behind the C ABI.  Tensors must live on the current CUDA (HIP) device.
 from __future__ import annotations
 
 import ctypes
-from dataclasses import dataclass
+from dataclasses import dataclass, fields
 from functools import lru_cache
 from typing import Optional
 
@@ -159,14 +159,23 @@ def fp8_product(a, w) -> torch.Tensor:
     return out
 
 
+def _int32(n: int, name: str):
+    if not -(1 << 31) <= n < 1 << 31:  # (ctypes would wrap it)
+        raise ValueError(f"{name} must fit 32 bits, got {n}")
+
+
 # The small calls' host time counts: the library is asked once for each size.
 @lru_cache(maxsize=4096)
 def _workspace(name: str, dims, *rest) -> int:
+    for n in (*dims, *rest):
+        _int32(n, "a size")
     return getattr(abi.lib(), name)(ctypes.byref(abi.Dims(*dims)), *rest)
 
 
 @lru_cache(maxsize=4096)
 def _adapter_workspace(T: int, K: int, N: int, r: int, L: int, back: int) -> int:
+    for n in (T, K, N, r, L):
+        _int32(n, "a size")
     return abi.lib().ep_adapter_workspace(ctypes.byref(abi.AdapterDims(T, K, N, r, L)), back)
 
 
@@ -242,8 +251,13 @@ class Router:
     def __post_init__(self):
         if self.score not in ("softmax", "sigmoid"):
             raise ValueError(f"score must be softmax or sigmoid, got {self.score!r}")
+        for n in (self.num_topk, self.num_groups, self.topk_groups):
+            _int32(n, "a router's count")
         rule = abi.RouterRule(self.score == "sigmoid", self.num_groups, self.topk_groups, bool(self.normalize), self.scale)
         object.__setattr__(self, "_raw", ctypes.byref(rule))  # (which keeps it alive)
+
+    def __reduce__(self):  # (an address is neither copied nor pickled)
+        return type(self), tuple(getattr(self, f.name) for f in fields(self))
 
 
 @dataclass
@@ -790,6 +804,8 @@ class Buffer:
         if logits.dim() != 2:
             _need(logits, logits.dtype, "logits", 2)
         _row(logits, torch.bfloat16 if bf16 else torch.float32, (logits.shape[0], self.num_experts), "logits")
+        if logits.shape[0] >> 31:
+            _int32(logits.shape[0], "the number of tokens")
         return int(bf16)
 
     def route(self, logits: torch.Tensor, router: Router, bias: Optional[torch.Tensor] = None,

@@ -3,7 +3,10 @@ device call, and the binding turns down tensors of another type, shape or place.
 
 from __future__ import annotations
 
+import copy
 import ctypes
+import dataclasses
+import pickle
 
 import pytest
 import torch
@@ -82,3 +85,18 @@ def test_binding_refuses_before_the_library():
         buf.route(torch.zeros((4, 8)), r)  # not on the device
     with pytest.raises(ValueError, match="score must be"):
         epm.Router(2, score="tanh")
+
+
+def test_a_router_is_copied_pickled_and_compared_by_what_it_says():
+    r = epm.Router(6, score="sigmoid", num_groups=8, topk_groups=4, normalize=False, scale=2.5)
+    for other in (copy.copy(r), copy.deepcopy({"r": r})["r"], pickle.loads(pickle.dumps(r)), dataclasses.replace(r)):
+        assert other == r and hash(other) == hash(r)
+        raw = other._raw._obj
+        assert (raw.score, raw.num_groups, raw.topk_groups, raw.normalize, raw.scale) == (1, 8, 4, 0, 2.5)
+
+
+def test_counts_past_32_bits_do_not_wrap():
+    for wrong in (dict(num_topk=2 ** 32 + 8), dict(num_topk=8, num_groups=2 ** 32 + 1),
+                  dict(num_topk=8, topk_groups=-2 ** 40)):
+        with pytest.raises(ValueError, match="32 bits"):
+            epm.Router(**wrong)
