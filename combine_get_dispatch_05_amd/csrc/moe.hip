@@ -3,9 +3,13 @@
 //   logits = x Wr^T, route (route.h), y[t] = residual[t] + sum_k w_k (silu(x Wg^T) * (x Wu^T)) W2^T
 // The weights of the reached experts are read once and are the cost.  They go straight from
 // memory into the matrix instruction's registers, 16 weight rows by the tokens of one
-// expert, K shared out over the waves of a block, each keeping kAhead steps of 128 bytes a row
+// expert, K shared out over the waves of a block, each keeping ahead() steps of 128 bytes a row
 // in flight.  FP8 weights are widened to bf16 there, exactly, so that rows and
 // activations keep their bf16 values.
+// Bound by the weights where there are many, 32 tokens on 64 FP8 experts of 2048 x 7168: 472 us for 2.8 GB,
+// 6.0 TB/s (logits 11, choice 14, gate and up 316, down 156).  One token, eight experts: FP8 2048 x 7168 82 us
+// (5 + 52 + 25) for 356 MB; bf16 768 x 2048 22 us (3 + 13.5 + 7.4) for 76 MB, three launches whose starts and ends
+// are half of it.
 #include "route.h"
 #include "stream.h"
 
@@ -209,9 +213,8 @@ __global__ __launch_bounds__(1024) void moe_select_kernel(RouteRule r, int T, Mo
     for (int i = threadIdx.x; i < T * r.topk; i += 1024) {
         const int t = i / r.topk;
         const int e = ids[i];
-        if (e >= 0) {
+        if (e >= 0)
             work.pair_weight[start[e] + __popcll(mask[e] & ((1ull << t) - 1))] = weights[i];
-        }
     }
 }
 
@@ -283,9 +286,8 @@ __device__ __forceinline__ void gate_tile(const MoeArgs &a, const ActiveExpert &
             const int64_t at = int64_t(x.start + m0 + i) * a.I + n0 + c;
             const uint2 b = pack4(v);
             *reinterpret_cast<uint2 *>(a.work.act + at) = b;
-            if constexpr (kActPlanes<FP8> == 2) {
+            if constexpr (kActPlanes<FP8> == 2)
                 *reinterpret_cast<uint2 *>(a.work.act + a.work.act_plane / 2 + at) = pack4(lost(v, b));
-            }
         }
     }
     __syncthreads();
@@ -329,8 +331,8 @@ __device__ __forceinline__ ActiveExpert choose_one(const MoeArgs &a, const MoeCh
     return ActiveExpert{e, int(blockIdx.y), e >= 0, 0, 1};
 }
 
-// 32 columns a block, so that the tokens' loads serve twice the weights, where an expert's tokens are few.
-// Up to a token a wave (ONE: one): the same, and the blockIdx.y-th of the experts that some token chose.
+// Up to a token a wave: each wave chooses for one, the block takes the blockIdx.y-th of the experts that some token
+// chose.  In a launch of its own the choice takes 5.5 us and its start.
 constexpr int kChooseTokens = kGateWaves;
 template <int V>
 __device__ __forceinline__ ActiveExpert choose_few(const MoeArgs &a, const MoeChoice &c, float *lds)
@@ -403,6 +405,7 @@ __device__ __forceinline__ ActiveExpert choose_few(const MoeArgs &a, const MoeCh
     return x;
 }
 
+// 32 columns a block, so that the tokens' loads serve twice the weights, where an expert's tokens are few; else 16 by 16.
 template <bool FP8, bool TAIL, int V, bool ONE>
 __global__ __launch_bounds__(kGateWaves *kWave) void moe_gate_kernel(MoeArgs a, MoeChoice c)
 {
@@ -549,7 +552,6 @@ __global__ __launch_bounds__(kDownWaves *kWave) void moe_down_kernel(MoeArgs a, 
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Lays the workspace out at base; returns its bytes.
 // Blocks that share a tile's K: some 256 in all.
 int logit_splits(int T, int E)
 {
@@ -678,7 +680,7 @@ hipError_t launch_moe(const RouteRule &rule, const MoeCall &c, hipStream_t strea
             go(moe_down_kernel<false, true, COLS>);
     };
     // 8 columns a block where blocks of 16 would be fewer than the compute units (H = 2048, eight experts of 768: 6.6
-    // against 8.2 us; where they are not, 16 share the activations' loads: H = 7168, FP8, 24.9 against 32)
+    // against 8.2 us, with activations of one bf16 value; where they are not, 16 share the activations' loads: H = 7168, FP8, 24.9 against 32)
     if (c.H < 16 * compute_units())
         down(std::integral_constant<int, 8>());
     else

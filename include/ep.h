@@ -689,7 +689,8 @@ const char *ep_last_hip_error(void);
  * 2.2: ep_pool_stats and the capped pool; 2.3: ep_get_dispatch_layout_noalloc
  * and EP_ERR_TOO_LARGE; 2.4: the destination-major dispatch and gather-form
  * combine tuning shapes (code X*10000).  The expert operations (ep_rms_norm to
- * ep_expert_ffn_backward) were added without a new number: look the symbol up. */
+ * ep_expert_ffn_backward), the router (ep_route*), ep_ll_moe and the adapters (ep_adapter_*)
+ * were added without a new number: look the symbol up. */
 int ep_version(void);
 
 #ifdef __cplusplus
