@@ -112,6 +112,13 @@ SHAPES = [  # T, H, I, E, router, bias, fp8, fp32 router, residual
     (20, 1280, 256, 8, epm.Router(2), True, True, False, False),
     (64, 512, 384, 2, epm.Router(2), False, True, False, True),
     (40, 256, 128, 130, epm.Router(6), False, True, False, False),
+    (1, 256, 64, 200, epm.Router(8, **SIGMOID), True, False, False, False),
+    (1, 128, 40, 512, epm.Router(64), False, False, True, True),
+    (6, 256, 64, 132, epm.Router(4, **SIGMOID), True, False, False, True),
+    (8, 128, 64, 512, epm.Router(10), False, False, False, False),
+    (4, 256, 128, 300, epm.Router(12), True, True, False, True),
+    (8, 192, 320, 100, epm.Router(4), False, False, False, False),  # 320 blocks of the gate
+    (8, 192, 256, 100, epm.Router(4), False, False, False, False),  # 256
 ]
 
 
