@@ -594,7 +594,7 @@ struct AdapterGradArgs {
 // registers; the waves' sums meet in LDS.
 template <int RT>
 constexpr int kGradStage = 64 * 128 + 2 * 64 * RT * 32;
-template <int RT, bool DOWN>
+template <int RT, bool DOWN, bool SCAN>
 __device__ __forceinline__ void adapter_grad(const AdapterGradArgs &g, int block, char *lds)
 {
     const AdapterArgs &a = g.a;
@@ -602,7 +602,18 @@ __device__ __forceinline__ void adapter_grad(const AdapterGradArgs &g, int block
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int width = g.width[DOWN ? 0 : 1], chunks = (width + 63) / 64;
     const int l = block / chunks, n = block % chunks * 64;
-    const int from = a.offsets[l], count = a.offsets[l + 1] - from;
+    constexpr int kRound = kAdapterWaves * 64;
+    int t0 = wave * 64, from = 0, count, first;
+    if constexpr (SCAN) {  // (one round: the list is in registers before the LDS is loaded)
+        static_assert(kScanTokens <= kRound, "one round");
+        int *list = reinterpret_cast<int *>(lds);
+        count = scan_tokens<kAdapterWaves>(a, l, list, list + kScanTokens);
+        first = t0 + lane < count ? list[t0 + lane] : 0;
+        __syncthreads();
+    } else {
+        from = a.offsets[l];
+        count = a.offsets[l + 1] - from;
+    }
     const char *wide = g.wide[DOWN ? 0 : 1], *narrow = g.narrow[DOWN ? 0 : 1];
     lds_char *own = (lds_char *)lds + wave * kGradStage<RT>, *small = own + 64 * 128;
     auto send = [&](int t0, int mine) {  // mine: the token of step row `lane`
@@ -624,12 +635,12 @@ __device__ __forceinline__ void adapter_grad(const AdapterGradArgs &g, int block
                            small + (u * CH + j) * kWave * 16);
         }
     };
-    auto tokens = [&](int t0) { return t0 + lane < count ? a.order[from + t0 + lane] : 0; };
-    constexpr int kRound = kAdapterWaves * 64;
+    auto tokens = [&](int t0) { return !SCAN && t0 + lane < count ? a.order[from + t0 + lane] : 0; };
     f32x4 acc[4][RT] = {};
-    int t0 = wave * 64;
+    if constexpr (!SCAN)
+        first = tokens(t0);
     if (t0 < count)
-        send(t0, tokens(t0));
+        send(t0, first);
     int next = tokens(t0 + kRound);
     for (; t0 < count; t0 += kRound) {
         landed<0>();
@@ -697,15 +708,15 @@ __device__ __forceinline__ void adapter_grad(const AdapterGradArgs &g, int block
     }
 }
 
-template <int RT>
+template <int RT, bool SCAN>
 __global__ __launch_bounds__(kAdapterThreads) void adapter_grads_kernel(AdapterGradArgs g)
 {
     constexpr int kStages = kAdapterWaves * kGradStage<RT>, kSums = kAdapterWaves * RT * 4 * kWave * 16;
     __shared__ __attribute__((aligned(128))) char lds[kStages > kSums ? kStages : kSums];
     if (int(blockIdx.x) < g.blocks)
-        adapter_grad<RT, true>(g, blockIdx.x, lds);
+        adapter_grad<RT, true, SCAN>(g, blockIdx.x, lds);
     else
-        adapter_grad<RT, false>(g, int(blockIdx.x) - g.blocks, lds);
+        adapter_grad<RT, false, SCAN>(g, int(blockIdx.x) - g.blocks, lds);
 }
 
 // ---------------------------------------------------------------- launches
@@ -886,7 +897,7 @@ hipError_t launch_adapter_backward(const AdapterShape &s, const void *dy, const 
     AdapterArgs a = adapter_args(s, w);
     if (log_enabled())
         log_launch("adapter_product_backward: T=%d K=%d N=%d r=%d L=%d", s.T, s.K, s.N, s.r, s.L);
-    hipError_t e = group_tokens(a, stream);
+    hipError_t e = scans(s.T, s.L) ? hipSuccess : group_tokens(a, stream);
     if (e == hipSuccess && s.T > 0)
         e = shrink<true>(a, dy, up, s.N, stream);
     if (e == hipSuccess && s.T > 0)
@@ -906,7 +917,9 @@ hipError_t launch_adapter_backward(const AdapterShape &s, const void *dy, const 
     g.blocks = s.L * ((s.K + 63) / 64);
     const unsigned all = unsigned(g.blocks + s.L * ((s.N + 63) / 64));
     return by_rank(s.r, [&](auto rt) {
-        hipLaunchKernelGGL((adapter_grads_kernel<decltype(rt)::value>), dim3(all), dim3(kAdapterThreads), 0, stream, g);
+        constexpr int RT = decltype(rt)::value;
+        hipLaunchKernelGGL((scans(s.T, s.L) ? adapter_grads_kernel<RT, true> : adapter_grads_kernel<RT, false>), dim3(all),
+                           dim3(kAdapterThreads), 0, stream, g);
         return hipGetLastError();
     });
 }

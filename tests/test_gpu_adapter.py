@@ -103,6 +103,7 @@ SHAPES = [  # T, K, N, r, L, share without an adapter
     (65, 1024, 264, 40, 1, 0.0), (128, 2048, 512, 16, 64, 0.1), (130, 264, 520, 128, 5, 0.1), (33, 64, 64, 104, 1, 0.0),
     (600, 640, 1032, 8, 70, 0.1), (700, 520, 328, 72, 2, 0.6), (1500, 256, 512, 64, 7, 0.0), (2100, 128, 136, 16, 200, 0.3),
     (5000, 64, 64, 32, 3, 0.05), (300, 4096, 64, 128, 2, 0.0), (40, 8, 2048, 8, 4, 0.2),
+    (256, 264, 200, 128, 1, 0.0), (256, 64, 128, 32, 127, 0.3), (257, 64, 128, 16, 2, 0.0), (200, 64, 136, 24, 128, 0.3),
 ]
 
 
@@ -128,6 +129,17 @@ def test_runs_one_adapter_and_none():
     assert (hidden == 0).all() and (ddown == 0).all() and (dup == 0).all()
     out, _ = epm.adapter_product(x, odd, down, up, scales)
     assert (out == 0).all()
+
+
+@pytest.mark.parametrize("T", [12, 200])
+def test_ids_that_name_no_adapter_among_few_tokens(T):
+    x, down, up, scales, base, dy, dxb = made(T, 192, 200, 16, 6)
+    odd = torch.tensor([-1, 6, 1 << 40, -(1 << 50)], device="cuda").repeat(T // 4)
+    out, hidden, dx, ddown, dup = check(odd, x, down, up, scales, base, dy, dxb)
+    assert torch.equal(out, base) and torch.equal(dx, dxb)
+    assert (hidden == 0).all() and (ddown == 0).all() and (dup == 0).all()
+    odd[::3] = 5
+    check(odd, x, down, up, scales, base, dy, dxb)
 
 
 def test_rows_and_adapters_that_are_not_finite_stay_alone():
