@@ -205,10 +205,10 @@ def adapter_product(x: torch.Tensor, adapter_ids: torch.Tensor, down: torch.Tens
     out = torch.empty(T, N, dtype=torch.bfloat16, device=at)
     hidden = torch.empty(2, T, r, dtype=torch.bfloat16, device=at) if save else None
     size = _adapter_workspace(*d, 0)
-    work = torch.empty(size, dtype=torch.uint8, device=at)
+    work = torch.empty(size, dtype=torch.uint8, device=at) if size else None
     abi.check(abi.lib().ep_adapter_product(
         ctypes.byref(abi.AdapterDims(*d)), x.data_ptr(), adapter_ids.data_ptr(), down.data_ptr(), up.data_ptr(),
-        scales.data_ptr(), abi.address(base), out.data_ptr(), abi.address(hidden), work.data_ptr(), size,
+        scales.data_ptr(), abi.address(base), out.data_ptr(), abi.address(hidden), abi.address(work), size,
         abi.raw_stream(dev)), "ep_adapter_product")
     return out, hidden
 

@@ -7,7 +7,7 @@
 // base.  All of it is bound by memory: each row is read and written once.
 // 8192 tokens, K = N = 7168, rank 64, 16 adapters: 111 us (sort 8, shrink 39, expand 64) for 352 MB of rows, 3.2 TB/s.
 // A step of 4096 tokens, N = 4096, rank 32, 8 adapters: 116 us (sort 5 twice; out 16 + 22, dx 12 + 30, the
-// gradients 25) for 369 MB of rows, dy among them twice.  One token 11 us, of which 9 are the kernel's; 128 tokens on 64 adapters 14 (6.7 + 6.9).
+// gradients 25) for 369 MB of rows, dy among them twice.  One token 9.6 us, of which 8.8 are the kernel's; 128 tokens on 64 adapters 14 (6.7 + 6.9).
 #include "stream.h"
 
 namespace ep {
@@ -740,7 +740,7 @@ int shrink_splits(int64_t T, int L, int r, int width)
 }
 
 // One launch for few tokens, as long as every block that makes h again has a compute unit to itself and
-// little to read: 8 tokens, K = 7168, rank 16, a call 10.8 us against 13.4 in two launches (the host's time); rank 64 27.8
+// little to read: 8 tokens, K = 7168, rank 16, a call 9.6 us against 13.4 in two launches (the host's time); rank 64 27.8
 // in two, 36.9 in one.
 bool few(const AdapterShape &s)
 {
@@ -856,13 +856,18 @@ hipError_t expand(AdapterArgs &a, const void *w, int width, const void *base, vo
 
 }  // namespace
 
-size_t adapter_workspace(const AdapterShape &s, bool back) { return adapter_layout(s, back, nullptr, nullptr); }
+// One launch hands nothing on.
+size_t adapter_workspace(const AdapterShape &s, bool back)
+{
+    return !back && few(s) ? 0 : adapter_layout(s, back, nullptr, nullptr);
+}
 
 hipError_t launch_adapter(const AdapterShape &s, const void *x, const void *down, const void *up, const void *base, void *out,
                           void *hidden, void *workspace, hipStream_t stream)
 {
-    AdapterWork w;
-    adapter_layout(s, false, static_cast<char *>(workspace), &w);
+    AdapterWork w{};
+    if (workspace != nullptr)
+        adapter_layout(s, false, static_cast<char *>(workspace), &w);
     AdapterArgs a = adapter_args(s, w);
     if (log_enabled())
         log_launch("adapter_product: T=%d K=%d N=%d r=%d L=%d splits=%d", s.T, s.K, s.N, s.r, s.L,

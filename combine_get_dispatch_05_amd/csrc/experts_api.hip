@@ -150,13 +150,14 @@ int ep_adapter_product(const ep_adapter_dims *dims, const void *x, const int64_t
     const int rc = check_adapters(dims);
     if (rc != EP_OK)
         return rc;
+    const size_t need = ep_adapter_workspace(dims, 0);
     if (down == nullptr || up == nullptr || scales == nullptr ||
-        (dims->num_tokens > 0 && (x == nullptr || adapter_ids == nullptr || out == nullptr || workspace == nullptr)))
+        (dims->num_tokens > 0 && (x == nullptr || adapter_ids == nullptr || out == nullptr || (workspace == nullptr && need > 0))))
         return EP_ERR_INVALID;
     if (!al(x, 16) || !al(down, 16) || !al(up, 16) || !al(base, 16) || !al(out, 16) || !al(hidden, 16) ||
         !al(workspace, 256) || !al(adapter_ids, 8) || !al(scales, 4))
         return EP_ERR_ALIGN;
-    if (workspace_bytes < ep_adapter_workspace(dims, 0))
+    if (workspace_bytes < need)
         return EP_ERR_CAPACITY;
     if (dims->num_tokens == 0)
         return EP_OK;

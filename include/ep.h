@@ -582,7 +582,8 @@ int ep_ll_moe(const ep_dims *dims, int32_t inter, const ep_router *router, const
  *   hidden [2][T][rank] bf16, nullable: h, which the backward pass takes, as the sum of its bf16 value
  *     and of what that rounding lost (zeros without an adapter)
  * in, out and rank % 8 == 0 (EP_ERR_ALIGN), rank <= 128, L <= 8192.  workspace: ep_adapter_workspace(dims, 0)
- * bytes, 256-byte aligned (EP_ERR_CAPACITY if workspace_bytes is less).  No host sync.
+ * bytes, 256-byte aligned (EP_ERR_CAPACITY if workspace_bytes is less; 0, so that it may be null, for a few
+ * tokens).  No host sync.
  */
 typedef struct ep_adapter_dims {
     int32_t num_tokens;   /* T */

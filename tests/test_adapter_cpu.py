@@ -22,8 +22,8 @@ def dims(*a):
 
 @pytest.mark.parametrize("back", [False, True], ids=["forward", "backward"])
 def test_adapter_rules(back):
-    n = L.ep_adapter_workspace(dims(16, 256, 128, 16, 4), int(back))
-    assert n >= 6 * 4 + 16 * 4 + 16 * 16 * 4
+    n = L.ep_adapter_workspace(dims(32, 256, 128, 16, 4), int(back))
+    assert n >= 6 * 4 + 32 * 4 + 32 * 16 * 4
     if back:
         f, small = L.ep_adapter_product_backward, {"ids": M4, "scales": M2}
         ptrs = ["dy", "x", "ids", "down", "up", "scales", "hidden", "dx_base", "dx", "ddown", "dup"]
@@ -31,7 +31,7 @@ def test_adapter_rules(back):
     else:
         f, small = L.ep_adapter_product, {"ids": M4, "scales": M2}
         ptrs, free = ["x", "ids", "down", "up", "scales", "base", "out", "hidden"], {"base", "hidden"}
-    good = {"d": dims(16, 256, 128, 16, 4), **{p: A for p in ptrs}, "work": A, "size": n, "stream": None}
+    good = {"d": dims(32, 256, 128, 16, 4), **{p: A for p in ptrs}, "work": A, "size": n, "stream": None}
     for p in ptrs:
         if p not in free:
             assert call(f, good, **{p: None}) == INV, p
@@ -60,6 +60,9 @@ def test_workspace_holds_what_the_launches_write():
                            (1 << 24, 1 << 20, 8, 128, 8192), (3, 1 << 20, 1 << 20, 128, 8192)):
         for back in (0, 1):
             n = L.ep_adapter_workspace(dims(T, K, N, r, ad), back)
+            if not back and T <= 16 and r <= 64 and r * K <= 1 << 17:  # one launch
+                assert n == 0
+                continue
             padded = 16 if r <= 16 else 32 if r <= 32 else 64 if r <= 64 else 128
             height = 64 if r <= 64 else 32
             tiles = T // height + min(ad + 1, T)
