@@ -251,8 +251,9 @@ class Router:
     def __post_init__(self):
         if self.score not in ("softmax", "sigmoid"):
             raise ValueError(f"score must be softmax or sigmoid, got {self.score!r}")
-        for n in (self.num_topk, self.num_groups, self.topk_groups):
-            _int32(n, "a router's count")
+        if (self.num_topk | self.num_groups | self.topk_groups) >> 31:
+            for n in (self.num_topk, self.num_groups, self.topk_groups):
+                _int32(n, "a router's count")
         rule = abi.RouterRule(self.score == "sigmoid", self.num_groups, self.topk_groups, bool(self.normalize), self.scale)
         object.__setattr__(self, "_raw", ctypes.byref(rule))  # (which keeps it alive)
 
