@@ -3,10 +3,10 @@
 //   dh[t] = c_a (dy[t] B_a),  dx[t] = dx_base[t] + dh[t] A_a,  dA_a = sum_t dh[t]^T x[t],  dB_a = sum_t dy[t]^T h[t]
 // A block takes a tile of tokens that share an adapter: of few tokens it looks for them itself, more are sorted by
 // adapter first.  The inner products to the rank (shrink) split K over waves and blocks; the products back
-// (expand) sum those parts, round h to bf16, the matrix instruction's operand, and add the
+// (expand) sum those parts to h and add the
 // base.  All of it is bound by memory: each row is read and written once.
-// 8192 tokens, K = N = 7168, rank 64, 16 adapters: 111 us (sort 8, shrink 39, expand 64) for 352 MB of rows, 3.2 TB/s.
-// A step of 4096 tokens, N = 4096, rank 32, 8 adapters: 116 us (sort 5 twice; out 16 + 22, dx 12 + 30, the
+// 8192 tokens, K = N = 7168, rank 64, 16 adapters: 113 us (sort 8, shrink 39, expand 67) for 352 MB of rows, 3.1 TB/s.
+// A step of 4096 tokens, N = 4096, rank 32, 8 adapters: 117 us (sort 5 twice; out 16 + 22, dx 12 + 30, the
 // gradients 25) for 369 MB of rows, dy among them twice.  One token 9.6 us, of which 8.8 are the kernel's; 128 tokens on 64 adapters 14 (6.7 + 6.9).
 #include "stream.h"
 
@@ -316,25 +316,21 @@ __global__ __launch_bounds__(kAdapterThreads) void adapter_shrink_kernel(Adapter
 
 // ------------------------------------------------------------------ expand
 
-// Four values of a token's h for the gradients, which are sums of its products: one rounding there would be as much
-// as the gradients' own.
-__device__ __forceinline__ void keep_hidden(const AdapterArgs &a, int token, int k, const f32x4 &v, const uint2 &b)
-{
-    uint16_t *to = a.hidden + int64_t(token) * a.r + k;
-    *reinterpret_cast<uint2 *>(to) = b;
-    *reinterpret_cast<uint2 *>(to + int64_t(a.T) * a.r) = pack4(lost(v, b));
-}
-
 // out rows of one tile, columns [n0, n1) in steps of 64 a wave.  A wave stages its own weights in LDS; its results turn
-// there, 16 tokens at a time, so that eight lanes read and write a whole line of a row.
+// there, 16 tokens at a time, so that eight lanes read and write a whole line of a row.  h is the matrix instruction's
+// operand, as the sum of its bf16 value and of what that rounding lost: with one value the result's error against 64
+// bits is 1.2 to 1.4 times that of its own rounding, and two cost 64.2 -> 67.3 us (8192 rows of 7168, rank 64), nothing at
+// smaller ranks.  Up to rank 16 both lie in one operand of 32, over the weights twice.
 constexpr int kTurnRow = 68;  // floats: 16 rows of 64, four apart in the banks
 template <int RT, bool COL, int W>
 struct ExpandLds {
     static constexpr int KS = (RT + 1) / 2;  // matrix steps of 32
     static constexpr int kHidden = kTokenTiles<RT> * 16 * KS * 32;  // bf16 values
+    static constexpr int kPlanes = RT == 1 ? 1 : 2, kRest = RT == 1 ? 16 : kHidden;  // from a value to what it lost
+    static constexpr int kQuads = RT == 1 ? 4 : KS * 8;                              // of a token
     char weights[W][COL ? KS * 32 * 128 : (RT + 3) / 4 * 64 * kStepBytes];
     union {  // h is in registers before the first results turn
-        uint16_t hidden[kHidden];
+        uint16_t hidden[kPlanes * kHidden];
         float turn[W][16 * kTurnRow];
     };
 };
@@ -343,22 +339,27 @@ template <int RT, int MT, bool COL, int W, class MakeH>
 __device__ __forceinline__ void expand_tile(const AdapterArgs &a, int adapter, const int *tokens, int rows,
                                             ExpandLds<RT, COL, W> &lds, int n0, int n1, MakeH make_h)
 {
-    constexpr int KS = (RT + 1) / 2;
+    using Lds = ExpandLds<RT, COL, W>;
+    constexpr int KS = Lds::KS, PL = Lds::kPlanes;
     using PS = NearRowStage<64, kWave>;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), g = lane >> 4;
     const int width = int(a.width);
     const bool adapted = adapter < a.L;
     lds_char *own = (lds_char *)lds.weights[wave];
     float *turn = lds.turn[wave];
-    bf16x8 h[MT][KS];
-    int64_t row[MT][2];  // of the line that this lane reads and writes a chunk of; -1: none
+    bf16x8 h[MT][KS][PL];
+    int row[MT][2];  // the token whose line this lane reads and writes a chunk of; -1: none
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int at = m * 16 + i * 8 + (lane >> 3);
-            row[m][i] = at < rows ? int64_t(tokens[at]) * width + (lane & 7) * 8 : -1;
+            row[m][i] = at < rows ? tokens[at] : -1;
         }
+    auto place = [&](int token, int n) {  // (worked out each time: kept, the addresses cost a wave its place, 6.7 -> 10.1 us
+        hold(token);                      // with 128 tokens on 64 adapters of rank 16)
+        return int64_t(token) * width + (lane & 7) * 8 + n;
+    };
     const char *w = a.p + int64_t(adapter) * a.r * width * 2;
     u32x4 b[MT][2] = {};
     auto send = [&](int n) {
@@ -386,7 +387,7 @@ __device__ __forceinline__ void expand_tile(const AdapterArgs &a, int adapter, c
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     if (row[m][i] >= 0 && n + (lane & 7) * 8 < width)
-                        b[m][i] = *reinterpret_cast<const u32x4 *>(a.base + row[m][i] + n);
+                        b[m][i] = *reinterpret_cast<const u32x4 *>(a.base + place(row[m][i], n));
         }
     };
     int n = n0 + wave * 64;
@@ -397,7 +398,10 @@ __device__ __forceinline__ void expand_tile(const AdapterArgs &a, int adapter, c
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int s = 0; s < KS; ++s)
-            h[m][s] = *reinterpret_cast<const bf16x8 *>(lds.hidden + (m * 16 + (lane & 15)) * (KS * 32) + s * 32 + g * 8);
+#pragma unroll
+            for (int u = 0; u < PL; ++u)
+                h[m][s][u] = *reinterpret_cast<const bf16x8 *>(lds.hidden + u * Lds::kRest +
+                                                               (m * 16 + (lane & 15)) * (KS * 32) + s * 32 + g * 8);
     __syncthreads();
     for (; n < n1; n += W * 64) {
         landed<0>();
@@ -412,14 +416,15 @@ __device__ __forceinline__ void expand_tile(const AdapterArgs &a, int adapter, c
         f32x4 acc[4][MT] = {};
         bf16x8 p[4][KS];
         if (adapted) {
+            const int from = PL == 1 ? lane & 31 : lane;  // (k 16 to 31 is k 0 to 15 again)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int s = 0; s < KS; ++s) {
                     if constexpr (COL)
-                        p[j][s] = transposed(own, 128, s * 32, [&](int q) { return j * 16 + q * 4; }, lane);
+                        p[j][s] = transposed(own, 128, s * 32, [&](int q) { return j * 16 + q * 4; }, from);
                     else
-                        p[j][s] = PS::frag(own + (s >> 1) * PS::kBytes, j * 16, s & 1, lane);
+                        p[j][s] = PS::frag(own + (s >> 1) * PS::kBytes, j * 16, s & 1, from);
                 }
         }
         // read before the same LDS is loaded again
@@ -433,7 +438,9 @@ __device__ __forceinline__ void expand_tile(const AdapterArgs &a, int adapter, c
                 for (int s = 0; s < KS; ++s)
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
-                        acc[j][m] = mfma_bf16(p[j][s], h[m][s], acc[j][m]);
+#pragma unroll
+                        for (int u = 0; u < PL; ++u)
+                            acc[j][m] = mfma_bf16(p[j][s], h[m][s][u], acc[j][m]);
         }
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
@@ -451,7 +458,7 @@ __device__ __forceinline__ void expand_tile(const AdapterArgs &a, int adapter, c
                                  cvt_bf16x2(hi[0] + bf16_lo(c[2]), hi[1] + bf16_hi(c[2])),
                                  cvt_bf16x2(hi[2] + bf16_lo(c[3]), hi[3] + bf16_hi(c[3]))};
                 if (row[m][i] >= 0 && n + (lane & 7) * 8 < width)
-                    __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(a.out + row[m][i] + n));
+                    __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(a.out + place(row[m][i], n)));
             }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         }
@@ -468,8 +475,8 @@ __global__ __launch_bounds__(kAdapterThreads) void adapter_expand_kernel(Adapter
         // h: the parts' sum, scaled, in bf16; zeros past the rank and the rows
         auto make_h = [&] {
             const float scale = adapter < a.L ? a.scales[adapter] : 0.0f;
-            for (int i = threadIdx.x; i < MT * 16 * KS * 8; i += kAdapterThreads) {
-                const int m = i / (KS * 8), k = i % (KS * 8) * 4;
+            for (int i = threadIdx.x; i < MT * 16 * lds.kQuads; i += kAdapterThreads) {
+                const int m = i / lds.kQuads, k = i % lds.kQuads * 4;
                 f32x4 v = {};
                 if (adapter < a.L && m < rows && k < a.r) {
                     const float *from = a.parts + int64_t(tokens[m]) * RP + k;
@@ -485,10 +492,14 @@ __global__ __launch_bounds__(kAdapterThreads) void adapter_expand_kernel(Adapter
                     }
                     v *= scale;
                 }
-                const uint2 b = pack4(v);
+                const uint2 b = pack4(v), rest = pack4(lost(v, b));
                 *reinterpret_cast<uint2 *>(lds.hidden + m * KS * 32 + k) = b;
-                if (a.hidden != nullptr && blockIdx.y == 0 && m < rows && k < a.r)
-                    keep_hidden(a, tokens[m], k, v, b);
+                *reinterpret_cast<uint2 *>(lds.hidden + lds.kRest + m * KS * 32 + k) = rest;
+                if (a.hidden != nullptr && blockIdx.y == 0 && m < rows && k < a.r) {
+                    uint16_t *to = a.hidden + int64_t(tokens[m]) * a.r + k;
+                    *reinterpret_cast<uint2 *>(to) = b;
+                    *reinterpret_cast<uint2 *>(to + int64_t(a.T) * a.r) = rest;
+                }
             }
             __syncthreads();
         };
@@ -557,8 +568,8 @@ __global__ __launch_bounds__(kFewWaves *kWave) void adapter_few_kernel(AdapterAr
                     few_parts<RT, 1, TAIL>(a, adapter, tokens, rows, parts);
             }
             __syncthreads();
-            for (int i = threadIdx.x; i < 16 * KS * 8; i += kFewWaves * kWave) {
-                const int m = i / (KS * 8), k = i % (KS * 8) * 4;
+            for (int i = threadIdx.x; i < 16 * lds.kQuads; i += kFewWaves * kWave) {
+                const int m = i / lds.kQuads, k = i % lds.kQuads * 4;
                 f32x4 v = {};
                 if (m < rows && k < a.r && adapter < a.L) {
 #pragma unroll
@@ -566,10 +577,14 @@ __global__ __launch_bounds__(kFewWaves *kWave) void adapter_few_kernel(AdapterAr
                         v += *reinterpret_cast<const f32x4 *>(parts + (w * 16 + m) * (RT * 16) + k);
                     v *= a.scales[adapter];
                 }
-                const uint2 b = pack4(v);
+                const uint2 b = pack4(v), rest = pack4(lost(v, b));
                 *reinterpret_cast<uint2 *>(lds.hidden + m * KS * 32 + k) = b;
-                if (a.hidden != nullptr && blockIdx.y == 0 && m < rows && k < a.r)
-                    keep_hidden(a, tokens[m], k, v, b);
+                *reinterpret_cast<uint2 *>(lds.hidden + lds.kRest + m * KS * 32 + k) = rest;
+                if (a.hidden != nullptr && blockIdx.y == 0 && m < rows && k < a.r) {
+                    uint16_t *to = a.hidden + int64_t(tokens[m]) * a.r + k;
+                    *reinterpret_cast<uint2 *>(to) = b;
+                    *reinterpret_cast<uint2 *>(to + int64_t(a.T) * a.r) = rest;
+                }
             }
             __syncthreads();
         };
@@ -842,7 +857,7 @@ hipError_t expand(AdapterArgs &a, const void *w, int width, const void *base, vo
         const bool scan = scans(a.T, a.L);
         const int64_t tiles = most_tiles(a.T, a.L, a.r), runs = (width + kRun - 1) / kRun;
         // Blocks that share a tile's columns: two a compute unit, each then has several steps behind its start (8192 rows
-        // of 7168, rank 64: 64.0 us, with four 68.3); four where each finds its tokens itself, many of them none
+        // of 7168, rank 64, h as one value: 64.0 us, with four 68.3); four where each finds its tokens itself, many of them none
         // (128 tokens on 64 adapters: 6.9 us, with two 7.4).
         int64_t n = (scan ? 4 : 2) * kCard / tiles;
         n = n < 1 ? 1 : n < runs ? n : runs;

@@ -575,8 +575,8 @@ int ep_ll_moe(const ep_dims *dims, int32_t inter, const ep_router *router, const
 /*
  * Low-rank adapters of many requests beside a shared projection (ep_fp8_product's, or any other): token t
  * uses adapter a = adapter_ids[t], none if that is outside [0, num_adapters).
- *   h[t] = scales[a] * (x[t] down_a^T),  out[t] = bf16_rne( base[t] + bf16_rne(h[t]) up_a^T )
- * with fp32 sums; a token without an adapter gets base[t] (zeros without a base).
+ *   h[t] = scales[a] * (x[t] down_a^T),  out[t] = bf16_rne( base[t] + h[t] up_a^T )
+ * with fp32 sums and h kept to 2^-16 of itself (an infinite up gives infinities or NaN); a token without an adapter gets base[t] (zeros without a base).
  *   x [T][in] bf16, adapter_ids int64 [T], down [L][rank][in], up [L][out][rank] bf16, scales fp32 [L]
  *   base [T][out] bf16, nullable; out [T][out] may be the same memory as base
  *   hidden [2][T][rank] bf16, nullable: h, which the backward pass takes, as the sum of its bf16 value
@@ -599,7 +599,7 @@ int ep_adapter_product(const ep_adapter_dims *dims, const void *x, const int64_t
 
 /*
  * Gradients of ep_adapter_product given dy [T][out] bf16 (base's gradient is dy itself; scales are constants):
- *   dh[t] = scales[a] * (dy[t] up_a),  dx[t] = bf16_rne( dx_base[t] + bf16_rne(dh[t]) down_a )
+ *   dh[t] = scales[a] * (dy[t] up_a),  dx[t] = bf16_rne( dx_base[t] + dh[t] down_a )
  *   ddown_a = bf16_rne( sum_t dh[t]^T x[t] ),  dup_a = bf16_rne( sum_t dy[t]^T h[t] ),  in a fixed order,
  * h and dh there to 2^-16 of themselves (an infinite dy or x gives infinities or NaN)
  * dx_base [T][in] (nullable) is the projection's own gradient of x; dx may be the same memory.  ddown and

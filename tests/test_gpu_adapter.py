@@ -1,7 +1,8 @@
 """Low-rank adapters and their gradients against the formulas in 64 bits.
 
 Bounds, per element: fp32 sums of n terms 2 (n + 8) U of the summed magnitudes, half a bf16 step (2^-8) for
-h, dh and every result, and what an error of h or dh gives behind its second product."""
+every result and its square for h and dh, which are sums of two bf16 values, and what an error of h or dh gives behind
+its second product."""
 
 from __future__ import annotations
 
@@ -78,16 +79,15 @@ def check(ids, x, down, up, scales, base, dy, dx_base):
         eh_ = eh_ + BF * (h.abs() + eh_)
         rh[t], eh[t] = h, eh_
         ro[t] += h @ B.t()
-        eo[t] += (eh_ + err(r) * (h.abs() + eh_)) @ B.abs().t()
+        e2 = es[t] + BF * BF * h.abs()  # (as the sum of two values; 2 r products)
+        eo[t] += (e2 + err(2 * r) * (h.abs() + e2) * (1 + BF)) @ B.abs().t()
         dh, ed = c * (ya @ B), c * (ya.abs() @ B.abs()) * (err(N) + 2 * U)
-        ed = ed + BF * (dh.abs() + ed)
+        ed = ed * (1 + BF) + BF * BF * dh.abs()
         rx[t] += dh @ A
-        ex[t] += (ed + err(r) * (dh.abs() + ed)) @ A.abs()
+        ex[t] += (ed + err(2 * r) * (dh.abs() + ed) * (1 + BF)) @ A.abs()
         kept = hidden[0, t].double() + hidden[1, t].double()
         rd, ref = dh.t() @ xa, ya.t() @ kept
-        # (dh is kept to 2^-16 of itself there, hidden is as it was kept)
-        ek = c * (ya.abs() @ B.abs()) * (err(N) + 2 * U) + BF * BF * dh.abs()
-        close(ddown[a], rd, rd.abs() * BF + (ek + err(len(t)) * (dh.abs() + ek)).t() @ xa.abs() * (1 + BF) + TINY, f"ddown {a}")
+        close(ddown[a], rd, rd.abs() * BF + (ed + err(len(t)) * (dh.abs() + ed)).t() @ xa.abs() * (1 + BF) + TINY, f"ddown {a}")
         close(dup[a], ref, ref.abs() * BF + err(len(t)) * (ya.abs().t() @ hidden[:, t].double().abs().sum(0)) + TINY, f"dup {a}")
     close(hidden[0], rh, eh + TINY, "hidden")
     # the two together are h to 2^-16 of it, besides its sums
