@@ -188,7 +188,10 @@ __device__ __forceinline__ bool keep_groups(const RouteRule &r, T (&key)[V], int
     // (of the fp32 keys alone; the largest of the negated is the lowest)
     const float low = -unordered(wave_max(keep ? ordered(-float(score)) : 0u));
     const float high = unordered(wave_max(keep || group >= r.groups ? 0u : ordered(float(score))));
-    return high > -INFINITY && !(low - high > float(slack) * (1.0f + fabsf(low)));
+    // a sum is off by what its two keys are, which goes with their size: with biases that cancel the sum is small, its
+    // error is not
+    const float most = wave_max(fmaxf(one > none ? fabsf(float(one)) : 0.0f, two > none ? fabsf(float(two)) : 0.0f));
+    return high > -INFINITY && !(low - high > float(slack) * (1.0f + most));
 }
 
 // The K largest keys, largest first, ties to the lowest index: lane k returns the k-th, -1 where
