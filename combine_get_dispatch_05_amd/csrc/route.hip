@@ -357,9 +357,10 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteBack
             d = whole ? s * (ds - inner) : 0.0f;
             d += r.normalize ? add : 0.0f;
         } else {
-            const float s = raw(l);
             const float ds = add + (whole && sum != 0.0f ? (q_at(j) - inner) / sum : 0.0f);
-            d = ds * s * (1.0f - s);
+            // s (1 - s), from exp(-|l|): 1 - s of a rounded s would be nothing from l = 17 on
+            const float x = expf(-fabsf(l)), y = 1.0f + x;
+            d = ds * (x / (y * y));
         }
         put_logit<BF16>(a.dlogits, row + at, d);
     });

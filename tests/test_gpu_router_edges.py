@@ -10,7 +10,9 @@ import torch
 pytestmark = pytest.mark.gpu
 
 import combine_get_dispatch_05_amd as epm  # noqa: E402
-from test_gpu_router import choose, gen  # noqa: E402
+from test_gpu_router import choose, close, gen, weigh  # noqa: E402
+
+U = 2.0 ** -24
 
 
 @pytest.fixture(autouse=True)
@@ -62,3 +64,43 @@ def test_the_layer_with_biases_that_cancel_inside_a_group(T):
         want = choose((x.double() @ wr.double().t()).float().double(), r, bias)
         _, idx, _ = buf.low_latency_moe(x, wr, r, w13, w2, bias=bias)
         assert torch.equal(idx, want)
+
+
+@pytest.mark.parametrize("E", [12, 128, 512, 600])
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("with_sums", [False, True])
+def test_sigmoid_gradient_of_large_logits(E, normalize, with_sums):
+    """s (1 - s) keeps its digits on both sides.  The slope of a logit is exact but for its exponential (2 U), a sum, a
+    square and a quotient (5 U with what the sum's rounding does in the square); a choice's part of ds is a product, normalised a difference of
+    the slot's own gradient and the mean over 6 slots, over their sum; the sums' part one of a mean over E."""
+    g = gen(E)
+    T, K = 30, 6
+    l = torch.tensor([-80.0, -30, -17, -16, -10, 0, 10, 16, 17, 20, 30, 80], device="cuda").repeat(T, -(-E // 12))[:, :E]
+    l = (l + torch.rand((T, E), generator=g, device="cuda")).gather(1, torch.rand((T, E), generator=g, device="cuda").argsort(1))
+    r = epm.Router(K, score="sigmoid", normalize=normalize, scale=1.5)
+    buf = epm.Buffer(1, E)
+    idx = torch.rand((T, E), generator=g, device="cuda").argsort(1)[:, :K].contiguous()  # any experts, not the largest alone
+    dw = torch.randn((T, K), generator=g, device="cuda")
+    q = torch.randn(E, generator=g, device="cuda") if with_sums else None
+    dl = buf.route_backward(dw, l, idx, r, dscore_sums=q)
+    ld = l.double()
+    s = torch.sigmoid(ld)
+    slope = s * torch.sigmoid(-ld)
+    c = dw.double() * r.scale
+    mag = c.abs()
+    if normalize:
+        share = weigh(s, idx, epm.Router(K, score="sigmoid"), ld)
+        of = s.gather(1, idx).sum(1, keepdim=True) + 1e-20
+        c, mag = (c - (c * share).sum(1, keepdim=True)) / of, (mag + (mag * share).sum(1, keepdim=True)) / of
+    ds = torch.zeros_like(ld).scatter_add(1, idx, c)
+    mag = torch.zeros_like(ld).scatter_add(1, idx, mag)
+    if with_sums:
+        total, p = s.sum(1, keepdim=True), s / s.sum(1, keepdim=True)
+        ds = ds + (q.double() - (q.double() * p).sum(1, keepdim=True)) / total
+        mag = mag + (q.double().abs() + (q.double().abs() * p).sum(1, keepdim=True)) / total
+    # (sums over a row: at most 40 terms deep)
+    rel = 16 * U if not (normalize or with_sums) else 128 * U
+    close(dl, ds * slope, mag * slope * rel + 2.0 ** -120, "dlogits")
+    if not (normalize or with_sums):
+        got = dl.gather(1, idx)[(dw.abs() > 0.01) & (l.gather(1, idx).abs() < 60)]
+        assert (got != 0).all()
