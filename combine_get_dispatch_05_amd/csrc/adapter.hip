@@ -601,7 +601,7 @@ struct AdapterGradArgs {
     const char *narrow[2];  // dh, h: [2][T][r], sums of two bf16 values
     uint16_t *out[2];       // dA [L][r][K], dB [L][N][r]
     int width[2];
-    int blocks;             // of the first
+    int blocks[2];          // of both
 };
 
 // 64 columns of one adapter: sum over its tokens of wide[t][c] * narrow[t][j].  The waves share out the tokens, 64 a
@@ -728,10 +728,11 @@ __global__ __launch_bounds__(kAdapterThreads) void adapter_grads_kernel(AdapterG
 {
     constexpr int kStages = kAdapterWaves * kGradStage<RT>, kSums = kAdapterWaves * RT * 4 * kWave * 16;
     __shared__ __attribute__((aligned(128))) char lds[kStages > kSums ? kStages : kSums];
-    if (int(blockIdx.x) < g.blocks)
-        adapter_grad<RT, true, SCAN>(g, blockIdx.x, lds);
-    else
-        adapter_grad<RT, false, SCAN>(g, int(blockIdx.x) - g.blocks, lds);
+    const int block = int(blockIdx.y) * int(kRowGrid) + int(blockIdx.x);  // (row_grid; fewer than 2^28)
+    if (block < g.blocks[0])
+        adapter_grad<RT, true, SCAN>(g, block, lds);
+    else if (block - g.blocks[0] < g.blocks[1])
+        adapter_grad<RT, false, SCAN>(g, block - g.blocks[0], lds);
 }
 
 // ---------------------------------------------------------------- launches
@@ -934,12 +935,12 @@ hipError_t launch_adapter_backward(const AdapterShape &s, const void *dy, const 
     g.out[1] = static_cast<uint16_t *>(dup);
     g.width[0] = s.K;
     g.width[1] = s.N;
-    g.blocks = s.L * ((s.K + 63) / 64);
-    const unsigned all = unsigned(g.blocks + s.L * ((s.N + 63) / 64));
+    for (int i = 0; i < 2; ++i)
+        g.blocks[i] = s.L * ((g.width[i] + 63) / 64);
     return by_rank(s.r, [&](auto rt) {
         constexpr int RT = decltype(rt)::value;
-        hipLaunchKernelGGL((scans(s.T, s.L) ? adapter_grads_kernel<RT, true> : adapter_grads_kernel<RT, false>), dim3(all),
-                           dim3(kAdapterThreads), 0, stream, g);
+        hipLaunchKernelGGL((scans(s.T, s.L) ? adapter_grads_kernel<RT, true> : adapter_grads_kernel<RT, false>),
+                           row_grid(int64_t(g.blocks[0]) + g.blocks[1]), dim3(kAdapterThreads), 0, stream, g);
         return hipGetLastError();
     });
 }

@@ -213,6 +213,7 @@ hipError_t launch_moe(const RouteRule &rule, const MoeCall &call, hipStream_t st
 
 constexpr int kMaxRank = 128;
 constexpr int kMaxAdapters = 8192;
+constexpr int64_t kMaxGradBlocks = int64_t(1) << 27;  // of 64 columns of an adapter: at rank 8 weights and gradients of 275 GB
 
 struct AdapterShape {
     int T, K, N, r, L;

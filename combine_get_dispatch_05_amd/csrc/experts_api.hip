@@ -182,9 +182,9 @@ int ep_adapter_product_backward(const ep_adapter_dims *dims, const void *dy, con
     if (!al(dy, 16) || !al(x, 16) || !al(down, 16) || !al(up, 16) || !al(hidden, 16) || !al(dx_base, 16) || !al(dx, 16) ||
         !al(ddown, 16) || !al(dup, 16) || !al(workspace, 256) || !al(adapter_ids, 8) || !al(scales, 4))
         return EP_ERR_ALIGN;
-    // the gradients' blocks are one launch
+    // the gradients' blocks are one launch, counted in 32 bits
     const int64_t runs = (int64_t(dims->in_features) + 63) / 64 + (int64_t(dims->out_features) + 63) / 64;
-    if (dims->num_adapters * runs > kMaxTileBlocks)
+    if (dims->num_adapters * runs > kMaxGradBlocks)
         return EP_ERR_INVALID;
     if (workspace_bytes < ep_adapter_workspace(dims, 1))
         return EP_ERR_CAPACITY;

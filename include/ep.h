@@ -604,6 +604,8 @@ int ep_adapter_product(const ep_adapter_dims *dims, const void *x, const int64_t
  * h and dh there to 2^-16 of themselves (an infinite dy or x gives infinities or NaN)
  * dx_base [T][in] (nullable) is the projection's own gradient of x; dx may be the same memory.  ddown and
  * dup are overwritten whole (zeros for adapters without tokens).  hidden is ep_adapter_product's.
+ * num_adapters * (ceil(in / 64) + ceil(out / 64)) <= 2^27 (EP_ERR_INVALID past it: weights and gradients of
+ * 275 GB and more).
  * workspace: ep_adapter_workspace(dims, 1) bytes.  No host sync.
  */
 int ep_adapter_product_backward(const ep_adapter_dims *dims, const void *dy, const void *x,
