@@ -37,7 +37,8 @@ constexpr int ahead(bool fp8, int C, int RT, int MT, int planes = 1)
     return n < 2 ? 2 : n < 4 ? n : 4;
 }
 
-constexpr int kLogitSplits = 8;  // at most
+constexpr int kLogitSplits = 8;    // at most, a power of two
+constexpr int kLogitLeaves = 256;  // at most, likewise
 
 // The activation between the products is the matrix instruction's operand.  One rounding to bf16 makes the result's
 // error against 64 bits 1.4 times what its own rounding is (2.4e-3 of the norm instead of 1.7e-3).  Beside bf16
@@ -58,81 +59,140 @@ struct MoeWork {
 
 // ----------------------------------------------------------------- router
 
-// logits[t][e] in 64 bits, so that a choice depends neither on the batch nor on the order of a sum.
-// Eight values of a router row as doubles.
-template <bool F32>
-__device__ __forceinline__ void router8(const void *w, int64_t v, double (&d)[8])
+// logits[t][e] in 64 bits, so that a choice does not depend on fp32's order of a sum, and in one order, so that it does
+// not depend on the batch: chunks of eight values lie in `leaves` classes, chunk v in class v % leaves; a class is a
+// sum of its own, four chunks at a time and value by value of them; and the classes are the leaves of a binary tree.
+__host__ __device__ inline int logit_leaves(int V)
 {
-    if constexpr (F32) {
-        const float4 a = static_cast<const float4 *>(w)[2 * v], b = static_cast<const float4 *>(w)[2 * v + 1];
-        d[0] = a.x, d[1] = a.y, d[2] = a.z, d[3] = a.w, d[4] = b.x, d[5] = b.y, d[6] = b.z, d[7] = b.w;
-    } else {
-        const u32x4 a = static_cast<const u32x4 *>(w)[v];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            d[2 * q] = bf16_lo(a[q]), d[2 * q + 1] = bf16_hi(a[q]);
-    }
+    int n = 4 * kLogitSplits;  // (one a wave at least)
+    while (n < kLogitLeaves && n * 4 < V)
+        n *= 2;
+    return n;
 }
 
-// One token: an expert a block.
+// Eight values of a row, zeros where there are none.
 template <bool F32>
-__global__ __launch_bounds__(256) void moe_logits_kernel(const u32x4 *x, const void *w_router, int E, int V, double *logits)
-{
-    __shared__ double red[4];
-    const int e = blockIdx.x;
-    double acc = 0;
-    for (int v = threadIdx.x; v < V; v += 256) {
-        double w[8];
-        router8<F32>(w_router, int64_t(e) * V + v, w);
-        const u32x4 b = x[v];
+struct Chunk {
+    u32x4 bits[F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void *row, int v, int V)
+    {
+        const u32x4 none = {};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            acc = fma(w[2 * q], double(bf16_lo(b[q])), acc);
-            acc = fma(w[2 * q + 1], double(bf16_hi(b[q])), acc);
+        for (int h = 0; h < (F32 ? 2 : 1); ++h) {
+            const u32x4 b = static_cast<const u32x4 *>(row)[int64_t(v < V ? v : V - 1) * (F32 ? 2 : 1) + h];
+            bits[h] = v < V ? b : none;
         }
     }
-    acc = wave_sum(acc);
+    __device__ __forceinline__ double at(int i) const
+    {
+        if constexpr (F32)
+            return __uint_as_float(bits[i >> 2][i & 3]);
+        else
+            return i & 1 ? bf16_hi(bits[0][i >> 1]) : bf16_lo(bits[0][i >> 1]);
+    }
+};
+template <bool F32>
+__device__ __forceinline__ const void *router_row(const void *w, int e, int V)
+{
+    return static_cast<const u32x4 *>(w) + int64_t(e) * V * (F32 ? 2 : 1);
+}
+
+// One token: an expert a block, a class a thread (H = 7168, 256 experts: 4.9 us, on the matrix cores 8.3).
+template <bool F32>
+__global__ __launch_bounds__(256) void moe_logits_one_kernel(const u32x4 *x, const void *w_router, int E, int V, double *logits)
+{
+    __shared__ double red[4];
+    const int leaves = logit_leaves(V), leaf = threadIdx.x;
+    const void *row = router_row<F32>(w_router, blockIdx.x, V);
+    double acc = 0;
+    if (leaf < leaves)
+        for (int v = leaf; v < V; v += 4 * leaves) {
+            Chunk<F32> w[4];
+            Chunk<false> q[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                w[g].load(row, v + g * leaves, V);
+                q[g].load(x, v + g * leaves, V);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    acc = fma(w[g].at(i), q[g].at(i), acc);
+        }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1)
+        acc += __shfl_xor(acc, d);
     if ((threadIdx.x & 63) == 0)
         red[threadIdx.x >> 6] = acc;
     __syncthreads();
     if (threadIdx.x == 0)
-        logits[e] = red[0] + red[1] + red[2] + red[3];
+        logits[blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// More: 16 experts by 16 tokens a block on the matrix cores, K shared out over its waves and gridDim.z blocks.
+// More: 16 experts by 16 tokens a block on the matrix cores, whose 64-bit instruction adds its four products one after the
+// other, each rounded, as fma() does.  A wave has whole branches of the tree, gridDim.z blocks share a tile's.
 template <bool F32>
-__global__ __launch_bounds__(256) void moe_logits_tile_kernel(const u32x4 *x, const void *w_router, int T, int E, int V,
-                                                              double *logits)
+__global__ __launch_bounds__(256) void moe_logits_kernel(const u32x4 *x, const void *w_router, int T, int E, int V,
+                                                         double *logits)
 {
     typedef double f64x4 __attribute__((ext_vector_type(4)));
     __shared__ double sums[4][16][16];
+    constexpr int kOnce = 8, kLevels = 3;  // classes whose loads are in flight together; levels above them inside a wave
+    static_assert(kLogitLeaves / 4 <= kOnce << kLevels, "a wave's branches");
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16;
     const int e = e0 + (lane & 15) < E ? e0 + (lane & 15) : E - 1, t = t0 + (lane & 15) < T ? t0 + (lane & 15) : T - 1;
-    const int steps = (V + 3) / 4, part = int(blockIdx.z) * 4 + wave, of = int(gridDim.z) * 4;
-    f64x4 acc = {};
-    for (int s = steps * part / of; s < steps * (part + 1) / of; ++s) {
-        const int v = s * 4 + (lane >> 4);
-        double w[8] = {}, q[8] = {};
-        if (v < V) {
-            router8<F32>(w_router, int64_t(e) * V + v, w);
-            router8<false>(x, int64_t(t) * V + v, q);
+    const void *row = router_row<F32>(w_router, e, V), *token = router_row<false>(x, t, V);
+    const int leaves = logit_leaves(V), per = leaves / (4 * int(gridDim.z));
+    f64x4 left[kLevels], sum = {};  // of a level's pair, the first
+    for (int n = 0; n * kOnce < per; ++n) {
+        const int first = (int(blockIdx.z) * 4 + wave) * per + n * kOnce;
+        f64x4 acc[kOnce] = {};
+        for (int v0 = first; v0 < V; v0 += 4 * leaves) {
+            Chunk<F32> w[kOnce];
+            Chunk<false> q[kOnce];
+#pragma unroll
+            for (int k = 0; k < kOnce; ++k)
+                if (k < per) {
+                    w[k].load(row, v0 + k + (lane >> 4) * leaves, V);
+                    q[k].load(token, v0 + k + (lane >> 4) * leaves, V);
+                }
+#pragma unroll
+            for (int k = 0; k < kOnce; ++k)
+                if (k < per)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        acc[k] = __builtin_amdgcn_mfma_f64_16x16x4f64(w[k].at(c), q[k].at(c), acc[k], 0, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            acc = __builtin_amdgcn_mfma_f64_16x16x4f64(w[i], q[i], acc, 0, 0, 0);
+        for (int d = 1; d < kOnce; d <<= 1)
+#pragma unroll
+            for (int k = 0; k < kOnce; k += 2 * d)
+                acc[k] += acc[k + d];
+        sum = acc[0];
+        bool pair = true;  // (a binary counter: where a level's first is there, the two go up together)
+#pragma unroll
+        for (int k = 0; k < kLevels; ++k) {
+            const bool second = n >> k & 1;
+            if (pair && second)
+                sum = left[k] + sum;
+            else if (pair)
+                left[k] = sum;
+            pair = pair && second;
+        }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)  // expert 4 i + l / 16, token l % 16
-        sums[wave][lane & 15][4 * i + (lane >> 4)] = acc[i];
+    for (int k = 0; k < 4; ++k)  // expert 4 k + l / 16, token l % 16
+        sums[wave][lane & 15][4 * k + (lane >> 4)] = sum[k];
     __syncthreads();
     const int i = threadIdx.x >> 4, j = threadIdx.x & 15;
     if (t0 + i < T && e0 + j < E)
         logits[(int64_t(blockIdx.z) * T + t0 + i) * E + e0 + j] =
-            sums[0][i][j] + sums[1][i][j] + sums[2][i][j] + sums[3][i][j];
+            (sums[0][i][j] + sums[1][i][j]) + (sums[2][i][j] + sums[3][i][j]);
 }
 
-// The sum of the parts, all loads in flight; -inf past the last expert.
+// The sum of the blocks' parts, the upper levels of their tree, all loads in flight; -inf past the last expert.
 __device__ __forceinline__ float logit_of(const MoeWork &work, int T, int E, int t, int e)
 {
     double part[kLogitSplits] = {};
@@ -141,9 +201,24 @@ __device__ __forceinline__ float logit_of(const MoeWork &work, int T, int E, int
         if (i < work.splits && e < E)
             part[i] = work.logits[(int64_t(i) * T + t) * E + e];
 #pragma unroll
-    for (int i = 1; i < kLogitSplits; ++i)
-        part[0] += part[i];
+    for (int n = kLogitSplits / 2; n > 0; n /= 2)
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+            part[i] = part[2 * i] + part[2 * i + 1];
     return e < E ? float(part[0]) : -INFINITY;
+}
+
+// The logit of expert e out of the lane that has it.
+template <int V>
+__device__ __forceinline__ float held_logit(const float (&l)[V], int e)
+{
+    float v = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const float o = __shfl(l[j], e & 63);
+        v = e >> 6 == j ? o : v;
+    }
+    return v;
 }
 
 // All tokens' choices, and the pairs by expert: bit t of an expert's mask is token t.
@@ -315,7 +390,7 @@ __device__ __forceinline__ ActiveExpert choose_one(const MoeArgs &a, const MoeCh
             bias[j] = r.bias != nullptr && e < r.experts ? r.bias[e] : 0.0f;
         }
         const int e = route_row(r, l, bias, live_experts<V>(r, lane), lane, reinterpret_cast<double *>(lds), false, false, s,
-                                [&](int i) { return float(a.work.logits[i]); }, w);
+                                [&](int i) { return held_logit(l, i); }, w);
         chosen[lane] = e;
         if (blockIdx.x == 0 && blockIdx.y == 0 && lane < r.topk) {
             c.topk_idx[lane] = e;
@@ -350,15 +425,15 @@ __device__ __forceinline__ ActiveExpert choose_few(const MoeArgs &a, const MoeCh
     __syncthreads();
     if (t < a.T) {
         float l[V], s[V] = {}, bias[V], w;
-        auto logit = [&](int e) { return logit_of(a.work, a.T, r.experts, t, e); };
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int e = j * 64 + lane;
-            l[j] = logit(e);
+            l[j] = logit_of(a.work, a.T, r.experts, t, e);
             bias[j] = r.bias != nullptr && e < r.experts ? r.bias[e] : 0.0f;
         }
         double *scratch = reinterpret_cast<double *>(lds) + t * V * 64;
-        const int e = route_row(r, l, bias, live_experts<V>(r, lane), lane, scratch, false, false, s, logit, w);
+        const int e = route_row(r, l, bias, live_experts<V>(r, lane), lane, scratch, false, false, s,
+                                [&](int i) { return held_logit(l, i); }, w);
         if (lane < r.topk) {
             ids[t * r.topk + lane] = int16_t(e);
             weights[t * r.topk + lane] = w;
@@ -552,13 +627,16 @@ __global__ __launch_bounds__(kDownWaves *kWave) void moe_down_kernel(MoeArgs a, 
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Blocks that share a tile's K: some 256 in all.
+// Blocks that share a tile's K: at most 256 in all, and whole branches of the classes' tree.
 int logit_splits(int T, int E)
 {
     if (T <= 1)
         return 1;
-    const int n = 256 / ((E + 15) / 16 * ((T + 15) / 16));
-    return n < 1 ? 1 : n < kLogitSplits ? n : kLogitSplits;
+    const int tiles = (E + 15) / 16 * ((T + 15) / 16);
+    int n = kLogitSplits;
+    while (n > 1 && n * tiles > 256)
+        n /= 2;
+    return n;
 }
 
 // Lays the workspace out at base; returns its bytes.
@@ -598,10 +676,10 @@ hipError_t launch_moe(const RouteRule &rule, const MoeCall &c, hipStream_t strea
         log_launch("ll_moe: T=%d H=%d I=%d E=%d K=%d%s", c.T, c.H, c.I, E, rule.topk, fp8 ? " fp8" : "");
     const u32x4 *x = static_cast<const u32x4 *>(c.x);
     if (c.T == 1)
-        hipLaunchKernelGGL((c.router_f32 ? moe_logits_kernel<true> : moe_logits_kernel<false>), dim3(E), dim3(256), 0, stream, x,
-                           c.w_router, E, V, a.work.logits);
+        hipLaunchKernelGGL((c.router_f32 ? moe_logits_one_kernel<true> : moe_logits_one_kernel<false>), dim3(E), dim3(256), 0,
+                           stream, x, c.w_router, E, V, a.work.logits);
     else
-        hipLaunchKernelGGL((c.router_f32 ? moe_logits_tile_kernel<true> : moe_logits_tile_kernel<false>),
+        hipLaunchKernelGGL((c.router_f32 ? moe_logits_kernel<true> : moe_logits_kernel<false>),
                            dim3((E + 15) / 16, (c.T + 15) / 16, a.work.splits), dim3(256), 0, stream, x, c.w_router, c.T, E, V,
                            a.work.logits);
     hipError_t e = hipGetLastError();

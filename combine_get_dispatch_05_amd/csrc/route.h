@@ -360,7 +360,8 @@ __device__ __forceinline__ int route_row(const RouteRule &r, const float (&l)[V]
     if (unsure)
         e = choose_exactly(r, l, bias, live, lane, scratch);
     const bool have = e >= 0;
-    const float v = have ? at(e) : -INFINITY;
+    const float of = at(have ? e : 0);  // (every lane takes part)
+    const float v = have ? of : -INFINITY;
     float one, sum;
     if (r.soft && r.normalize) {  // the softmax of the chosen alone
         const float big = wave_max(v);

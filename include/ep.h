@@ -550,7 +550,7 @@ int ep_route_backward(const ep_dims *dims, const ep_router *router, const float 
 /*
  * A whole mixture-of-experts layer for a few tokens: router, experts and combine in one call, no rows
  * packed in between.
- *   logits[t][e] = fp32(x[t] . w_router[e]), summed in 64 bits
+ *   logits[t][e] = fp32(x[t] . w_router[e]), summed in 64 bits, in one order for every num_tokens
  *   topk_idx, topk_weights as ep_route gives them for these logits
  *   y[t] = bf16_rne( residual[t] + sum over its experts, fp32, of weight * (act W2^T) ), act as for
  *          ep_ll_expert_ffn, kept to 2^-16 of itself between the products beside bf16 weights and
