@@ -510,7 +510,9 @@ int ep_expert_ffn_backward(const ep_dims *dims, int32_t inter, const ep_expert_g
  * An expert whose logit is -inf or NaN, or whose rank is masked, is not chosen.  Slots for which
  * nothing is left get -1 and weight 0.  The choice is that of exact keys: gaps within fp32 rounding are
  * decided in 64 bits.  Weights are fp32.  Scores are not changed by the mask.  A row of
- * -inf alone has scores 0; a softmax row with +inf or NaN has NaN for scores and weights.
+ * -inf alone has scores 0.  A softmax row with +inf or NaN has NaN for scores: with a bias it has no keys
+ * and nothing is chosen, without one its weights are NaN, but normalised ones, which are of the chosen logits
+ * alone, only where +inf is among those.  A NaN logit makes all of its row's part of the score sums NaN.
  */
 #define EP_SCORE_SOFTMAX 0
 #define EP_SCORE_SIGMOID 1

@@ -2,6 +2,7 @@
 
 from __future__ import annotations
 
+import math
 import sys
 
 import pytest
@@ -104,3 +105,34 @@ def test_sigmoid_gradient_of_large_logits(E, normalize, with_sums):
     if not (normalize or with_sums):
         got = dl.gather(1, idx)[(dw.abs() > 0.01) & (l.gather(1, idx).abs() < 60)]
         assert (got != 0).all()
+
+
+@pytest.mark.parametrize("E", [40, 640])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_softmax_rows_that_are_not_finite(E, bad):
+    """Scores that are NaN are no keys beside a bias; weights of the chosen alone do not see a NaN that is not chosen."""
+    l = torch.arange(E, device="cuda").flip(0).float().repeat(2, 1) / E
+    l[0, 5] = bad
+    buf, none = epm.Buffer(1, E), torch.zeros(E, device="cuda")
+    for normalize in (False, True):
+        r = epm.Router(3, normalize=normalize)
+        idx, w, sums = buf.route(l, r, bias=none, score_sums=True)
+        assert (idx[0] == -1).all() and (w[0] == 0).all() and idx[1].tolist() == [0, 1, 2]
+        assert sums.isnan().all()
+        idx, w, sums = buf.route(l, r, score_sums=True)
+        assert idx.tolist() == [[5, 0, 1] if bad == math.inf else [0, 1, 2], [0, 1, 2]] and sums.isnan().all()
+        assert w[1].isfinite().all()
+        if bad == math.inf or not normalize:
+            assert w[0].isnan().all()
+        else:
+            assert torch.equal(w[0], w[1])
+
+
+@pytest.mark.parametrize("E", [40, 640])
+def test_sigmoid_rows_with_a_nan_leave_the_others_choice_and_weights(E):
+    l = torch.zeros((2, E), device="cuda")
+    l[0, 1] = math.nan
+    buf, r = epm.Buffer(1, E), epm.Router(2, score="sigmoid", normalize=False)
+    for bias in (None, torch.zeros(E, device="cuda")):
+        idx, w, sums = buf.route(l, r, bias=bias, score_sums=True)
+        assert idx.tolist() == [[0, 2], [0, 1]] and (w == 0.5).all() and sums.isnan().all()
