@@ -3,11 +3,14 @@
 //   dh[t] = c_a (dy[t] B_a),  dx[t] = dx_base[t] + dh[t] A_a,  dA_a = sum_t dh[t]^T x[t],  dB_a = sum_t dy[t]^T h[t]
 // A block takes a tile of tokens that share an adapter: of few tokens it looks for them itself, more are sorted by
 // adapter first.  The inner products to the rank (shrink) split K over waves and blocks; the products back
-// (expand) sum those parts to h and add the
-// base.  All of it is bound by memory: each row is read and written once.
-// 8192 tokens, K = N = 7168, rank 64, 16 adapters: 113 us (sort 8, shrink 39, expand 67) for 352 MB of rows, 3.1 TB/s.
+// (expand) sum those parts to h and add the base.  Rows are what it has to move: the forward pass reads and writes each
+// once, the backward pass reads x once, and dy twice, for dh and for dB.
+// 8192 tokens, K = N = 7168, rank 64, 16 adapters: 113 us (sort 8, shrink 39, expand 67) for 352 MB of rows, 3.1 TB/s;
+// both products hold more than 256 registers (264 and 292 with the accumulators), so one block runs on a compute unit
+// and nothing hides its waits.
 // A step of 4096 tokens, N = 4096, rank 32, 8 adapters: 117 us (sort 5 twice; out 16 + 22, dx 12 + 30, the
-// gradients 25) for 369 MB of rows, dy among them twice.  One token 9.6 us, of which 8.8 are the kernel's; 128 tokens on 64 adapters 14 (6.7 + 6.9).
+// gradients 25) for 369 MB of rows, dy among them twice; two blocks of each product a unit, two of the gradients'.
+// One token 9.6 us, of which 8.8 are the kernel's; 128 tokens on 64 adapters 14 (6.7 + 6.9).
 #include "stream.h"
 
 namespace ep {
@@ -15,7 +18,9 @@ namespace ep {
 namespace {
 
 constexpr int kAdapterThreads = 256, kAdapterWaves = kAdapterThreads / kWave;
-constexpr int kCard = 256;  // compute units that launches are shaped for (results do not depend on it, nor workspaces on the device)
+// Compute units that launches are shaped for, the same on every device, so that workspaces and results are too: it decides,
+// with T, L and r, how sums over K are split.
+constexpr int kCard = 256;
 
 struct AdapterArgs {
     int T, L, r;
@@ -35,7 +40,8 @@ struct AdapterArgs {
 
 // ---------------------------------------------------------------- grouping
 
-// Block a: where adapter a's tokens start, and they in order.  Block L: those with no adapter.
+// Block a: where adapter a's tokens start, and they in order.  Block L: those with no adapter.  Each block reads all ids
+// twice: 8 us for 8192 tokens on 16 adapters, 15 on 1024; 131072 tokens take 210 on 1024 and 1190 on 8192.
 constexpr int kSortThreads = 1024;
 __global__ __launch_bounds__(kSortThreads) void adapter_group_kernel(AdapterArgs a)
 {
@@ -532,7 +538,8 @@ __device__ __forceinline__ void few_parts(const AdapterArgs &a, int adapter, con
         prow[j] = w + int64_t(row < a.r ? row : a.r - 1) * width * 2;
     }
     f32x4 acc[TILES][1] = {};
-    // (a run of 14 steps, K = 7168, goes in two rounds)
+    // steps in flight: as many as some 100 registers hold, 12, 20 and 36 a step; 7 for 8, as runs are rounded up to them and
+    // 14 steps (K = 7168) are two rounds
     stream<false, TAIL, (RT == 1 ? 7 : RT == 2 ? 5 : 3), C>(prow, none, qrow, steps * wave / kFewWaves,
                                                            steps * (wave + 1) / kFewWaves, width * 2, lane, acc);
 #pragma unroll
@@ -747,7 +754,8 @@ int64_t most_tiles(int64_t T, int L, int r)
 }
 // Blocks of a launch that go by tile, or by adapter.
 unsigned tile_blocks(int64_t T, int L, int r) { return unsigned(scans(T, L) ? L + 1 : most_tiles(T, L, r)); }
-// Blocks that share a tile's K: so many that the card is full twice, each wave at least one step.
+// Blocks that share a tile's K: as many as make two a compute unit, each wave at least one step.  Up to rank 32 two or
+// three fit a unit's registers; of rank 64 and more one does, and the second follows it.
 int shrink_splits(int64_t T, int L, int r, int width)
 {
     const int64_t steps = (width + 63) / 64, most = (steps + kAdapterWaves - 1) / kAdapterWaves;
@@ -756,8 +764,11 @@ int shrink_splits(int64_t T, int L, int r, int width)
 }
 
 // One launch for few tokens, as long as every block that makes h again has a compute unit to itself and
-// little to read: 8 tokens, K = 7168, rank 16, a call 9.6 us against 13.4 in two launches (the host's time); rank 64 27.8
-// in two, 36.9 in one.
+// little to read.  r K <= 2^17 lies between two borders (us, one launch against two, one token on 8 adapters, N = 2048; 16
+// tokens and N = 7168 give the same).  Called one by one, where the host's time counts, one launch wins up to twice that:
+// rank 16, K = 7168 9.8 against 14.0; rank 64, K = 1024 9.6 against 14.0, K = 2048 11.1 against 14.0, K = 4096 13.9 against
+// 13.8.  Replayed in a graph it wins up to half of it: rank 16, K = 2048 6.4 against 7.2, K = 4096 8.1 against 7.7, K = 7168
+// 8.3 against 8.6; rank 64, K = 1024 7.2 against 8.5, K = 2048 11.2 against 8.5 (that kernel spills 16 registers).
 bool few(const AdapterShape &s)
 {
     const int64_t runs = (s.N + kFewWaves * 64 - 1) / (kFewWaves * 64);
@@ -857,9 +868,9 @@ hipError_t expand(AdapterArgs &a, const void *w, int width, const void *base, vo
         constexpr int kRun = kAdapterWaves * 64;
         const bool scan = scans(a.T, a.L);
         const int64_t tiles = most_tiles(a.T, a.L, a.r), runs = (width + kRun - 1) / kRun;
-        // Blocks that share a tile's columns: two a compute unit, each then has several steps behind its start (8192 rows
-        // of 7168, rank 64, h as one value: 64.0 us, with four 68.3); four where each finds its tokens itself, many of them none
-        // (128 tokens on 64 adapters: 6.9 us, with two 7.4).
+        // Blocks that share a tile's columns: as many as make two a compute unit, each then has several steps behind its start
+        // (8192 rows of 7168, rank 64, where one fits a unit, h as one value: 64.0 us, with four 68.3); four where each finds
+        // its tokens itself, many of them none (128 tokens on 64 adapters, rank 16, where two fit: 6.9 us, with two 7.4).
         int64_t n = (scan ? 4 : 2) * kCard / tiles;
         n = n < 1 ? 1 : n < runs ? n : runs;
         const int columns = int((runs + n - 1) / n) * kRun;

@@ -7,7 +7,7 @@
 // in flight.  FP8 weights are widened to bf16 there, exactly, so that rows and
 // activations keep their bf16 values.
 // Bound by the weights where there are many, 32 tokens on 64 FP8 experts of 2048 x 7168: 472 us for 2.8 GB,
-// 6.0 TB/s (logits 11, choice 14, gate and up 316, down 156).  One token, eight experts: FP8 2048 x 7168 82 us
+// 6.0 TB/s (logits 9, choice 13, gate and up 310, down 151).  One token, eight experts: FP8 2048 x 7168 82 us
 // (5 + 52 + 25) for 356 MB; bf16 768 x 2048 22 us (3 + 13.5 + 7.4) for 76 MB, three launches whose starts and ends
 // are half of it.
 #include "route.h"

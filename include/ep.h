@@ -562,7 +562,8 @@ int ep_route_backward(const ep_dims *dims, const ep_router *router, const float 
  * w13 [E][2 inter][hidden], w2 [E][hidden][inter]: bf16, or with w13_scale and w2_scale (both or neither)
  * FP8 codes and scales as for ep_ll_expert_ffn_fp8.  Beside FP8 weights too, x and
  * act are bf16: every product is exact and summed in fp32, the scales applied once per 128 of K.
- * A token's experts do not depend on the batch it comes in.
+ * A token's experts and weights do not depend on the batch it comes in; y's rounding can, as the batch decides how
+ * its sums are split.
  * num_tokens <= 64 and E <= 512 (EP_ERR_TOO_LARGE); hidden % 8 == 0 and inter % 8 == 0, with FP8
  * % 128 (EP_ERR_ALIGN).  workspace: ep_ll_moe_workspace() bytes, 256-byte aligned
  * (EP_ERR_CAPACITY if workspace_bytes is less).  No host sync.
@@ -583,6 +584,9 @@ int ep_ll_moe(const ep_dims *dims, int32_t inter, const ep_router *router, const
  *   base [T][out] bf16, nullable; out [T][out] may be the same memory as base
  *   hidden [2][T][rank] bf16, nullable: h, which the backward pass takes, as the sum of its bf16 value
  *     and of what that rounding lost (zeros without an adapter)
+ * The same call gives the same bits every time; a token's result can differ in its rounding with T and L, which
+ * decide how the sums over in are split.  Past 256 tokens or 127 adapters the tokens are sorted by adapter first, in
+ * a time that grows with T * L (8 us for 8192 tokens on 16 adapters, 15 on 1024, 0.2 ms for 131072 on 1024, 1.2 ms on 8192).
  * in, out and rank % 8 == 0 (EP_ERR_ALIGN), rank <= 128, L <= 8192.  workspace: ep_adapter_workspace(dims, 0)
  * bytes, 256-byte aligned (EP_ERR_CAPACITY if workspace_bytes is less; 0, so that it may be null, for a few
  * tokens).  No host sync.
