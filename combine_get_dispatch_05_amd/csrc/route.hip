@@ -223,6 +223,11 @@ __global__ __launch_bounds__(kRouteThreads) void route_wide_kernel(RouteArgs a)
 //             normalised: dl_k += share_k (c_k - sum c share)
 //   sigmoid:  ds = (q - sum q p) / sum s  +  c at the chosen
 //             (normalised: (c_k - sum c share) / sum of the chosen),  dl = ds s (1 - s)
+//
+// Where one expert is nearly all of a mean, its own difference from it is nothing but roundings.  The differences sum to
+// zero under the mean's weights, so that of an expert with more than half of them is taken from the others', which keep
+// their digits.
+constexpr float kLead = 0.5f;
 
 struct RouteBackArgs {
     RouteRule rule;
@@ -302,11 +307,16 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteBack
         }
         const float share = have ? one / of : 0.0f;
         const float mean = wave_sum(c * share);  // (every lane takes part)
-        mine = !have ? 0.0f : r.soft ? share * (c - mean) : (c - mean) / of;
+        float off = have ? c - mean : 0.0f;
+        if (wave_ballot(share > kLead) != 0) {  // sum share (c - mean) = mean (1 - sum share)
+            const float rest = wave_sum(share > kLead ? 0.0f : share * off);
+            off = share > kLead ? ((r.soft ? 0.0f : mean * (kShareFloor / of)) - rest) / share : off;
+        }
+        mine = !have ? 0.0f : r.soft ? share * off : off / of;
     } else
         mine = c;
     // row statistics
-    float big = 0.0f, sum = 0.0f, per = 0.0f, inner = 0.0f, score[R] = {};
+    float big = 0.0f, sum = 0.0f, per = 0.0f, inner = 0.0f, most = 0.0f, score[R] = {};
     const bool whole = a.dsums != nullptr || (r.soft && !r.normalize);  // every logit has a gradient
     auto raw = [&](float l) { return r.soft ? expf(l - big) : 1.0f / (1.0f + expf(-l)); };
     auto q_at = [&](int j) { return a.dsums != nullptr && j * 64 + lane < r.experts ? a.dsums[j * 64 + lane] : 0.0f; };
@@ -322,6 +332,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteBack
             if constexpr (VREG > 0)
                 score[j] = s;
             sum += s;
+            most = fmaxf(most, s);
             inner += q_at(j) * s;
         });
         sum = wave_sum(sum);
@@ -344,21 +355,45 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteBack
             for (int j = 0; j < R; ++j)
                 adds[j] += o == j * 64 + lane ? m : 0.0f;
         });
-    each([&](int j, float l) {
-        const int at = j * 64 + lane;
+    auto add_of = [&](int j) {
         float add = VREG > 0 ? adds[VREG > 0 ? j : 0] : 0.0f;
         if constexpr (VREG == 0)
-            slots([&](int o, float m) { add += o == at ? m : 0.0f; });
+            slots([&](int o, float m) { add += o == j * 64 + lane ? m : 0.0f; });
+        return add;
+    };
+    // p, and ds - sum p ds, of an expert of the row
+    auto p_of = [&](int j, float l) {
+        return whole && j * 64 + lane < r.experts ? (VREG > 0 ? score[VREG > 0 ? j : 0] : raw(l)) * per : 0.0f;
+    };
+    float held_off[R] = {};
+    auto off_of = [&](int j) {
+        return VREG > 0 ? held_off[VREG > 0 ? j : 0] : q_at(j) + (r.soft && !r.normalize ? add_of(j) : 0.0f) - inner;
+    };
+    if constexpr (VREG > 0)
+        if (whole)
+#pragma unroll
+            for (int j = 0; j < R; ++j)
+                held_off[j] = q_at(j) + (r.soft && !r.normalize ? adds[j] : 0.0f) - inner;
+    float rest = 0.0f;
+    const bool led = wave_ballot(most * per > kLead) != 0;
+    if (led) {
+        each([&](int j, float l) {
+            const float p = p_of(j, l);
+            rest += p > kLead ? 0.0f : p * off_of(j);
+        });
+        rest = wave_sum(rest);
+    }
+    each([&](int j, float l) {
+        const int at = j * 64 + lane;
+        const float p = p_of(j, l), off = led && p > kLead ? -rest / p : off_of(j);
+        const float add = !r.soft || r.normalize ? add_of(j) : 0.0f;
         if (at >= r.experts)
             return;
         float d;
         if (r.soft) {
-            const float s = whole ? (VREG > 0 ? score[VREG > 0 ? j : 0] : raw(l)) * per : 0.0f;
-            const float ds = q_at(j) + (r.normalize ? 0.0f : add);
-            d = whole ? s * (ds - inner) : 0.0f;
-            d += r.normalize ? add : 0.0f;
+            d = (whole ? p * off : 0.0f) + add;
         } else {
-            const float ds = add + (whole && sum != 0.0f ? (q_at(j) - inner) / sum : 0.0f);
+            const float ds = add + (whole && sum != 0.0f ? off / sum : 0.0f);
             // s (1 - s), from exp(-|l|): 1 - s of a rounded s would be nothing from l = 17 on
             const float x = expf(-fabsf(l)), y = 1.0f + x;
             d = ds * (x / (y * y));

@@ -136,3 +136,57 @@ def test_sigmoid_rows_with_a_nan_leave_the_others_choice_and_weights(E):
     for bias in (None, torch.zeros(E, device="cuda")):
         idx, w, sums = buf.route(l, r, bias=bias, score_sums=True)
         assert idx.tolist() == [[0, 2], [0, 1]] and (w == 0.5).all() and sums.isnan().all()
+
+
+def centred(p, v):
+    """p_i sum_j p_j (v_i - v_j) for weights p whose sum is one, and the magnitudes: no difference from a mean, so that it keeps
+    its digits where one weight is nearly one."""
+    d = v[:, :, None] - v[:, None, :]
+    m = (v.abs()[:, :, None] + v.abs()[:, None, :]) * (1 - torch.eye(v.shape[1], dtype=v.dtype, device=v.device))
+    return p * (d * p[:, None, :]).sum(2), p * (m * p[:, None, :]).sum(2)
+
+
+@pytest.mark.parametrize("E", [12, 128, 512, 600])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("with_sums", [False, True])
+def test_gradient_where_one_expert_is_nearly_everything(E, score, normalize, with_sums):
+    """One logit some 16 to 30 past all others: what is left of its gradient is of the others' size.  Scores are off by
+    (64 + 2 span) U, sums over a row are at most 40 terms deep; a difference is off by what its two sides are, here taken
+    without the part that they have in common."""
+    g = gen(E)
+    T, K, soft = 40, 5, score == "softmax"
+    l = torch.randn((T, E), generator=g, device="cuda")
+    top = torch.randint(0, E, (T, 1), generator=g, device="cuda")
+    gap = 16 + 14 * torch.rand((T, 1), generator=g, device="cuda")
+    l = (l if soft else l - gap - 8).scatter(1, top, gap if soft else torch.randn((T, 1), generator=g, device="cuda") - 4)
+    buf, r = epm.Buffer(1, E), epm.Router(K, score=score, normalize=normalize, scale=1.5)
+    idx, _, _ = buf.route(l, r)
+    assert (idx[:, :1] == top).all()
+    dw = torch.randn((T, K), generator=g, device="cuda")
+    q = torch.randn(E, generator=g, device="cuda") if with_sums else None
+    dl = buf.route_backward(dw, l, idx, r, dscore_sums=q)
+    ld = l.double()
+    s = torch.softmax(ld, 1) if soft else torch.sigmoid(ld)
+    p = s / s.sum(1, keepdim=True)
+    c = dw.double() * r.scale
+    qd = q.double().expand(T, E) if with_sums else torch.zeros((T, E), dtype=torch.float64, device="cuda")
+    one = s.gather(1, idx)
+    share = one / one.sum(1, keepdim=True)
+    if soft:
+        ref, mag = centred(p, qd if normalize else qd.scatter_add(1, idx, c))
+        if normalize:
+            a, m = centred(share, c)
+            ref, mag = ref.scatter_add(1, idx, a), mag.scatter_add(1, idx, m)
+    else:
+        a, m = centred(p, qd)  # p (q - sum q p): over p and the sum of the scores, which is over s
+        ref, mag = a / s, m / s
+        a, m = c, c.abs()
+        if normalize:  # (beside the sum of the chosen, 1e-20 leaves that much of each c)
+            of = one.sum(1, keepdim=True) + 1e-20
+            a, m = centred(share, c)
+            a, m = (a / share + c * (1e-20 / of)) / of, (m / share + c.abs() * (1e-20 / of)) / of
+        slope = s * torch.sigmoid(-ld)
+        ref, mag = ref.scatter_add(1, idx, a) * slope, mag.scatter_add(1, idx, m) * slope
+    rel = (64 + 2 * float(l.max() - l.min())) * U
+    close(dl, ref, mag * 2 * rel + 2.0 ** -120, "dlogits")
