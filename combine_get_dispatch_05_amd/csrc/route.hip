@@ -90,7 +90,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a)
 }
 
 // More experts than a wave holds: a block a token, keys of 64 bits in LDS, each thread every
-// 256th of them.  4096 tokens of 1024 experts in 8 groups: 165 us for 17 MB, and 30 for the gradient; the time is the
+// 256th of them.  4096 tokens of 1024 experts in 8 groups: 165 us for 17 MB, and 32 for the gradient; the time is the
 // K choices one after the other, each with four barriers, and the groups' scan by a thread each.
 template <class Op>
 __device__ __forceinline__ double block_reduce(double v, double *red, Op op)
@@ -385,7 +385,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteBack
     }
     each([&](int j, float l) {
         const int at = j * 64 + lane;
-        const float p = p_of(j, l), off = led && p > kLead ? -rest / p : off_of(j);
+        const float p = r.soft || led ? p_of(j, l) : 0.0f, off = led && p > kLead ? -rest / p : off_of(j);
         const float add = !r.soft || r.normalize ? add_of(j) : 0.0f;
         if (at >= r.experts)
             return;
