@@ -191,7 +191,9 @@ __device__ __forceinline__ bool keep_groups(const RouteRule &r, T (&key)[V], int
     // a sum is off by what its two keys are, which goes with their size: with biases that cancel the sum is small, its
     // error is not
     const float most = wave_max(fmaxf(one > none ? fabsf(float(one)) : 0.0f, two > none ? fabsf(float(two)) : 0.0f));
-    return high > -INFINITY && !(low - high > float(slack) * (1.0f + most));
+    // (two keys near the lowest number, as of barred experts, are not the -inf of a group without any)
+    const bool past = one > none && !(score > none);
+    return wave_ballot(past) != 0 || (high > -INFINITY && !(low - high > float(slack) * (1.0f + most)));
 }
 
 // The K largest keys, largest first, ties to the lowest index: lane k returns the k-th, -1 where

@@ -190,3 +190,26 @@ def test_gradient_where_one_expert_is_nearly_everything(E, score, normalize, wit
         ref, mag = ref.scatter_add(1, idx, a) * slope, mag.scatter_add(1, idx, m) * slope
     rel = (64 + 2 * float(l.max() - l.min())) * U
     close(dl, ref, mag * 2 * rel + 2.0 ** -120, "dlogits")
+
+
+@pytest.mark.parametrize("E", [48, 384, 960])
+@pytest.mark.parametrize("low", [torch.finfo(torch.float32).min, -3e38])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_barred_experts_come_before_those_that_cannot_be_chosen(E, low, score):
+    """A bias near the lowest number bars experts; two of a group sum to less than fp32 holds.  Groups on masked ranks have
+    no expert at all and come after them, wherever they lie."""
+    g = gen(E)
+    l = torch.randn((300, E), generator=g, device="cuda")
+    bias = torch.zeros(E, device="cuda")
+    size = E // 24
+    for group in (2, 3, 7, 8, 9, 15, 20):
+        bias[group * size:(group + 1) * size] = low
+    masked = [0, 1, 4, 5, 6, 10, 11, 16, 17, 18, 21, 22, 23]  # groups, which are ranks here; 12, 13, 14 and 19 are as usual
+    off = [e for e in range(E) if e // size in masked]
+    buf = epm.Buffer(24, E)
+    for rank in masked:
+        buf.low_latency_update_mask_buffer(rank, True)
+    for kept in (3, 5, 8, 11, 13):
+        r = epm.Router(min(64, 12 * size), score=score, num_groups=24, topk_groups=kept)
+        idx, _, _ = buf.route(l, r, bias=bias)
+        assert torch.equal(idx, choose(l.double(), r, bias, off)), kept
