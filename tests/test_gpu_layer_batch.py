@@ -42,3 +42,22 @@ def test_experts_whose_logits_hang_on_the_order_of_a_sum(E, H, f32):
         for t0 in (0, 64 - T):
             _, i, w = buf.low_latency_moe(x[t0:t0 + T].contiguous(), wr, r, w13, w2)
             assert torch.equal(i, idx[t0:t0 + T]) and torch.equal(w, wt[t0:t0 + T]), (T, t0)
+
+
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,H,I", [(40, 256, 8), (100, 8192, 8), (100, 264, 1032), (300, 16392, 8)])
+def test_weights_are_the_same_bits_wherever_the_choice_is_made(E, H, I, score, normalize):
+    """In the gate's blocks (one token; up to eight where those are few) or in a launch of its own."""
+    g = gen(E + H)
+    x = torch.randn((64, H), generator=g, device="cuda").to(torch.bfloat16)
+    wr = torch.randn((E, H), generator=g, device="cuda") * 2 / H ** 0.5
+    w13 = torch.zeros((E, 2 * I, H), dtype=torch.bfloat16, device="cuda")
+    w2 = torch.zeros((E, H, I), dtype=torch.bfloat16, device="cuda")
+    bias = torch.randn(E, generator=g, device="cuda") * 0.1
+    buf, r = epm.Buffer(1, E), epm.Router(3, score=score, num_groups=4, topk_groups=2, normalize=normalize)
+    _, idx, wt = buf.low_latency_moe(x, wr, r, w13, w2, bias=bias)
+    for T in (1, 2, 3, 8, 9, 20):
+        for t0 in (0, 30, 64 - T):
+            _, i, w = buf.low_latency_moe(x[t0:t0 + T].contiguous(), wr, r, w13, w2, bias=bias)
+            assert torch.equal(i, idx[t0:t0 + T]) and torch.equal(w, wt[t0:t0 + T]), (T, t0)
